@@ -18,10 +18,17 @@ CUDA kernels; calling any op without the built library raises.
     accept_tree(target_logits, draft_ids, parents, context_lens=None)
         -> (accepted, next, path); then kv_compact(k_cache, v_cache, block_tables,
         context_lens, path, accepted) moves the accepted branch's cached rows
+    kv="int4" on the _quant calls and kv_compact: a cache held in 4 bits
+        (caches uint8 [NB,K,16,H/2], scales uint8 [NB,K,16,H/32])
+    kv_append_slots(k_new, v_new, k_cache, v_cache, slots) / kv_gather_slots(...):
+        packed rows [M,K,H] into and out of a cache of any kind, by slot
+    plan_blocks(context_lens, new_lens, block_tables, held, free_ring, ring_state)
+        -> lengths, blocks and slots of a step, made on the GPU
 """
 from __future__ import annotations
 
 import ctypes
+import typing
 
 import torch
 
@@ -32,7 +39,7 @@ __all__ = ["kv_append", "kv_append_quant", "decode_attention", "verify_attention
            "decode_attention_quant", "verify_attention_quant", "append_decode_attention_quant",
            "append_verify_attention_quant", "append_decode_attention",
            "append_verify_attention", "accept_prefix", "accept_sampled", "accept_tree",
-           "kv_compact",
+           "kv_compact", "kv_append_slots", "kv_gather_slots", "plan_blocks", "BlockPlan",
            "attention_workspace_size", "reset_workspaces", "GqaError", "Status", "Shape"]
 
 
@@ -83,7 +90,12 @@ def _need_quant_cache(cache, scale, name):
 def kv_append_quant(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables,
                     context_lens, *, kv="int8", status=None, stream=None, pdl=False):
     """gqa_kv_append_quant: quantize k_new / v_new [B,T,K,H] (fp16 / bf16) row
-    by row into one-byte caches [NB,16,K,H] and their scales fp32 [NB,K,16]."""
+    by row into one-byte caches [NB,16,K,H] and their scales fp32 [NB,K,16].
+    kv="int4" (gqa_kv_append_fourbit): into 4-bit caches uint8 [NB,K,16,H/2] and
+    their scales uint8 [NB,K,16,H/32]."""
+    if kv == "int4":
+        return _append4(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables,
+                        context_lens, status, stream, pdl)
     _lib._need(k_new, "k_new", ndim=4)
     _lib._need(v_new, "v_new", k_new.dtype, 4)
     _need_quant_cache(k_cache, k_scale, "k_cache")
@@ -216,6 +228,10 @@ def append_verify_attention(q, k_new, v_new, k_cache, v_cache, block_tables, con
 def _attention_quant(fn_name, q, k_cache, v_cache, k_scale, v_scale, block_tables,
                      context_lens, out, scale, workspace, status, stream, pdl, early_kv, kv,
                      window=0, tree_mask=None):
+    if kv == "int4":
+        return _attention4(q, None, None, k_cache, v_cache, k_scale, v_scale, block_tables,
+                           context_lens, out, scale, workspace, status, stream, pdl, early_kv,
+                           window, tree_mask, "decode" in fn_name)
     _lib._need(q, "q", ndim=4)
     if tree_mask is not None:
         _lib._need(tree_mask, "tree_mask", torch.int64, 2)  # uint64 bits, held as int64
@@ -251,8 +267,9 @@ def _attention_quant(fn_name, q, k_cache, v_cache, k_scale, v_scale, block_table
 def decode_attention_quant(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
                            *, kv="int8", out=None, scale=None, workspace=None, status=None,
                            stream=None, pdl=False, early_kv=False, window=0):
-    """gqa_decode_attention_quant over a one-byte cache (kv = "int8" / "e4m3");
-    window > 0 is local attention as in decode_attention."""
+    """gqa_decode_attention_quant over a one-byte cache (kv = "int8" / "e4m3"),
+    or gqa_attention_fourbit over a 4-bit one (kv = "int4", layouts as in
+    kv_append_quant); window > 0 is local attention as in decode_attention."""
     return _attention_quant("gqa_decode_attention_quant", q, k_cache, v_cache, k_scale, v_scale,
                             block_tables, context_lens, out, scale, workspace, status, stream,
                             pdl, early_kv, kv, window)
@@ -261,7 +278,8 @@ def decode_attention_quant(q, k_cache, v_cache, k_scale, v_scale, block_tables, 
 def verify_attention_quant(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
                            *, kv="int8", out=None, scale=None, workspace=None, status=None,
                            stream=None, pdl=False, early_kv=False, window=0, tree_mask=None):
-    """gqa_verify_attention_quant over a one-byte cache (kv = "int8" / "e4m3");
+    """gqa_verify_attention_quant over a one-byte cache (kv = "int8" / "e4m3"), or
+    gqa_attention_fourbit over a 4-bit one (kv = "int4");
     window > 0 is local attention and tree_mask (int64 [B,T] holding the uint64
     mask rows) tree verification, as in verify_attention
     (gqa_tree_verify_attention_quant)."""
@@ -273,6 +291,10 @@ def verify_attention_quant(q, k_cache, v_cache, k_scale, v_scale, block_tables, 
 def _append_attention_quant(fn_name, q, k_new, v_new, k_cache, v_cache, k_scale, v_scale,
                             block_tables, context_lens, out, scale, workspace, status, stream,
                             pdl, early_kv, kv, window):
+    if kv == "int4":
+        return _attention4(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables,
+                           context_lens, out, scale, workspace, status, stream, pdl, early_kv,
+                           window, None, "decode" in fn_name)
     _lib._need(q, "q", ndim=4)
     _lib._need(k_new, "k_new", q.dtype, 4)
     _lib._need(v_new, "v_new", q.dtype, 4)
@@ -307,7 +329,8 @@ def append_decode_attention_quant(q, k_new, v_new, k_cache, v_cache, k_scale, v_
                                   pdl=False, early_kv=False, window=0):
     """gqa_append_decode_attention_quant: kv_append_quant of the new token and
     decode attention over the one-byte cache in one call (two launches; the
-    caches and their scales are written)."""
+    caches and their scales are written); kv = "int4" gives
+    gqa_append_attention_fourbit."""
     return _append_attention_quant("gqa_append_decode_attention_quant", q, k_new, v_new,
                                    k_cache, v_cache, k_scale, v_scale, block_tables,
                                    context_lens, out, scale, workspace, status, stream, pdl,
@@ -319,7 +342,8 @@ def append_verify_attention_quant(q, k_new, v_new, k_cache, v_cache, k_scale, v_
                                   scale=None, workspace=None, status=None, stream=None,
                                   pdl=False, early_kv=False, window=0):
     """gqa_append_verify_attention_quant: the T new tokens appended to the
-    one-byte cache and verify attention over it, in one call (two launches)."""
+    one-byte cache and verify attention over it, in one call (two launches);
+    kv = "int4" gives gqa_append_attention_fourbit."""
     return _append_attention_quant("gqa_append_verify_attention_quant", q, k_new, v_new,
                                    k_cache, v_cache, k_scale, v_scale, block_tables,
                                    context_lens, out, scale, workspace, status, stream, pdl,
@@ -418,7 +442,11 @@ def kv_compact(k_cache, v_cache, block_tables, context_lens, path, accepted, *, 
     context_lens[b] - 1 - a, context_lens as accept_tree left them) takes the
     cached K and V rows of node path[b][j-1].  Caches [NB,16,K,H] in q's dtype
     (kv="same"), or one-byte caches with their scales fp32 [NB,K,16]
-    (kv="int8" / "e4m3").  The tree size T is path.shape[1] + 1."""
+    (kv="int8" / "e4m3"), or 4-bit caches uint8 [NB,K,16,H/2] with theirs uint8
+    [NB,K,16,H/32] (kv="int4").  The tree size T is path.shape[1] + 1."""
+    if kv == "int4":
+        return _compact4(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, path,
+                         accepted, status, stream, pdl)
     if kv == "same":
         _lib._need(k_cache, "k_cache", ndim=4)
         _lib._need(v_cache, "v_cache", k_cache.dtype, 4)
@@ -481,3 +509,289 @@ def accept_sampled(target_probs, draft_probs, draft_ids, uniforms, context_lens=
                                        _status_arg(status), _lib._stream(stream))
     _lib._check("gqa_accept_sampled", rc)
     return accepted, next_token
+
+
+# ---- 4-bit cache -------------------------------------------------------------------------
+def _need_cache4(cache, scale, name):
+    _lib._need(cache, name, torch.uint8, 4)
+    _lib._need(scale, name + " scale", torch.uint8, 4)
+    NB, K, bs, half = cache.shape
+    if tuple(scale.shape) != (NB, K, bs, half // 16):
+        raise ValueError(f"{name} scale must be [{NB},{K},{bs},{half // 16}], got "
+                         f"{tuple(scale.shape)}")
+
+
+def _need_caches4(k_cache, v_cache, k_scale, v_scale):
+    _need_cache4(k_cache, k_scale, "k_cache")
+    _need_cache4(v_cache, v_scale, "v_cache")
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+
+
+def _need_tables(block_tables, context_lens, B):
+    _lib._need(block_tables, "block_tables", torch.int32, 2)
+    _lib._need(context_lens, "context_lens", torch.int32, 1)
+    if block_tables.shape[0] != B or context_lens.shape[0] != B:
+        raise ValueError(f"block_tables and context_lens must have {B} rows")
+
+
+def _need_rows4(x, name, B, T, K, dtype):
+    _lib._need(x, name, dtype, 4)
+    if tuple(x.shape[:3]) != (B, T, K):
+        raise ValueError(f"{name} must be [{B},{T},{K},H], got {tuple(x.shape)}")
+
+
+def _append4(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+             status, stream, pdl):
+    _need_caches4(k_cache, v_cache, k_scale, v_scale)
+    _lib._need(k_new, "k_new", ndim=4)
+    B, T = k_new.shape[:2]
+    _need_rows4(k_new, "k_new", B, T, k_cache.shape[1], None)
+    _need_rows4(v_new, "v_new", B, T, k_cache.shape[1], k_new.dtype)
+    if v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must have the same shape")
+    _need_tables(block_tables, context_lens, B)
+    shape = _lib.make_shape4(k_new, k_cache, block_tables.shape[1], None, B=B, T=T,
+                             N=k_cache.shape[1], flags=_lib.FLAG_PDL if pdl else 0)
+    P = _lib._ptr
+    dev = _lib.one_device(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables,
+                          context_lens, status)
+    with _lib.on_device(dev, stream) as s:
+        rc = _lib.lib().gqa_kv_append_fourbit(
+            ctypes.byref(shape), P(k_new), P(v_new), P(k_cache), P(v_cache), P(k_scale),
+            P(v_scale), P(block_tables), P(context_lens), _status_arg(status), _lib._stream(s))
+    _lib._check("gqa_kv_append_fourbit", rc)
+
+
+def _attention4(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                out, scale, workspace, status, stream, pdl, early_kv, window, tree_mask, decode):
+    _lib._need(q, "q", ndim=4)
+    B, T, N, H = q.shape
+    if decode and T != 1:
+        raise _lib.GqaError("gqa_attention_fourbit", _lib.Status.ERR_SHAPE)  # decode: T == 1
+    _need_caches4(k_cache, v_cache, k_scale, v_scale)
+    _need_tables(block_tables, context_lens, B)
+    fused = k_new is not None
+    if fused:
+        _need_rows4(k_new, "k_new", B, T, k_cache.shape[1], q.dtype)
+        _need_rows4(v_new, "v_new", B, T, k_cache.shape[1], q.dtype)
+        if k_new.shape[3] != H or v_new.shape[3] != H:
+            raise ValueError(f"k_new and v_new must have head size {H}")
+    if tree_mask is not None:
+        _lib._need(tree_mask, "tree_mask", torch.int64, 2)  # uint64 bits, held as int64
+        if tuple(tree_mask.shape) != (B, T):
+            raise ValueError(f"tree_mask must be [B,T] = {(B, T)}")
+    flags = (_lib.FLAG_PDL if pdl else 0) | (_lib.FLAG_EARLY_KV if early_kv else 0)
+    shape = _lib.make_shape4(q, k_cache, block_tables.shape[1], scale, B=B, T=T, N=N,
+                             flags=flags, window=window)
+    if out is not None:
+        _lib._need(out, "out", q.dtype, 4)
+        if out.shape != q.shape:
+            raise ValueError(f"out must be {tuple(q.shape)}, got {tuple(out.shape)}")
+    if workspace is not None:
+        _lib._need(workspace, "workspace", torch.uint8)
+    P = _lib._ptr
+    dev = _lib.one_device(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables,
+                          context_lens, tree_mask, out, workspace, status)
+    name = "gqa_append_attention_fourbit" if fused else "gqa_attention_fourbit"
+    new = (P(k_new), P(v_new)) if fused else ()
+    with _lib.on_device(dev, stream) as s:
+        if out is None:
+            out = torch.empty_like(q)
+        nbytes = _lib.workspace_size(shape)
+        if workspace is None:
+            workspace = _lib.get_workspace4(nbytes, dev, s)
+        rc = getattr(_lib.lib(), name)(
+            ctypes.byref(shape), P(q), *new, P(k_cache), P(v_cache), P(k_scale), P(v_scale),
+            P(block_tables), P(context_lens), P(tree_mask), P(out), P(workspace),
+            workspace.numel(), _status_arg(status), _lib._stream(s))
+    _lib._check(name, rc)
+    return out
+
+
+def _compact4(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, path, accepted,
+              status, stream, pdl):
+    _need_caches4(k_cache, v_cache, k_scale, v_scale)
+    B = block_tables.shape[0]
+    _need_tables(block_tables, context_lens, B)
+    _lib._need(path, "path", torch.int32, 2)
+    _lib._need(accepted, "accepted", torch.int32, 1)
+    if accepted.shape[0] != B or path.shape[0] != B:
+        raise ValueError(f"accepted and path must have {B} rows")
+    NB, K, bs, half = k_cache.shape
+    shape = _lib.Shape(B=B, T=path.shape[1] + 1, N=K, K=K, H=2 * half, block_size=bs,
+                       num_blocks=NB, max_blocks_per_seq=block_tables.shape[1], dtype=0,
+                       scale=0.0, flags=_lib.FLAG_PDL if pdl else 0, window=0,
+                       kv_dtype=_lib.KV_DTYPES["int4"])
+    P = _lib._ptr
+    dev = _lib.one_device(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, path,
+                          accepted, status)
+    with _lib.on_device(dev, stream) as s:
+        rc = _lib.lib().gqa_kv_compact_fourbit(
+            ctypes.byref(shape), P(k_cache), P(v_cache), P(k_scale), P(v_scale),
+            P(block_tables), P(context_lens), P(path), P(accepted), _status_arg(status),
+            _lib._stream(s))
+    _lib._check("gqa_kv_compact_fourbit", rc)
+
+
+# ---- rows by slot --------------------------------------------------------------------------
+def _slots_shape(rows, k_cache, v_cache, k_scale, v_scale, kv, pdl):
+    """Checks caches and packed rows [M,K,H] of a call by slot; its shape."""
+    if kv not in _lib.KV_DTYPES:
+        raise ValueError(f"kv must be one of {sorted(_lib.KV_DTYPES)}, got {kv!r}")
+    if rows.dtype not in _lib._DTYPES:
+        raise ValueError(f"dtype {rows.dtype} unsupported (fp16 / bf16)")
+    H = rows.shape[2]
+    flags = _lib.FLAG_PDL if pdl else 0
+    if kv == "int4":
+        _need_caches4(k_cache, v_cache, k_scale, v_scale)
+        K = k_cache.shape[1]
+        shape = _lib.make_shape4(rows, k_cache, 1, None, B=0, T=1, N=K, flags=flags)
+    else:
+        if kv == "same":
+            _lib._need(k_cache, "k_cache", rows.dtype, 4)
+            _lib._need(v_cache, "v_cache", rows.dtype, 4)
+            if k_scale is not None or v_scale is not None:
+                raise ValueError('kv="same" takes no scales')
+        else:
+            _need_quant_cache(k_cache, k_scale, "k_cache")
+            _need_quant_cache(v_cache, v_scale, "v_cache")
+        if k_cache.shape != v_cache.shape:
+            raise ValueError("k_cache and v_cache must have the same shape")
+        NB, bs, K, Hc = k_cache.shape
+        if Hc != H:
+            raise ValueError(f"head size mismatch: {H} vs {Hc}")
+        shape = _lib.Shape(B=0, T=1, N=K, K=K, H=H, block_size=bs, num_blocks=NB,
+                           max_blocks_per_seq=1, dtype=_lib._DTYPES[rows.dtype], scale=0.0,
+                           flags=flags, window=0, kv_dtype=_lib.KV_DTYPES[kv])
+    if rows.shape[1] != K:
+        raise ValueError(f"rows have {rows.shape[1]} KV heads, the cache {K}")
+    return shape
+
+
+def kv_append_slots(k_new, v_new, k_cache, v_cache, slots, *, k_scale=None, v_scale=None,
+                    kv="same", status=None, stream=None, pdl=False):
+    """gqa_kv_append_slots: packed rows k_new / v_new [M,K,H] (fp16 / bf16) into
+    the slots slots[i] = block * 16 + row (int32 [M], -1: no slot) of a cache of
+    any kind: kv="same" ([NB,16,K,H] in the rows' dtype, no scales), "int8" /
+    "e4m3" (one byte, scales fp32 [NB,K,16]) or "int4" ([NB,K,16,H/2], scales
+    uint8 [NB,K,16,H/32]).  The slots of one call must differ."""
+    _lib._need(k_new, "k_new", ndim=3)
+    _lib._need(v_new, "v_new", k_new.dtype, 3)
+    if v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must have the same shape")
+    _lib._need(slots, "slots", torch.int32, 1)
+    M = k_new.shape[0]
+    if slots.shape[0] != M:
+        raise ValueError(f"slots must have {M} entries, got {slots.shape[0]}")
+    shape = _slots_shape(k_new, k_cache, v_cache, k_scale, v_scale, kv, pdl)
+    P = _lib._ptr
+    dev = _lib.one_device(k_new, v_new, k_cache, v_cache, k_scale, v_scale, slots, status)
+    with _lib.on_device(dev, stream) as s:
+        rc = _lib.lib().gqa_kv_append_slots(ctypes.byref(shape), M, P(k_new), P(v_new),
+                                            P(k_cache), P(v_cache), P(k_scale), P(v_scale),
+                                            P(slots), _status_arg(status), _lib._stream(s))
+    _lib._check("gqa_kv_append_slots", rc)
+
+
+def kv_gather_slots(k_cache, v_cache, slots, *, k_scale=None, v_scale=None, kv="same",
+                    dtype=None, k_out=None, v_out=None, status=None, stream=None, pdl=False):
+    """gqa_kv_gather_slots: the cached rows of slots (int32 [M]; -1: zeros) as
+    packed rows [M,K,H] in `dtype` (fp16 / bf16; the cache's own for
+    kv="same").  Returns (k_out, v_out).  Caches and scales as in
+    kv_append_slots."""
+    _lib._need(slots, "slots", torch.int32, 1)
+    _lib._need(k_cache, "k_cache", ndim=4)
+    M = slots.shape[0]
+    K, H = ((k_cache.shape[1], 2 * k_cache.shape[3]) if kv == "int4"
+            else (k_cache.shape[2], k_cache.shape[3]))
+    if dtype is None:
+        dtype = k_cache.dtype if kv == "same" else (torch.bfloat16 if k_out is None
+                                                    else k_out.dtype)
+    given = [(t, n) for t, n in ((k_out, "k_out"), (v_out, "v_out")) if t is not None]
+    for t, n in given:
+        _lib._need(t, n, dtype, 3)
+        if tuple(t.shape) != (M, K, H):
+            raise ValueError(f"{n} must be [{M},{K},{H}], got {tuple(t.shape)}")
+    dev = _lib.one_device(k_cache, v_cache, k_scale, v_scale, slots, k_out, v_out, status)
+    P = _lib._ptr
+    with _lib.on_device(dev, stream) as s:
+        k_out = torch.empty((M, K, H), dtype=dtype, device=dev) if k_out is None else k_out
+        v_out = torch.empty((M, K, H), dtype=dtype, device=dev) if v_out is None else v_out
+        shape = _slots_shape(k_out, k_cache, v_cache, k_scale, v_scale, kv, pdl)
+        rc = _lib.lib().gqa_kv_gather_slots(ctypes.byref(shape), M, P(k_cache), P(v_cache),
+                                            P(k_scale), P(v_scale), P(slots), P(k_out),
+                                            P(v_out), _status_arg(status), _lib._stream(s))
+    _lib._check("gqa_kv_gather_slots", rc)
+    return k_out, v_out
+
+
+# ---- blocks of a step ------------------------------------------------------------------------
+class BlockPlan(typing.NamedTuple):
+    """What plan_blocks returns (block_tables and free_ring are updated in place)."""
+    context_lens: torch.Tensor  # int32 [B] lengths with the new tokens
+    held: torch.Tensor          # int32 [B] block-table entries in use
+    ring_state: torch.Tensor    # int32 [2] head and count of the free ring
+    cu_new: torch.Tensor        # int32 [B+1] first new token of each sequence
+    slots: typing.Optional[torch.Tensor]      # int32 [max_tokens], -1 past the last
+    positions: typing.Optional[torch.Tensor]  # int32 [max_tokens], -1 past the last
+
+
+def plan_blocks(context_lens, new_lens, block_tables, held, free_ring, ring_state, *,
+                max_tokens=None, context_lens_out=None, held_out=None, ring_state_out=None,
+                cu_new=None, slots=None, positions=None, in_place=False, status=None,
+                stream=None, pdl=False) -> BlockPlan:
+    """gqa_plan_blocks: grow every sequence by new_lens[b] tokens (int32 [B]; -1:
+    finished, all its blocks go back), taking free block ids from the ring
+    (free_ring int32 [num_blocks], ring_state int32 [2] = head, count) into
+    block_tables [B, max_blocks] and returning those past ceil(length / 16);
+    held int32 [B] counts each table's entries in use.  Slots and positions are
+    made for up to max_tokens new tokens (default: the length of `slots`;
+    neither given: no slot map).  The lengths, counts and state come back in new
+    tensors, in the given ones, or with in_place=True in the inputs' own."""
+    for t, n, d in ((context_lens, "context_lens", 1), (new_lens, "new_lens", 1),
+                    (block_tables, "block_tables", 2), (held, "held", 1),
+                    (free_ring, "free_ring", 1), (ring_state, "ring_state", 1)):
+        _lib._need(t, n, torch.int32, d)
+    B, mb = block_tables.shape
+    if any(t.shape[0] != B for t in (context_lens, new_lens, held)):
+        raise ValueError(f"context_lens, new_lens and held must have {B} entries")
+    if ring_state.shape[0] != 2:
+        raise ValueError("ring_state must be [2]: head and count")
+    if max_tokens is None:
+        max_tokens = -1 if slots is None else slots.shape[0]
+    if in_place:
+        if any(t is not None for t in (context_lens_out, held_out, ring_state_out)):
+            raise ValueError("in_place=True takes no output tensors for what it updates")
+        context_lens_out, held_out, ring_state_out = context_lens, held, ring_state
+    dev = _lib.one_device(context_lens, new_lens, block_tables, held, free_ring, ring_state,
+                          context_lens_out, held_out, ring_state_out, cu_new, slots, positions,
+                          status)
+    P = _lib._ptr
+    with _lib.on_device(dev, stream) as s:
+        def made(t, n, size):
+            if t is None:
+                return torch.empty(size, dtype=torch.int32, device=dev)
+            _lib._need(t, n, torch.int32, 1)
+            if t.shape[0] != size:
+                raise ValueError(f"{n} must have {size} entries, got {t.shape[0]}")
+            return t
+
+        context_lens_out = made(context_lens_out, "context_lens_out", B)
+        held_out = made(held_out, "held_out", B)
+        ring_state_out = made(ring_state_out, "ring_state_out", 2)
+        cu_new = made(cu_new, "cu_new", B + 1)
+        if max_tokens >= 0:
+            slots = made(slots, "slots", max_tokens)
+            positions = made(positions, "positions", max_tokens)
+        elif positions is not None:
+            raise ValueError("positions need slots or max_tokens")
+        some = max_tokens > 0
+        rc = _lib.lib().gqa_plan_blocks(
+            B, mb, free_ring.shape[0], max_tokens, P(context_lens), P(new_lens), P(held),
+            P(ring_state), P(free_ring), P(block_tables), P(context_lens_out), P(held_out),
+            P(ring_state_out), P(cu_new), P(slots) if some else None,
+            P(positions) if some else None, _lib.FLAG_PDL if pdl else 0, _status_arg(status),
+            _lib._stream(s))
+    _lib._check("gqa_plan_blocks", rc)
+    return BlockPlan(context_lens_out, held_out, ring_state_out, cu_new, slots, positions)

@@ -33,9 +33,10 @@ class Status(enum.IntEnum):
     ERR_TIMEOUT = 9
     ERR_PROBS = 10
     ERR_TREE = 11
+    ERR_BLOCKS = 12
 
 
-KV_DTYPES = {"same": 0, "int8": 1, "e4m3": 2}
+KV_DTYPES = {"same": 0, "int8": 1, "e4m3": 2, "int4": 3}
 
 
 class GqaError(RuntimeError):
@@ -71,7 +72,9 @@ EXPORTS = ("gqa_version", "gqa_status_string", "gqa_kv_append",
            "gqa_decode_attention_quant", "gqa_verify_attention_quant",
            "gqa_append_decode_attention_quant", "gqa_append_verify_attention_quant",
            "gqa_tree_verify_attention_quant", "gqa_accept_tree", "gqa_kv_compact",
-           "gqa_attention_engine")
+           "gqa_attention_engine", "gqa_kv_append_fourbit", "gqa_attention_fourbit",
+           "gqa_append_attention_fourbit", "gqa_kv_compact_fourbit", "gqa_kv_append_slots",
+           "gqa_kv_gather_slots", "gqa_plan_blocks")
 
 
 def lib() -> ctypes.CDLL:
@@ -130,6 +133,18 @@ def lib() -> ctypes.CDLL:
         L.gqa_accept_tree.argtypes = [I, I, I] + [P] * 8 + [ctypes.c_size_t, P, P]
         L.gqa_kv_compact.restype = I
         L.gqa_kv_compact.argtypes = [S] + [P] * 10
+        Z, N = ctypes.c_size_t, ctypes.c_int64
+        for name, args in (
+                ("gqa_kv_append_fourbit", [S] + [P] * 10),
+                ("gqa_attention_fourbit", [S] + [P] * 10 + [Z, P, P]),
+                ("gqa_append_attention_fourbit", [S] + [P] * 12 + [Z, P, P]),
+                ("gqa_kv_compact_fourbit", [S] + [P] * 10),
+                ("gqa_kv_append_slots", [S, N] + [P] * 9),
+                ("gqa_kv_gather_slots", [S, N] + [P] * 9),
+                ("gqa_plan_blocks", [I] * 4 + [P] * 12 + [ctypes.c_uint, P, P])):
+            f = getattr(L, name)
+            f.restype = I
+            f.argtypes = args
         _lib = L
         return L
 
@@ -182,6 +197,64 @@ def make_shape(q_or_new: torch.Tensor, k_cache: torch.Tensor, block_tables: torc
                  num_blocks=NB, max_blocks_per_seq=block_tables.shape[1],
                  dtype=_DTYPES[q_or_new.dtype], scale=float(scale or 0.0), flags=int(flags),
                  window=int(window), kv_dtype=KV_DTYPES[kv])
+
+
+def one_device(*tensors) -> torch.device:
+    """The device all the given tensors (None skipped) are on."""
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) != 1:
+        raise ValueError(f"tensors must be on one device, got {sorted(map(str, devs))}")
+    return devs.pop()
+
+
+class on_device:
+    """`with on_device(dev, stream) as s`: dev is the current device inside and
+    s the stream to launch on (`stream`, or the current one of dev), current
+    too, so that outputs allocated inside belong to it."""
+
+    def __init__(self, dev: torch.device, stream=None):
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        self.dev, self.stream = dev, stream
+
+    def __enter__(self):
+        self._d = torch.cuda.device(self.dev)
+        self._d.__enter__()
+        s = torch.cuda.current_stream(self.dev) if self.stream is None else self.stream
+        self._s = torch.cuda.stream(s)
+        self._s.__enter__()
+        return s
+
+    def __exit__(self, *exc):
+        self._s.__exit__(*exc)
+        self._d.__exit__(*exc)
+
+
+def make_shape4(rows: torch.Tensor, k_cache: torch.Tensor, max_blocks: int, scale, *, B: int,
+                T: int, N: int, flags: int = 0, window: int = 0) -> Shape:
+    """The shape of a 4-bit cache call: caches [NB,K,16,H/2]; rows [.., H]."""
+    NB, K, bs, half = k_cache.shape
+    H = rows.shape[-1]
+    if 2 * half != H:
+        raise ValueError(f"head size mismatch: {H} vs {2 * half} (two codes a byte)")
+    if rows.dtype not in _DTYPES:
+        raise ValueError(f"dtype {rows.dtype} unsupported (fp16 / bf16)")
+    return Shape(B=B, T=T, N=N, K=K, H=H, block_size=bs, num_blocks=NB,
+                 max_blocks_per_seq=max_blocks, dtype=_DTYPES[rows.dtype],
+                 scale=float(scale or 0.0), flags=int(flags), window=int(window),
+                 kv_dtype=KV_DTYPES["int4"])
+
+
+def get_workspace4(nbytes: int, device, stream) -> torch.Tensor:
+    """The workspace of a 4-bit attention call: the attention workspace of the
+    stream.  Under graph capture a buffer of the graph's own, its ticket region
+    cleared by every replay: two graphs captured on one stream may then run at
+    the same time (a caller that passes its own workspace saves the clearing)."""
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        ws[:1 << 14].zero_()  # one int32 ticket per thread block
+        return ws
+    return get_workspace(nbytes, device, stream)
 
 
 _ws_cache: dict = {}

@@ -24,6 +24,77 @@ gqa_status check_common(const gqa_shape* s) {
     return GQA_OK;
 }
 
+// The shape of a 4-bit call: the common checks on everything but kv_dtype.
+gqa_status check_fourbit(const gqa_shape* s) {
+    if (!s) return GQA_ERR_NULL;
+    if (s->kv_dtype != GQA_KV_INT4) return GQA_ERR_DTYPE;
+    gqa_shape sh = *s;
+    sh.kv_dtype = GQA_KV_SAME;
+    const gqa_status st = check_common(&sh);
+    if (st != GQA_OK) return st;
+    // the other kernels do not serve it
+    if (s->flags & (GQA_FLAG_WARP_MMA | GQA_FLAG_TENSOR_MEMORY | GQA_FLAG_DIRECT))
+        return GQA_ERR_SHAPE;
+    return GQA_OK;
+}
+
+gqa_status attention_fourbit_entry(const gqa_shape* s, bool fused, const void* q,
+                                   const void* k_new, const void* v_new, const uint8_t* k_cache,
+                                   const uint8_t* v_cache, const uint8_t* k_scale,
+                                   const uint8_t* v_scale, const int32_t* block_tables,
+                                   const int32_t* context_lens, const uint64_t* tree_mask,
+                                   void* out, void* workspace, size_t ws_bytes,
+                                   int32_t* dev_status, void* stream) {
+    gqa_status st = check_fourbit(s);
+    if (st != GQA_OK) return st;
+    if (tree_mask && (s->window > 0 || s->T > 64)) return GQA_ERR_SHAPE;
+    if (s->B == 0) return GQA_OK;
+    if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_tables || !context_lens ||
+        !out || (fused && (!k_new || !v_new)))
+        return GQA_ERR_NULL;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scale) ||
+        !aligned16(v_scale) || !aligned16(out) || (fused && (!aligned16(k_new) || !aligned16(v_new))))
+        return GQA_ERR_ALIGN;
+    if (tree_mask && (reinterpret_cast<uintptr_t>(tree_mask) & 7u) != 0) return GQA_ERR_ALIGN;
+    size_t need = 0;
+    st = gqa::fourbit_workspace_bytes(*s, &need);
+    if (st != GQA_OK) return st;
+    if (!workspace || ws_bytes < need) return GQA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return GQA_ERR_ALIGN;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (fused) {
+        st = gqa::launch_kv_append_slots(
+            *s, (long long)s->B * s->T, k_new, v_new, const_cast<uint8_t*>(k_cache),
+            const_cast<uint8_t*>(v_cache), const_cast<uint8_t*>(k_scale),
+            const_cast<uint8_t*>(v_scale), nullptr, block_tables, context_lens, dev_status, cs);
+        if (st != GQA_OK) return st;
+    }
+    return gqa::launch_attention_fourbit(*s, q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                                         context_lens, tree_mask, out, workspace, ws_bytes,
+                                         dev_status, cs);
+}
+
+// Arguments of the calls that move rows by slot.
+gqa_status check_slots(const gqa_shape* s, long long rows, const void* k, const void* v,
+                       const void* k_cache, const void* v_cache, const void* k_scale,
+                       const void* v_scale, const int32_t* slots) {
+    if (!s) return GQA_ERR_NULL;
+    gqa_shape sh = *s;
+    if (sh.kv_dtype == GQA_KV_INT4) sh.kv_dtype = GQA_KV_SAME;
+    const gqa_status st = check_common(&sh);
+    if (st != GQA_OK) return st;
+    if (rows < 0 || rows > (1ll << 31) - 1) return GQA_ERR_SHAPE;
+    const bool scaled = s->kv_dtype != GQA_KV_SAME;
+    if (!scaled && (k_scale || v_scale)) return GQA_ERR_DTYPE;  // the rows carry no scales
+    if (rows == 0) return GQA_OK;
+    if (!k || !v || !k_cache || !v_cache || !slots || (scaled && (!k_scale || !v_scale)))
+        return GQA_ERR_NULL;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) ||
+        !aligned16(k_scale) || !aligned16(v_scale))
+        return GQA_ERR_ALIGN;
+    return GQA_OK;
+}
+
 gqa_status attention_entry(const gqa_shape* s, bool decode_only, bool fused, const void* q,
                            const void* k_new, const void* v_new, const void* k_cache,
                            const void* v_cache, const int32_t* block_tables,
@@ -99,7 +170,7 @@ gqa_status attention_entry(const gqa_shape* s, bool decode_only, bool fused, con
 
 extern "C" {
 
-int gqa_version(void) { return 200; }
+int gqa_version(void) { return 300; }
 
 const char* gqa_status_string(int status) {
     switch (status) {
@@ -115,6 +186,7 @@ const char* gqa_status_string(int status) {
         case GQA_ERR_TIMEOUT: return "bounded wait inside a kernel timed out";
         case GQA_ERR_PROBS: return "invalid probability, uniform or empty distribution";
         case GQA_ERR_TREE: return "draft tree parent or accepted path out of range";
+        case GQA_ERR_BLOCKS: return "no free blocks or token slots left, or an inconsistent free ring";
         default: return "unknown status";
     }
 }
@@ -154,6 +226,8 @@ gqa_status gqa_kv_append_quant(const gqa_shape* shape, const void* k_new, const 
 }
 
 int gqa_attention_engine(const gqa_shape* shape) {
+    if (shape && shape->kv_dtype == GQA_KV_INT4)
+        return check_fourbit(shape) == GQA_OK ? GQA_ENGINE_FOURBIT : 0;
     if (check_common(shape) != GQA_OK) return 0;
     const bool force_warp = (shape->flags & GQA_FLAG_WARP_MMA) != 0;
     const bool force_tc = (shape->flags & GQA_FLAG_TENSOR_MEMORY) != 0;
@@ -168,6 +242,11 @@ int gqa_attention_engine(const gqa_shape* shape) {
 }
 
 size_t gqa_attention_workspace_size(const gqa_shape* shape) {
+    if (shape && shape->kv_dtype == GQA_KV_INT4) {
+        size_t need = 0;
+        if (check_fourbit(shape) != GQA_OK) return 0;
+        return gqa::fourbit_workspace_bytes(*shape, &need) == GQA_OK ? need : 0;
+    }
     if (check_common(shape) != GQA_OK) return 0;
     // the largest need of the kernels that may serve the shape (the direct
     // kernel uses none, so its flag does not change the size)
@@ -395,6 +474,116 @@ gqa_status gqa_accept_sampled(int B, int T, int V, const float* target_probs,
                                       T > 1 ? draft_ids : nullptr, uniforms, accepted,
                                       next_token, context_lens_inout, dev_status,
                                       static_cast<cudaStream_t>(stream));
+}
+
+gqa_status gqa_kv_append_fourbit(const gqa_shape* shape, const void* k_new, const void* v_new,
+                                 uint8_t* k_cache, uint8_t* v_cache, uint8_t* k_scale,
+                                 uint8_t* v_scale, const int32_t* block_tables,
+                                 const int32_t* context_lens, int32_t* dev_status, void* stream) {
+    const gqa_status st = check_fourbit(shape);
+    if (st != GQA_OK) return st;
+    if (shape->B == 0) return GQA_OK;
+    if (!k_new || !v_new || !k_cache || !v_cache || !k_scale || !v_scale || !block_tables ||
+        !context_lens)
+        return GQA_ERR_NULL;
+    if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_cache) || !aligned16(v_cache) ||
+        !aligned16(k_scale) || !aligned16(v_scale))
+        return GQA_ERR_ALIGN;
+    return gqa::launch_kv_append_slots(*shape, (long long)shape->B * shape->T, k_new, v_new,
+                                       k_cache, v_cache, k_scale, v_scale, nullptr, block_tables,
+                                       context_lens, dev_status, static_cast<cudaStream_t>(stream));
+}
+
+gqa_status gqa_attention_fourbit(const gqa_shape* shape, const void* q, const uint8_t* k_cache,
+                                 const uint8_t* v_cache, const uint8_t* k_scale,
+                                 const uint8_t* v_scale, const int32_t* block_tables,
+                                 const int32_t* context_lens, const uint64_t* tree_mask,
+                                 void* out, void* workspace, size_t workspace_bytes,
+                                 int32_t* dev_status, void* stream) {
+    return attention_fourbit_entry(shape, false, q, nullptr, nullptr, k_cache, v_cache, k_scale,
+                                   v_scale, block_tables, context_lens, tree_mask, out,
+                                   workspace, workspace_bytes, dev_status, stream);
+}
+
+gqa_status gqa_append_attention_fourbit(const gqa_shape* shape, const void* q, const void* k_new,
+                                        const void* v_new, uint8_t* k_cache, uint8_t* v_cache,
+                                        uint8_t* k_scale, uint8_t* v_scale,
+                                        const int32_t* block_tables, const int32_t* context_lens,
+                                        const uint64_t* tree_mask, void* out, void* workspace,
+                                        size_t workspace_bytes, int32_t* dev_status,
+                                        void* stream) {
+    return attention_fourbit_entry(shape, true, q, k_new, v_new, k_cache, v_cache, k_scale,
+                                   v_scale, block_tables, context_lens, tree_mask, out,
+                                   workspace, workspace_bytes, dev_status, stream);
+}
+
+gqa_status gqa_kv_compact_fourbit(const gqa_shape* shape, uint8_t* k_cache, uint8_t* v_cache,
+                                  uint8_t* k_scale, uint8_t* v_scale,
+                                  const int32_t* block_tables, const int32_t* context_lens,
+                                  const int32_t* path, const int32_t* accepted,
+                                  int32_t* dev_status, void* stream) {
+    const gqa_status st = check_fourbit(shape);
+    if (st != GQA_OK) return st;
+    if (shape->T > 64) return GQA_ERR_SHAPE;
+    if (shape->B == 0 || shape->T == 1) return GQA_OK;  // nothing can move
+    if (!k_cache || !v_cache || !k_scale || !v_scale || !block_tables || !context_lens || !path ||
+        !accepted)
+        return GQA_ERR_NULL;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scale) || !aligned16(v_scale))
+        return GQA_ERR_ALIGN;
+    return gqa::launch_kv_compact(*shape, k_cache, v_cache, k_scale, v_scale, block_tables,
+                                  context_lens, path, accepted, dev_status,
+                                  static_cast<cudaStream_t>(stream));
+}
+
+gqa_status gqa_kv_append_slots(const gqa_shape* shape, int64_t rows, const void* k_new,
+                               const void* v_new, void* k_cache, void* v_cache, void* k_scale,
+                               void* v_scale, const int32_t* slots, int32_t* dev_status,
+                               void* stream) {
+    const gqa_status st = check_slots(shape, rows, k_new, v_new, k_cache, v_cache, k_scale,
+                                      v_scale, slots);
+    if (st != GQA_OK || rows == 0) return st;
+    return gqa::launch_kv_append_slots(*shape, rows, k_new, v_new, k_cache, v_cache, k_scale,
+                                       v_scale, slots, nullptr, nullptr, dev_status,
+                                       static_cast<cudaStream_t>(stream));
+}
+
+gqa_status gqa_kv_gather_slots(const gqa_shape* shape, int64_t rows, const void* k_cache,
+                               const void* v_cache, const void* k_scale, const void* v_scale,
+                               const int32_t* slots, void* k_out, void* v_out,
+                               int32_t* dev_status, void* stream) {
+    const gqa_status st = check_slots(shape, rows, k_out, v_out, k_cache, v_cache, k_scale,
+                                      v_scale, slots);
+    if (st != GQA_OK || rows == 0) return st;
+    return gqa::launch_kv_gather_slots(*shape, rows, k_cache, v_cache, k_scale, v_scale, slots,
+                                       k_out, v_out, dev_status,
+                                       static_cast<cudaStream_t>(stream));
+}
+
+gqa_status gqa_plan_blocks(int B, int max_blocks_per_seq, int num_blocks, int max_tokens,
+                           const int32_t* context_lens, const int32_t* new_lens,
+                           const int32_t* held, const int32_t* ring_state, int32_t* free_ring,
+                           int32_t* block_tables, int32_t* context_lens_out, int32_t* held_out,
+                           int32_t* ring_state_out, int32_t* cu_new, int32_t* slots,
+                           int32_t* positions, unsigned int flags, int32_t* dev_status,
+                           void* stream) {
+    if (B < 0 || B > 16384 || max_blocks_per_seq < 1 || num_blocks < 1 || max_tokens < -1)
+        return GQA_ERR_SHAPE;
+    if ((long long)num_blocks * 16 > (1ll << 31) - 1 ||
+        (long long)max_blocks_per_seq * 16 > (1ll << 30) ||
+        (long long)B * max_blocks_per_seq > (1ll << 31) - 1)
+        return GQA_ERR_SHAPE;
+    if (!ring_state || !free_ring || !ring_state_out || !cu_new) return GQA_ERR_NULL;
+    if (B > 0 && (!context_lens || !new_lens || !held || !block_tables || !context_lens_out ||
+                  !held_out))
+        return GQA_ERR_NULL;
+    if ((max_tokens > 0) != (slots != nullptr) || (positions && !slots)) return GQA_ERR_NULL;
+    return gqa::launch_plan_blocks(B, max_blocks_per_seq, num_blocks, max_tokens,
+                                   context_lens, new_lens, held, ring_state, free_ring,
+                                   block_tables, context_lens_out, held_out, ring_state_out,
+                                   cu_new, slots, positions,
+                                   (flags & (GQA_FLAG_PDL | GQA_FLAG_EARLY_KV)) != 0, dev_status,
+                                   static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -26,14 +26,19 @@ constexpr int kThreads = 128;
 constexpr int kMaxT = 64;
 constexpr int kMaxRowVec = 16;  // 16-byte chunks of one cached row (H = 128, 2-byte elements)
 
+// HEAD_MAJOR: the 4-bit cache's [block][KV head][row] order (fourbit.cuh); the
+// others keep [block][row][KV head].  Scale: the unit a row's scales move in,
+// [block][KV head][row] in every cache -- an fp32 (one byte codes), or H/32
+// bytes of 4-bit scales.
+template <bool HEAD_MAJOR, typename Scale>
 __global__ void __launch_bounds__(kThreads)
-    kv_compact_kernel(uint4* k_cache, uint4* v_cache, float* k_scale, float* v_scale,
+    kv_compact_kernel(uint4* k_cache, uint4* v_cache, Scale* k_scale, Scale* v_scale,
                       const int32_t* __restrict__ block_tables,
                       const int32_t* __restrict__ context_lens, const int32_t* __restrict__ path,
                       const int32_t* __restrict__ accepted, int32_t* status, int T, int K,
                       int row_vec, int max_blocks, int num_blocks) {
     __shared__ uint4 stage[2 * (kMaxT - 1) * kMaxRowVec];
-    __shared__ float sscale[2 * (kMaxT - 1)];
+    __shared__ Scale sscale[2 * (kMaxT - 1)];
     __shared__ int spath[kMaxT];
     griddep_launch_dependents();
     griddep_wait();  // accepted, path and context_lens follow the acceptance kernel
@@ -71,6 +76,10 @@ __global__ void __launch_bounds__(kThreads)
         return;
     }
     if (a == 0) return;
+    auto row_of = [&](long long pos) -> size_t {
+        const size_t blk = table[pos >> 4];
+        return HEAD_MAJOR ? (blk * K + k) * 16 + (pos & 15) : (blk * 16 + (pos & 15)) * K + k;
+    };
     // every source row (K then V chunks of node p_j's row) into shared memory ...
     const int per_node = 2 * row_vec;
     const int items = a * per_node;
@@ -78,7 +87,7 @@ __global__ void __launch_bounds__(kThreads)
         const int j = it / per_node, r = it - j * per_node;
         const int v = r >= row_vec, c = r - v * row_vec;
         const long long pos = base + spath[j];
-        const size_t off = (((size_t)table[pos >> 4] * 16 + (pos & 15)) * K + k) * row_vec + c;
+        const size_t off = row_of(pos) * row_vec + c;
         stage[it] = (v ? v_cache : k_cache)[off];
     }
     if (k_scale && tid < 2 * a) {
@@ -92,7 +101,7 @@ __global__ void __launch_bounds__(kThreads)
         const int j = it / per_node, r = it - j * per_node;
         const int v = r >= row_vec, c = r - v * row_vec;
         const long long pos = base + 1 + j;
-        const size_t off = (((size_t)table[pos >> 4] * 16 + (pos & 15)) * K + k) * row_vec + c;
+        const size_t off = row_of(pos) * row_vec + c;
         (v ? v_cache : k_cache)[off] = stage[it];
     }
     if (k_scale && tid < 2 * a) {
@@ -104,14 +113,14 @@ __global__ void __launch_bounds__(kThreads)
 
 }  // namespace
 
-gqa_status launch_kv_compact(const gqa_shape& s, void* k_cache, void* v_cache, float* k_scale,
-                             float* v_scale, const int32_t* block_tables,
+gqa_status launch_kv_compact(const gqa_shape& s, void* k_cache, void* v_cache, void* k_scale,
+                             void* v_scale, const int32_t* block_tables,
                              const int32_t* context_lens, const int32_t* path,
                              const int32_t* accepted, int32_t* dev_status, cudaStream_t stream) {
     if (s.B == 0 || s.T <= 1) return GQA_OK;
     if (s.T > kMaxT || s.K > 65535) return GQA_ERR_SHAPE;
-    const int esize = s.kv_dtype == GQA_KV_SAME ? 2 : 1;
-    const int row_vec = s.H * esize / 16;
+    const bool fourbit = s.kv_dtype == GQA_KV_INT4;
+    const int row_vec = (fourbit ? s.H / 2 : s.kv_dtype == GQA_KV_SAME ? 2 * s.H : s.H) / 16;
     if (row_vec < 1 || row_vec > kMaxRowVec) return GQA_ERR_SHAPE;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)s.B, (unsigned)s.K, 1);
@@ -122,10 +131,19 @@ gqa_status launch_kv_compact(const gqa_shape& s, void* k_cache, void* v_cache, f
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = (s.flags & (GQA_FLAG_PDL | GQA_FLAG_EARLY_KV)) ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(
-        &cfg, kv_compact_kernel, static_cast<uint4*>(k_cache), static_cast<uint4*>(v_cache),
-        k_scale, v_scale, block_tables, context_lens, path, accepted, dev_status, s.T, s.K,
-        row_vec, s.max_blocks_per_seq, s.num_blocks);
+    auto launch = [&](auto kernel, auto* ks, auto* vs) {
+        return cudaLaunchKernelEx(&cfg, kernel, static_cast<uint4*>(k_cache),
+                                  static_cast<uint4*>(v_cache), ks, vs, block_tables,
+                                  context_lens, path, accepted, dev_status, s.T, s.K, row_vec,
+                                  s.max_blocks_per_seq, s.num_blocks);
+    };
+    const cudaError_t e =
+        !fourbit ? launch(kv_compact_kernel<false, float>, static_cast<float*>(k_scale),
+                          static_cast<float*>(v_scale))
+        : s.H == 128 ? launch(kv_compact_kernel<true, uint32_t>, static_cast<uint32_t*>(k_scale),
+                              static_cast<uint32_t*>(v_scale))
+                     : launch(kv_compact_kernel<true, uint16_t>, static_cast<uint16_t*>(k_scale),
+                              static_cast<uint16_t*>(v_scale));
     return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GQA_OK : GQA_ERR_CUDA;
 }
 

@@ -1,0 +1,315 @@
+// kv_slots.cu -- rows written into and read from a paged cache by position:
+//   kv_append_fourbit  the T newest tokens of every sequence into a 4-bit cache,
+//                      by block table (as gqa_kv_append)
+//   kv_append_slots    packed rows [M][K][H] of any number of requests into a
+//                      cache of any kind, by a slot per row (block * 16 + row)
+//   kv_gather_slots    the way back: rows [M][K][H] in the dtype of the shape
+//
+// CS336 lecture 10 §"PagedAttention" (fixed-size blocks; a token's place is its
+// block and its row); the quantization is that of kv_quant.cu (one byte) and
+// fourbit.cuh (4 bits).
+//
+// All of it is moving bytes: the floor is the 16-bit side plus the cache side
+// once.  A thread owns 8 consecutive elements (one 16-byte access on the 16-bit
+// side); four threads share a 4-bit group and H/8 a row, so maxima take two
+// (or log2(H/8)) shuffles inside the warp and every row is written as one
+// contiguous piece.
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "fourbit.cuh"
+#include "launch.h"
+#include "ptx.cuh"
+
+namespace gqa {
+namespace {
+
+constexpr int kSlotThreads = 256;
+constexpr int kKvFourbit = GQA_KV_INT4;
+
+struct SlotParams {
+    const uint4* k_new;  // rows [M][K][H]
+    const uint4* v_new;
+    uint4* k_out;
+    uint4* v_out;
+    uint8_t* k_cache;
+    uint8_t* v_cache;
+    void* k_scale;
+    void* v_scale;
+    const int32_t* slots;  // [M]; nullptr: by block table
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    int32_t* status;
+    long long M;
+    int T, K, max_blocks, num_blocks;
+};
+
+template <bool BF16>
+__device__ __forceinline__ void widen8(uint4 w, float (&x)[8]) {
+    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = Elt<BF16>::lo(a[i]);
+        x[2 * i + 1] = Elt<BF16>::hi(a[i]);
+    }
+}
+
+// Max over the N threads (a power of two, aligned in the warp) that share it.
+template <int N>
+__device__ __forceinline__ float max_over(float a) {
+#pragma unroll
+    for (int o = 1; o < N; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    return a;
+}
+
+// Cache slot of row i (token t of sequence b by block table), -1: none.
+__device__ __forceinline__ int slot_of(const SlotParams& p, long long i, bool reporter) {
+    if (p.slots) {
+        const int s = __ldg(p.slots + i);
+        if (s >= 0 && (s >> 4) < p.num_blocks) return s;
+        if (s != -1 && reporter) report(p.status, GQA_ERR_BLOCK_ID);
+        return -1;
+    }
+    const int b = (int)(i / p.T), t = (int)(i - (long long)b * p.T);
+    const int ctx = __ldg(p.context_lens + b);
+    if (ctx < p.T || ctx > p.max_blocks * 16) {
+        if (reporter) report(p.status, GQA_ERR_CONTEXT);
+        return -1;
+    }
+    const int pos = ctx - p.T + t;
+    const int blk = __ldg(p.block_tables + (size_t)b * p.max_blocks + (pos >> 4));
+    if (blk < 0 || blk >= p.num_blocks) {
+        if (reporter) report(p.status, GQA_ERR_BLOCK_ID);
+        return -1;
+    }
+    return blk * 16 + (pos & 15);
+}
+
+// Eight elements of a row (part c of H/8) of KV head k into slot s.
+template <bool BF16, int KIND, int H>
+__device__ __forceinline__ void put8(const SlotParams& p, uint8_t* cache, void* scale, int s,
+                                     int k, int c, uint4 w) {
+    constexpr int P = H / 8;  // threads per row
+    const size_t blk = (size_t)(s >> 4);
+    const int row = s & 15;
+    if constexpr (KIND == GQA_KV_SAME) {
+        if (s >= 0)
+            reinterpret_cast<uint4*>(cache)[((blk * 16 + row) * p.K + k) * P + c] = w;
+        return;
+    }
+    float x[8];
+    widen8<BF16>(w, x);
+    float a = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(x[e]));
+    if constexpr (KIND == kKvFourbit) {
+        a = max_over<kQ4Group / 8>(a);
+        const uint32_t sc = q4_scale_code(a);
+        const float sv = q4_scale_value(sc);
+        uint32_t word = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) word |= q4_code(x[e], sv) << (4 * e);
+        if (s >= 0) {
+            const size_t r = (blk * p.K + k) * 16 + row;
+            reinterpret_cast<uint32_t*>(cache)[r * P + c] = word;
+            if ((c & 3) == 0) static_cast<uint8_t*>(scale)[r * (H / kQ4Group) + (c >> 2)] = (uint8_t)sc;
+        }
+    } else {
+        a = max_over<P>(a);
+        const float sv = __fdiv_rn(a, KIND == GQA_KV_INT8 ? 127.f : 448.f);
+        uint32_t word[2] = {0u, 0u};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            uint32_t code = 0;
+            if (sv != 0.f) {
+                const float y = __fdiv_rn(x[e], sv);
+                if (KIND == GQA_KV_INT8) {
+                    int r = (y != y) ? 0 : __float2int_rn(y);
+                    code = (uint32_t)(min(127, max(-128, r)) & 0xff);
+                } else {
+                    code = (uint32_t)__nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
+                }
+            }
+            word[e >> 2] |= code << (8 * (e & 3));
+        }
+        if (s >= 0) {
+            reinterpret_cast<uint2*>(cache)[((blk * 16 + row) * p.K + k) * P + c] =
+                make_uint2(word[0], word[1]);
+            if (c == 0) static_cast<float*>(scale)[(blk * p.K + k) * 16 + row] = sv;
+        }
+    }
+}
+
+// Items: row i, KV head k, part c, keys and values of one item together.
+template <bool BF16, int KIND, int H>
+__global__ void __launch_bounds__(kSlotThreads) kv_put_kernel(const SlotParams p) {
+    constexpr int P = H / 8;
+    griddep_launch_dependents();
+    griddep_wait();
+    const long long items = p.M * p.K * P;
+    const long long stride = (long long)gridDim.x * kSlotThreads;
+    // whole warps stay in the loop together (the shuffles)
+    for (long long it = (long long)blockIdx.x * kSlotThreads + threadIdx.x;
+         it - (threadIdx.x & 31) < items; it += stride) {
+        const bool on = it < items;
+        const long long rk = (on ? it : items - 1) / P;
+        const int c = (int)(it % P);
+        const long long i = rk / p.K;
+        const int k = (int)(rk - i * p.K);
+        uint4 kw = make_uint4(0, 0, 0, 0), vw = kw;
+        if (on) {
+            kw = __ldg(p.k_new + it);
+            vw = __ldg(p.v_new + it);
+        }
+        const int s = on ? slot_of(p, i, c == 0 && k == 0) : -1;
+        put8<BF16, KIND, H>(p, p.k_cache, p.k_scale, s, k, c, kw);
+        put8<BF16, KIND, H>(p, p.v_cache, p.v_scale, s, k, c, vw);
+    }
+}
+
+// Eight elements of KV head k's row in slot s, in the 16-bit type.
+template <bool BF16, int KIND, int H>
+__device__ __forceinline__ uint4 take8(const SlotParams& p, const uint8_t* cache,
+                                       const void* scale, int s, int k, int c) {
+    constexpr int P = H / 8;
+    if (s < 0) return make_uint4(0, 0, 0, 0);
+    const size_t blk = (size_t)(s >> 4);
+    const int row = s & 15;
+    float x[8];
+    if constexpr (KIND == GQA_KV_SAME) {
+        return __ldg(reinterpret_cast<const uint4*>(cache) + ((blk * 16 + row) * p.K + k) * P + c);
+    } else if constexpr (KIND == kKvFourbit) {
+        const size_t r = (blk * p.K + k) * 16 + row;
+        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(cache) + r * P + c);
+        const float sv = q4_scale_value(
+            __ldg(static_cast<const uint8_t*>(scale) + r * (H / kQ4Group) + (c >> 2)));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = (float)((int)((w >> (4 * e)) & 15u) - 8) * sv;
+    } else {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(cache) +
+                              ((blk * 16 + row) * p.K + k) * P + c);
+        const float sv = __ldg(static_cast<const float*>(scale) + (blk * p.K + k) * 16 + row);
+        const uint32_t a[2] = {w.x, w.y};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t code = (a[e >> 2] >> (8 * (e & 3))) & 0xffu;
+            if (KIND == GQA_KV_INT8)
+                x[e] = (float)(int8_t)code * sv;
+            else
+                x[e] = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code,
+                                                                  __NV_E4M3))) * sv;
+        }
+    }
+    return make_uint4(Elt<BF16>::pack(x[0], x[1]), Elt<BF16>::pack(x[2], x[3]),
+                      Elt<BF16>::pack(x[4], x[5]), Elt<BF16>::pack(x[6], x[7]));
+}
+
+template <bool BF16, int KIND, int H>
+__global__ void __launch_bounds__(kSlotThreads) kv_take_kernel(const SlotParams p) {
+    constexpr int P = H / 8;
+    griddep_launch_dependents();
+    griddep_wait();
+    const long long items = p.M * p.K * P;
+    for (long long it = (long long)blockIdx.x * kSlotThreads + threadIdx.x; it < items;
+         it += (long long)gridDim.x * kSlotThreads) {
+        const long long rk = it / P;
+        const int c = (int)(it % P);
+        const long long i = rk / p.K;
+        const int k = (int)(rk - i * p.K);
+        const int s = slot_of(p, i, c == 0 && k == 0);
+        const uint4 kw = take8<BF16, KIND, H>(p, p.k_cache, p.k_scale, s, k, c);
+        const uint4 vw = take8<BF16, KIND, H>(p, p.v_cache, p.v_scale, s, k, c);
+        p.k_out[it] = kw;
+        p.v_out[it] = vw;
+    }
+}
+
+template <bool PUT, bool BF16, int KIND, int H>
+const void* slot_kernel() {
+    return PUT ? reinterpret_cast<const void*>(&kv_put_kernel<BF16, KIND, H>)
+               : reinterpret_cast<const void*>(&kv_take_kernel<BF16, KIND, H>);
+}
+template <bool PUT, bool BF16, int H>
+const void* slot_kernel_kind(int kind) {
+    switch (kind) {
+        case GQA_KV_SAME: return slot_kernel<PUT, BF16, GQA_KV_SAME, H>();
+        case GQA_KV_INT8: return slot_kernel<PUT, BF16, GQA_KV_INT8, H>();
+        case GQA_KV_E4M3: return slot_kernel<PUT, BF16, GQA_KV_E4M3, H>();
+        default: return slot_kernel<PUT, BF16, kKvFourbit, H>();
+    }
+}
+template <bool PUT>
+const void* pick_slot_kernel(const gqa_shape& s) {
+    const bool bf16 = s.dtype == GQA_BF16;
+    if (s.H == 128)
+        return bf16 ? slot_kernel_kind<PUT, true, 128>(s.kv_dtype)
+                    : slot_kernel_kind<PUT, false, 128>(s.kv_dtype);
+    return bf16 ? slot_kernel_kind<PUT, true, 64>(s.kv_dtype)
+                : slot_kernel_kind<PUT, false, 64>(s.kv_dtype);
+}
+
+gqa_status launch_slots(const gqa_shape& s, const void* kernel, SlotParams& p,
+                        cudaStream_t stream) {
+    const long long items = p.M * s.K * (s.H / 8);
+    if (items == 0) return GQA_OK;
+    const int sms = device_sm_count();
+    if (sms <= 0) return GQA_ERR_CUDA;
+    const long long need = (items + kSlotThreads - 1) / kSlotThreads, cap = (long long)sms * 32;
+    p.T = s.T;
+    p.K = s.K;
+    p.max_blocks = s.max_blocks_per_seq;
+    p.num_blocks = s.num_blocks;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(need < cap ? need : cap));
+    cfg.blockDim = dim3(kSlotThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = (s.flags & (GQA_FLAG_PDL | GQA_FLAG_EARLY_KV)) ? 1 : 0;
+    void* args[] = {&p};
+    const cudaError_t e = cudaLaunchKernelExC(&cfg, kernel, args);
+    return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GQA_OK : GQA_ERR_CUDA;
+}
+
+}  // namespace
+
+gqa_status launch_kv_append_slots(const gqa_shape& s, long long rows, const void* k_new,
+                                  const void* v_new, void* k_cache, void* v_cache, void* k_scale,
+                                  void* v_scale, const int32_t* slots,
+                                  const int32_t* block_tables, const int32_t* context_lens,
+                                  int32_t* dev_status, cudaStream_t stream) {
+    SlotParams p = {};
+    p.k_new = static_cast<const uint4*>(k_new);
+    p.v_new = static_cast<const uint4*>(v_new);
+    p.k_cache = static_cast<uint8_t*>(k_cache);
+    p.v_cache = static_cast<uint8_t*>(v_cache);
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.slots = slots;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.status = dev_status;
+    p.M = rows;
+    return launch_slots(s, pick_slot_kernel<true>(s), p, stream);
+}
+
+gqa_status launch_kv_gather_slots(const gqa_shape& s, long long rows, const void* k_cache,
+                                  const void* v_cache, const void* k_scale, const void* v_scale,
+                                  const int32_t* slots, void* k_out, void* v_out,
+                                  int32_t* dev_status, cudaStream_t stream) {
+    SlotParams p = {};
+    p.k_out = static_cast<uint4*>(k_out);
+    p.v_out = static_cast<uint4*>(v_out);
+    p.k_cache = static_cast<uint8_t*>(const_cast<void*>(k_cache));
+    p.v_cache = static_cast<uint8_t*>(const_cast<void*>(v_cache));
+    p.k_scale = const_cast<void*>(k_scale);
+    p.v_scale = const_cast<void*>(v_scale);
+    p.slots = slots;
+    p.status = dev_status;
+    p.M = rows;
+    return launch_slots(s, pick_slot_kernel<false>(s), p, stream);
+}
+
+}  // namespace gqa

@@ -63,9 +63,9 @@ gqa_status launch_accept_prefix(int B, int T, int V, const float* logits,
                                 cudaStream_t stream);
 
 // Moves the cached rows of an accepted tree branch behind its root (see
-// gqa_kv_compact); k_scale / v_scale non-null for one-byte caches.
-gqa_status launch_kv_compact(const gqa_shape& s, void* k_cache, void* v_cache, float* k_scale,
-                             float* v_scale, const int32_t* block_tables,
+// gqa_kv_compact); k_scale / v_scale non-null for one-byte and 4-bit caches.
+gqa_status launch_kv_compact(const gqa_shape& s, void* k_cache, void* v_cache, void* k_scale,
+                             void* v_scale, const int32_t* block_tables,
                              const int32_t* context_lens, const int32_t* path,
                              const int32_t* accepted, int32_t* dev_status, cudaStream_t stream);
 
@@ -105,6 +105,35 @@ gqa_status launch_tc_attention(const gqa_shape& s, const void* q, const void* k_
                                const int32_t* context_lens, const uint64_t* tree_mask, void* out,
                                void* workspace, size_t flags_bytes, int32_t* dev_status,
                                cudaStream_t stream);
+
+// 4-bit cache: attention over it (T >= 1, window, tree mask; own kernel and
+// workspace layout), and the moves of rows by slot or by block table, which
+// serve every cache type (slots == nullptr: by block table, rows = B * T).
+gqa_status fourbit_workspace_bytes(const gqa_shape& s, size_t* bytes);
+gqa_status launch_attention_fourbit(const gqa_shape& s, const void* q, const uint8_t* k_cache,
+                                    const uint8_t* v_cache, const uint8_t* k_scale,
+                                    const uint8_t* v_scale, const int32_t* block_tables,
+                                    const int32_t* context_lens, const uint64_t* tree_mask,
+                                    void* out, void* workspace, size_t ws_bytes,
+                                    int32_t* dev_status, cudaStream_t stream);
+gqa_status launch_kv_append_slots(const gqa_shape& s, long long rows, const void* k_new,
+                                  const void* v_new, void* k_cache, void* v_cache, void* k_scale,
+                                  void* v_scale, const int32_t* slots,
+                                  const int32_t* block_tables, const int32_t* context_lens,
+                                  int32_t* dev_status, cudaStream_t stream);
+gqa_status launch_kv_gather_slots(const gqa_shape& s, long long rows, const void* k_cache,
+                                  const void* v_cache, const void* k_scale, const void* v_scale,
+                                  const int32_t* slots, void* k_out, void* v_out,
+                                  int32_t* dev_status, cudaStream_t stream);
+
+// Block tables, slots and lengths of a step (see gqa_plan_blocks).
+gqa_status launch_plan_blocks(int B, int max_blocks, int num_blocks, int tokens,
+                              const int32_t* context_lens, const int32_t* new_lens,
+                              const int32_t* held, const int32_t* ring_state, int32_t* free_ring,
+                              int32_t* block_tables, int32_t* context_lens_out,
+                              int32_t* held_out, int32_t* ring_state_out, int32_t* cu_new,
+                              int32_t* slots, int32_t* positions, bool pdl, int32_t* dev_status,
+                              cudaStream_t stream);
 
 // Cached per-device SM count (0 on failure).
 int device_sm_count();

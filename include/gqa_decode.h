@@ -16,6 +16,13 @@
  *                        sampling: modified rejection sampling)
  *   gqa_accept_tree      greedy acceptance over a draft tree, and
  *   gqa_kv_compact       the kept branch's cached rows moved behind its root
+ *   gqa_kv_append_fourbit, gqa_attention_fourbit, gqa_append_attention_fourbit,
+ *   gqa_kv_compact_fourbit  a cache held in 4 bits: append, decode / verify /
+ *                        tree attention, both in one call, compaction
+ *   gqa_kv_append_slots / gqa_kv_gather_slots  packed rows of several requests
+ *                        into and out of a cache of any kind, by slot
+ *   gqa_plan_blocks      block tables, slot maps and lengths of a step from the
+ *                        requests' lengths
  *
  * Sources (web pages, cited by title and section):
  *   "CS336, лекции 10 и 12: инференс и оценка моделей" (CS336 lectures 10/12,
@@ -82,15 +89,18 @@ typedef enum {
     GQA_ERR_TIMEOUT = 9,   /* device: a bounded wait inside a kernel gave up */
     GQA_ERR_PROBS = 10,    /* device: an entry read is not a probability in [0,1], a
                               uniform is not in [0,1), or a row has no weight */
-    GQA_ERR_TREE = 11      /* device: a draft tree's parent entry, or an accepted
+    GQA_ERR_TREE = 11,     /* device: a draft tree's parent entry, or an accepted
                               branch passed to gqa_kv_compact, is out of range */
+    GQA_ERR_BLOCKS = 12    /* device (gqa_plan_blocks): no free blocks or token slots
+                              left for a sequence, or an inconsistent free ring */
 } gqa_status;
 
 typedef enum { GQA_F16 = 0, GQA_BF16 = 1 } gqa_dtype;
 
-/* Element type of the KV cache: the dtype of q (2 bytes), or one-byte codes
- * with an fp32 scale per cached row (see gqa_kv_append_quant). */
-typedef enum { GQA_KV_SAME = 0, GQA_KV_INT8 = 1, GQA_KV_E4M3 = 2 } gqa_kv_dtype;
+/* Element type of the KV cache: the dtype of q (2 bytes), one-byte codes with an
+ * fp32 scale per cached row (see gqa_kv_append_quant), or 4-bit codes with a
+ * scale per 32 elements (see gqa_kv_append_fourbit). */
+typedef enum { GQA_KV_SAME = 0, GQA_KV_INT8 = 1, GQA_KV_E4M3 = 2, GQA_KV_INT4 = 3 } gqa_kv_dtype;
 
 /* Problem sizes, in the pages' notation (CS336 lecture 10, §"Напоминание:
  * трансформер"): B sequences, T new query tokens per sequence, N query heads,
@@ -110,7 +120,7 @@ typedef struct {
     int window;             /* local attention: > 0 limits each query to the last
                                `window` positions up to itself; 0 = all */
     int kv_dtype;           /* gqa_kv_dtype of the caches; GQA_KV_SAME except for
-                               the _quant calls */
+                               the _quant, _fourbit and _slots calls */
 } gqa_shape;
 
 /* Local (sliding-window) attention, for the attention calls: CS336 lecture 10
@@ -168,6 +178,7 @@ typedef struct {
 #define GQA_ENGINE_WARP_MMA 1
 #define GQA_ENGINE_TENSOR_MEMORY 2
 #define GQA_ENGINE_DIRECT 3
+#define GQA_ENGINE_FOURBIT 4 /* kv_dtype GQA_KV_INT4: one kernel serves it */
 int gqa_attention_engine(const gqa_shape *shape);
 
 /* Library version (major*10000 + minor*100 + patch). */
@@ -544,6 +555,129 @@ gqa_status gqa_accept_sampled(int B, int T, int V, const float *target_probs,
                               const double *uniforms, int32_t *accepted,
                               int32_t *next_token, int32_t *context_lens_inout,
                               int32_t *dev_status, void *stream);
+
+/* 4-bit cache.  The quantization section of "جعل inference رخيصًا: KV cache
+ * وbatching والتكميم" carried to four bits: symmetric absolute-maximum
+ * quantization with a scale per group of 32 consecutive elements of a row (one
+ * token of one KV head).  For a group with a = max|x|:
+ *   s = a / 7 rounded to nearest even on the ue5m3 grid (an f16 number without
+ *       sign and with three mantissa bits: byte b stands for the f16 bits b << 7),
+ *       at most 9216;  code c = x / s rounded to nearest even, within [-7, 7]
+ *       (both divisions in IEEE fp32);  s = 0 (a / 7 <= 2^-18): all codes 0
+ *   the cached value is c * s, exactly a number of either 16-bit type; elements
+ *       beyond 64512 saturate; a NaN element becomes 0
+ *   caches    bytes [num_blocks][K][16][H/2]: element 2i of a row in the low half
+ *             of byte i, element 2i+1 in the high half, each stored as c + 8.
+ *             The KV head is outside the row, so one head's tile of a block is
+ *             contiguous (unlike the other caches' [num_blocks][16][K][H]).
+ *   k_scale, v_scale  bytes [num_blocks][K][16][H/32]: the groups' scales
+ * 4.25 bits an element.  H in {64, 128}; caches and scales 16-byte aligned;
+ * shape->kv_dtype is GQA_KV_INT4; other requirements and device errors as
+ * gqa_kv_append. */
+gqa_status gqa_kv_append_fourbit(const gqa_shape *shape, const void *k_new, const void *v_new,
+                                 uint8_t *k_cache, uint8_t *v_cache, uint8_t *k_scale,
+                                 uint8_t *v_scale, const int32_t *block_tables,
+                                 const int32_t *context_lens, int32_t *dev_status, void *stream);
+
+/* Attention over a 4-bit cache, T >= 1: gqa_decode_attention /
+ * gqa_verify_attention, or with tree_mask != NULL gqa_tree_verify_attention, with
+ * K_b[j] and V_b[j] the cached values above.  H = 64 or 128, windows (not with
+ * a tree mask), T * (N/K) <= 8192; more than 16 query rows per KV head run in
+ * chunks of 16, each reading the KV head's blocks.  The products run on f16
+ * tensor-core operands with fp32 accumulation: cached values are exact in f16,
+ * q rows in bf16 are scaled by a power of two first (exact down to 2^-31 of
+ * the row's largest element), probabilities are rounded to f16.
+ * Workspace: gqa_attention_workspace_size(shape) bytes with that kv_dtype, zero-
+ * filled before first use and left so, as for the other attention calls (the
+ * two kinds may share one buffer).  GQA_FLAG_EARLY_KV acts as GQA_FLAG_PDL; the
+ * flags that force a kernel give GQA_ERR_SHAPE. */
+gqa_status gqa_attention_fourbit(const gqa_shape *shape, const void *q, const uint8_t *k_cache,
+                                 const uint8_t *v_cache, const uint8_t *k_scale,
+                                 const uint8_t *v_scale, const int32_t *block_tables,
+                                 const int32_t *context_lens, const uint64_t *tree_mask,
+                                 void *out, void *workspace, size_t workspace_bytes,
+                                 int32_t *dev_status, void *stream);
+
+/* gqa_kv_append_fourbit, then gqa_attention_fourbit: the same results. */
+gqa_status gqa_append_attention_fourbit(const gqa_shape *shape, const void *q, const void *k_new,
+                                        const void *v_new, uint8_t *k_cache, uint8_t *v_cache,
+                                        uint8_t *k_scale, uint8_t *v_scale,
+                                        const int32_t *block_tables, const int32_t *context_lens,
+                                        const uint64_t *tree_mask, void *out, void *workspace,
+                                        size_t workspace_bytes, int32_t *dev_status,
+                                        void *stream);
+
+/* gqa_kv_compact over a 4-bit cache: a row's codes and scales move as they are. */
+gqa_status gqa_kv_compact_fourbit(const gqa_shape *shape, uint8_t *k_cache, uint8_t *v_cache,
+                                  uint8_t *k_scale, uint8_t *v_scale,
+                                  const int32_t *block_tables, const int32_t *context_lens,
+                                  const int32_t *path, const int32_t *accepted,
+                                  int32_t *dev_status, void *stream);
+
+/* Rows by slot.  CS336 lecture 10 §"PagedAttention": a token's place is a block
+ * and a row in it; slots[i] = block * 16 + row is that of packed row i, so rows
+ * of requests of any lengths (the prompts of a step, say) go in one call.
+ *   shape      K, H, num_blocks, dtype (of the packed rows) and kv_dtype are
+ *              used; the other fields only have to be valid (T = 1, N = K, ...)
+ *   rows       M >= 0 packed rows; k_new, v_new, k_out, v_out [M][K][H] in dtype
+ *   caches     of any kind: kv_dtype GQA_KV_SAME (scales NULL), GQA_KV_INT8 /
+ *              GQA_KV_E4M3 (fp32 scales [num_blocks][K][16]), GQA_KV_INT4 (above)
+ *   slots      int32 [M]; -1: no row (append skips it, gather gives zeros)
+ * gqa_kv_append_slots stores what the appends by block table store, bit for bit.
+ * gqa_kv_gather_slots returns the cached values rounded once to dtype.  Slots of
+ * one append must differ (two rows of one slot: either, or a mix of the two).
+ * Device errors: a slot that is neither -1 nor in [0, 16 * num_blocks) counts as
+ * -1 (GQA_ERR_BLOCK_ID).  GQA_FLAG_PDL in shape->flags as elsewhere. */
+gqa_status gqa_kv_append_slots(const gqa_shape *shape, int64_t rows, const void *k_new,
+                               const void *v_new, void *k_cache, void *v_cache, void *k_scale,
+                               void *v_scale, const int32_t *slots, int32_t *dev_status,
+                               void *stream);
+gqa_status gqa_kv_gather_slots(const gqa_shape *shape, int64_t rows, const void *k_cache,
+                               const void *v_cache, const void *k_scale, const void *v_scale,
+                               const int32_t *slots, void *k_out, void *v_out,
+                               int32_t *dev_status, void *stream);
+
+/* Block tables, slot maps and lengths of a step.  §"PagedAttention" (blocks
+ * handed out as sequences grow, returned when they end) on the GPU: lengths
+ * that only the device knows (gqa_accept_prefix) need no trip to the host.
+ *   context_lens  int32 [B] tokens held now
+ *   new_lens      int32 [B] tokens to add (>= 0), or -1: the request is finished
+ *                 and gives every block back (its length becomes 0)
+ *   held          int32 [B] entries of its block table in use, >= ceil(len / 16)
+ *                 (more after a rejection shortened the sequence)
+ *   free_ring     int32 [num_blocks], the free block ids: ring_state = {head,
+ *                 count}, entries head .. head+count-1 modulo num_blocks
+ * With target = context_lens + new_lens (0 for -1) and need = ceil(target/16),
+ * in sequence order: need > held takes need - held ids from the head of the ring
+ * into block_tables[b][held..]; need < held returns entries need .. held-1 to its
+ * tail (those table entries keep their old ids).  Ids returned by a call can be
+ * taken from the next call on.  Outputs:
+ *   context_lens_out, held_out [B], ring_state_out [2]   target, need and the new
+ *                 state; each may be its input's own buffer (in place)
+ *   cu_new        int32 [B+1], exclusive prefix of the tokens added
+ *   slots         int32 [max_tokens]: of token t of sequence b, entry cu_new[b]+t,
+ *                 the slot (block * 16 + row) of position context_lens[b] + t; -1
+ *                 from cu_new[B] on
+ *   positions     int32 [max_tokens] (or NULL): that position; -1 likewise
+ * max_tokens = -1 (slots and positions NULL): tables and lengths only; 0: no
+ * sequence may add tokens (slots NULL too).
+ * A sequence is refused, left as it was and given no tokens (GQA_ERR_BLOCKS), if
+ * the free ids or the max_tokens entries do not cover it and everything the
+ * sequences before it asked for; one that asks for no ids is not refused for
+ * lack of ids.  Other device errors: negative or oversized lengths, or held out
+ * of range (GQA_ERR_CONTEXT, left as it was); a ring state out of range, or more
+ * ids returned than the ring has room for (GQA_ERR_BLOCKS, nothing taken /
+ * nothing returned); an id outside [0, num_blocks) in the ring
+ * (GQA_ERR_BLOCK_ID; it goes to the table, its slots are -1).
+ * Integers only: the result does not depend on the schedule.  Requires
+ * 0 <= B <= 16384 and B * max_blocks_per_seq < 2^31; flags: GQA_FLAG_PDL. */
+gqa_status gqa_plan_blocks(int B, int max_blocks_per_seq, int num_blocks, int max_tokens,
+                           const int32_t *context_lens, const int32_t *new_lens,
+                           const int32_t *held, const int32_t *ring_state, int32_t *free_ring,
+                           int32_t *block_tables, int32_t *context_lens_out, int32_t *held_out,
+                           int32_t *ring_state_out, int32_t *cu_new, int32_t *slots,
+                           int32_t *positions, unsigned int flags, int32_t *dev_status,
+                           void *stream);
 
 #ifdef __cplusplus
 }

@@ -1,6 +1,7 @@
 """fp64 CPU oracle for paged GQA decode/verify attention, KV append, greedy
 prefix acceptance, speculative sampling, greedy acceptance over a draft tree and the
-cache compaction after it, and the one-byte (int8 / e4m3) KV cache.
+cache compaction after it, the one-byte (int8 / e4m3) KV cache, and (fourbit.py)
+the 4-bit one and the block planner.
 
 TEST INFRASTRUCTURE ONLY: the tests, the package smoke check and the bench's CPU
 baseline leg may import this package; the product path never does.  It shares no
@@ -24,4 +25,5 @@ from .oracle import (  # noqa: F401
     argmax,
     num_threads,
 )
+from . import fourbit  # noqa: F401
 from .recompute import causal_attention_full  # noqa: F401

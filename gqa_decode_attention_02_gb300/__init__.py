@@ -511,7 +511,35 @@ def accept_sampled(target_probs, draft_probs, draft_ids, uniforms, context_lens=
     return accepted, next_token
 
 
-# ---- 4-bit cache -------------------------------------------------------------------------
+# ---- 4-bit cache, rows by slot, blocks of a step ------------------------------------------
+# These calls are a few microseconds of GPU work at batch sizes where the host's
+# part counts, so a combination of sizes and types is checked in full once: the
+# checked C shape is kept under everything the checks looked at, and a later call
+# of the same kind only makes sure that its tensors are contiguous and on one GPU.
+_checked: dict = {}
+
+
+def _gpu_of(tensors) -> int:
+    """The GPU all tensors are on if every one of them is contiguous; else -1."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != dev or not t.is_contiguous():
+            return -1
+    return dev
+
+
+def _here(dev: int, stream) -> bool:
+    """A call on GPU `dev` can go straight to the current stream."""
+    return stream is None and dev == torch.cuda.current_device()
+
+
+def _remember(key, shape):
+    if len(_checked) >= 4096:  # sizes keep changing (prompt lengths): start over
+        _checked.clear()
+    _checked[key] = shape = (shape, ctypes.byref(shape))
+    return shape
+
+
 def _need_cache4(cache, scale, name):
     _lib._need(cache, name, torch.uint8, 4)
     _lib._need(scale, name + " scale", torch.uint8, 4)
@@ -541,8 +569,8 @@ def _need_rows4(x, name, B, T, K, dtype):
         raise ValueError(f"{name} must be [{B},{T},{K},H], got {tuple(x.shape)}")
 
 
-def _append4(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
-             status, stream, pdl):
+def _append4_shape(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                   pdl):
     _need_caches4(k_cache, v_cache, k_scale, v_scale)
     _lib._need(k_new, "k_new", ndim=4)
     B, T = k_new.shape[:2]
@@ -551,28 +579,31 @@ def _append4(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables, con
     if v_new.shape != k_new.shape:
         raise ValueError("k_new and v_new must have the same shape")
     _need_tables(block_tables, context_lens, B)
-    shape = _lib.make_shape4(k_new, k_cache, block_tables.shape[1], None, B=B, T=T,
-                             N=k_cache.shape[1], flags=_lib.FLAG_PDL if pdl else 0)
-    P = _lib._ptr
-    dev = _lib.one_device(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables,
-                          context_lens, status)
+    return _lib.make_shape4(k_new, k_cache, block_tables.shape[1], None, B=B, T=T,
+                            N=k_cache.shape[1], flags=_lib.FLAG_PDL if pdl else 0)
+
+
+def _append4(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+             status, stream, pdl):
+    ts = (k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
+    st = _status_arg(status)
+    shape = _append4_shape(*ts, pdl)
+    dev = _lib.one_device(*ts, status)
     with _lib.on_device(dev, stream) as s:
-        rc = _lib.lib().gqa_kv_append_fourbit(
-            ctypes.byref(shape), P(k_new), P(v_new), P(k_cache), P(v_cache), P(k_scale),
-            P(v_scale), P(block_tables), P(context_lens), _status_arg(status), _lib._stream(s))
+        rc = _lib.lib().gqa_kv_append_fourbit(ctypes.byref(shape), *(t.data_ptr() for t in ts),
+                                              st, s.cuda_stream)
     _lib._check("gqa_kv_append_fourbit", rc)
 
 
-def _attention4(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
-                out, scale, workspace, status, stream, pdl, early_kv, window, tree_mask, decode):
+def _attention4_shape(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables,
+                      context_lens, scale, flags, window, tree_mask, decode):
     _lib._need(q, "q", ndim=4)
     B, T, N, H = q.shape
     if decode and T != 1:
         raise _lib.GqaError("gqa_attention_fourbit", _lib.Status.ERR_SHAPE)  # decode: T == 1
     _need_caches4(k_cache, v_cache, k_scale, v_scale)
     _need_tables(block_tables, context_lens, B)
-    fused = k_new is not None
-    if fused:
+    if k_new is not None:
         _need_rows4(k_new, "k_new", B, T, k_cache.shape[1], q.dtype)
         _need_rows4(v_new, "v_new", B, T, k_cache.shape[1], q.dtype)
         if k_new.shape[3] != H or v_new.shape[3] != H:
@@ -581,31 +612,67 @@ def _attention4(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table
         _lib._need(tree_mask, "tree_mask", torch.int64, 2)  # uint64 bits, held as int64
         if tuple(tree_mask.shape) != (B, T):
             raise ValueError(f"tree_mask must be [B,T] = {(B, T)}")
-    flags = (_lib.FLAG_PDL if pdl else 0) | (_lib.FLAG_EARLY_KV if early_kv else 0)
-    shape = _lib.make_shape4(q, k_cache, block_tables.shape[1], scale, B=B, T=T, N=N,
-                             flags=flags, window=window)
-    if out is not None:
+    return _lib.make_shape4(q, k_cache, block_tables.shape[1], scale, B=B, T=T, N=N,
+                            flags=flags, window=window)
+
+
+def _attention4(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                out, scale, workspace, status, stream, pdl, early_kv, window, tree_mask, decode):
+    ts = [q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens]
+    if k_new is not None:
+        ts += (k_new, v_new)
+    if tree_mask is not None:
+        ts.append(tree_mask)
+    try:
+        dev = _gpu_of(ts)
+        key = (dev, scale, pdl, early_kv, window, decode, k_new is None, tree_mask is None,
+               *[(t.shape, t.dtype) for t in ts])
+        shape = _checked.get(key)
+    except (AttributeError, TypeError):
+        shape, dev = None, -1
+    if shape is None or dev < 0:
+        flags = (_lib.FLAG_PDL if pdl else 0) | (_lib.FLAG_EARLY_KV if early_kv else 0)
+        made = _attention4_shape(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale,
+                                 block_tables, context_lens, scale, flags, window, tree_mask,
+                                 decode)
+        dev = _lib.one_device(*ts).index
+        with torch.cuda.device(dev):
+            made.nbytes = _lib.workspace_size(made)
+        shape = _remember((dev, *key[1:]), made)
+    if not _here(dev, stream):
+        with _lib.on_device(torch.device("cuda", dev), stream):
+            return _attention4(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables,
+                               context_lens, out, scale, workspace, status, None, pdl, early_kv,
+                               window, tree_mask, decode)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
         _lib._need(out, "out", q.dtype, 4)
         if out.shape != q.shape:
             raise ValueError(f"out must be {tuple(q.shape)}, got {tuple(out.shape)}")
-    if workspace is not None:
+        _lib.one_device(q, out)
+    st = None
+    if status is not None:
+        st = _status_arg(status)
+        _lib.one_device(q, status)
+    cs = _lib.raw_stream(dev)
+    if workspace is None:
+        workspace = _lib.get_workspace4(shape[0].nbytes, dev, cs)
+    else:
         _lib._need(workspace, "workspace", torch.uint8)
-    P = _lib._ptr
-    dev = _lib.one_device(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables,
-                          context_lens, tree_mask, out, workspace, status)
-    name = "gqa_append_attention_fourbit" if fused else "gqa_attention_fourbit"
-    new = (P(k_new), P(v_new)) if fused else ()
-    with _lib.on_device(dev, stream) as s:
-        if out is None:
-            out = torch.empty_like(q)
-        nbytes = _lib.workspace_size(shape)
-        if workspace is None:
-            workspace = _lib.get_workspace4(nbytes, dev, s)
-        rc = getattr(_lib.lib(), name)(
-            ctypes.byref(shape), P(q), *new, P(k_cache), P(v_cache), P(k_scale), P(v_scale),
-            P(block_tables), P(context_lens), P(tree_mask), P(out), P(workspace),
-            workspace.numel(), _status_arg(status), _lib._stream(s))
-    _lib._check(name, rc)
+        _lib.one_device(q, workspace)
+    mask = None if tree_mask is None else tree_mask.data_ptr()
+    at = [t.data_ptr() for t in ts[:7]]
+    if k_new is None:
+        rc = _lib.lib().gqa_attention_fourbit(shape[1], *at, mask, out.data_ptr(),
+                                              workspace.data_ptr(), workspace.numel(), st, cs)
+    else:
+        rc = _lib.lib().gqa_append_attention_fourbit(
+            shape[1], at[0], k_new.data_ptr(), v_new.data_ptr(), *at[1:], mask, out.data_ptr(),
+            workspace.data_ptr(), workspace.numel(), st, cs)
+    if rc:
+        raise _lib.GqaError("gqa_attention_fourbit" if k_new is None
+                            else "gqa_append_attention_fourbit", rc)
     return out
 
 
@@ -623,14 +690,11 @@ def _compact4(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, pa
                        num_blocks=NB, max_blocks_per_seq=block_tables.shape[1], dtype=0,
                        scale=0.0, flags=_lib.FLAG_PDL if pdl else 0, window=0,
                        kv_dtype=_lib.KV_DTYPES["int4"])
-    P = _lib._ptr
-    dev = _lib.one_device(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, path,
-                          accepted, status)
-    with _lib.on_device(dev, stream) as s:
-        rc = _lib.lib().gqa_kv_compact_fourbit(
-            ctypes.byref(shape), P(k_cache), P(v_cache), P(k_scale), P(v_scale),
-            P(block_tables), P(context_lens), P(path), P(accepted), _status_arg(status),
-            _lib._stream(s))
+    ts = (k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, path, accepted)
+    st = _status_arg(status)
+    with _lib.on_device(_lib.one_device(*ts, status), stream) as s:
+        rc = _lib.lib().gqa_kv_compact_fourbit(ctypes.byref(shape), *(t.data_ptr() for t in ts),
+                                               st, s.cuda_stream)
     _lib._check("gqa_kv_compact_fourbit", rc)
 
 
@@ -669,6 +733,32 @@ def _slots_shape(rows, k_cache, v_cache, k_scale, v_scale, kv, pdl):
     return shape
 
 
+def _slots_call(rows, k_cache, v_cache, k_scale, v_scale, slots, kv, pdl):
+    """(shape, device index, tensors) of a call by slot; rows: k and v [M,K,H]."""
+    k, v = rows
+    ts = [k, v, k_cache, v_cache, slots]
+    if k_scale is not None or v_scale is not None:
+        ts += (k_scale, v_scale)
+    try:
+        dev = _gpu_of(ts)
+        key = (kv, pdl, *[(t.shape, t.dtype) for t in ts])
+        shape = _checked.get(key)
+    except (AttributeError, TypeError):
+        shape, dev = None, -1
+    if shape is None or dev < 0:
+        _lib._need(k, "k_new", ndim=3)
+        _lib._need(v, "v_new", k.dtype, 3)
+        if v.shape != k.shape:
+            raise ValueError("k_new and v_new must have the same shape")
+        _lib._need(slots, "slots", torch.int32, 1)
+        if slots.shape[0] != k.shape[0]:
+            raise ValueError(f"slots must have {k.shape[0]} entries, got {slots.shape[0]}")
+        made = _slots_shape(k, k_cache, v_cache, k_scale, v_scale, kv, pdl)
+        dev = _lib.one_device(*ts).index
+        shape = _remember(key, made)
+    return shape, dev
+
+
 def kv_append_slots(k_new, v_new, k_cache, v_cache, slots, *, k_scale=None, v_scale=None,
                     kv="same", status=None, stream=None, pdl=False):
     """gqa_kv_append_slots: packed rows k_new / v_new [M,K,H] (fp16 / bf16) into
@@ -676,53 +766,66 @@ def kv_append_slots(k_new, v_new, k_cache, v_cache, slots, *, k_scale=None, v_sc
     any kind: kv="same" ([NB,16,K,H] in the rows' dtype, no scales), "int8" /
     "e4m3" (one byte, scales fp32 [NB,K,16]) or "int4" ([NB,K,16,H/2], scales
     uint8 [NB,K,16,H/32]).  The slots of one call must differ."""
-    _lib._need(k_new, "k_new", ndim=3)
-    _lib._need(v_new, "v_new", k_new.dtype, 3)
-    if v_new.shape != k_new.shape:
-        raise ValueError("k_new and v_new must have the same shape")
-    _lib._need(slots, "slots", torch.int32, 1)
-    M = k_new.shape[0]
-    if slots.shape[0] != M:
-        raise ValueError(f"slots must have {M} entries, got {slots.shape[0]}")
-    shape = _slots_shape(k_new, k_cache, v_cache, k_scale, v_scale, kv, pdl)
-    P = _lib._ptr
-    dev = _lib.one_device(k_new, v_new, k_cache, v_cache, k_scale, v_scale, slots, status)
-    with _lib.on_device(dev, stream) as s:
-        rc = _lib.lib().gqa_kv_append_slots(ctypes.byref(shape), M, P(k_new), P(v_new),
-                                            P(k_cache), P(v_cache), P(k_scale), P(v_scale),
-                                            P(slots), _status_arg(status), _lib._stream(s))
-    _lib._check("gqa_kv_append_slots", rc)
+    shape, dev = _slots_call((k_new, v_new), k_cache, v_cache, k_scale, v_scale, slots, kv, pdl)
+    if not _here(dev, stream):
+        with _lib.on_device(torch.device("cuda", dev), stream):
+            return kv_append_slots(k_new, v_new, k_cache, v_cache, slots, k_scale=k_scale,
+                                   v_scale=v_scale, kv=kv, status=status, pdl=pdl)
+    st = None
+    if status is not None:
+        st = _status_arg(status)
+        _lib.one_device(k_new, status)
+    rc = _lib.lib().gqa_kv_append_slots(
+        shape[1], k_new.shape[0], k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
+        None if v_scale is None else v_scale.data_ptr(), slots.data_ptr(), st,
+        _lib.raw_stream(dev))
+    if rc:
+        raise _lib.GqaError("gqa_kv_append_slots", rc)
 
 
 def kv_gather_slots(k_cache, v_cache, slots, *, k_scale=None, v_scale=None, kv="same",
                     dtype=None, k_out=None, v_out=None, status=None, stream=None, pdl=False):
     """gqa_kv_gather_slots: the cached rows of slots (int32 [M]; -1: zeros) as
-    packed rows [M,K,H] in `dtype` (fp16 / bf16; the cache's own for
-    kv="same").  Returns (k_out, v_out).  Caches and scales as in
-    kv_append_slots."""
-    _lib._need(slots, "slots", torch.int32, 1)
-    _lib._need(k_cache, "k_cache", ndim=4)
-    M = slots.shape[0]
+    packed rows [M,K,H] in `dtype` (fp16 / bf16; default k_out's, or the cache's
+    own for kv="same", else bf16).  Returns (k_out, v_out).  Caches and scales as
+    in kv_append_slots."""
+    if not (isinstance(k_cache, torch.Tensor) and isinstance(slots, torch.Tensor)):
+        raise TypeError("k_cache and slots must be torch.Tensors")
+    if k_cache.dim() != 4 or slots.dim() != 1:
+        raise ValueError("k_cache must have 4 dims and slots 1")
+    if not _here(k_cache.get_device(), stream):
+        if not k_cache.is_cuda:
+            raise ValueError("k_cache must be a CUDA tensor (the library has no CPU path)")
+        with _lib.on_device(k_cache.device, stream):
+            return kv_gather_slots(k_cache, v_cache, slots, k_scale=k_scale, v_scale=v_scale,
+                                   kv=kv, dtype=dtype, k_out=k_out, v_out=v_out, status=status,
+                                   pdl=pdl)
     K, H = ((k_cache.shape[1], 2 * k_cache.shape[3]) if kv == "int4"
             else (k_cache.shape[2], k_cache.shape[3]))
     if dtype is None:
-        dtype = k_cache.dtype if kv == "same" else (torch.bfloat16 if k_out is None
-                                                    else k_out.dtype)
-    given = [(t, n) for t, n in ((k_out, "k_out"), (v_out, "v_out")) if t is not None]
-    for t, n in given:
-        _lib._need(t, n, dtype, 3)
-        if tuple(t.shape) != (M, K, H):
-            raise ValueError(f"{n} must be [{M},{K},{H}], got {tuple(t.shape)}")
-    dev = _lib.one_device(k_cache, v_cache, k_scale, v_scale, slots, k_out, v_out, status)
-    P = _lib._ptr
-    with _lib.on_device(dev, stream) as s:
-        k_out = torch.empty((M, K, H), dtype=dtype, device=dev) if k_out is None else k_out
-        v_out = torch.empty((M, K, H), dtype=dtype, device=dev) if v_out is None else v_out
-        shape = _slots_shape(k_out, k_cache, v_cache, k_scale, v_scale, kv, pdl)
-        rc = _lib.lib().gqa_kv_gather_slots(ctypes.byref(shape), M, P(k_cache), P(v_cache),
-                                            P(k_scale), P(v_scale), P(slots), P(k_out),
-                                            P(v_out), _status_arg(status), _lib._stream(s))
-    _lib._check("gqa_kv_gather_slots", rc)
+        dtype = (k_out.dtype if k_out is not None else k_cache.dtype if kv == "same"
+                 else torch.bfloat16)
+    want = (slots.shape[0], K, H)
+    if k_out is None:
+        k_out = torch.empty(want, dtype=dtype, device=k_cache.device)
+    if v_out is None:
+        v_out = torch.empty_like(k_out)
+    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
+        if tuple(t.shape) != want or t.dtype != dtype:
+            raise ValueError(f"{n} must be {list(want)} of {dtype}, got {tuple(t.shape)}, {t.dtype}")
+    shape, dev = _slots_call((k_out, v_out), k_cache, v_cache, k_scale, v_scale, slots, kv, pdl)
+    st = None
+    if status is not None:
+        st = _status_arg(status)
+        _lib.one_device(k_cache, status)
+    rc = _lib.lib().gqa_kv_gather_slots(
+        shape[1], want[0], k_cache.data_ptr(), v_cache.data_ptr(),
+        None if k_scale is None else k_scale.data_ptr(),
+        None if v_scale is None else v_scale.data_ptr(), slots.data_ptr(), k_out.data_ptr(),
+        v_out.data_ptr(), st, _lib.raw_stream(dev))
+    if rc:
+        raise _lib.GqaError("gqa_kv_gather_slots", rc)
     return k_out, v_out
 
 
@@ -737,6 +840,24 @@ class BlockPlan(typing.NamedTuple):
     positions: typing.Optional[torch.Tensor]  # int32 [max_tokens], -1 past the last
 
 
+def _plan_check(ins, outs, max_tokens):
+    """Checks plan_blocks' tensors (outs: (tensor or None, name, entries))."""
+    for t, n, d in zip(ins, ("context_lens", "new_lens", "block_tables", "held", "free_ring",
+                             "ring_state"), (1, 1, 2, 1, 1, 1)):
+        _lib._need(t, n, torch.int32, d)
+    B = ins[2].shape[0]
+    if any(ins[i].shape[0] != B for i in (0, 1, 3)):
+        raise ValueError(f"context_lens, new_lens and held must have {B} entries")
+    if ins[5].shape[0] != 2:
+        raise ValueError("ring_state must be [2]: head and count")
+    for t, n, size in outs:
+        if t is not None:
+            _lib._need(t, n, torch.int32, 1)
+            if t.shape[0] != size:
+                raise ValueError(f"{n} must have {size} entries, got {t.shape[0]}")
+    _lib.one_device(*ins, *(t for t, _, _ in outs))
+
+
 def plan_blocks(context_lens, new_lens, block_tables, held, free_ring, ring_state, *,
                 max_tokens=None, context_lens_out=None, held_out=None, ring_state_out=None,
                 cu_new=None, slots=None, positions=None, in_place=False, status=None,
@@ -749,49 +870,67 @@ def plan_blocks(context_lens, new_lens, block_tables, held, free_ring, ring_stat
     made for up to max_tokens new tokens (default: the length of `slots`;
     neither given: no slot map).  The lengths, counts and state come back in new
     tensors, in the given ones, or with in_place=True in the inputs' own."""
-    for t, n, d in ((context_lens, "context_lens", 1), (new_lens, "new_lens", 1),
-                    (block_tables, "block_tables", 2), (held, "held", 1),
-                    (free_ring, "free_ring", 1), (ring_state, "ring_state", 1)):
-        _lib._need(t, n, torch.int32, d)
-    B, mb = block_tables.shape
-    if any(t.shape[0] != B for t in (context_lens, new_lens, held)):
-        raise ValueError(f"context_lens, new_lens and held must have {B} entries")
-    if ring_state.shape[0] != 2:
-        raise ValueError("ring_state must be [2]: head and count")
-    if max_tokens is None:
-        max_tokens = -1 if slots is None else slots.shape[0]
+    ins = (context_lens, new_lens, block_tables, held, free_ring, ring_state)
     if in_place:
-        if any(t is not None for t in (context_lens_out, held_out, ring_state_out)):
+        if not (context_lens_out is held_out is ring_state_out is None):
             raise ValueError("in_place=True takes no output tensors for what it updates")
         context_lens_out, held_out, ring_state_out = context_lens, held, ring_state
-    dev = _lib.one_device(context_lens, new_lens, block_tables, held, free_ring, ring_state,
-                          context_lens_out, held_out, ring_state_out, cu_new, slots, positions,
-                          status)
-    P = _lib._ptr
-    with _lib.on_device(dev, stream) as s:
-        def made(t, n, size):
-            if t is None:
-                return torch.empty(size, dtype=torch.int32, device=dev)
-            _lib._need(t, n, torch.int32, 1)
-            if t.shape[0] != size:
-                raise ValueError(f"{n} must have {size} entries, got {t.shape[0]}")
-            return t
-
-        context_lens_out = made(context_lens_out, "context_lens_out", B)
-        held_out = made(held_out, "held_out", B)
-        ring_state_out = made(ring_state_out, "ring_state_out", 2)
-        cu_new = made(cu_new, "cu_new", B + 1)
-        if max_tokens >= 0:
-            slots = made(slots, "slots", max_tokens)
-            positions = made(positions, "positions", max_tokens)
-        elif positions is not None:
-            raise ValueError("positions need slots or max_tokens")
-        some = max_tokens > 0
-        rc = _lib.lib().gqa_plan_blocks(
-            B, mb, free_ring.shape[0], max_tokens, P(context_lens), P(new_lens), P(held),
-            P(ring_state), P(free_ring), P(block_tables), P(context_lens_out), P(held_out),
-            P(ring_state_out), P(cu_new), P(slots) if some else None,
-            P(positions) if some else None, _lib.FLAG_PDL if pdl else 0, _status_arg(status),
-            _lib._stream(s))
-    _lib._check("gqa_plan_blocks", rc)
+    if max_tokens is None:
+        max_tokens = -1 if slots is None else slots.shape[0]
+    if max_tokens < 0 and (slots is not None or positions is not None):
+        raise ValueError("positions need slots or max_tokens")
+    given = [t for t in (context_lens_out, held_out, ring_state_out, cu_new, slots, positions)
+             if t is not None]
+    try:
+        key = ("plan", max_tokens, context_lens_out is None, held_out is None,
+               ring_state_out is None, cu_new is None, slots is None,
+               *[(t.shape, t.dtype) for t in (*ins, *given)])
+        known = key in _checked
+        dev = _gpu_of((*ins, *given))
+    except (AttributeError, TypeError):
+        known, dev = False, -1
+    if not known or dev < 0:
+        B = block_tables.shape[0] if isinstance(block_tables, torch.Tensor) else 0
+        _plan_check(ins, ((context_lens_out, "context_lens_out", B), (held_out, "held_out", B),
+                          (ring_state_out, "ring_state_out", 2), (cu_new, "cu_new", B + 1),
+                          (slots, "slots", max_tokens), (positions, "positions", max_tokens)),
+                    max_tokens)
+        _remember(key, _lib.Shape())
+        dev = context_lens.get_device()
+    if not _here(dev, stream):
+        with _lib.on_device(torch.device("cuda", dev), stream):
+            return plan_blocks(*ins, max_tokens=max_tokens,
+                               context_lens_out=None if in_place else context_lens_out,
+                               held_out=None if in_place else held_out,
+                               ring_state_out=None if in_place else ring_state_out,
+                               cu_new=cu_new, slots=slots, positions=positions,
+                               in_place=in_place, status=status, pdl=pdl)
+    B, mb = block_tables.shape
+    if context_lens_out is None:
+        context_lens_out = torch.empty_like(context_lens)
+    if held_out is None:
+        held_out = torch.empty_like(held)
+    if ring_state_out is None:
+        ring_state_out = torch.empty_like(ring_state)
+    if cu_new is None:
+        cu_new = context_lens.new_empty(B + 1)
+    if max_tokens >= 0:
+        if slots is None:
+            slots = context_lens.new_empty(max_tokens)
+        if positions is None:
+            positions = context_lens.new_empty(max_tokens)
+    st = None
+    if status is not None:
+        st = _status_arg(status)
+        _lib.one_device(context_lens, status)
+    some = max_tokens > 0
+    rc = _lib.lib().gqa_plan_blocks(
+        B, mb, free_ring.shape[0], max_tokens, context_lens.data_ptr(), new_lens.data_ptr(),
+        held.data_ptr(), ring_state.data_ptr(), free_ring.data_ptr(), block_tables.data_ptr(),
+        context_lens_out.data_ptr(), held_out.data_ptr(), ring_state_out.data_ptr(),
+        cu_new.data_ptr(), slots.data_ptr() if some else None,
+        positions.data_ptr() if some else None, _lib.FLAG_PDL if pdl else 0, st,
+        _lib.raw_stream(dev))
+    if rc:
+        raise _lib.GqaError("gqa_plan_blocks", rc)
     return BlockPlan(context_lens_out, held_out, ring_state_out, cu_new, slots, positions)

@@ -80,6 +80,8 @@ EXPORTS = ("gqa_version", "gqa_status_string", "gqa_kv_append",
 def lib() -> ctypes.CDLL:
     """Load the CUDA library (once).  Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -245,16 +247,29 @@ def make_shape4(rows: torch.Tensor, k_cache: torch.Tensor, max_blocks: int, scal
                  kv_dtype=KV_DTYPES["int4"])
 
 
-def get_workspace4(nbytes: int, device, stream) -> torch.Tensor:
-    """The workspace of a 4-bit attention call: the attention workspace of the
-    stream.  Under graph capture a buffer of the graph's own, its ticket region
+def raw_stream(index: int) -> int:
+    """The current cudaStream_t of GPU `index`."""
+    return _raw_stream(index)
+
+
+# torch's own accessor where it has one (it makes no Stream object: ~1 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
+def get_workspace4(nbytes: int, index: int, stream: int) -> torch.Tensor:
+    """The workspace of a 4-bit attention call on the current stream (`stream`, of
+    GPU `index`): that stream's attention workspace.  Under graph capture a buffer of the graph's own, its ticket region
     cleared by every replay: two graphs captured on one stream may then run at
     the same time (a caller that passes its own workspace saves the clearing)."""
     if torch.cuda.is_current_stream_capturing():
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{index}")
         ws[:1 << 14].zero_()  # one int32 ticket per thread block
         return ws
-    return get_workspace(nbytes, device, stream)
+    ws = _ws_cache.get((index, stream, "attention"))
+    if ws is None or ws.numel() < nbytes:
+        ws = get_workspace(nbytes, f"cuda:{index}")
+    return ws
 
 
 _ws_cache: dict = {}

@@ -54,7 +54,9 @@ namespace {
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int kStepTiles = 2;    // tiles a warp computes per step
 constexpr int kSlots = 2;        // steps in a warp's buffer
-constexpr int kQ4SegUnits = 6;   // start-up cost of a segment, in tiles
+constexpr int kQ4SegUnits = 3;   // start-up cost of a segment, in tiles per warp
+constexpr int kQ4CutCost = 6;    // what cutting segments costs a CTA, in tiles per warp
+constexpr float kQ4None = -1e30f;  // maximum of no scores: finite, so references need no test
 constexpr float kQ4Gap = 8.0f;   // log2-domain slack before rescaling
 constexpr size_t kQ4FlagBytes = 262144; // tickets, one per CTA (as large as the other kernels' region)
 constexpr long long kQ4MaxRows = 8192;  // T*G
@@ -77,6 +79,8 @@ struct Q4Params {
     int max_blocks, num_blocks;
     int window;
     float scale_log2;
+    uint32_t code_stride, scale_stride;  // bytes of a block's codes, scales
+    uint32_t ex[2];  // 0x64006400, 0x54005400 (see q4_values)
 };
 
 template <int H>
@@ -101,7 +105,7 @@ __device__ __forceinline__ int q4_blocks(int ctx, int T, int max_blocks, int win
                ? ((ctx + 15) >> 4) - q4_first_block(ctx, T, window)
                : 0;
 }
-__device__ __forceinline__ int q4_units(int nblk) { return nblk > 0 ? nblk + kQ4SegUnits : 0; }
+__device__ __forceinline__ int q4_units(int nblk, int seg) { return nblk > 0 ? nblk + seg : 0; }
 
 // The pieces of segments in one CTA's range of units, in order.
 struct Pieces {
@@ -110,6 +114,7 @@ struct Pieces {
     int start;       // unit of the segment's first tile
     int i0, i1;      // this CTA's tiles of it
     int c0, c1;      // the range
+    int seg;         // a segment's start-up units
 
     __device__ void load(const Q4Params& p) {
         ctx = __ldg(p.context_lens + b);
@@ -123,20 +128,21 @@ struct Pieces {
     }
     // From the segment holding unit c0 (sequence b_, whose first unit is base):
     // the first piece with tiles; false if the range holds none.
-    __device__ bool begin(const Q4Params& p, int b_, int base, int lo, int hi) {
+    __device__ bool begin(const Q4Params& p, int b_, int base, int lo, int hi, int seg_) {
         c0 = lo;
         c1 = hi;
         b = b_;
         if (c0 >= c1) return false;
         load(p);
-        const int u = q4_units(nblk);
+        seg = seg_;
+        const int u = q4_units(nblk, seg);
         k = (c0 - base) / u;
-        start = base + k * u + kQ4SegUnits;
+        start = base + k * u + seg;
         return clip() || next(p);
     }
     __device__ bool next(const Q4Params& p) {
         while (true) {
-            start += nblk + kQ4SegUnits;
+            start += nblk + seg;
             if (start >= c1) return false;  // later segments start later still
             if (++k == p.KC) {
                 k = 0;
@@ -150,99 +156,183 @@ struct Pieces {
     }
 };
 
-// Copies of one step (tiles i, i+1 of a piece, those below i1) into a slot.
-// K rows go to row r ^ ((r >> 2) & 1) at H = 128 (r ^ 2 * that at H = 64) and V
-// chunks to c ^ 2 * ((r >> 1) & 1): the fragment loads are then free of bank
-// conflicts.
-template <int H>
-__device__ __forceinline__ void q4_copy_tile(uint32_t dst, const Q4Params& p, int blk, int kv,
-                                             int lane) {
-    using L = Q4<H>;
-    const size_t tile = (size_t)blk * p.K + kv;
-    const uint8_t* kc = p.k_cache + tile * L::kCodes + lane * 16;
-    const uint8_t* vc = p.v_cache + tile * L::kCodes + lane * 16;
-    if constexpr (H == 128) {
-        const int r = lane >> 2, c = lane & 3;
-        const uint32_t ko = (uint32_t)((r ^ ((r >> 2) & 1)) * 64 + c * 16);
-        const uint32_t vo = (uint32_t)(r * 64 + ((c ^ (r & 2)) << 4));
-        cp_async_16(dst + ko, kc);
-        cp_async_16(dst + 512 + ko, kc + 512);  // rows 8..15: the same swizzle
-        cp_async_16(dst + L::kCodes + vo, vc);
-        cp_async_16(dst + L::kCodes + 512 + vo, vc + 512);
-    } else {
-        const int r = lane >> 1, c = lane & 1;
-        const uint32_t ko = (uint32_t)((r ^ ((r >> 1) & 2)) * 32 + c * 16);
-        cp_async_16(dst + ko, kc);
-        cp_async_16(dst + L::kCodes + lane * 16, vc);
-    }
-    constexpr int kSc = L::kScales / 16;  // 16-byte pieces of each scale tile
-    if (lane < 2 * kSc) {
-        const bool v = lane >= kSc;
-        const int c = v ? lane - kSc : lane;
-        cp_async_16(dst + 2 * L::kCodes + lane * 16,
-                    (v ? p.v_scale : p.k_scale) + tile * L::kScales + c * 16);
-    }
+// 16-byte cp.async with constant offsets on both sides.
+template <int DST, int SRC>
+__device__ __forceinline__ void q4_cp16(uint32_t dst, const uint8_t* src) {
+    asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src),
+                 "n"(DST), "n"(SRC)
+                 : "memory");
 }
 
-__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
-    return v;
-}
-template <int W>
-__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[W]) {
-    if constexpr (W == 4) {
-        const uint4 v = ld_shared_v4(addr);
-        w[0] = v.x;
-        w[1] = v.y;
-        w[2] = v.z;
-        w[3] = v.w;
-    } else if constexpr (W == 2) {
-        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
-    } else {
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+// A lane's part of copying tiles of one KV head into a slot.  K rows go to row
+// r ^ ((r >> 2) & 1) at H = 128 (r ^ 2 * that at H = 64) and V chunks to
+// c ^ 2 * ((r >> 1) & 1): the fragment loads are then free of bank conflicts.
+template <int H>
+struct Q4Copy {
+    using L = Q4<H>;
+    static constexpr int kSc = L::kScales / 16;  // 16-byte pieces of a scale tile
+    const uint8_t *k, *v, *s;  // of block 0
+    uint32_t ko, vo, so;       // offsets in a tile
+
+    __device__ void lane_offsets(int lane) {
+        if constexpr (H == 128) {
+            const int r = lane >> 2, c = lane & 3;  // rows 8..15: the same swizzle
+            ko = (uint32_t)((r ^ ((r >> 2) & 1)) * 64 + c * 16);
+            vo = (uint32_t)(L::kCodes + r * 64 + ((c ^ (r & 2)) << 4));
+        } else {
+            const int r = lane >> 1, c = lane & 1;
+            ko = (uint32_t)((r ^ ((r >> 1) & 2)) * 32 + c * 16);
+            vo = (uint32_t)(L::kCodes + lane * 16);
+        }
+        so = (uint32_t)(2 * L::kCodes + lane * 16);
     }
-}
+    __device__ void head(const Q4Params& p, int kv, int lane) {
+        k = p.k_cache + (size_t)kv * L::kCodes + lane * 16;
+        v = p.v_cache + (size_t)kv * L::kCodes + lane * 16;
+        s = lane < kSc ? p.k_scale + (size_t)kv * L::kScales + lane * 16
+                       : p.v_scale + (size_t)kv * L::kScales + (lane - kSc) * 16;
+    }
+    // base + blk * stride, one instruction
+    static __device__ __forceinline__ const uint8_t* at(const uint8_t* base, uint32_t blk,
+                                                        uint32_t stride) {
+        uint64_t r;
+        asm("mad.wide.u32 %0, %1, %2, %3;"
+            : "=l"(r)
+            : "r"(blk), "r"(stride), "l"(reinterpret_cast<uint64_t>(base)));
+        return reinterpret_cast<const uint8_t*>(r);
+    }
+    template <int J>  // tile J of the slot at dst
+    __device__ __forceinline__ void tile(uint32_t dst, uint32_t blk, const Q4Params& p,
+                                         int lane) const {
+        const uint8_t* ks = at(k, blk, p.code_stride);
+        const uint8_t* vs = at(v, blk, p.code_stride);
+        q4_cp16<J * L::kTile, 0>(dst + ko, ks);
+        q4_cp16<J * L::kTile, 0>(dst + vo, vs);
+        if constexpr (H == 128) {
+            q4_cp16<J * L::kTile + 512, 512>(dst + ko, ks);
+            q4_cp16<J * L::kTile + 512, 512>(dst + vo, vs);
+        }
+        if (lane < 2 * kSc) q4_cp16<J * L::kTile, 0>(dst + so, at(s, blk, p.scale_stride));
+    }
+};
+
 __device__ __forceinline__ __half2 as_h2(uint32_t x) {
     return *reinterpret_cast<__half2*>(&x);
 }
 __device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
 
+// W words of shared memory
+template <int W>
+__device__ __forceinline__ void q4_words(const uint8_t* at, uint32_t (&w)[W]) {
+    if constexpr (W == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(at);
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
+    } else if constexpr (W == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(at);
+        w[0] = v.x;
+        w[1] = v.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(at);
+    }
+}
+
+__device__ __forceinline__ void q4_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                       uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+        "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Scales of the two codes of a pair, times 2^-7, as f16x2 (exact: the smallest
+// scale is 2^-17, f16's last bit 2^-24), and what turns biased codes into values.
+// The 2^7 comes back with the score factors and the final rows.
+constexpr float kQ4Unit = 128.f;
+struct Q4Scale {
+    __half2 s, n10, n6;  // s, -1024 s, -64 s
+    __device__ __forceinline__ explicit Q4Scale(uint32_t bits) {
+        s = __hmul2(as_h2(bits), as_h2(0x20002000u));    // 2^-7
+        n10 = __hmul2(as_h2(bits), as_h2(0xc800c800u));  // -8
+        n6 = __hmul2(as_h2(bits), as_h2(0xb800b800u));   // -0.5
+    }
+};
+
 // Four code pairs of a word -- nibbles i of its two halves, i = 0..3 -- times
-// their scales (low half, high half), as f16x2; exact.
-__device__ __forceinline__ void q4_values(uint32_t x, __half2 s, uint32_t (&v)[4]) {
-    const __half2 o0 = as_h2(0x64086408u);  // 1024 + 8
-    const __half2 o1 = as_h2(0x54805480u);  // 64 + 8
+// their scales.  Or-ed under an exponent a nibble n = c + 8 is 1024 + n (bits
+// 0-3 under 0x6400, ex[0]) or 64 + n (bits 4-7 under 0x5400, ex[1]; both come as
+// kernel parameters, or each of these lines is two instructions).
+// FAST: one fma each, (1024 + n) s - 1024 s = n s, every term exact (n s has 8
+// bits, the offset is a power of two; scales below 8192), and the 8 s too much
+// per code comes off elsewhere.  Otherwise c s, in two steps.
+template <bool FAST>
+__device__ __forceinline__ void q4_values(uint32_t x, const Q4Scale& f, const uint32_t (&ex)[2],
+                                          uint32_t (&v)[4]) {
     const uint32_t y = x >> 8;
-    v[0] = as_u32(__hmul2(__hsub2(as_h2((x & 0x000f000fu) | 0x64006400u), o0), s));
-    v[1] = as_u32(__hmul2(__hsub2(as_h2((x & 0x00f000f0u) | 0x54005400u), o1), s));
-    v[2] = as_u32(__hmul2(__hsub2(as_h2((y & 0x000f000fu) | 0x64006400u), o0), s));
-    v[3] = as_u32(__hmul2(__hsub2(as_h2((y & 0x00f000f0u) | 0x54005400u), o1), s));
+    const __half2 t0 = as_h2((x & 0x000f000fu) | ex[0]);
+    const __half2 t1 = as_h2((x & 0x00f000f0u) | ex[1]);
+    const __half2 t2 = as_h2((y & 0x000f000fu) | ex[0]);
+    const __half2 t3 = as_h2((y & 0x00f000f0u) | ex[1]);
+    if constexpr (FAST) {
+        v[0] = as_u32(__hfma2(t0, f.s, f.n10));
+        v[1] = as_u32(__hfma2(t1, f.s, f.n6));
+        v[2] = as_u32(__hfma2(t2, f.s, f.n10));
+        v[3] = as_u32(__hfma2(t3, f.s, f.n6));
+    } else {
+        const __half2 o10 = as_h2(0x64086408u), o6 = as_h2(0x54805480u);  // 1032, 72
+        v[0] = as_u32(__hmul2(__hsub2(t0, o10), f.s));
+        v[1] = as_u32(__hmul2(__hsub2(t1, o6), f.s));
+        v[2] = as_u32(__hmul2(__hsub2(t2, o10), f.s));
+        v[3] = as_u32(__hmul2(__hsub2(t3, o6), f.s));
+    }
 }
 
 // A warp's state for one piece of a segment: NW tiles of 8 query rows.
 template <int H, bool BF16, int NW>
 struct Q4Warp {
     using L = Q4<H>;
-    using E = Elt<false>;  // the mma's operands are f16 for either type of q
     const Q4Params& p;
     const int lane, g, q4;
-    int r0[NW];  // first of this lane's two query rows (of R), per tile
-    int lim0[NW], lim1[NW];       // last position rows r0, r0 + 1 see
+    const uint32_t ex[2];
+    uint32_t kro, vro, sko, svo;  // this lane's offsets in a tile
+    uint32_t cko;                 // ... and of the 8 scale bytes it looks over
+    int lim0[NW], lim1[NW];  // last position that rows 8u + 2*q4 (+1) see
     int rbase, rend, b, kv, ctx;
-    uint32_t qf[NW][L::kSteps][2];
+    int edge_lo, edge_hi;  // tiles <= edge_lo or >= edge_hi hold hidden positions
+    uint32_t qf[NW][L::kSteps][2], qc[NW];
     float acc[NW][L::kSteps][4];
+    // sums that ride along with the PV product as one more row tile: [0], [1]
+    // sum p s of this lane's group (what n = c + 8 adds, times 1/8) and [2], [3]
+    // sum p, each for rows 2*q4, 2*q4 + 1
+    float sum[NW][4];
     float sl0[NW], sl1[NW];  // score factor to the log2 domain, per row
-    float m0[NW], m1[NW], l0[NW], l1[NW];
+    float m0[NW], m1[NW];
     bool bad;
 
     __device__ Q4Warp(const Q4Params& p_)
-        : p(p_), lane(threadIdx.x & 31), g((threadIdx.x & 31) >> 2), q4(threadIdx.x & 3) {}
+        : p(p_), lane(threadIdx.x & 31), g((threadIdx.x & 31) >> 2), q4(threadIdx.x & 3),
+          ex{p_.ex[0], p_.ex[1]} {
+        const int ta = token();
+        const int ra = H == 128 ? (ta ^ ((ta >> 2) & 1)) : (ta ^ ((ta >> 1) & 2));
+        kro = (uint32_t)(ra * L::kRow + q4 * (L::kRow / 4));
+        vro = L::kCodes + (H == 128 ? (uint32_t)(q4 * 64 + ((((g >> 1) ^ (q4 & 2)) << 4) |
+                                                            ((g & 1) << 3)))
+                                    : (uint32_t)(q4 * 32 + g * 4));
+        sko = (uint32_t)(2 * L::kCodes + ta * L::kGroups + q4 * L::kGroups / 4);
+        svo = (uint32_t)(2 * L::kCodes + L::kScales + q4 * L::kGroups + g * L::kGroups / 8);
+        cko = (uint32_t)((lane >> 4) * L::kTile + 2 * L::kCodes + (lane & 15) * (L::kScales / 8));
+    }
+    // Score rows g, g + 8 are tokens token(), token() + 8 of a tile; V's k pairs
+    // are then tokens q4, q4 + 4 and q4 + 8, q4 + 12.
+    __device__ __forceinline__ int token() const { return (g >> 1) + 4 * (g & 1); }
 
     // q rows of the segment as B fragments.  Row u*8+g, dims H/4*q4 ..: word j
     // of a token's codes meets steps 2j (nibbles 0|4, 1|5) and 2j+1 (2|6, 3|7).
-    // bf16 rows are scaled by a power of two that puts their largest element
-    // near 2^14: f16 then holds every bf16 q exactly down to 2^-31 of it.
+    // Rows are scaled by a power of two that puts their largest element in [64,
+    // 128): f16 then holds an element of either type exactly down to 2^-20 of
+    // the largest, and to within 2^-31 of it below that.
     __device__ void begin(const Pieces& s) {
         b = s.b;
         ctx = s.ctx;
@@ -250,13 +340,20 @@ struct Q4Warp {
         rbase = (s.k - kv * p.C) * p.Rc;
         rend = min(p.R, rbase + p.Rc);
         bad = false;
+        // hidden somewhere: new positions (the first only by a tree mask, but then a
+        // chain mask and none take the same steps), past the end, or at or below the
+        // last row's window
+        edge_hi = ((ctx - p.T) >> 4) - s.f0;
+        edge_lo = p.window > 0 ? ((ctx - 1 - p.window) >> 4) - s.f0 : -1;
+        if (p.window > 0 && ctx - 1 < p.window) edge_lo = -1;
 #pragma unroll
         for (int u = 0; u < NW; ++u) {
-            r0[u] = rbase + 8 * u + 2 * q4;
-            lim0[u] = ctx - p.T + min(r0[u] / p.G, p.T - 1);
-            lim1[u] = ctx - p.T + min((r0[u] + 1) / p.G, p.T - 1);
-            m0[u] = m1[u] = -INFINITY;
-            l0[u] = l1[u] = 0.f;
+            const int r0 = rbase + 8 * u + 2 * q4;
+            lim0[u] = ctx - p.T + min(r0 / p.G, p.T - 1);
+            lim1[u] = ctx - p.T + min((r0 + 1) / p.G, p.T - 1);
+            m0[u] = m1[u] = kQ4None;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[u][e] = 0.f;
 #pragma unroll
             for (int mt = 0; mt < L::kSteps; ++mt)
 #pragma unroll
@@ -279,27 +376,33 @@ struct Q4Warp {
                     w[4 * i + 3] = x.w;
                 }
             }
-            float back = 1.f;
-            if constexpr (BF16) {
-                uint32_t top = 0u;  // largest exponent field of the row
+            float top = 0.f;
 #pragma unroll
-                for (int i = 0; i < H / 8; ++i)
-                    top = max(top, max((w[i] >> 7) & 0xffu, (w[i] >> 23) & 0xffu));
-                top = max(top, __shfl_xor_sync(FULL, top, 1));
-                top = max(top, __shfl_xor_sync(FULL, top, 2));
-                const int e = min(max(127 + 14 - (int)top, -112), 112);  // row times 2^e
-                const float f = __uint_as_float((uint32_t)(127 + e) << 23);
-                back = __uint_as_float((uint32_t)(127 - e) << 23);
+            for (int i = 0; i < H / 8; ++i)
+                top = fmaxf(top, fmaxf(fabsf(Elt<BF16>::lo(w[i])), fabsf(Elt<BF16>::hi(w[i]))));
+            top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
+            const int e = min(max(127 + 6 - (int)(__float_as_uint(top) >> 23), -112), 112);
+            const float f = __uint_as_float((uint32_t)(127 + e) << 23);  // row times 2^e
+            const float back = __uint_as_float((uint32_t)(127 - e) << 23);
+            float qsum = 0.f;
 #pragma unroll
-                for (int i = 0; i < H / 8; ++i)
-                    w[i] = E::pack(__uint_as_float(w[i] << 16) * f,
-                                   __uint_as_float(w[i] & 0xffff0000u) * f);
+            for (int i = 0; i < H / 8; ++i) {
+                w[i] = Elt<false>::pack(Elt<BF16>::lo(w[i]) * f, Elt<BF16>::hi(w[i]) * f);
+                qsum += Elt<false>::lo(w[i]) + Elt<false>::hi(w[i]);
             }
+            // -8 times this lane's part of the row's sum, as two f16 terms (22 bits;
+            // at most 8 * 32 * 128): meets the scales in one more k-step
+            const float c8 = -8.f * qsum;
+            const float hi = __half2float(__float2half_rn(c8));
+            qc[u] = Elt<false>::pack(hi, c8 - hi);
             // the factors of the rows this lane's scores belong to (rows 2*q4 and
             // 2*q4 + 1 sit in lanes 8*q4 and 8*q4 + 4); never 0, which a hidden
             // position's -inf must not meet
-            sl0[u] = fmaxf(p.scale_log2 * __shfl_sync(FULL, back, 8 * q4), 1.17549435e-38f);
-            sl1[u] = fmaxf(p.scale_log2 * __shfl_sync(FULL, back, 8 * q4 + 4), 1.17549435e-38f);
+            sl0[u] = fmaxf(kQ4Unit * p.scale_log2 * __shfl_sync(FULL, back, 8 * q4),
+                           1.17549435e-38f);
+            sl1[u] = fmaxf(kQ4Unit * p.scale_log2 * __shfl_sync(FULL, back, 8 * q4 + 4),
+                           1.17549435e-38f);
 #pragma unroll
             for (int j = 0; j < L::kKWords; ++j)
 #pragma unroll
@@ -310,14 +413,13 @@ struct Q4Warp {
         }
     }
 
-    // Hide score entries of tile position tb (of this lane's tokens tb + ta and
-    // tb + ta + 8) from the rows that do not see them.
+    // Hide score entries of tile position tb (of this lane's tokens) from the rows
+    // that do not see them.
     __device__ __forceinline__ void mask(float (&sc)[4], int u, int tb) const {
-        const int ta = (g >> 1) + 4 * (g & 1);
         const int wl = p.window > 0 ? p.window : (1 << 30);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int pos = tb + ta + (e >> 1) * 8;
+            const int pos = tb + token() + (e >> 1) * 8;
             const int lim = (e & 1) ? lim1[u] : lim0[u];
             bool off = pos > lim || pos <= lim - wl;
             if (p.tree_mask) {
@@ -331,57 +433,92 @@ struct Q4Warp {
         }
     }
 
-    // One step: nt tiles (1 or 2) whose first position is tb, in the slot at sm.
-    __device__ __forceinline__ void step(uint32_t sm, int tb, int nt) {
-        const int ta = (g >> 1) + 4 * (g & 1);  // this lane's K tokens: ta, ta + 8
-        float sc[kStepTiles][NW][4];
+    // Scores of a tile.  FAST: its codes come as n s; -8 s sum q is added by one
+    // more k-step (scales times the qc of begin).
+    template <bool FAST>
+    __device__ __forceinline__ void scores(float (&sc)[NW][4], const uint8_t* tile) {
+        const Q4Scale fa((uint32_t)tile[sko] * 0x00800080u);
+        const Q4Scale fb((uint32_t)tile[sko + 8 * L::kGroups] * 0x00800080u);
+        uint32_t wa[L::kKWords], wb[L::kKWords];
+        q4_words(tile + kro, wa);
+        q4_words(tile + kro + 8 * L::kRow, wb);
 #pragma unroll
-        for (int j = 0; j < kStepTiles; ++j) {
+        for (int u = 0; u < NW; ++u) {
 #pragma unroll
-            for (int u = 0; u < NW; ++u)
+            for (int e = 0; e < 4; ++e) sc[u][e] = 0.f;
+            if constexpr (FAST) q4_mma(sc[u], as_u32(fa.s), as_u32(fb.s), 0u, 0u, qc[u], 0u);
+        }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sc[j][u][e] = 0.f;
-            const uint32_t kb = sm + j * L::kTile;
-            const int ra = H == 128 ? (ta ^ ((ta >> 2) & 1)) : (ta ^ ((ta >> 1) & 2));
-            uint32_t wa[L::kKWords], wb[L::kKWords];
-            lds_words(kb + ra * L::kRow + q4 * (L::kRow / 4), wa);
-            lds_words(kb + (ra + 8) * L::kRow + q4 * (L::kRow / 4), wb);
-            const uint32_t sb = kb + 2 * L::kCodes + ta * L::kGroups + q4 * L::kGroups / 4;
-            const __half2 s_a = as_h2(lds_u8(sb) * 0x00800080u);
-            const __half2 s_b = as_h2(lds_u8(sb + 8 * L::kGroups) * 0x00800080u);
+        for (int i = 0; i < L::kKWords; ++i) {
+            uint32_t va[4], vb[4];
+            q4_values<FAST>(wa[i], fa, ex, va);
+            q4_values<FAST>(wb[i], fb, ex, vb);
 #pragma unroll
-            for (int i = 0; i < L::kKWords; ++i) {
-                uint32_t va[4], vb[4];
-                q4_values(wa[i], s_a, va);
-                q4_values(wb[i], s_b, vb);
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t a[4] = {va[2 * h], vb[2 * h], va[2 * h + 1], vb[2 * h + 1]};
+                for (int u = 0; u < NW; ++u)
+                    q4_mma(sc[u], va[2 * h], vb[2 * h], va[2 * h + 1], vb[2 * h + 1],
+                           qf[u][2 * i + h][0], qf[u][2 * i + h][1]);
+        }
+    }
+
+    // O^T += V^T P^T of a tile.  The probabilities enter the product as f16 (half
+    // an ulp is 2^-11 of them, below the output's own rounding); their sum takes the
+    // rounded ones, so the weights still add up to one.
+    template <bool FAST>
+    __device__ __forceinline__ void values(const float (&sc)[NW][4], const uint8_t* tile, int tb) {
+        uint32_t pb[NW][2];
 #pragma unroll
-                    for (int u = 0; u < NW; ++u)
-                        E::mma(sc[j][u], a, qf[u][2 * i + h][0], qf[u][2 * i + h][1]);
-                }
+        for (int u = 0; u < NW; ++u) {
+            const float e0 = fast_exp2(fmaf(sc[u][0], sl0[u], -m0[u]));
+            const float e1 = fast_exp2(fmaf(sc[u][1], sl1[u], -m1[u]));
+            const float e2 = fast_exp2(fmaf(sc[u][2], sl0[u], -m0[u]));
+            const float e3 = fast_exp2(fmaf(sc[u][3], sl1[u], -m1[u]));
+            pb[u][0] = movm_t(Elt<false>::pack(e0, e1));
+            pb[u][1] = movm_t(Elt<false>::pack(e2, e3));
+        }
+        uint32_t s[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[x] = tile[svo + 4 * x * L::kGroups];  // tokens q4 + 4x
+        if constexpr (!FAST) {
+            // Rows past the context or below every window may hold anything: scale 0
+            // makes their values zeros.
+            const int lo = p.window > 0 ? ctx - p.T - p.window + 1 : 0;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int pos = tb + q4 + 4 * x;
+                if (pos >= ctx || pos < lo) s[x] = 0u;
             }
         }
-        // masks: only where some position of the step is hidden from some row
-        const int last = tb + 16 * nt - 1;
-        const bool edge = nt < kStepTiles || last > ctx - p.T - (p.tree_mask ? 1 : 0) ||
-                          (p.window > 0 && tb < ctx - p.window);
-        if (edge) {
+        const Q4Scale f01((s[0] << 7) | (s[1] << 23)), f23((s[2] << 7) | (s[3] << 23));
+        constexpr uint32_t kOnes = 0x3c003c00u;
 #pragma unroll
-            for (int j = 0; j < kStepTiles; ++j)
+        for (int u = 0; u < NW; ++u)
+            q4_mma(sum[u], FAST ? as_u32(f01.s) : 0u, kOnes, FAST ? as_u32(f23.s) : 0u, kOnes,
+                   pb[u][0], pb[u][1]);
+        uint32_t w[4][L::kVWords];
 #pragma unroll
-                for (int u = 0; u < NW; ++u) {
-                    if (j < nt) {
-                        mask(sc[j][u], u, tb + 16 * j);
-                    } else {
+        for (int i = 0; i < 4; ++i) q4_words(tile + vro + i * 4 * L::kRow, w[i]);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) sc[j][u][e] = -INFINITY;
-                    }
-                }
-        }
-        // running maximum: rescale only when it grows by more than 2^kQ4Gap
-        float ref0[NW], ref1[NW];
+        for (int i = 0; i < L::kVWords; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t sel = h ? 0x7632u : 0x5410u;
+                uint32_t va[4], vc[4];
+                q4_values<FAST>(prmt(w[0][i], w[1][i], sel), f01, ex, va);
+                q4_values<FAST>(prmt(w[2][i], w[3][i], sel), f23, ex, vc);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int u = 0; u < NW; ++u)
+                        q4_mma(acc[u][4 * i + 2 * h + x], va[2 * x], va[2 * x + 1], vc[2 * x],
+                               vc[2 * x + 1], pb[u][0], pb[u][1]);
+            }
+    }
+
+    // Running maximum over the scores of a step: rescale only when it grows by more
+    // than 2^kQ4Gap.
+    __device__ __forceinline__ void raise(const float (&sc)[kStepTiles][NW][4]) {
 #pragma unroll
         for (int u = 0; u < NW; ++u) {
             float x0 = sc[0][u][0], x1 = sc[0][u][1];
@@ -403,108 +540,77 @@ struct Q4Warp {
                 const float f1 = up1 ? fast_exp2(m1[u] - x1) : 1.f;
                 if (up0) m0[u] = x0;
                 if (up1) m1[u] = x1;
-                l0[u] *= f0;
-                l1[u] *= f1;
 #pragma unroll
-                for (int mt = 0; mt < L::kSteps; ++mt) {
-                    acc[u][mt][0] *= f0;
-                    acc[u][mt][1] *= f1;
-                    acc[u][mt][2] *= f0;
-                    acc[u][mt][3] *= f1;
-                }
+                for (int e = 0; e < 4; ++e) sum[u][e] *= (e & 1) ? f1 : f0;
+#pragma unroll
+                for (int mt = 0; mt < L::kSteps; ++mt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[u][mt][e] *= (e & 1) ? f1 : f0;
             }
-            ref0[u] = m0[u] == -INFINITY ? 0.f : m0[u];
-            ref1[u] = m1[u] == -INFINITY ? 0.f : m1[u];
         }
-        // O^T += V^T P^T, tile by tile.  The probabilities enter the product as
-        // f16 (half an ulp is 2^-12 of them, below the output's own rounding);
-        // their sum stays fp32.
+    }
+
+    // One step: nt tiles (1 or 2) from tile i of the segment (first position tb),
+    // in the given slot.  Nearly every step is whole, sees all its positions and
+    // has scales below 8192, and takes the straight path.
+    __device__ __forceinline__ void step(const uint8_t* slot, int i, int tb, int nt) {
+        uint32_t c[L::kScales / 32];  // this lane's share of the step's scale bytes
+        q4_words(slot + cko, c);
+        uint32_t top = 0u;
+#pragma unroll
+        for (int x = 0; x < L::kScales / 32; ++x) top |= c[x] & (c[x] << 1) & (c[x] << 2);
+        const bool large = (top & 0x80808080u) != 0u;  // a byte of 224 or more
+        float sc[kStepTiles][NW][4];
+        if (!__any_sync(FULL, large) && nt == kStepTiles && i + nt <= edge_hi && i > edge_lo) {
+#pragma unroll
+            for (int j = 0; j < kStepTiles; ++j) scores<true>(sc[j], slot + j * L::kTile);
+            raise(sc);
+#pragma unroll
+            for (int j = 0; j < kStepTiles; ++j)
+                values<true>(sc[j], slot + j * L::kTile, 0);
+            return;
+        }
 #pragma unroll
         for (int j = 0; j < kStepTiles; ++j) {
-            if (j >= nt) break;  // warp-uniform
-            uint32_t pb[NW][2];
+            if (j < nt) {
+                scores<false>(sc[j], slot + j * L::kTile);
 #pragma unroll
-            for (int u = 0; u < NW; ++u) {
-                const float e0 = fast_exp2(fmaf(sc[j][u][0], sl0[u], -ref0[u]));
-                const float e1 = fast_exp2(fmaf(sc[j][u][1], sl1[u], -ref1[u]));
-                const float e2 = fast_exp2(fmaf(sc[j][u][2], sl0[u], -ref0[u]));
-                const float e3 = fast_exp2(fmaf(sc[j][u][3], sl1[u], -ref1[u]));
-                l0[u] += e0 + e2;
-                l1[u] += e1 + e3;
-                pb[u][0] = movm_t(E::pack(e0, e1));
-                pb[u][1] = movm_t(E::pack(e2, e3));
+                for (int u = 0; u < NW; ++u) mask(sc[j][u], u, tb + 16 * j);
+            } else {
+#pragma unroll
+                for (int u = 0; u < NW; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[j][u][e] = -INFINITY;
             }
-            const uint32_t vb = sm + j * L::kTile + L::kCodes;
-            const uint32_t sb = sm + j * L::kTile + 2 * L::kCodes + L::kScales +
-                                q4 * L::kGroups + g * L::kGroups / 8;
-            uint32_t w[4][L::kVWords], s[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {  // tokens q4 + 4i
-                const int r = q4 + 4 * i;
-                const uint32_t off =
-                    H == 128 ? (uint32_t)(r * 64 + ((((g >> 1) ^ (q4 & 2)) << 4) | ((g & 1) << 3)))
-                             : (uint32_t)(r * 32 + g * 4);
-                lds_words(vb + off, w[i]);
-                s[i] = lds_u8(sb + 4 * i * L::kGroups);
-            }
-            // Rows past the context or below every window may hold anything:
-            // scale 0 makes their values zeros.
-            const int t0 = tb + 16 * j, lo = p.window > 0 ? ctx - p.T - p.window + 1 : 0;
-            if (t0 + 16 > ctx || t0 < lo) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int pos = t0 + q4 + 4 * i;
-                    if (pos >= ctx || pos < lo) s[i] = 0u;
-                }
-            }
-            const __half2 s01 = as_h2((s[0] << 7) | (s[1] << 23));
-            const __half2 s23 = as_h2((s[2] << 7) | (s[3] << 23));
-#pragma unroll
-            for (int i = 0; i < L::kVWords; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t sel = h ? 0x7632u : 0x5410u;
-                    uint32_t va[4], vc[4];
-                    q4_values(prmt(w[0][i], w[1][i], sel), s01, va);
-                    q4_values(prmt(w[2][i], w[3][i], sel), s23, vc);
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int mt = 4 * i + 2 * h + x;
-                        const uint32_t a[4] = {va[2 * x], va[2 * x + 1], vc[2 * x],
-                                               vc[2 * x + 1]};
-#pragma unroll
-                        for (int u = 0; u < NW; ++u) E::mma(acc[u][mt], a, pb[u][0], pb[u][1]);
-                    }
-                }
         }
+        raise(sc);
+#pragma unroll
+        for (int j = 0; j < kStepTiles; ++j)
+            if (j < nt) values<false>(sc[j], slot + j * L::kTile, tb + 16 * j);
     }
 
     // This warp's (max, sum, accumulator) of every row to its scratch rows.
     __device__ void save(float* head, float* rows) {
 #pragma unroll
         for (int u = 0; u < NW; ++u) {
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-                l0[u] += __shfl_xor_sync(FULL, l0[u], o);
-                l1[u] += __shfl_xor_sync(FULL, l1[u], o);
-            }
             const int r = 8 * u + 2 * q4;
             if (g == 0) {
                 head[r] = m0[u];
                 head[r + 1] = m1[u];
-                head[8 * NW + r] = l0[u];
-                head[8 * NW + r + 1] = l1[u];
+                head[8 * NW + r] = sum[u][2];
+                head[8 * NW + r + 1] = sum[u][3];
             }
+            const float c0 = -8.f * sum[u][0], c1 = -8.f * sum[u][1];  // n s to c s
             float* d0 = rows + r * L::kRowFloats + g * (H / 8);
             float* d1 = d0 + L::kRowFloats;
 #pragma unroll
             for (int i = 0; i < L::kSteps / 2; ++i) {
                 reinterpret_cast<float4*>(d0)[i] =
-                    make_float4(acc[u][2 * i][0], acc[u][2 * i][2], acc[u][2 * i + 1][0],
-                                acc[u][2 * i + 1][2]);
+                    make_float4(acc[u][2 * i][0] + c0, acc[u][2 * i][2] + c0,
+                                acc[u][2 * i + 1][0] + c0, acc[u][2 * i + 1][2] + c0);
                 reinterpret_cast<float4*>(d1)[i] =
-                    make_float4(acc[u][2 * i][1], acc[u][2 * i][3], acc[u][2 * i + 1][1],
-                                acc[u][2 * i + 1][3]);
+                    make_float4(acc[u][2 * i][1] + c1, acc[u][2 * i][3] + c1,
+                                acc[u][2 * i + 1][1] + c1, acc[u][2 * i + 1][3] + c1);
             }
         }
         if (lane == 0) head[16 * NW] = bad ? 1.f : 0.f;
@@ -512,7 +618,7 @@ struct Q4Warp {
 };
 
 __device__ __forceinline__ float q4_weight(float m, float M) {
-    return m == -INFINITY ? 0.f : fast_exp2(m - M);
+    return fast_exp2(m - M);  // 0 for kQ4None unless all are
 }
 
 template <int H, bool BF16>
@@ -533,47 +639,157 @@ struct Q4Part {
     static constexpr int kFloats = kHead + 8 * NW * H;
 };
 
+// Fold pieces first .. last of a split segment (the whole block): the weights of
+// every (piece, row) first, a warp per row; then the accumulators, the threads in
+// groups that take a share of the pieces each.  All orders are fixed by the sizes.
+template <int H, bool BF16, int NW>
+__device__ __noinline__ void fold_pieces(const Q4Params& p, int b, int kv, int rbase, int nrows,
+                                         int first, int last, float* scratch) {
+    using Part = Q4Part<H, NW>;
+    constexpr int kRows = 8 * NW;
+    __shared__ float s_max[kRows], s_sum[kRows];
+    __shared__ int s_bad;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = blockDim.x >> 5;
+    const int n = last - first + 1;
+    auto sec = [&](int c) {  // piece c
+        return p.partials + ((size_t)(first + c) * 2 + (c == 0 ? 1 : 0)) * Part::kFloats;
+    };
+    // weights [piece][row], then 4 floats a thread for the groups' sums
+    const int room = (W * kRows * Q4<H>::kRowFloats - 4 * (int)blockDim.x) / kRows;
+    float4* sums = reinterpret_cast<float4*>(scratch + room * kRows);
+    if (tid == 0) s_bad = 0;
+    __syncthreads();  // everyone is done with the scratch
+    for (int r = warp; r < nrows; r += W) {
+        float M = kQ4None;
+        bool bad = false;
+        for (int c = lane; c < n; c += 32) {
+            M = fmaxf(M, __ldcg(sec(c) + r));
+            bad |= __ldcg(sec(c) + 16 * NW) != 0.f;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
+        float l = 0.f;
+        for (int c = lane; c < n; c += 32) {
+            const float f = q4_weight(__ldcg(sec(c) + r), M);
+            l = fmaf(f, __ldcg(sec(c) + kRows + r), l);
+            if (c < room) scratch[c * kRows + r] = f;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(FULL, l, o);
+        if (lane == 0) {
+            s_max[r] = M;
+            s_sum[r] = l;
+        }
+        if (bad) s_bad = 1;
+    }
+    __syncthreads();
+    const int items = nrows * (H / 4);
+    const int groups = max(1, min((int)blockDim.x / items, n));
+    const int each = (n + groups - 1) / groups;
+    for (int x0 = 0; x0 < items; x0 += blockDim.x) {
+        const int gi = tid / items, x = groups > 1 ? tid - gi * items : x0 + tid;
+        const bool on = groups > 1 ? gi < groups : x < items;
+        const int r = x / (H / 4), d = x % (H / 4) * 4;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (on) {
+            const int lo = groups > 1 ? gi * each : 0, hi = groups > 1 ? min(n, lo + each) : n;
+#pragma unroll 8
+            for (int c = lo; c < hi; ++c) {
+                const float f = c < room ? scratch[c * kRows + r]
+                                         : q4_weight(__ldcg(sec(c) + r), s_max[r]);
+                const float4 v =
+                    __ldcg(reinterpret_cast<const float4*>(sec(c) + Part::kHead + r * H + d));
+                o.x = fmaf(f, v.x, o.x);
+                o.y = fmaf(f, v.y, o.y);
+                o.z = fmaf(f, v.z, o.z);
+                o.w = fmaf(f, v.w, o.w);
+            }
+        }
+        if (groups > 1) {
+            if (on) sums[tid] = o;
+            __syncthreads();
+            if (on && gi == 0)
+                for (int y = 1; y < groups; ++y) {
+                    const float4 v = sums[y * items + x];
+                    o.x += v.x;
+                    o.y += v.y;
+                    o.z += v.z;
+                    o.w += v.w;
+                }
+        }
+        if (on && gi == 0 || on && groups == 1) {
+            const float iv = kQ4Unit / s_sum[r];
+            o = s_bad ? make_float4(0.f, 0.f, 0.f, 0.f)
+                      : make_float4(o.x * iv, o.y * iv, o.z * iv, o.w * iv);
+            q4_store4<H, BF16>(p, b, kv, rbase + r, d, o);
+        }
+    }
+}
+
 template <int H, bool BF16, int NW>
 __global__ void __launch_bounds__(NW == 1 ? 512 : 384, 1) q4_attention_kernel(const Q4Params p) {
     using L = Q4<H>;
     using Part = Q4Part<H, NW>;
     constexpr int kRows = 8 * NW;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ int s_scan[16], s_b, s_base, s_last;
+    __shared__ int s_scan[16], s_long[16], s_b, s_base, s_last;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = blockDim.x >> 5;
     float* heads = reinterpret_cast<float*>(smem + (size_t)W * kSlots * L::kSlot);
     float* scratch = heads + W * Part::kHead;
     griddep_launch_dependents();
     griddep_wait();
 
+    const int seg = kQ4SegUnits * W;
     // ---- this CTA's range of units --------------------------------------------------
     const int per = (p.B + blockDim.x - 1) / blockDim.x;
     const int lo = min(p.B, tid * per), hi = min(p.B, lo + per);
-    int local = 0;
-    for (int b = lo; b < hi; ++b)
-        local += q4_units(q4_blocks(p.context_lens[b], p.T, p.max_blocks, p.window));
+    int local = 0, longest = 0;
+    for (int b = lo; b < hi; ++b) {
+        const int n = q4_blocks(p.context_lens[b], p.T, p.max_blocks, p.window);
+        local += q4_units(n, seg);
+        longest = max(longest, n);
+    }
+    longest = __reduce_max_sync(FULL, longest);
     int incl = local;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(FULL, incl, o);
         if (lane >= o) incl += v;
     }
-    if (lane == 31) s_scan[warp] = incl;
+    if (lane == 31) {
+        s_scan[warp] = incl;
+        s_long[warp] = longest;
+    }
     __syncthreads();
     int before = 0, total = 0;
     for (int w = 0; w < W; ++w) {
         before += w < warp ? s_scan[w] : 0;
         total += s_scan[w];
+        longest = max(longest, s_long[w]);
     }
     total *= p.KC;
     const int excl = (before + incl - local) * p.KC;
     const int quota = max((int)(((long long)total + gridDim.x - 1) / gridDim.x), 2 * kStepTiles * W);
-    const int c0 = min((long long)total, (long long)blockIdx.x * quota);
-    const int c1 = min((long long)total, (long long)c0 + quota);
-    if (c0 < c1 && excl <= c0 && c0 < excl + local * p.KC) {
+    // Whole segments, one per CTA, where there is a CTA for each and the longest
+    // exceeds an equal share by less than cutting segments costs (about 6 tiles a
+    // warp: two more trips through L2 and a fold).
+    const bool whole = p.B * p.KC <= (int)gridDim.x && longest <= quota + kQ4CutCost * W;
+    int c0 = min((long long)total, (long long)blockIdx.x * quota);
+    int c1 = min((long long)total, (long long)c0 + quota);
+    if (whole) {
+        c0 = c1 = 0;
+        const int b = blockIdx.x / p.KC;
+        if (b < p.B) {
+            const int u = q4_units(q4_blocks(p.context_lens[b], p.T, p.max_blocks, p.window), seg);
+            c0 = (blockIdx.x - b * p.KC) * u;  // units counted from the sequence's own
+            c1 = c0 + u;
+            s_b = b;
+            s_base = 0;
+        }
+    } else if (c0 < c1 && excl <= c0 && c0 < excl + local * p.KC) {
         int base = excl;
         for (int b = lo; b < hi; ++b) {
-            const int n = p.KC * q4_units(q4_blocks(p.context_lens[b], p.T, p.max_blocks, p.window));
+            const int n = p.KC * q4_units(q4_blocks(p.context_lens[b], p.T, p.max_blocks, p.window), seg);
             if (c0 < base + n) {
                 s_b = b;
                 s_base = base;
@@ -595,84 +811,106 @@ __global__ void __launch_bounds__(NW == 1 ? 512 : 384, 1) q4_attention_kernel(co
     if (c0 >= c1) return;
 
     // ---- stream the range -------------------------------------------------------------
-    const uint32_t ring = smem_addr(smem + (size_t)warp * kSlots * L::kSlot);
+    // The piece being computed and the one being copied; their state is looked at
+    // only when a piece ends, so it lives in shared memory.
+    __shared__ Pieces s_piece[2][16];
+    Pieces& cur = s_piece[0][warp];
+    Pieces& fet = s_piece[1][warp];
+    const uint8_t* ring = smem + (size_t)warp * kSlots * L::kSlot;
+    const uint32_t ring_at = smem_addr(ring);
     float* head = heads + warp * Part::kHead;
     float* rows = scratch + (size_t)warp * kRows * L::kRowFloats;
     Q4Warp<H, BF16, NW> cs(p);
-    Pieces cur, fet;  // the piece being computed, and the one being copied
-    bool more = cur.begin(p, s_b, s_base, c0, c1);
-    fet = cur;
-    bool fmore = more;
-    int fi = fet.i0 + kStepTiles * warp;  // next tile to copy
-    int fst = 0, fkv = fet.k / p.C;       // its step within the piece, its KV head
-    int ids = 0;                          // block ids of 16 steps, from step fst & ~15
-    int fs = 0;                           // steps copied (ring position)
-    unsigned badbits = 0;                 // per slot: an invalid block id
+    Q4Copy<H> cp;
+    cp.lane_offsets(lane);
+    bool more, fmore;
+    int fi = 0, fend = 0;  // next tile to copy, end of its piece
+    int fl = 0;            // its place among the block ids held
+    int ids = 0;           // block ids of 16 steps, two a step
+    static_assert(kSlots == 2, "slots alternate, one step is in flight");
+    uint32_t fslot = 0;    // slot to copy into
+    bool fbad = false;     // the step copied last has an invalid block id
+    {
+        Pieces t;
+        more = fmore = t.begin(p, s_b, s_base, c0, c1, seg);
+        if (lane == 0) cur = fet = t;
+        if (more) {
+            fi = t.i0 + kStepTiles * warp;
+            fend = t.i1;
+            cp.head(p, t.k / p.C, lane);
+        }
+        __syncwarp();
+    }
+    const int hop = kStepTiles * W;
     // Copy this warp's next step, in whichever piece it lies.
     auto fetch = [&]() {
-        while (fmore && fi >= fet.i1) {
-            fmore = fet.next(p);
-            fi = fet.i0 + kStepTiles * warp;
-            fst = 0;
-            fkv = fet.k / p.C;
+        if (fi >= fend && fmore) {
+            Pieces t = fet;
+            do {
+                fmore = t.next(p);
+                fi = t.i0 + kStepTiles * warp;
+            } while (fmore && fi >= t.i1);
+            fend = fmore ? t.i1 : 0;
+            fl = 0;
+            if (fmore) cp.head(p, t.k / p.C, lane);
+            __syncwarp();
+            if (lane == 0) fet = t;
+            __syncwarp();
         }
         if (fmore) {
-            if ((fst & 15) == 0) {
-                const int i = fi + kStepTiles * W * (lane >> 1) + (lane & 1);
-                ids = i < fet.i1 ? __ldg(p.block_tables + (size_t)fet.b * p.max_blocks + fet.f0 + i)
-                                 : 0;
+            if (fl == 0) {
+                const int i = fi + hop * (lane >> 1) + (lane & 1);
+                ids = i < fend ? __ldg(p.block_tables + (size_t)fet.b * p.max_blocks + fet.f0 + i)
+                               : 0;
             }
-            const uint32_t dst = ring + (fs % kSlots) * L::kSlot;
-            bool bad = false;
-#pragma unroll
-            for (int j = 0; j < kStepTiles; ++j) {
-                const int blk = __shfl_sync(FULL, ids, 2 * (fst & 15) + j);
-                if (fi + j < fet.i1) {
-                    if (blk >= 0 && blk < p.num_blocks)
-                        q4_copy_tile<H>(dst + j * L::kTile, p, blk, fkv, lane);
-                    else
-                        bad = true;
-                }
+            const uint32_t dst = ring_at + fslot;
+            const uint32_t blk0 = __shfl_sync(FULL, ids, fl), blk1 = __shfl_sync(FULL, ids, fl + 1);
+            const bool two = fi + 1 < fend;  // (else blk1 is 0, no id being held for it)
+            if (max(blk0, blk1) < (uint32_t)p.num_blocks) {
+                cp.template tile<0>(dst, blk0, p, lane);
+                if (two) cp.template tile<1>(dst, blk1, p, lane);
+            } else {
+                fbad = true;
+                if (lane == 0) report(p.status, GQA_ERR_BLOCK_ID);
             }
-            const unsigned bit = 1u << (fs % kSlots);
-            badbits = bad ? badbits | bit : badbits & ~bit;
-            if (bad && lane == 0) report(p.status, GQA_ERR_BLOCK_ID);
-            fi += kStepTiles * W;
-            ++fst;
-            ++fs;
+            fi += hop;
+            fl = (fl + 2) & 31;
+            fslot = L::kSlot - fslot;
         }
         cp_async_commit();  // empty past the end: the count of groups stays in step
     };
 #pragma unroll
     for (int i = 0; i < kSlots - 1; ++i) fetch();
-    int done = 0;  // steps computed
+    uint32_t slot = 0;  // of the step being computed
     while (more) {
         cs.begin(cur);
-        for (int i = cur.i0 + kStepTiles * warp; i < cur.i1; i += kStepTiles * W) {
+        const int iend = cur.i1, f0 = cur.f0;
+        for (int i = cur.i0 + kStepTiles * warp; i < iend; i += hop) {
+            const bool bad = fbad;
+            fbad = false;
             __syncwarp();  // every lane is done with the slot the copy overwrites
             fetch();
             asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 1) : "memory");
             __syncwarp();  // the other lanes' copies too
-            if (badbits >> (done % kSlots) & 1u)
+            if (bad)
                 cs.bad = true;
             else
-                cs.step(ring + (done % kSlots) * L::kSlot, (cur.f0 + i) * 16,
-                        min(kStepTiles, cur.i1 - i));
-            ++done;
+                cs.step(ring + slot, i, (f0 + i) * 16, min(kStepTiles, iend - i));
+            slot = L::kSlot - slot;
         }
         // ---- the warps meet -----------------------------------------------------------
         cs.save(head, rows);
         __syncthreads();
         const int nrows = cs.rend - cs.rbase;
         const int first = cur.start / quota, last = (cur.start + cur.nblk - 1) / quota;
-        const bool split = first != last;
+        const bool split = !whole && first != last;
         const int me = blockIdx.x;
         float* part = p.partials + ((size_t)me * 2 + (me == first ? 1 : 0)) * Part::kFloats;
         bool bad = false;
         for (int w = 0; w < W; ++w) bad |= heads[w * Part::kHead + 16 * NW] != 0.f;
         for (int x = tid; x < nrows * (H / 4); x += blockDim.x) {
             const int r = x / (H / 4), d = x % (H / 4) * 4;
-            float M = -INFINITY;
+            float M = kQ4None;
             for (int w = 0; w < W; ++w) M = fmaxf(M, heads[w * Part::kHead + r]);
             float l = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -687,7 +925,7 @@ __global__ void __launch_bounds__(NW == 1 ? 512 : 384, 1) q4_attention_kernel(co
                 o.w += f * v.w;
             }
             if (!split) {
-                const float iv = (!bad && l != 0.f) ? 1.f / l : 0.f;
+                const float iv = (!bad && l != 0.f) ? kQ4Unit / l : 0.f;
                 if (bad)
                     o = make_float4(0.f, 0.f, 0.f, 0.f);
                 else
@@ -712,42 +950,14 @@ __global__ void __launch_bounds__(NW == 1 ? 512 : 384, 1) q4_attention_kernel(co
                 __threadfence();
             }
             __syncthreads();
-            if (s_last) {  // every piece is in: fold them in order
-                auto sec = [&](int c) {
-                    return p.partials + ((size_t)c * 2 + (c == first ? 1 : 0)) * Part::kFloats;
-                };
-                for (int x = tid; x < nrows * (H / 4); x += blockDim.x) {
-                    const int r = x / (H / 4), d = x % (H / 4) * 4;
-                    float M = -INFINITY;
-                    bool any = false;
-                    for (int c = first; c <= last; ++c) {
-                        M = fmaxf(M, __ldcg(sec(c) + r));
-                        any |= __ldcg(sec(c) + 16 * NW) != 0.f;
-                    }
-                    float l = 0.f;
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int c = first; c <= last; ++c) {
-                        const float f = q4_weight(__ldcg(sec(c) + r), M);
-                        l += f * __ldcg(sec(c) + kRows + r);
-                        const float4 v = __ldcg(
-                            reinterpret_cast<const float4*>(sec(c) + Part::kHead + r * H + d));
-                        o.x += f * v.x;
-                        o.y += f * v.y;
-                        o.z += f * v.z;
-                        o.w += f * v.w;
-                    }
-                    const float iv = 1.f / l;
-                    if (any)
-                        o = make_float4(0.f, 0.f, 0.f, 0.f);
-                    else
-                        o = make_float4(o.x * iv, o.y * iv, o.z * iv, o.w * iv);
-                    q4_store4<H, BF16>(p, cs.b, cs.kv, cs.rbase + r, d, o);
-                }
-            }
+            if (s_last) fold_pieces<H, BF16, NW>(p, cs.b, cs.kv, cs.rbase, nrows, first, last, scratch);
         }
         __syncthreads();  // the scratch is free again
-        more = cur.next(p);
+        Pieces t = cur;
+        more = t.next(p);
+        __syncwarp();
+        if (lane == 0) cur = t;
+        __syncwarp();
     }
     cp_async_wait_all();
 }
@@ -776,7 +986,7 @@ gqa_status q4_plan(const gqa_shape& s, Q4Plan* pl) {
     pl->Rc = (int)((R + pl->C - 1) / pl->C);
     const long long segs = (long long)s.B * s.K * pl->C;
     // units are 32-bit in the kernel
-    if (segs * ((long long)s.max_blocks_per_seq + kQ4SegUnits) > (1ll << 31) - 1)
+    if (segs * ((long long)s.max_blocks_per_seq + 16 * kQ4SegUnits) > (1ll << 31) - 1)
         return GQA_ERR_SHAPE;
     const int sms = device_sm_count();
     if (sms <= 0) return GQA_ERR_CUDA;
@@ -784,7 +994,7 @@ gqa_status q4_plan(const gqa_shape& s, Q4Plan* pl) {
     // another when a segment ends; few segments: large ones, so that a segment
     // is cut into few pieces.
     const int most = pl->NW == 1 ? 16 : 12;
-    pl->W = segs >= 2 * sms ? 4 : most;
+    pl->W = segs > 2 * sms ? 4 : segs > sms ? most / 2 : most;
     const int slot = (s.H == 128 ? Q4<128>::kSlot : Q4<64>::kSlot);
     pl->part_floats = (size_t)(16 * pl->NW + 4) + (size_t)8 * pl->NW * s.H;
     pl->smem = (size_t)pl->W * (kSlots * slot + (16 * pl->NW + 4) * 4 +
@@ -801,7 +1011,7 @@ gqa_status q4_plan(const gqa_shape& s, Q4Plan* pl) {
         auto it = q4_resident.find(key);
         if (it == q4_resident.end()) {
             if (cudaFuncSetAttribute(pl->kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     227 * 1024 - 1024) != cudaSuccess ||
+                                     226 * 1024 - 2048) != cudaSuccess ||
                 cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, pl->kernel, 32 * pl->W,
                                                               pl->smem) != cudaSuccess ||
                 resident < 1) {
@@ -864,6 +1074,10 @@ gqa_status launch_attention_fourbit(const gqa_shape& s, const void* q, const uin
     p.window = s.window;
     const float scale = s.scale > 0.f ? s.scale : 1.f / sqrtf((float)s.H);
     p.scale_log2 = scale * 1.4426950408889634f;
+    p.code_stride = (uint32_t)s.K * (uint32_t)(16 * s.H / 2);
+    p.scale_stride = (uint32_t)s.K * (uint32_t)(16 * s.H / kQ4Group);
+    p.ex[0] = 0x64006400u;
+    p.ex[1] = 0x54005400u;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)pl.grid);
     cfg.blockDim = dim3(32u * pl.W);

@@ -29,24 +29,40 @@ namespace gqa {
 constexpr int kQ4Group = 32;            // elements per scale
 constexpr uint32_t kQ4MaxScale = 225u;  // ue5m3 code of 9216
 
-// a / 7 rounded to ue5m3, nearest even, saturating.  a is max|x|, not NaN.
+// a / 7 rounded to ue5m3, nearest even, saturating.  a is the magnitude of an f16
+// or bf16 element (at most 11 significant bits), so a / 7 either is a midpoint of
+// the grid exactly or is at least 2^-12 of itself away from one: the product with
+// 1 / 7 (2^-23 off), rounded to 17 bits first, decides as the quotient does.
 __device__ __forceinline__ uint32_t q4_scale_code(float a) {
-    const float y = __fdiv_rn(a, 7.f);
+    const uint32_t u = (__float_as_uint(a * 0.14285714924335480f) + 0x40u) & 0xffffff80u;
+    const float y = __uint_as_float(u);
     if (y >= 9216.f) return kQ4MaxScale;
     if (y < 6.103515625e-05f) return (uint32_t)__float2int_rn(y * 131072.f);  // steps of 2^-17
-    const uint32_t u = __float_as_uint(y);
     // keep three mantissa bits of 23, then rebias the exponent from 127 to 15
     return ((u + 0x7ffffu + ((u >> 20) & 1u)) >> 20) - (112u << 3);
+}
+// Scale codes whose elements may lie beyond 7.5 scales: the last one (saturation)
+// and those below 2^-14 (a coarser grid).
+__device__ __forceinline__ bool q4_scale_clips(uint32_t code) {
+    return code - 8u >= kQ4MaxScale - 8u;
 }
 __device__ __forceinline__ float q4_scale_value(uint32_t code) {
     return __half2float(__ushort_as_half((unsigned short)(code << 7)));
 }
-// The 4-bit code of x under scale value s, as stored (c + 8).  NaN: zero.
-__device__ __forceinline__ uint32_t q4_code(float x, float s) {
-    if (s == 0.f) return 8u;
-    const float y = __fdiv_rn(x, s);
-    const int r = (y != y) ? 0 : __float2int_rn(fminf(fmaxf(y, -7.f), 7.f));
-    return (uint32_t)(r + 8);
+// Reciprocal of a scale value for q4_code; 0 for 0.
+__device__ __forceinline__ float q4_scale_inverse(float s) {
+    return s == 0.f ? 0.f : __frcp_rn(s);
+}
+// The 4-bit code of x under a scale of inverse r, as stored (c + 8).  By the same
+// distance argument x * r + 384, rounded to the 2^-15 that numbers near 384 have,
+// meets the midpoints between codes exactly where x / s does and stays off them
+// elsewhere; adding 1.5 * 2^23 then rounds to the integer, nearest even.
+// CLIP: keep within [-7, 7].
+template <bool CLIP>
+__device__ __forceinline__ uint32_t q4_code(float x, float r) {
+    float z = fmaf(x, r, 384.f);
+    if (CLIP) z = fminf(fmaxf(z, 377.f), 391.f);
+    return __float_as_uint(z + 12582536.f) & 15u;  // 1.5 * 2^23 - 384 + 8
 }
 
 }  // namespace gqa

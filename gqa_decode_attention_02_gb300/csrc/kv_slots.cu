@@ -11,9 +11,12 @@
 //
 // All of it is moving bytes: the floor is the 16-bit side plus the cache side
 // once.  A thread owns 8 consecutive elements (one 16-byte access on the 16-bit
-// side); four threads share a 4-bit group and H/8 a row, so maxima take two
-// (or log2(H/8)) shuffles inside the warp and every row is written as one
-// contiguous piece.
+// side) of a key and a value row; four threads share a 4-bit group and H/8 a row, so
+// maxima take two (or log2(H/8)) shuffles inside the warp and every row is written
+// as one contiguous piece.  At 4 bits the arithmetic comes close to the bytes (a
+// warp handles 1 KB of rows): maxima are taken on the packed 16-bit patterns,
+// codes without a division (fourbit.cuh), and clipping is left to the warps whose
+// scales need it.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
@@ -40,8 +43,9 @@ struct SlotParams {
     const int32_t* block_tables;
     const int32_t* context_lens;
     int32_t* status;
-    long long M;
-    int T, K, max_blocks, num_blocks;
+    uint32_t rows, T, K;
+    uint32_t kmul, kshift;  // i / K = (umulhi(i, kmul) + i) >> kshift, i < 2^31
+    int max_blocks, num_blocks;
 };
 
 template <bool BF16>
@@ -63,26 +67,69 @@ __device__ __forceinline__ float max_over(float a) {
 }
 
 // Cache slot of row i (token t of sequence b by block table), -1: none.
-__device__ __forceinline__ int slot_of(const SlotParams& p, long long i, bool reporter) {
+__device__ __forceinline__ int slot_of(const SlotParams& p, uint32_t i, bool reporter) {
     if (p.slots) {
         const int s = __ldg(p.slots + i);
         if (s >= 0 && (s >> 4) < p.num_blocks) return s;
         if (s != -1 && reporter) report(p.status, GQA_ERR_BLOCK_ID);
         return -1;
     }
-    const int b = (int)(i / p.T), t = (int)(i - (long long)b * p.T);
+    const uint32_t b = i / p.T, t = i - b * p.T;
     const int ctx = __ldg(p.context_lens + b);
-    if (ctx < p.T || ctx > p.max_blocks * 16) {
+    if (ctx < (int)p.T || ctx > p.max_blocks * 16) {
         if (reporter) report(p.status, GQA_ERR_CONTEXT);
         return -1;
     }
-    const int pos = ctx - p.T + t;
+    const int pos = ctx - (int)p.T + (int)t;
     const int blk = __ldg(p.block_tables + (size_t)b * p.max_blocks + (pos >> 4));
     if (blk < 0 || blk >= p.num_blocks) {
         if (reporter) report(p.status, GQA_ERR_BLOCK_ID);
         return -1;
     }
     return blk * 16 + (pos & 15);
+}
+
+// Row and KV head of item it of H/8 parts each.
+template <int H>
+__device__ __forceinline__ void item_of(const SlotParams& p, uint32_t it, uint32_t* row,
+                                        uint32_t* k, uint32_t* c) {
+    const uint32_t rk = it / (H / 8);
+    *c = it % (H / 8);
+    *row = (__umulhi(rk, p.kmul) + rk) >> p.kshift;
+    *k = rk - *row * p.K;
+}
+
+// Largest magnitude of a group; a NaN element becomes zero.
+// Magnitudes of 16-bit floats compare as integers, two at a time.
+template <bool BF16>
+__device__ __forceinline__ float group_max(uint4& w) {
+    constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;
+    auto top = [&](const uint4& v) {
+        const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                    __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+        return max(m & 0xffffu, m >> 16);
+    };
+    uint32_t m = top(w);
+    if (m > kInf) {  // rare: drop the NaN elements
+        auto clean = [&](uint32_t x) {
+            if ((x & 0x7fffu) > kInf) x &= 0xffff0000u;
+            if ((x >> 16 & 0x7fffu) > kInf) x &= 0x0000ffffu;
+            return x;
+        };
+        w = make_uint4(clean(w.x), clean(w.y), clean(w.z), clean(w.w));
+        m = top(w);
+    }
+#pragma unroll
+    for (int o = 1; o < kQ4Group / 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return Elt<BF16>::lo(m);
+}
+
+template <bool CLIP>
+__device__ __forceinline__ uint32_t code_word(const float (&x)[8], float r) {
+    uint32_t word = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) word |= q4_code<CLIP>(x[e], r) << (4 * e);
+    return word;
 }
 
 // Eight elements of a row (part c of H/8) of KV head k into slot s.
@@ -98,23 +145,22 @@ __device__ __forceinline__ void put8(const SlotParams& p, uint8_t* cache, void* 
         return;
     }
     float x[8];
-    widen8<BF16>(w, x);
-    float a = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(x[e]));
     if constexpr (KIND == kKvFourbit) {
-        a = max_over<kQ4Group / 8>(a);
-        const uint32_t sc = q4_scale_code(a);
-        const float sv = q4_scale_value(sc);
-        uint32_t word = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) word |= q4_code(x[e], sv) << (4 * e);
+        const uint32_t sc = q4_scale_code(group_max<BF16>(w));
+        const float r = q4_scale_inverse(q4_scale_value(sc));
+        widen8<BF16>(w, x);
+        const uint32_t word = __any_sync(0xffffffffu, q4_scale_clips(sc)) ? code_word<true>(x, r)
+                                                                          : code_word<false>(x, r);
         if (s >= 0) {
             const size_t r = (blk * p.K + k) * 16 + row;
             reinterpret_cast<uint32_t*>(cache)[r * P + c] = word;
             if ((c & 3) == 0) static_cast<uint8_t*>(scale)[r * (H / kQ4Group) + (c >> 2)] = (uint8_t)sc;
         }
     } else {
+        widen8<BF16>(w, x);
+        float a = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(x[e]));
         a = max_over<P>(a);
         const float sv = __fdiv_rn(a, KIND == GQA_KV_INT8 ? 127.f : 448.f);
         uint32_t word[2] = {0u, 0u};
@@ -143,19 +189,15 @@ __device__ __forceinline__ void put8(const SlotParams& p, uint8_t* cache, void* 
 // Items: row i, KV head k, part c, keys and values of one item together.
 template <bool BF16, int KIND, int H>
 __global__ void __launch_bounds__(kSlotThreads) kv_put_kernel(const SlotParams p) {
-    constexpr int P = H / 8;
     griddep_launch_dependents();
     griddep_wait();
-    const long long items = p.M * p.K * P;
-    const long long stride = (long long)gridDim.x * kSlotThreads;
-    // whole warps stay in the loop together (the shuffles)
-    for (long long it = (long long)blockIdx.x * kSlotThreads + threadIdx.x;
-         it - (threadIdx.x & 31) < items; it += stride) {
+    const uint32_t items = p.rows * p.K * (H / 8), stride = gridDim.x * kSlotThreads;
+    // whole warps stay in the loop together (the shuffles); it < 2^31 + 2^24
+    for (uint32_t it = blockIdx.x * kSlotThreads + threadIdx.x; it - (threadIdx.x & 31) < items;
+         it += stride) {
         const bool on = it < items;
-        const long long rk = (on ? it : items - 1) / P;
-        const int c = (int)(it % P);
-        const long long i = rk / p.K;
-        const int k = (int)(rk - i * p.K);
+        uint32_t i, k, c;
+        item_of<H>(p, on ? it : items - 1, &i, &k, &c);
         uint4 kw = make_uint4(0, 0, 0, 0), vw = kw;
         if (on) {
             kw = __ldg(p.k_new + it);
@@ -167,6 +209,37 @@ __global__ void __launch_bounds__(kSlotThreads) kv_put_kernel(const SlotParams p
     }
 }
 
+// Eight 4-bit values as 16-bit numbers, exactly: a nibble n = c + 8 or-ed under an
+// exponent is 1024 + n (f16) or 128 + n (bf16); minus the offset, times the scale.
+template <bool BF16>
+__device__ __forceinline__ uint4 expand8(uint32_t w, uint32_t sc) {
+    uint32_t v[4];  // nibbles i and i + 4
+    if constexpr (BF16) {
+        const uint32_t sb = __float_as_uint(q4_scale_value(sc)) >> 16;  // 4 bits: exact
+        const uint32_t s2 = sb | sb << 16, off = 0x43084308u;           // 128 + 8
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t t = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+            const __nv_bfloat162 y = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&t),
+                                                     *reinterpret_cast<const __nv_bfloat162*>(&off)),
+                                             *reinterpret_cast<const __nv_bfloat162*>(&s2));
+            v[i] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+    } else {
+        const uint32_t s2 = sc * 0x00800080u, off = 0x64086408u;  // 1024 + 8
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t t = ((w >> (4 * i)) & 0x000f000fu) | 0x64006400u;
+            const __half2 y = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&t),
+                                              *reinterpret_cast<const __half2*>(&off)),
+                                      *reinterpret_cast<const __half2*>(&s2));
+            v[i] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+    }
+    return make_uint4(prmt(v[0], v[1], 0x5410u), prmt(v[2], v[3], 0x5410u),
+                      prmt(v[0], v[1], 0x7632u), prmt(v[2], v[3], 0x7632u));
+}
+
 // Eight elements of KV head k's row in slot s, in the 16-bit type.
 template <bool BF16, int KIND, int H>
 __device__ __forceinline__ uint4 take8(const SlotParams& p, const uint8_t* cache,
@@ -175,17 +248,15 @@ __device__ __forceinline__ uint4 take8(const SlotParams& p, const uint8_t* cache
     if (s < 0) return make_uint4(0, 0, 0, 0);
     const size_t blk = (size_t)(s >> 4);
     const int row = s & 15;
-    float x[8];
     if constexpr (KIND == GQA_KV_SAME) {
         return __ldg(reinterpret_cast<const uint4*>(cache) + ((blk * 16 + row) * p.K + k) * P + c);
     } else if constexpr (KIND == kKvFourbit) {
         const size_t r = (blk * p.K + k) * 16 + row;
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(cache) + r * P + c);
-        const float sv = q4_scale_value(
+        return expand8<BF16>(
+            __ldg(reinterpret_cast<const uint32_t*>(cache) + r * P + c),
             __ldg(static_cast<const uint8_t*>(scale) + r * (H / kQ4Group) + (c >> 2)));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = (float)((int)((w >> (4 * e)) & 15u) - 8) * sv;
     } else {
+        float x[8];
         const uint2 w = __ldg(reinterpret_cast<const uint2*>(cache) +
                               ((blk * 16 + row) * p.K + k) * P + c);
         const float sv = __ldg(static_cast<const float*>(scale) + (blk * p.K + k) * 16 + row);
@@ -199,23 +270,20 @@ __device__ __forceinline__ uint4 take8(const SlotParams& p, const uint8_t* cache
                 x[e] = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code,
                                                                   __NV_E4M3))) * sv;
         }
+        return make_uint4(Elt<BF16>::pack(x[0], x[1]), Elt<BF16>::pack(x[2], x[3]),
+                          Elt<BF16>::pack(x[4], x[5]), Elt<BF16>::pack(x[6], x[7]));
     }
-    return make_uint4(Elt<BF16>::pack(x[0], x[1]), Elt<BF16>::pack(x[2], x[3]),
-                      Elt<BF16>::pack(x[4], x[5]), Elt<BF16>::pack(x[6], x[7]));
 }
 
 template <bool BF16, int KIND, int H>
 __global__ void __launch_bounds__(kSlotThreads) kv_take_kernel(const SlotParams p) {
-    constexpr int P = H / 8;
     griddep_launch_dependents();
     griddep_wait();
-    const long long items = p.M * p.K * P;
-    for (long long it = (long long)blockIdx.x * kSlotThreads + threadIdx.x; it < items;
-         it += (long long)gridDim.x * kSlotThreads) {
-        const long long rk = it / P;
-        const int c = (int)(it % P);
-        const long long i = rk / p.K;
-        const int k = (int)(rk - i * p.K);
+    const uint32_t items = p.rows * p.K * (H / 8);
+    for (uint32_t it = blockIdx.x * kSlotThreads + threadIdx.x; it < items;
+         it += gridDim.x * kSlotThreads) {
+        uint32_t i, k, c;
+        item_of<H>(p, it, &i, &k, &c);
         const int s = slot_of(p, i, c == 0 && k == 0);
         const uint4 kw = take8<BF16, KIND, H>(p, p.k_cache, p.k_scale, s, k, c);
         const uint4 vw = take8<BF16, KIND, H>(p, p.v_cache, p.v_scale, s, k, c);
@@ -248,19 +316,24 @@ const void* pick_slot_kernel(const gqa_shape& s) {
                 : slot_kernel_kind<PUT, false, 64>(s.kv_dtype);
 }
 
-gqa_status launch_slots(const gqa_shape& s, const void* kernel, SlotParams& p,
+// `rows` rows from `p`, in launches of fewer than 2^31 items.
+gqa_status launch_slots(const gqa_shape& s, const void* kernel, SlotParams p, long long rows,
                         cudaStream_t stream) {
-    const long long items = p.M * s.K * (s.H / 8);
-    if (items == 0) return GQA_OK;
+    const long long per_row = (long long)s.K * (s.H / 8);
+    if (rows == 0) return GQA_OK;
     const int sms = device_sm_count();
     if (sms <= 0) return GQA_ERR_CUDA;
-    const long long need = (items + kSlotThreads - 1) / kSlotThreads, cap = (long long)sms * 32;
-    p.T = s.T;
-    p.K = s.K;
+    p.T = (uint32_t)s.T;
+    p.K = (uint32_t)s.K;
     p.max_blocks = s.max_blocks_per_seq;
     p.num_blocks = s.num_blocks;
+    while ((1ll << p.kshift) < s.K) ++p.kshift;
+    p.kmul = (uint32_t)(((1ull << 32) * ((1ull << p.kshift) - (uint64_t)s.K)) / (uint64_t)s.K + 1);
+    if (per_row >= (1ll << 31)) return GQA_ERR_SHAPE;
+    long long most = ((1ll << 31) - 1) / per_row;
+    if (!p.slots) most = most / s.T * s.T;  // whole sequences
+    if (most < 1) return GQA_ERR_SHAPE;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(need < cap ? need : cap));
     cfg.blockDim = dim3(kSlotThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -268,9 +341,31 @@ gqa_status launch_slots(const gqa_shape& s, const void* kernel, SlotParams& p,
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = (s.flags & (GQA_FLAG_PDL | GQA_FLAG_EARLY_KV)) ? 1 : 0;
-    void* args[] = {&p};
-    const cudaError_t e = cudaLaunchKernelExC(&cfg, kernel, args);
-    return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GQA_OK : GQA_ERR_CUDA;
+    while (rows > 0) {
+        const long long n = rows < most ? rows : most, items = n * per_row;
+        const long long need = (items + kSlotThreads - 1) / kSlotThreads, cap = (long long)sms * 32;
+        p.rows = (uint32_t)n;
+        cfg.gridDim = dim3((unsigned)(need < cap ? need : cap));
+        void* args[] = {&p};
+        if (cudaLaunchKernelExC(&cfg, kernel, args) != cudaSuccess ||
+            cudaGetLastError() != cudaSuccess)
+            return GQA_ERR_CUDA;
+        rows -= n;
+        if (p.k_new) {
+            p.k_new += items;
+            p.v_new += items;
+        } else {
+            p.k_out += items;
+            p.v_out += items;
+        }
+        if (p.slots) {
+            p.slots += n;
+        } else {
+            p.block_tables += n / s.T * s.max_blocks_per_seq;
+            p.context_lens += n / s.T;
+        }
+    }
+    return GQA_OK;
 }
 
 }  // namespace
@@ -291,8 +386,7 @@ gqa_status launch_kv_append_slots(const gqa_shape& s, long long rows, const void
     p.block_tables = block_tables;
     p.context_lens = context_lens;
     p.status = dev_status;
-    p.M = rows;
-    return launch_slots(s, pick_slot_kernel<true>(s), p, stream);
+    return launch_slots(s, pick_slot_kernel<true>(s), p, rows, stream);
 }
 
 gqa_status launch_kv_gather_slots(const gqa_shape& s, long long rows, const void* k_cache,
@@ -308,8 +402,7 @@ gqa_status launch_kv_gather_slots(const gqa_shape& s, long long rows, const void
     p.v_scale = const_cast<void*>(v_scale);
     p.slots = slots;
     p.status = dev_status;
-    p.M = rows;
-    return launch_slots(s, pick_slot_kernel<false>(s), p, stream);
+    return launch_slots(s, pick_slot_kernel<false>(s), p, rows, stream);
 }
 
 }  // namespace gqa

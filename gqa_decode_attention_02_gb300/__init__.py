@@ -228,10 +228,6 @@ def append_verify_attention(q, k_new, v_new, k_cache, v_cache, block_tables, con
 def _attention_quant(fn_name, q, k_cache, v_cache, k_scale, v_scale, block_tables,
                      context_lens, out, scale, workspace, status, stream, pdl, early_kv, kv,
                      window=0, tree_mask=None):
-    if kv == "int4":
-        return _attention4(q, None, None, k_cache, v_cache, k_scale, v_scale, block_tables,
-                           context_lens, out, scale, workspace, status, stream, pdl, early_kv,
-                           window, tree_mask, "decode" in fn_name)
     _lib._need(q, "q", ndim=4)
     if tree_mask is not None:
         _lib._need(tree_mask, "tree_mask", torch.int64, 2)  # uint64 bits, held as int64
@@ -270,6 +266,10 @@ def decode_attention_quant(q, k_cache, v_cache, k_scale, v_scale, block_tables, 
     """gqa_decode_attention_quant over a one-byte cache (kv = "int8" / "e4m3"),
     or gqa_attention_fourbit over a 4-bit one (kv = "int4", layouts as in
     kv_append_quant); window > 0 is local attention as in decode_attention."""
+    if kv == "int4":
+        return _attention4(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                           None, None, out, scale, workspace, status, stream, pdl, early_kv,
+                           window, None, True)
     return _attention_quant("gqa_decode_attention_quant", q, k_cache, v_cache, k_scale, v_scale,
                             block_tables, context_lens, out, scale, workspace, status, stream,
                             pdl, early_kv, kv, window)
@@ -283,6 +283,10 @@ def verify_attention_quant(q, k_cache, v_cache, k_scale, v_scale, block_tables, 
     window > 0 is local attention and tree_mask (int64 [B,T] holding the uint64
     mask rows) tree verification, as in verify_attention
     (gqa_tree_verify_attention_quant)."""
+    if kv == "int4":
+        return _attention4(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                           None, None, out, scale, workspace, status, stream, pdl, early_kv,
+                           window, tree_mask, False)
     return _attention_quant("gqa_verify_attention_quant", q, k_cache, v_cache, k_scale, v_scale,
                             block_tables, context_lens, out, scale, workspace, status, stream,
                             pdl, early_kv, kv, window, tree_mask)
@@ -292,8 +296,8 @@ def _append_attention_quant(fn_name, q, k_new, v_new, k_cache, v_cache, k_scale,
                             block_tables, context_lens, out, scale, workspace, status, stream,
                             pdl, early_kv, kv, window):
     if kv == "int4":
-        return _attention4(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables,
-                           context_lens, out, scale, workspace, status, stream, pdl, early_kv,
+        return _attention4(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                           k_new, v_new, out, scale, workspace, status, stream, pdl, early_kv,
                            window, None, "decode" in fn_name)
     _lib._need(q, "q", ndim=4)
     _lib._need(k_new, "k_new", q.dtype, 4)
@@ -519,20 +523,6 @@ def accept_sampled(target_probs, draft_probs, draft_ids, uniforms, context_lens=
 _checked: dict = {}
 
 
-def _gpu_of(tensors) -> int:
-    """The GPU all tensors are on if every one of them is contiguous; else -1."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t.get_device() != dev or not t.is_contiguous():
-            return -1
-    return dev
-
-
-def _here(dev: int, stream) -> bool:
-    """A call on GPU `dev` can go straight to the current stream."""
-    return stream is None and dev == torch.cuda.current_device()
-
-
 def _remember(key, shape):
     if len(_checked) >= 4096:  # sizes keep changing (prompt lengths): start over
         _checked.clear()
@@ -616,33 +606,43 @@ def _attention4_shape(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block
                             flags=flags, window=window)
 
 
-def _attention4(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+def _attention4(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, k_new, v_new,
                 out, scale, workspace, status, stream, pdl, early_kv, window, tree_mask, decode):
-    ts = [q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens]
-    if k_new is not None:
-        ts += (k_new, v_new)
-    if tree_mask is not None:
-        ts.append(tree_mask)
     try:
-        dev = _gpu_of(ts)
-        key = (dev, scale, pdl, early_kv, window, decode, k_new is None, tree_mask is None,
-               *[(t.shape, t.dtype) for t in ts])
-        shape = _checked.get(key)
+        dev = q.get_device()
+        key = (dev, decode, window, scale, pdl, early_kv, q.shape, q.dtype, k_cache.shape,
+               k_cache.dtype, v_cache.shape, v_cache.dtype, k_scale.shape, k_scale.dtype,
+               v_scale.shape, v_scale.dtype, block_tables.shape, block_tables.dtype,
+               context_lens.shape, context_lens.dtype)
+        fit = (q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+               and k_scale.is_contiguous() and v_scale.is_contiguous()
+               and block_tables.is_contiguous() and context_lens.is_contiguous()
+               and dev == k_cache.get_device() == v_cache.get_device() == k_scale.get_device()
+               == v_scale.get_device() == block_tables.get_device() == context_lens.get_device())
+        if k_new is not None:
+            key += (k_new.shape, k_new.dtype, v_new.shape, v_new.dtype)
+            fit = (fit and k_new.is_contiguous() and v_new.is_contiguous()
+                   and dev == k_new.get_device() == v_new.get_device())
+        if tree_mask is not None:
+            key += ("tree", tree_mask.shape, tree_mask.dtype)
+            fit = fit and tree_mask.is_contiguous() and dev == tree_mask.get_device()
+        shape = _checked.get(key) if fit else None
     except (AttributeError, TypeError):
-        shape, dev = None, -1
-    if shape is None or dev < 0:
+        key = shape = None
+    if shape is None:
         flags = (_lib.FLAG_PDL if pdl else 0) | (_lib.FLAG_EARLY_KV if early_kv else 0)
         made = _attention4_shape(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale,
                                  block_tables, context_lens, scale, flags, window, tree_mask,
                                  decode)
-        dev = _lib.one_device(*ts).index
+        dev = _lib.one_device(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables,
+                              context_lens, tree_mask).index
         with torch.cuda.device(dev):
             made.nbytes = _lib.workspace_size(made)
-        shape = _remember((dev, *key[1:]), made)
-    if not _here(dev, stream):
+        shape = _remember(key, made)
+    if stream is not None or dev != _lib.current_gpu():
         with _lib.on_device(torch.device("cuda", dev), stream):
-            return _attention4(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables,
-                               context_lens, out, scale, workspace, status, None, pdl, early_kv,
+            return _attention4(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                               k_new, v_new, out, scale, workspace, status, None, pdl, early_kv,
                                window, tree_mask, decode)
     if out is None:
         out = torch.empty_like(q)
@@ -661,15 +661,19 @@ def _attention4(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table
     else:
         _lib._need(workspace, "workspace", torch.uint8)
         _lib.one_device(q, workspace)
+    L = _lib.lib()
     mask = None if tree_mask is None else tree_mask.data_ptr()
-    at = [t.data_ptr() for t in ts[:7]]
     if k_new is None:
-        rc = _lib.lib().gqa_attention_fourbit(shape[1], *at, mask, out.data_ptr(),
-                                              workspace.data_ptr(), workspace.numel(), st, cs)
+        rc = L.gqa_attention_fourbit(
+            shape[1], q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), mask,
+            out.data_ptr(), workspace.data_ptr(), workspace.numel(), st, cs)
     else:
-        rc = _lib.lib().gqa_append_attention_fourbit(
-            shape[1], at[0], k_new.data_ptr(), v_new.data_ptr(), *at[1:], mask, out.data_ptr(),
-            workspace.data_ptr(), workspace.numel(), st, cs)
+        rc = L.gqa_append_attention_fourbit(
+            shape[1], q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(),
+            context_lens.data_ptr(), mask, out.data_ptr(), workspace.data_ptr(),
+            workspace.numel(), st, cs)
     if rc:
         raise _lib.GqaError("gqa_attention_fourbit" if k_new is None
                             else "gqa_append_attention_fourbit", rc)
@@ -733,19 +737,24 @@ def _slots_shape(rows, k_cache, v_cache, k_scale, v_scale, kv, pdl):
     return shape
 
 
-def _slots_call(rows, k_cache, v_cache, k_scale, v_scale, slots, kv, pdl):
-    """(shape, device index, tensors) of a call by slot; rows: k and v [M,K,H]."""
-    k, v = rows
-    ts = [k, v, k_cache, v_cache, slots]
-    if k_scale is not None or v_scale is not None:
-        ts += (k_scale, v_scale)
+def _slots_call(k, v, k_cache, v_cache, k_scale, v_scale, slots, kv, pdl):
+    """(checked shape, device index) of a call by slot; rows k and v [M,K,H]."""
     try:
-        dev = _gpu_of(ts)
-        key = (kv, pdl, *[(t.shape, t.dtype) for t in ts])
-        shape = _checked.get(key)
+        dev = k.get_device()
+        key = (kv, pdl, k.shape, k.dtype, v.shape, v.dtype, k_cache.shape, k_cache.dtype,
+               v_cache.shape, v_cache.dtype, slots.shape, slots.dtype)
+        fit = (k.is_contiguous() and v.is_contiguous() and k_cache.is_contiguous()
+               and v_cache.is_contiguous() and slots.is_contiguous()
+               and dev == v.get_device() == k_cache.get_device() == v_cache.get_device()
+               == slots.get_device())
+        if k_scale is not None or v_scale is not None:
+            key += (k_scale.shape, k_scale.dtype, v_scale.shape, v_scale.dtype)
+            fit = (fit and k_scale.is_contiguous() and v_scale.is_contiguous()
+                   and dev == k_scale.get_device() == v_scale.get_device())
+        shape = _checked.get(key) if fit else None
     except (AttributeError, TypeError):
-        shape, dev = None, -1
-    if shape is None or dev < 0:
+        key = shape = None
+    if shape is None:
         _lib._need(k, "k_new", ndim=3)
         _lib._need(v, "v_new", k.dtype, 3)
         if v.shape != k.shape:
@@ -754,7 +763,7 @@ def _slots_call(rows, k_cache, v_cache, k_scale, v_scale, slots, kv, pdl):
         if slots.shape[0] != k.shape[0]:
             raise ValueError(f"slots must have {k.shape[0]} entries, got {slots.shape[0]}")
         made = _slots_shape(k, k_cache, v_cache, k_scale, v_scale, kv, pdl)
-        dev = _lib.one_device(*ts).index
+        dev = _lib.one_device(k, v, k_cache, v_cache, k_scale, v_scale, slots).index
         shape = _remember(key, made)
     return shape, dev
 
@@ -766,8 +775,8 @@ def kv_append_slots(k_new, v_new, k_cache, v_cache, slots, *, k_scale=None, v_sc
     any kind: kv="same" ([NB,16,K,H] in the rows' dtype, no scales), "int8" /
     "e4m3" (one byte, scales fp32 [NB,K,16]) or "int4" ([NB,K,16,H/2], scales
     uint8 [NB,K,16,H/32]).  The slots of one call must differ."""
-    shape, dev = _slots_call((k_new, v_new), k_cache, v_cache, k_scale, v_scale, slots, kv, pdl)
-    if not _here(dev, stream):
+    shape, dev = _slots_call(k_new, v_new, k_cache, v_cache, k_scale, v_scale, slots, kv, pdl)
+    if stream is not None or dev != _lib.current_gpu():
         with _lib.on_device(torch.device("cuda", dev), stream):
             return kv_append_slots(k_new, v_new, k_cache, v_cache, slots, k_scale=k_scale,
                                    v_scale=v_scale, kv=kv, status=status, pdl=pdl)
@@ -794,7 +803,7 @@ def kv_gather_slots(k_cache, v_cache, slots, *, k_scale=None, v_scale=None, kv="
         raise TypeError("k_cache and slots must be torch.Tensors")
     if k_cache.dim() != 4 or slots.dim() != 1:
         raise ValueError("k_cache must have 4 dims and slots 1")
-    if not _here(k_cache.get_device(), stream):
+    if stream is not None or k_cache.get_device() != _lib.current_gpu():
         if not k_cache.is_cuda:
             raise ValueError("k_cache must be a CUDA tensor (the library has no CPU path)")
         with _lib.on_device(k_cache.device, stream):
@@ -814,7 +823,7 @@ def kv_gather_slots(k_cache, v_cache, slots, *, k_scale=None, v_scale=None, kv="
     for t, n in ((k_out, "k_out"), (v_out, "v_out")):
         if tuple(t.shape) != want or t.dtype != dtype:
             raise ValueError(f"{n} must be {list(want)} of {dtype}, got {tuple(t.shape)}, {t.dtype}")
-    shape, dev = _slots_call((k_out, v_out), k_cache, v_cache, k_scale, v_scale, slots, kv, pdl)
+    shape, dev = _slots_call(k_out, v_out, k_cache, v_cache, k_scale, v_scale, slots, kv, pdl)
     st = None
     if status is not None:
         st = _status_arg(status)
@@ -879,17 +888,25 @@ def plan_blocks(context_lens, new_lens, block_tables, held, free_ring, ring_stat
         max_tokens = -1 if slots is None else slots.shape[0]
     if max_tokens < 0 and (slots is not None or positions is not None):
         raise ValueError("positions need slots or max_tokens")
-    given = [t for t in (context_lens_out, held_out, ring_state_out, cu_new, slots, positions)
-             if t is not None]
+    outs = (context_lens_out, held_out, ring_state_out, cu_new, slots, positions)
     try:
-        key = ("plan", max_tokens, context_lens_out is None, held_out is None,
-               ring_state_out is None, cu_new is None, slots is None,
-               *[(t.shape, t.dtype) for t in (*ins, *given)])
-        known = key in _checked
-        dev = _gpu_of((*ins, *given))
+        dev = context_lens.get_device()
+        key = ("plan", max_tokens, context_lens.shape, context_lens.dtype, new_lens.shape,
+               new_lens.dtype, block_tables.shape, block_tables.dtype, held.shape, held.dtype,
+               free_ring.shape, free_ring.dtype, ring_state.shape, ring_state.dtype,
+               *[None if t is None else (t.shape, t.dtype) for t in outs])
+        fit = (context_lens.is_contiguous() and new_lens.is_contiguous()
+               and block_tables.is_contiguous() and held.is_contiguous()
+               and free_ring.is_contiguous() and ring_state.is_contiguous()
+               and dev == new_lens.get_device() == block_tables.get_device()
+               == held.get_device() == free_ring.get_device() == ring_state.get_device())
+        for t in outs:
+            if t is not None:
+                fit = fit and t.is_contiguous() and dev == t.get_device()
+        known = fit and key in _checked
     except (AttributeError, TypeError):
-        known, dev = False, -1
-    if not known or dev < 0:
+        key, known = None, False
+    if not known:
         B = block_tables.shape[0] if isinstance(block_tables, torch.Tensor) else 0
         _plan_check(ins, ((context_lens_out, "context_lens_out", B), (held_out, "held_out", B),
                           (ring_state_out, "ring_state_out", 2), (cu_new, "cu_new", B + 1),
@@ -897,7 +914,7 @@ def plan_blocks(context_lens, new_lens, block_tables, held, free_ring, ring_stat
                     max_tokens)
         _remember(key, _lib.Shape())
         dev = context_lens.get_device()
-    if not _here(dev, stream):
+    if stream is not None or dev != _lib.current_gpu():
         with _lib.on_device(torch.device("cuda", dev), stream):
             return plan_blocks(*ins, max_tokens=max_tokens,
                                context_lens_out=None if in_place else context_lens_out,

@@ -252,6 +252,12 @@ def raw_stream(index: int) -> int:
     return _raw_stream(index)
 
 
+def current_gpu() -> int:
+    """Index of the current GPU."""
+    return _current_gpu()
+
+
+_current_gpu = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 # torch's own accessor where it has one (it makes no Stream object: ~1 us a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda i: torch.cuda.current_stream(i).cuda_stream)

@@ -56,13 +56,14 @@ gqa_status attention_fourbit_entry(const gqa_shape* s, bool fused, const void* q
         !aligned16(v_scale) || !aligned16(out) || (fused && (!aligned16(k_new) || !aligned16(v_new))))
         return GQA_ERR_ALIGN;
     if (tree_mask && (reinterpret_cast<uintptr_t>(tree_mask) & 7u) != 0) return GQA_ERR_ALIGN;
-    size_t need = 0;
-    st = gqa::fourbit_workspace_bytes(*s, &need);
-    if (st != GQA_OK) return st;
-    if (!workspace || ws_bytes < need) return GQA_ERR_WORKSPACE;
+    if (!workspace) return GQA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return GQA_ERR_ALIGN;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (fused) {
+        size_t need = 0;  // nothing is appended by a call that then refuses
+        st = gqa::fourbit_workspace_bytes(*s, &need);
+        if (st != GQA_OK) return st;
+        if (ws_bytes < need) return GQA_ERR_WORKSPACE;
         st = gqa::launch_kv_append_slots(
             *s, (long long)s->B * s->T, k_new, v_new, const_cast<uint8_t*>(k_cache),
             const_cast<uint8_t*>(v_cache), const_cast<uint8_t*>(k_scale),

@@ -43,6 +43,7 @@
 #include <map>
 #include <mutex>
 #include <tuple>
+#include <type_traits>
 
 #include "fourbit.cuh"
 #include "launch.h"
@@ -53,13 +54,17 @@ namespace {
 
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int kStepTiles = 2;    // tiles a warp computes per step
-constexpr int kSlots = 2;        // steps in a warp's buffer
-constexpr int kQ4SegUnits = 3;   // start-up cost of a segment, in tiles per warp
+constexpr int kSlots = 3;        // steps in a warp's buffer: one computed, two in flight
+// Start-up cost of a segment, in tiles per warp (256 ragged sequences, 8 rows, 4
+// warps: 2.1-3.1 us a segment, 0.24 us a tile; 24 rows: 7 us, 0.15 us).
+constexpr int q4_seg_units(int NW) { return NW == 1 ? 3 : NW == 2 ? 5 : 8; }
+constexpr int kQ4Direct = 10;     // longest segment of a planless launch, in tiles per warp
 constexpr int kQ4CutCost = 6;    // what cutting segments costs a CTA, in tiles per warp
 constexpr float kQ4None = -1e30f;  // maximum of no scores: finite, so references need no test
 constexpr float kQ4Gap = 8.0f;   // log2-domain slack before rescaling
 constexpr size_t kQ4FlagBytes = 262144; // tickets, one per CTA (as large as the other kernels' region)
 constexpr long long kQ4MaxRows = 8192;  // T*G
+constexpr int kQ4MaxTiles = 3;          // row tiles of 8 per warp
 
 struct Q4Params {
     const void* q;
@@ -78,6 +83,8 @@ struct Q4Params {
     int C, Rc, KC;  // row chunks per KV head, rows per chunk, virtual heads K*C
     int max_blocks, num_blocks;
     int window;
+    int direct;  // a CTA per segment (the host's rule)
+    int bf16;    // type of q and out
     float scale_log2;
     uint32_t code_stride, scale_stride;  // bytes of a block's codes, scales
     uint32_t ex[2];  // 0x64006400, 0x54005400 (see q4_values)
@@ -120,6 +127,15 @@ struct Pieces {
         ctx = __ldg(p.context_lens + b);
         nblk = q4_blocks(ctx, p.T, p.max_blocks, p.window);
         f0 = q4_first_block(ctx, p.T, p.window);
+    }
+    // Virtual head k_ of sequence b_, whole; false for an invalid length.
+    __device__ bool one(const Q4Params& p, int b_, int k_) {
+        b = b_;
+        k = k_;
+        load(p);
+        seg = start = c0 = i0 = 0;
+        i1 = c1 = nblk;
+        return nblk > 0;
     }
     __device__ bool clip() {
         i0 = max(0, c0 - start);
@@ -289,19 +305,85 @@ __device__ __forceinline__ void q4_values(uint32_t x, const Q4Scale& f, const ui
     }
 }
 
-// A warp's state for one piece of a segment: NW tiles of 8 query rows.
-template <int H, bool BF16, int NW>
+// The q rows of a piece, in shared memory: every warp of the CTA needs the same.
+// Row u*8+g, dims H/4*q4 .. as B fragments: word j of a token's codes meets k-steps 2j
+// (nibbles 0|4, 1|5) and 2j+1 (2|6, 3|7).  Rows are scaled by a power of two that
+// puts their largest element in [64, 128): f16 then holds an element of either
+// type exactly down to 2^-20 of the largest, and to within 2^-31 of it below.
+template <int H, int NW>
+struct Q4Rows {
+    uint2 frag[NW][Q4<H>::kSteps][32];
+    // -8 times a lane's part of its row's sum, as two f16 terms (22 bits; at most
+    // 8 * 32 * 128): meets the scales in one more k-step
+    uint32_t corr[NW][32];
+    float factor[8 * NW];  // of the rows' scores, to the log2 domain
+
+    // This lane's raw words of row 8u + g of virtual head k of sequence b.
+    static __device__ __forceinline__ void load(const Q4Params& p, int b, int k, int u,
+                                                uint32_t (&w)[H / 8]) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, q4 = lane & 3;
+        const int kv = k / p.C, rb = (k - kv * p.C) * p.Rc, re = min(p.R, rb + p.Rc);
+        const int r = rb + 8 * u + g, t = r / p.G, gg = r - t * p.G;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const uint16_t*>(p.q) +
+            (((size_t)b * p.T + t) * p.N + (size_t)kv * p.G + gg) * H + q4 * (H / 4));
+#pragma unroll
+        for (int i = 0; i < H / 32; ++i) {
+            const uint4 x = r < re ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+            w[4 * i] = x.x;
+            w[4 * i + 1] = x.y;
+            w[4 * i + 2] = x.z;
+            w[4 * i + 3] = x.w;
+        }
+    }
+    __device__ __forceinline__ void make(const Q4Params& p, int u, uint32_t (&w)[H / 8]) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, q4 = lane & 3;
+        auto lo = [&](uint32_t x) { return p.bf16 ? Elt<true>::lo(x) : Elt<false>::lo(x); };
+        auto hi = [&](uint32_t x) { return p.bf16 ? Elt<true>::hi(x) : Elt<false>::hi(x); };
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < H / 8; ++i) top = fmaxf(top, fmaxf(fabsf(lo(w[i])), fabsf(hi(w[i]))));
+        top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
+        const int e = min(max(127 + 6 - (int)(__float_as_uint(top) >> 23), -112), 112);
+        const float f = __uint_as_float((uint32_t)(127 + e) << 23);  // row times 2^e
+        const float back = __uint_as_float((uint32_t)(127 - e) << 23);
+        float qsum = 0.f;
+#pragma unroll
+        for (int i = 0; i < H / 8; ++i) {
+            w[i] = Elt<false>::pack(lo(w[i]) * f, hi(w[i]) * f);
+            qsum += Elt<false>::lo(w[i]) + Elt<false>::hi(w[i]);
+        }
+        const float c8 = -8.f * qsum;
+        const float c8_hi = __half2float(__float2half_rn(c8));
+        corr[u][lane] = Elt<false>::pack(c8_hi, c8 - c8_hi);
+        // never 0, which a hidden position's -inf must not meet
+        if (q4 == 0) factor[8 * u + g] = fmaxf(kQ4Unit * p.scale_log2 * back, 1.17549435e-38f);
+#pragma unroll
+        for (int j = 0; j < H / 32; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                frag[u][2 * j + h][lane] =
+                    make_uint2(prmt(w[4 * j + h], w[4 * j + 2 + h], 0x5410u),
+                               prmt(w[4 * j + h], w[4 * j + 2 + h], 0x7632u));
+    }
+};
+
+// A warp's state for one piece of a segment: NW tiles of 8 query rows.  Several
+// tiles share every converted code, and read the q fragments from shared memory.
+template <int H, int NW>
 struct Q4Warp {
     using L = Q4<H>;
+    static constexpr bool kKeepQ = NW == 1;  // q fragments in registers
     const Q4Params& p;
+    const Q4Rows<H, NW>* qr;
     const int lane, g, q4;
     const uint32_t ex[2];
     uint32_t kro, vro, sko, svo;  // this lane's offsets in a tile
     uint32_t cko;                 // ... and of the 8 scale bytes it looks over
-    int lim0[NW], lim1[NW];  // last position that rows 8u + 2*q4 (+1) see
     int rbase, rend, b, kv, ctx;
     int edge_lo, edge_hi;  // tiles <= edge_lo or >= edge_hi hold hidden positions
-    uint32_t qf[NW][L::kSteps][2], qc[NW];
+    uint32_t qf[kKeepQ ? NW : 1][L::kSteps][2], qc[NW];
     float acc[NW][L::kSteps][4];
     // sums that ride along with the PV product as one more row tile: [0], [1]
     // sum p s of this lane's group (what n = c + 8 adds, times 1/8) and [2], [3]
@@ -311,8 +393,8 @@ struct Q4Warp {
     float m0[NW], m1[NW];
     bool bad;
 
-    __device__ Q4Warp(const Q4Params& p_)
-        : p(p_), lane(threadIdx.x & 31), g((threadIdx.x & 31) >> 2), q4(threadIdx.x & 3),
+    __device__ Q4Warp(const Q4Params& p_, const Q4Rows<H, NW>* qr_)
+        : p(p_), qr(qr_), lane(threadIdx.x & 31), g((threadIdx.x & 31) >> 2), q4(threadIdx.x & 3),
           ex{p_.ex[0], p_.ex[1]} {
         const int ta = token();
         const int ra = H == 128 ? (ta ^ ((ta >> 2) & 1)) : (ta ^ ((ta >> 1) & 2));
@@ -328,12 +410,8 @@ struct Q4Warp {
     // are then tokens q4, q4 + 4 and q4 + 8, q4 + 12.
     __device__ __forceinline__ int token() const { return (g >> 1) + 4 * (g & 1); }
 
-    // q rows of the segment as B fragments.  Row u*8+g, dims H/4*q4 ..: word j
-    // of a token's codes meets steps 2j (nibbles 0|4, 1|5) and 2j+1 (2|6, 3|7).
-    // Rows are scaled by a power of two that puts their largest element in [64,
-    // 128): f16 then holds an element of either type exactly down to 2^-20 of
-    // the largest, and to within 2^-31 of it below that.
-    __device__ void begin(const Pieces& s) {
+    // Start a piece, whose q rows are in *qr.
+    __device__ __forceinline__ void begin(const Pieces& s) {
         b = s.b;
         ctx = s.ctx;
         kv = s.k / p.C;
@@ -344,72 +422,25 @@ struct Q4Warp {
         // chain mask and none take the same steps), past the end, or at or below the
         // last row's window
         edge_hi = ((ctx - p.T) >> 4) - s.f0;
-        edge_lo = p.window > 0 ? ((ctx - 1 - p.window) >> 4) - s.f0 : -1;
-        if (p.window > 0 && ctx - 1 < p.window) edge_lo = -1;
+        edge_lo = p.window > 0 && ctx > p.window ? ((ctx - 1 - p.window) >> 4) - s.f0 : -1;
 #pragma unroll
         for (int u = 0; u < NW; ++u) {
-            const int r0 = rbase + 8 * u + 2 * q4;
-            lim0[u] = ctx - p.T + min(r0 / p.G, p.T - 1);
-            lim1[u] = ctx - p.T + min((r0 + 1) / p.G, p.T - 1);
             m0[u] = m1[u] = kQ4None;
+            sl0[u] = qr->factor[8 * u + 2 * q4];
+            sl1[u] = qr->factor[8 * u + 2 * q4 + 1];
+            qc[u] = qr->corr[u][lane];
 #pragma unroll
             for (int e = 0; e < 4; ++e) sum[u][e] = 0.f;
 #pragma unroll
-            for (int mt = 0; mt < L::kSteps; ++mt)
+            for (int mt = 0; mt < L::kSteps; ++mt) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[u][mt][e] = 0.f;
-            const int r = rbase + 8 * u + g;
-            uint32_t w[H / 8];
-#pragma unroll
-            for (int i = 0; i < H / 8; ++i) w[i] = 0u;
-            if (r < rend) {
-                const int t = r / p.G, gg = r - t * p.G;
-                const uint4* src = reinterpret_cast<const uint4*>(
-                    static_cast<const uint16_t*>(p.q) +
-                    (((size_t)b * p.T + t) * p.N + (size_t)kv * p.G + gg) * H + q4 * (H / 4));
-#pragma unroll
-                for (int i = 0; i < H / 32; ++i) {
-                    const uint4 x = __ldg(src + i);
-                    w[4 * i] = x.x;
-                    w[4 * i + 1] = x.y;
-                    w[4 * i + 2] = x.z;
-                    w[4 * i + 3] = x.w;
+                if constexpr (kKeepQ) {
+                    const uint2 f = qr->frag[u][mt][lane];
+                    qf[u][mt][0] = f.x;
+                    qf[u][mt][1] = f.y;
                 }
             }
-            float top = 0.f;
-#pragma unroll
-            for (int i = 0; i < H / 8; ++i)
-                top = fmaxf(top, fmaxf(fabsf(Elt<BF16>::lo(w[i])), fabsf(Elt<BF16>::hi(w[i]))));
-            top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
-            const int e = min(max(127 + 6 - (int)(__float_as_uint(top) >> 23), -112), 112);
-            const float f = __uint_as_float((uint32_t)(127 + e) << 23);  // row times 2^e
-            const float back = __uint_as_float((uint32_t)(127 - e) << 23);
-            float qsum = 0.f;
-#pragma unroll
-            for (int i = 0; i < H / 8; ++i) {
-                w[i] = Elt<false>::pack(Elt<BF16>::lo(w[i]) * f, Elt<BF16>::hi(w[i]) * f);
-                qsum += Elt<false>::lo(w[i]) + Elt<false>::hi(w[i]);
-            }
-            // -8 times this lane's part of the row's sum, as two f16 terms (22 bits;
-            // at most 8 * 32 * 128): meets the scales in one more k-step
-            const float c8 = -8.f * qsum;
-            const float hi = __half2float(__float2half_rn(c8));
-            qc[u] = Elt<false>::pack(hi, c8 - hi);
-            // the factors of the rows this lane's scores belong to (rows 2*q4 and
-            // 2*q4 + 1 sit in lanes 8*q4 and 8*q4 + 4); never 0, which a hidden
-            // position's -inf must not meet
-            sl0[u] = fmaxf(kQ4Unit * p.scale_log2 * __shfl_sync(FULL, back, 8 * q4),
-                           1.17549435e-38f);
-            sl1[u] = fmaxf(kQ4Unit * p.scale_log2 * __shfl_sync(FULL, back, 8 * q4 + 4),
-                           1.17549435e-38f);
-#pragma unroll
-            for (int j = 0; j < L::kKWords; ++j)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    qf[u][2 * j + h][0] = prmt(w[4 * j + h], w[4 * j + 2 + h], 0x5410u);
-                    qf[u][2 * j + h][1] = prmt(w[4 * j + h], w[4 * j + 2 + h], 0x7632u);
-                }
         }
     }
 
@@ -418,47 +449,66 @@ struct Q4Warp {
     __device__ __forceinline__ void mask(float (&sc)[4], int u, int tb) const {
         const int wl = p.window > 0 ? p.window : (1 << 30);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int pos = tb + token() + (e >> 1) * 8;
-            const int lim = (e & 1) ? lim1[u] : lim0[u];
-            bool off = pos > lim || pos <= lim - wl;
-            if (p.tree_mask) {
-                const int fn = ctx - p.T;
-                if (pos >= fn && pos < lim) {
-                    const uint64_t row = __ldg(p.tree_mask + (size_t)b * p.T + (lim - fn));
-                    off |= !((row >> (pos - fn)) & 1ull);
-                }
+        for (int h = 0; h < 2; ++h) {  // row rbase + 8u + 2*q4 + h, of new token t
+            const int t = min((rbase + 8 * u + 2 * q4 + h) / p.G, p.T - 1), lim = ctx - p.T + t;
+            const uint64_t row = p.tree_mask ? __ldg(p.tree_mask + (size_t)b * p.T + t) : ~0ull;
+#pragma unroll
+            for (int e = h; e < 4; e += 2) {
+                const int pos = tb + token() + (e >> 1) * 8, j = pos - (ctx - p.T);
+                const bool off = pos > lim || pos <= lim - wl ||
+                                 (j >= 0 && j < t && j < 64 && !((row >> j) & 1ull));
+                if (off) sc[e] = -INFINITY;
             }
-            if (off) sc[e] = -INFINITY;
         }
     }
 
-    // Scores of a tile.  FAST: its codes come as n s; -8 s sum q is added by one
-    // more k-step (scales times the qc of begin).
-    template <bool FAST>
-    __device__ __forceinline__ void scores(float (&sc)[NW][4], const uint8_t* tile) {
-        const Q4Scale fa((uint32_t)tile[sko] * 0x00800080u);
-        const Q4Scale fb((uint32_t)tile[sko + 8 * L::kGroups] * 0x00800080u);
-        uint32_t wa[L::kKWords], wb[L::kKWords];
-        q4_words(tile + kro, wa);
-        q4_words(tile + kro + 8 * L::kRow, wb);
+    // Scores of NT tiles.  FAST: their codes come as n s; -8 s sum q is added by one
+    // more k-step (scales times the rows' corr).
+    template <bool FAST, int NT>
+    __device__ __forceinline__ void scores(float (&sc)[NT][NW][4], const uint8_t* tiles) {
+        uint32_t wa[NT][L::kKWords], wb[NT][L::kKWords];
+        uint32_t sa[NT], sb[NT];
 #pragma unroll
-        for (int u = 0; u < NW; ++u) {
+        for (int j = 0; j < NT; ++j) {
+            const uint8_t* tile = tiles + j * L::kTile;
+            sa[j] = (uint32_t)tile[sko] * 0x00800080u;
+            sb[j] = (uint32_t)tile[sko + 8 * L::kGroups] * 0x00800080u;
+            q4_words(tile + kro, wa[j]);
+            q4_words(tile + kro + 8 * L::kRow, wb[j]);
+        }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[u][e] = 0.f;
-            if constexpr (FAST) q4_mma(sc[u], as_u32(fa.s), as_u32(fb.s), 0u, 0u, qc[u], 0u);
+        for (int j = 0; j < NT; ++j) {
+            const Q4Scale fa(sa[j]), fb(sb[j]);
+#pragma unroll
+            for (int u = 0; u < NW; ++u) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[j][u][e] = 0.f;
+                if constexpr (FAST)
+                    q4_mma(sc[j][u], as_u32(fa.s), as_u32(fb.s), 0u, 0u, qc[u], 0u);
+            }
         }
 #pragma unroll
         for (int i = 0; i < L::kKWords; ++i) {
-            uint32_t va[4], vb[4];
-            q4_values<FAST>(wa[i], fa, ex, va);
-            q4_values<FAST>(wb[i], fb, ex, vb);
+            uint32_t va[NT][4], vb[NT][4];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                q4_values<FAST>(wa[j][i], Q4Scale(sa[j]), ex, va[j]);
+                q4_values<FAST>(wb[j][i], Q4Scale(sb[j]), ex, vb[j]);
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int u = 0; u < NW; ++u)
-                    q4_mma(sc[u], va[2 * h], vb[2 * h], va[2 * h + 1], vb[2 * h + 1],
-                           qf[u][2 * i + h][0], qf[u][2 * i + h][1]);
+                for (int u = 0; u < NW; ++u) {
+                    uint2 f;
+                    if constexpr (kKeepQ)
+                        f = make_uint2(qf[u][2 * i + h][0], qf[u][2 * i + h][1]);
+                    else
+                        f = qr->frag[u][2 * i + h][lane];
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+                        q4_mma(sc[j][u], va[j][2 * h], vb[j][2 * h], va[j][2 * h + 1],
+                               vb[j][2 * h + 1], f.x, f.y);
+                }
         }
     }
 
@@ -562,8 +612,7 @@ struct Q4Warp {
         const bool large = (top & 0x80808080u) != 0u;  // a byte of 224 or more
         float sc[kStepTiles][NW][4];
         if (!__any_sync(FULL, large) && nt == kStepTiles && i + nt <= edge_hi && i > edge_lo) {
-#pragma unroll
-            for (int j = 0; j < kStepTiles; ++j) scores<true>(sc[j], slot + j * L::kTile);
+            scores<true, kStepTiles>(sc, slot);
             raise(sc);
 #pragma unroll
             for (int j = 0; j < kStepTiles; ++j)
@@ -573,7 +622,8 @@ struct Q4Warp {
 #pragma unroll
         for (int j = 0; j < kStepTiles; ++j) {
             if (j < nt) {
-                scores<false>(sc[j], slot + j * L::kTile);
+                scores<false, 1>(*reinterpret_cast<float (*)[1][NW][4]>(&sc[j]),
+                                 slot + j * L::kTile);
 #pragma unroll
                 for (int u = 0; u < NW; ++u) mask(sc[j][u], u, tb + 16 * j);
             } else {
@@ -589,8 +639,8 @@ struct Q4Warp {
             if (j < nt) values<false>(sc[j], slot + j * L::kTile, tb + 16 * j);
     }
 
-    // This warp's (max, sum, accumulator) of every row to its scratch rows.
-    __device__ void save(float* head, float* rows) {
+    // This warp's maxima and sums of every row, and the accumulators of row tile U.
+    __device__ __forceinline__ void save_head(float* head) const {
 #pragma unroll
         for (int u = 0; u < NW; ++u) {
             const int r = 8 * u + 2 * q4;
@@ -600,20 +650,23 @@ struct Q4Warp {
                 head[8 * NW + r] = sum[u][2];
                 head[8 * NW + r + 1] = sum[u][3];
             }
-            const float c0 = -8.f * sum[u][0], c1 = -8.f * sum[u][1];  // n s to c s
-            float* d0 = rows + r * L::kRowFloats + g * (H / 8);
-            float* d1 = d0 + L::kRowFloats;
-#pragma unroll
-            for (int i = 0; i < L::kSteps / 2; ++i) {
-                reinterpret_cast<float4*>(d0)[i] =
-                    make_float4(acc[u][2 * i][0] + c0, acc[u][2 * i][2] + c0,
-                                acc[u][2 * i + 1][0] + c0, acc[u][2 * i + 1][2] + c0);
-                reinterpret_cast<float4*>(d1)[i] =
-                    make_float4(acc[u][2 * i][1] + c1, acc[u][2 * i][3] + c1,
-                                acc[u][2 * i + 1][1] + c1, acc[u][2 * i + 1][3] + c1);
-            }
         }
         if (lane == 0) head[16 * NW] = bad ? 1.f : 0.f;
+    }
+    template <int U>
+    __device__ __forceinline__ void save_rows(float* rows) const {
+        const float c0 = -8.f * sum[U][0], c1 = -8.f * sum[U][1];  // n s to c s
+        float* d0 = rows + 2 * q4 * L::kRowFloats + g * (H / 8);
+        float* d1 = d0 + L::kRowFloats;
+#pragma unroll
+        for (int i = 0; i < L::kSteps / 2; ++i) {
+            reinterpret_cast<float4*>(d0)[i] =
+                make_float4(acc[U][2 * i][0] + c0, acc[U][2 * i][2] + c0,
+                            acc[U][2 * i + 1][0] + c0, acc[U][2 * i + 1][2] + c0);
+            reinterpret_cast<float4*>(d1)[i] =
+                make_float4(acc[U][2 * i][1] + c1, acc[U][2 * i][3] + c1,
+                            acc[U][2 * i + 1][1] + c1, acc[U][2 * i + 1][3] + c1);
+        }
     }
 };
 
@@ -621,14 +674,15 @@ __device__ __forceinline__ float q4_weight(float m, float M) {
     return fast_exp2(m - M);  // 0 for kQ4None unless all are
 }
 
-template <int H, bool BF16>
+template <int H>
 __device__ __forceinline__ void q4_store4(const Q4Params& p, int b, int kv, int r, int d,
                                           float4 v) {
     const int t = r / p.G, gg = r - t * p.G;
     uint16_t* dst = static_cast<uint16_t*>(p.out) +
                     (((size_t)b * p.T + t) * p.N + (size_t)kv * p.G + gg) * H + d;
     *reinterpret_cast<uint2*>(dst) =
-        make_uint2(Elt<BF16>::pack(v.x, v.y), Elt<BF16>::pack(v.z, v.w));
+        p.bf16 ? make_uint2(Elt<true>::pack(v.x, v.y), Elt<true>::pack(v.z, v.w))
+               : make_uint2(Elt<false>::pack(v.x, v.y), Elt<false>::pack(v.z, v.w));
 }
 
 // Partial of one piece in the workspace: max[8*NW], sum[8*NW], bad, pad, then
@@ -639,176 +693,244 @@ struct Q4Part {
     static constexpr int kFloats = kHead + 8 * NW * H;
 };
 
-// Fold pieces first .. last of a split segment (the whole block): the weights of
-// every (piece, row) first, a warp per row; then the accumulators, the threads in
-// groups that take a share of the pieces each.  All orders are fixed by the sizes.
-template <int H, bool BF16, int NW>
-__device__ __noinline__ void fold_pieces(const Q4Params& p, int b, int kv, int rbase, int nrows,
-                                         int first, int last, float* scratch) {
+// Where the warps' scratch is: the slot a warp has computed last is free until the
+// CTA leaves the piece.  (Shared memory is what bounds the copies in flight.)
+template <int H>
+struct Q4Free {
+    uint8_t* smem;       // the warps' rings
+    const uint32_t* at;  // offset of each warp's free slot
+    __device__ __forceinline__ uint8_t* of(int w) const { return smem + at[w]; }
+    __device__ __forceinline__ float* rows(int w) const { return reinterpret_cast<float*>(of(w)); }
+};
+
+// Fold pieces first .. last of a split segment (the whole block).  One trip for the
+// pieces' maxima and sums and, at the same time, for the first accumulators of
+// every thread; the threads form groups that take a share of the pieces each.
+// All orders are fixed by the sizes.
+template <int H, int NW>
+__device__ __forceinline__ void fold_pieces(const Q4Params& p, int b, int kv, int rbase, int nrows,
+                                         int first, int last, Q4Free<H> fr) {
     using Part = Q4Part<H, NW>;
-    constexpr int kRows = 8 * NW;
-    __shared__ float s_max[kRows], s_sum[kRows];
-    __shared__ int s_bad;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = blockDim.x >> 5;
+    constexpr int kRows = 8 * NW, kAhead = 4;
+    const int tid = threadIdx.x, W = blockDim.x >> 5;
     const int n = last - first + 1;
     auto sec = [&](int c) {  // piece c
         return p.partials + ((size_t)(first + c) * 2 + (c == 0 ? 1 : 0)) * Part::kFloats;
     };
-    // weights [piece][row], then 4 floats a thread for the groups' sums
-    const int room = (W * kRows * Q4<H>::kRowFloats - 4 * (int)blockDim.x) / kRows;
-    float4* sums = reinterpret_cast<float4*>(scratch + room * kRows);
-    if (tid == 0) s_bad = 0;
-    __syncthreads();  // everyone is done with the scratch
-    for (int r = warp; r < nrows; r += W) {
-        float M = kQ4None;
-        bool bad = false;
-        for (int c = lane; c < n; c += 32) {
-            M = fmaxf(M, __ldcg(sec(c) + r));
-            bad |= __ldcg(sec(c) + 16 * NW) != 0.f;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
-        float l = 0.f;
-        for (int c = lane; c < n; c += 32) {
-            const float f = q4_weight(__ldcg(sec(c) + r), M);
-            l = fmaf(f, __ldcg(sec(c) + kRows + r), l);
-            if (c < room) scratch[c * kRows + r] = f;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(FULL, l, o);
-        if (lane == 0) {
-            s_max[r] = M;
-            s_sum[r] = l;
-        }
-        if (bad) s_bad = 1;
-    }
-    __syncthreads();
+    // a free slot holds 16 bytes a lane for the groups' sums, then (max, sum) of the
+    // rows of every W-th piece
+    constexpr int kPer = (Q4<H>::kSlot - 512) / (8 * kRows);
+    const bool fits = n <= kPer * W;
+    auto ms = [&](int c, int r) {
+        return reinterpret_cast<float2*>(fr.of(c % W) + 512) + (c / W) * kRows + r;
+    };
+    auto global_ms = [&](int c, int r) {
+        return make_float2(__ldcg(sec(c) + r), __ldcg(sec(c) + kRows + r));
+    };
     const int items = nrows * (H / 4);
     const int groups = max(1, min((int)blockDim.x / items, n));
     const int each = (n + groups - 1) / groups;
+    const int gi = groups > 1 ? tid / items : 0;
+    const int lo = gi * each, hi = gi < groups ? min(n, lo + each) : lo;
+    int x = groups > 1 ? tid - gi * items : tid;
+    float4 v[kAhead];
+    auto load = [&](int c0) {
+        const float* at = sec(0) + Part::kHead + x / (H / 4) * H + x % (H / 4) * 4;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (x < items && c0 + j < hi)
+                v[j] = __ldcg(reinterpret_cast<const float4*>(at + (sec(c0 + j) - sec(0))));
+    };
+    load(lo);
+    bool bad = false;
+    for (int i = tid; i < n * nrows; i += blockDim.x) {
+        const int c = i / nrows, r = i - c * nrows;
+        if (fits) *ms(c, r) = global_ms(c, r);
+        bad |= __ldcg(sec(c) + 16 * NW) != 0.f;
+    }
+    bad = __syncthreads_or(bad);
     for (int x0 = 0; x0 < items; x0 += blockDim.x) {
-        const int gi = tid / items, x = groups > 1 ? tid - gi * items : x0 + tid;
-        const bool on = groups > 1 ? gi < groups : x < items;
-        const int r = x / (H / 4), d = x % (H / 4) * 4;
+        const int r = min(x, items - 1) / (H / 4), d = x % (H / 4) * 4;
+        float M = kQ4None;
+        for (int c = 0; c < n; ++c) M = fmaxf(M, fits ? ms(c, r)->x : __ldcg(sec(c) + r));
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (on) {
-            const int lo = groups > 1 ? gi * each : 0, hi = groups > 1 ? min(n, lo + each) : n;
-#pragma unroll 8
-            for (int c = lo; c < hi; ++c) {
-                const float f = c < room ? scratch[c * kRows + r]
-                                         : q4_weight(__ldcg(sec(c) + r), s_max[r]);
-                const float4 v =
-                    __ldcg(reinterpret_cast<const float4*>(sec(c) + Part::kHead + r * H + d));
-                o.x = fmaf(f, v.x, o.x);
-                o.y = fmaf(f, v.y, o.y);
-                o.z = fmaf(f, v.z, o.z);
-                o.w = fmaf(f, v.w, o.w);
+        float l = 0.f;
+        for (int c0 = lo; c0 < hi; c0 += kAhead) {
+            if (c0 > lo || x0 > 0) load(c0);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                if (c0 + j < hi) {
+                    const float2 m = fits ? *ms(c0 + j, r) : global_ms(c0 + j, r);
+                    const float f = q4_weight(m.x, M);
+                    l = fmaf(f, m.y, l);
+                    o.x = fmaf(f, v[j].x, o.x);
+                    o.y = fmaf(f, v[j].y, o.y);
+                    o.z = fmaf(f, v[j].z, o.z);
+                    o.w = fmaf(f, v[j].w, o.w);
+                }
             }
         }
-        if (groups > 1) {
-            if (on) sums[tid] = o;
+        if (groups > 1) {  // (one round of items then)
+            auto sums = [&](int t) { return reinterpret_cast<float4*>(fr.of(t >> 5)) + (t & 31); };
+            if (gi < groups) *sums(tid) = o;
             __syncthreads();
-            if (on && gi == 0)
+            if (gi == 0) {
                 for (int y = 1; y < groups; ++y) {
-                    const float4 v = sums[y * items + x];
-                    o.x += v.x;
-                    o.y += v.y;
-                    o.z += v.z;
-                    o.w += v.w;
+                    const float4 w = *sums(y * items + x);
+                    o.x += w.x;
+                    o.y += w.y;
+                    o.z += w.z;
+                    o.w += w.w;
                 }
+                for (int c = hi; c < n; ++c) {
+                    const float2 m = fits ? *ms(c, r) : global_ms(c, r);
+                    l = fmaf(q4_weight(m.x, M), m.y, l);
+                }
+            }
         }
-        if (on && gi == 0 || on && groups == 1) {
-            const float iv = kQ4Unit / s_sum[r];
-            o = s_bad ? make_float4(0.f, 0.f, 0.f, 0.f)
-                      : make_float4(o.x * iv, o.y * iv, o.z * iv, o.w * iv);
-            q4_store4<H, BF16>(p, b, kv, rbase + r, d, o);
+        if (gi == 0 && x < items) {
+            const float iv = kQ4Unit / l;
+            o = bad ? make_float4(0.f, 0.f, 0.f, 0.f)
+                    : make_float4(o.x * iv, o.y * iv, o.z * iv, o.w * iv);
+            q4_store4<H>(p, b, kv, rbase + r, d, o);
         }
+        x += blockDim.x;
     }
 }
 
-template <int H, bool BF16, int NW>
-__global__ void __launch_bounds__(NW == 1 ? 512 : 384, 1) q4_attention_kernel(const Q4Params p) {
+// Warps an SM's registers hold at each row count.
+constexpr int q4_sm_warps(int NW) { return NW == 1 ? 16 : NW == 2 ? 12 : 8; }
+
+template <int H, int NW>
+__global__ void __launch_bounds__(32 * q4_sm_warps(NW), 1) q4_attention_kernel(const Q4Params p) {
     using L = Q4<H>;
     using Part = Q4Part<H, NW>;
     constexpr int kRows = 8 * NW;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int s_scan[16], s_long[16], s_b, s_base, s_last;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = blockDim.x >> 5;
-    float* heads = reinterpret_cast<float*>(smem + (size_t)W * kSlots * L::kSlot);
-    float* scratch = heads + W * Part::kHead;
+    auto* qr = reinterpret_cast<Q4Rows<H, NW>*>(smem + (size_t)W * kSlots * L::kSlot);
+    float* heads = reinterpret_cast<float*>(qr + 1);
+    __shared__ uint32_t s_free[16];
+    const Q4Free<H> fr = {smem, s_free};
     griddep_launch_dependents();
     griddep_wait();
 
-    const int seg = kQ4SegUnits * W;
-    // ---- this CTA's range of units --------------------------------------------------
-    const int per = (p.B + blockDim.x - 1) / blockDim.x;
-    const int lo = min(p.B, tid * per), hi = min(p.B, lo + per);
-    int local = 0, longest = 0;
-    for (int b = lo; b < hi; ++b) {
-        const int n = q4_blocks(p.context_lens[b], p.T, p.max_blocks, p.window);
-        local += q4_units(n, seg);
-        longest = max(longest, n);
-    }
-    longest = __reduce_max_sync(FULL, longest);
-    int incl = local;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(FULL, incl, o);
-        if (lane >= o) incl += v;
-    }
-    if (lane == 31) {
-        s_scan[warp] = incl;
-        s_long[warp] = longest;
-    }
-    __syncthreads();
-    int before = 0, total = 0;
-    for (int w = 0; w < W; ++w) {
-        before += w < warp ? s_scan[w] : 0;
-        total += s_scan[w];
-        longest = max(longest, s_long[w]);
-    }
-    total *= p.KC;
-    const int excl = (before + incl - local) * p.KC;
-    const int quota = max((int)(((long long)total + gridDim.x - 1) / gridDim.x), 2 * kStepTiles * W);
-    // Whole segments, one per CTA, where there is a CTA for each and the longest
-    // exceeds an equal share by less than cutting segments costs (about 6 tiles a
-    // warp: two more trips through L2 and a fold).
-    const bool whole = p.B * p.KC <= (int)gridDim.x && longest <= quota + kQ4CutCost * W;
-    int c0 = min((long long)total, (long long)blockIdx.x * quota);
-    int c1 = min((long long)total, (long long)c0 + quota);
-    if (whole) {
-        c0 = c1 = 0;
-        const int b = blockIdx.x / p.KC;
-        if (b < p.B) {
-            const int u = q4_units(q4_blocks(p.context_lens[b], p.T, p.max_blocks, p.window), seg);
-            c0 = (blockIdx.x - b * p.KC) * u;  // units counted from the sequence's own
-            c1 = c0 + u;
-            s_b = b;
-            s_base = 0;
+    uint32_t qw[H / 8];  // warp u: raw words of row tile u of the next piece
+    Pieces piece;
+    bool more, whole = p.direct;
+    int quota = 1;
+    int ids = 0, fl = 32;  // block ids of 16 steps (two a step), the next one's place
+    // An invalid length: zeros for sequence b.
+    auto refuse = [&](int b) {
+        if (tid == 0) report(p.status, GQA_ERR_CONTEXT);
+        const size_t n16 = (size_t)p.T * p.N * H / 8;
+        uint4* dst = static_cast<uint4*>(p.out) + (size_t)b * n16;
+        for (size_t i = tid; i < n16; i += blockDim.x) dst[i] = make_uint4(0, 0, 0, 0);
+    };
+    if (p.direct) {
+        // ---- this CTA's segment: q, the first block ids and the length in one trip ------
+        const int b = blockIdx.x / p.KC, k = blockIdx.x - b * p.KC;
+        if (warp < NW) qr->load(p, b, k, warp, qw);
+        const int i = kStepTiles * (warp + W * (lane >> 1)) + (lane & 1);
+        if (p.window == 0 && i < p.max_blocks) ids = __ldg(p.block_tables + (size_t)b * p.max_blocks + i);
+        more = piece.one(p, b, k);
+        if (!more) {
+            if (k == 0) refuse(b);
+            return;
         }
-    } else if (c0 < c1 && excl <= c0 && c0 < excl + local * p.KC) {
-        int base = excl;
+        if (p.window == 0) {
+            fl = 0;
+            if (i >= piece.i1) ids = 0;  // an entry past the length
+        }
+    } else {
+        // ---- this CTA's range of units --------------------------------------------------
+        // Every warp adds up all lengths itself (up to 256 sequences; then the block does
+        // it together).
+        constexpr int seg_per_warp = q4_seg_units(NW);
+        const int seg = seg_per_warp * W;
+        const bool block = p.B > 256;
+        const int own = block ? tid : lane, owners = block ? (int)blockDim.x : 32;
+        const int per = (p.B + owners - 1) / owners;
+        const int lo = min(p.B, own * per), hi = min(p.B, lo + per);
+        int local = 0, longest = 0;
+        bool bad = false;
+#pragma unroll 4
         for (int b = lo; b < hi; ++b) {
-            const int n = p.KC * q4_units(q4_blocks(p.context_lens[b], p.T, p.max_blocks, p.window), seg);
-            if (c0 < base + n) {
-                s_b = b;
-                s_base = base;
-                break;
+            const int n = q4_blocks(__ldg(p.context_lens + b), p.T, p.max_blocks, p.window);
+            local += q4_units(n, seg);
+            longest = max(longest, n);
+            bad |= n == 0;
+        }
+        longest = __reduce_max_sync(FULL, longest);
+        int incl = local;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(FULL, incl, o);
+            if (lane >= o) incl += v;
+        }
+        int before = 0, total = __shfl_sync(FULL, incl, 31);
+        if (block) {
+            if (lane == 31) {
+                s_scan[warp] = incl;
+                s_long[warp] = longest;
             }
-            base += n;
+            bad = __syncthreads_or(bad);
+            total = 0;
+            for (int w = 0; w < W; ++w) {
+                before += w < warp ? s_scan[w] : 0;
+                total += s_scan[w];
+                longest = max(longest, s_long[w]);
+            }
+        } else {
+            bad = __any_sync(FULL, bad);
         }
-    }
-    // sequences of an invalid length: zeros
-    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-        if (q4_blocks(p.context_lens[b], p.T, p.max_blocks, p.window) == 0) {
-            if (tid == 0) report(p.status, GQA_ERR_CONTEXT);
-            const size_t n16 = (size_t)p.T * p.N * H / 8;
-            uint4* dst = static_cast<uint4*>(p.out) + (size_t)b * n16;
-            for (size_t i = tid; i < n16; i += blockDim.x) dst[i] = make_uint4(0, 0, 0, 0);
+        total *= p.KC;
+        const int excl = (before + incl - local) * p.KC, grid = gridDim.x;
+        quota = total / grid + (total % grid != 0);
+        quota = max(quota, 2 * kStepTiles * W);
+        // Whole segments, one per CTA, where there is a CTA for each and the longest
+        // exceeds an equal share by less than cutting segments costs (about 6 tiles a
+        // warp: two more trips through L2 and a fold).
+        whole = p.B * p.KC <= grid && longest <= quota + kQ4CutCost * W;
+        const int c0 = (int)min((long long)total, (long long)blockIdx.x * quota);
+        const int c1 = (int)min((long long)total, (long long)c0 + quota);
+        int at_b = 0, at_base = 0;
+        const bool mine = c0 < c1 && excl <= c0 && c0 < excl + local * p.KC;
+        if (mine) {  // the sequence that holds unit c0, and its first unit
+            at_base = excl;
+            for (at_b = lo;; ++at_b) {
+                const int n = p.KC * q4_units(q4_blocks(__ldg(p.context_lens + at_b), p.T,
+                                                        p.max_blocks, p.window), seg);
+                if (c0 < at_base + n) break;
+                at_base += n;
+            }
         }
+        if (bad)
+            for (int b = blockIdx.x; b < p.B; b += grid)
+                if (q4_blocks(p.context_lens[b], p.T, p.max_blocks, p.window) == 0) refuse(b);
+        if (whole) {
+            const int b = blockIdx.x / p.KC;
+            more = b < p.B && piece.one(p, b, blockIdx.x - b * p.KC);
+        } else {
+            if (block) {
+                if (mine) {
+                    s_b = at_b;
+                    s_base = at_base;
+                }
+                __syncthreads();
+                at_b = s_b;
+                at_base = s_base;
+            } else {
+                const int from = max(__ffs(__ballot_sync(FULL, mine)) - 1, 0);
+                at_b = __shfl_sync(FULL, at_b, from);
+                at_base = __shfl_sync(FULL, at_base, from);
+            }
+            more = piece.begin(p, at_b, at_base, c0, c1, seg);
+        }
+        if (!more) return;
+        if (warp < NW) qr->load(p, piece.b, piece.k, warp, qw);
     }
-    __syncthreads();
-    if (c0 >= c1) return;
 
     // ---- stream the range -------------------------------------------------------------
     // The piece being computed and the one being copied; their state is looked at
@@ -819,28 +941,16 @@ __global__ void __launch_bounds__(NW == 1 ? 512 : 384, 1) q4_attention_kernel(co
     const uint8_t* ring = smem + (size_t)warp * kSlots * L::kSlot;
     const uint32_t ring_at = smem_addr(ring);
     float* head = heads + warp * Part::kHead;
-    float* rows = scratch + (size_t)warp * kRows * L::kRowFloats;
-    Q4Warp<H, BF16, NW> cs(p);
     Q4Copy<H> cp;
     cp.lane_offsets(lane);
-    bool more, fmore;
-    int fi = 0, fend = 0;  // next tile to copy, end of its piece
-    int fl = 0;            // its place among the block ids held
-    int ids = 0;           // block ids of 16 steps, two a step
-    static_assert(kSlots == 2, "slots alternate, one step is in flight");
-    uint32_t fslot = 0;    // slot to copy into
-    bool fbad = false;     // the step copied last has an invalid block id
-    {
-        Pieces t;
-        more = fmore = t.begin(p, s_b, s_base, c0, c1, seg);
-        if (lane == 0) cur = fet = t;
-        if (more) {
-            fi = t.i0 + kStepTiles * warp;
-            fend = t.i1;
-            cp.head(p, t.k / p.C, lane);
-        }
-        __syncwarp();
-    }
+    cp.head(p, piece.k / p.C, lane);
+    bool fmore = true;
+    int fi = piece.i0 + kStepTiles * warp, fend = piece.i1;  // next tile to copy, its piece's end
+    const uint32_t ring_end = kSlots * L::kSlot;
+    uint32_t fslot = 0;  // slot to copy into
+    unsigned badq = 0;   // bit i: the i-th step from the one computed has a bad block id
+    if (lane == 0) cur = fet = piece;
+    __syncwarp();
     const int hop = kStepTiles * W;
     // Copy this warp's next step, in whichever piece it lies.
     auto fetch = [&]() {
@@ -851,14 +961,15 @@ __global__ void __launch_bounds__(NW == 1 ? 512 : 384, 1) q4_attention_kernel(co
                 fi = t.i0 + kStepTiles * warp;
             } while (fmore && fi >= t.i1);
             fend = fmore ? t.i1 : 0;
-            fl = 0;
+            fl = 32;
             if (fmore) cp.head(p, t.k / p.C, lane);
             __syncwarp();
             if (lane == 0) fet = t;
             __syncwarp();
         }
         if (fmore) {
-            if (fl == 0) {
+            if (fl == 32) {
+                fl = 0;
                 const int i = fi + hop * (lane >> 1) + (lane & 1);
                 ids = i < fend ? __ldg(p.block_tables + (size_t)fet.b * p.max_blocks + fet.f0 + i)
                                : 0;
@@ -870,75 +981,101 @@ __global__ void __launch_bounds__(NW == 1 ? 512 : 384, 1) q4_attention_kernel(co
                 cp.template tile<0>(dst, blk0, p, lane);
                 if (two) cp.template tile<1>(dst, blk1, p, lane);
             } else {
-                fbad = true;
+                badq |= 1u << (kSlots - 1);
                 if (lane == 0) report(p.status, GQA_ERR_BLOCK_ID);
             }
             fi += hop;
-            fl = (fl + 2) & 31;
-            fslot = L::kSlot - fslot;
+            fl += 2;
+            fslot += L::kSlot;
+            if (fslot == ring_end) fslot = 0;
         }
         cp_async_commit();  // empty past the end: the count of groups stays in step
     };
 #pragma unroll
-    for (int i = 0; i < kSlots - 1; ++i) fetch();
+    for (int i = 0; i < kSlots - 1; ++i) {
+        fetch();
+        badq >>= 1;
+    }
+    if (warp < NW) qr->make(p, warp, qw);
+    __syncthreads();
+    Q4Warp<H, NW> cs(p, qr);
     uint32_t slot = 0;  // of the step being computed
     while (more) {
         cs.begin(cur);
         const int iend = cur.i1, f0 = cur.f0;
         for (int i = cur.i0 + kStepTiles * warp; i < iend; i += hop) {
-            const bool bad = fbad;
-            fbad = false;
             __syncwarp();  // every lane is done with the slot the copy overwrites
             fetch();
             asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 1) : "memory");
             __syncwarp();  // the other lanes' copies too
-            if (bad)
+            if (badq & 1u)
                 cs.bad = true;
             else
                 cs.step(ring + slot, i, (f0 + i) * 16, min(kStepTiles, iend - i));
-            slot = L::kSlot - slot;
+            badq >>= 1;
+            slot += L::kSlot;
+            if (slot == ring_end) slot = 0;
         }
-        // ---- the warps meet -----------------------------------------------------------
-        cs.save(head, rows);
-        __syncthreads();
+        // ---- the warps meet, one row tile after another -------------------------------
+        cs.save_head(head);
+        // the slot computed last, or the one that would have been
+        const uint32_t mine = (slot == 0 ? ring_end : slot) - L::kSlot;
+        float* rows = reinterpret_cast<float*>(smem + (size_t)warp * ring_end + mine);
+        if (lane == 0) s_free[warp] = (uint32_t)warp * ring_end + mine;
+        __syncwarp();  // every lane is done with it
         const int nrows = cs.rend - cs.rbase;
         const int first = cur.start / quota, last = (cur.start + cur.nblk - 1) / quota;
         const bool split = !whole && first != last;
         const int me = blockIdx.x;
         float* part = p.partials + ((size_t)me * 2 + (me == first ? 1 : 0)) * Part::kFloats;
+        piece = cur;
+        more = piece.next(p);
+        if (more && warp < NW) qr->load(p, piece.b, piece.k, warp, qw);  // lands meanwhile
         bool bad = false;
-        for (int w = 0; w < W; ++w) bad |= heads[w * Part::kHead + 16 * NW] != 0.f;
-        for (int x = tid; x < nrows * (H / 4); x += blockDim.x) {
-            const int r = x / (H / 4), d = x % (H / 4) * 4;
-            float M = kQ4None;
-            for (int w = 0; w < W; ++w) M = fmaxf(M, heads[w * Part::kHead + r]);
-            float l = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int w = 0; w < W; ++w) {
-                const float f = q4_weight(heads[w * Part::kHead + r], M);
-                l += f * heads[w * Part::kHead + kRows + r];
-                const float4 v = *reinterpret_cast<const float4*>(
-                    scratch + ((size_t)w * kRows + r) * L::kRowFloats + d);
-                o.x += f * v.x;
-                o.y += f * v.y;
-                o.z += f * v.z;
-                o.w += f * v.w;
+        auto meet = [&](auto u_) {
+            constexpr int U = decltype(u_)::value;
+            if (U > 0) __syncthreads();  // the scratch is free again
+            cs.template save_rows<U>(rows);
+            __syncthreads();
+            if (U == 0) {
+                for (int w = 0; w < W; ++w) bad |= heads[w * Part::kHead + 16 * NW] != 0.f;
             }
-            if (!split) {
-                const float iv = (!bad && l != 0.f) ? kQ4Unit / l : 0.f;
-                if (bad)
-                    o = make_float4(0.f, 0.f, 0.f, 0.f);
-                else
-                    o = make_float4(o.x * iv, o.y * iv, o.z * iv, o.w * iv);
-                q4_store4<H, BF16>(p, cs.b, cs.kv, cs.rbase + r, d, o);
-            } else {
-                *reinterpret_cast<float4*>(part + Part::kHead + r * H + d) = o;
-                if (d == 0) {
-                    part[r] = M;
-                    part[kRows + r] = l;
+            if (U == NW - 1 && more && warp < NW) qr->make(p, warp, qw);  // the old rows are done with
+            for (int x = tid; x < min(8, nrows - 8 * U) * (H / 4); x += blockDim.x) {
+                const int r = 8 * U + x / (H / 4), d = x % (H / 4) * 4;
+                float M = kQ4None;
+                for (int w = 0; w < W; ++w) M = fmaxf(M, heads[w * Part::kHead + r]);
+                float l = 0.f;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int w = 0; w < W; ++w) {
+                    const float f = q4_weight(heads[w * Part::kHead + r], M);
+                    l += f * heads[w * Part::kHead + kRows + r];
+                    const float4 v = *reinterpret_cast<const float4*>(
+                        fr.rows(w) + (r - 8 * U) * L::kRowFloats + d);
+                    o.x += f * v.x;
+                    o.y += f * v.y;
+                    o.z += f * v.z;
+                    o.w += f * v.w;
+                }
+                if (!split) {
+                    const float iv = (!bad && l != 0.f) ? kQ4Unit / l : 0.f;
+                    if (bad)
+                        o = make_float4(0.f, 0.f, 0.f, 0.f);
+                    else
+                        o = make_float4(o.x * iv, o.y * iv, o.z * iv, o.w * iv);
+                    q4_store4<H>(p, cs.b, cs.kv, cs.rbase + r, d, o);
+                } else {
+                    *reinterpret_cast<float4*>(part + Part::kHead + r * H + d) = o;
+                    if (d == 0) {
+                        part[r] = M;
+                        part[kRows + r] = l;
+                    }
                 }
             }
-        }
+        };
+        meet(std::integral_constant<int, 0>{});
+        if constexpr (NW > 1) meet(std::integral_constant<int, 1>{});
+        if constexpr (NW > 2) meet(std::integral_constant<int, 2>{});
         if (split) {
             if (tid == 0) part[16 * NW] = bad ? 1.f : 0.f;
             __threadfence();
@@ -950,13 +1087,10 @@ __global__ void __launch_bounds__(NW == 1 ? 512 : 384, 1) q4_attention_kernel(co
                 __threadfence();
             }
             __syncthreads();
-            if (s_last) fold_pieces<H, BF16, NW>(p, cs.b, cs.kv, cs.rbase, nrows, first, last, scratch);
+            if (s_last) fold_pieces<H, NW>(p, cs.b, cs.kv, cs.rbase, nrows, first, last, fr);
         }
-        __syncthreads();  // the scratch is free again
-        Pieces t = cur;
-        more = t.next(p);
-        __syncwarp();
-        if (lane == 0) cur = t;
+        __syncthreads();  // the scratch is free again, the next piece's q rows are there
+        if (lane == 0) cur = piece;
         __syncwarp();
     }
     cp_async_wait_all();
@@ -964,15 +1098,27 @@ __global__ void __launch_bounds__(NW == 1 ? 512 : 384, 1) q4_attention_kernel(co
 
 // ---- host -----------------------------------------------------------------------------
 struct Q4Plan {
-    int NW, W, grid, C, Rc;
+    int NW, W, grid, C, Rc, direct;
     size_t smem, part_floats, workspace;
     const void* kernel;
 };
 
-template <int H, bool BF16>
-const void* q4_pick(int NW) {
-    return NW == 1 ? reinterpret_cast<const void*>(&q4_attention_kernel<H, BF16, 1>)
-                   : reinterpret_cast<const void*>(&q4_attention_kernel<H, BF16, 2>);
+template <int H, int NW>
+void q4_pick(Q4Plan* pl) {
+    pl->kernel = reinterpret_cast<const void*>(&q4_attention_kernel<H, NW>);
+    pl->part_floats = Q4Part<H, NW>::kFloats;
+    static_assert(8 * Q4<H>::kRowFloats * 4 <= Q4<H>::kSlot, "a row tile's scratch in a free slot");
+    pl->smem = (size_t)pl->W * (kSlots * Q4<H>::kSlot + Q4Part<H, NW>::kHead * 4) +
+               sizeof(Q4Rows<H, NW>);
+}
+template <int H>
+void q4_pick(Q4Plan* pl) {
+    if (pl->NW == 1)
+        q4_pick<H, 1>(pl);
+    else if (pl->NW == 2)
+        q4_pick<H, 2>(pl);
+    else
+        q4_pick<H, 3>(pl);
 }
 
 std::mutex q4_mu;
@@ -981,28 +1127,25 @@ std::map<std::tuple<int, const void*, int>, int> q4_resident;  // CTAs per SM
 gqa_status q4_plan(const gqa_shape& s, Q4Plan* pl) {
     const long long R = (long long)s.T * (s.N / s.K);
     if (R > kQ4MaxRows) return GQA_ERR_SHAPE;
-    pl->NW = R <= 8 ? 1 : 2;
-    pl->C = (int)((R + 8 * pl->NW - 1) / (8 * pl->NW));
+    // row chunks of up to 24 rows: every chunk converts the codes again
+    pl->C = (int)((R + 8 * kQ4MaxTiles - 1) / (8 * kQ4MaxTiles));
     pl->Rc = (int)((R + pl->C - 1) / pl->C);
+    pl->NW = (pl->Rc + 7) / 8;
     const long long segs = (long long)s.B * s.K * pl->C;
     // units are 32-bit in the kernel
-    if (segs * ((long long)s.max_blocks_per_seq + 16 * kQ4SegUnits) > (1ll << 31) - 1)
+    if (segs * ((long long)s.max_blocks_per_seq + 16 * q4_seg_units(kQ4MaxTiles)) > (1ll << 31) - 1)
         return GQA_ERR_SHAPE;
     const int sms = device_sm_count();
     if (sms <= 0) return GQA_ERR_CUDA;
     // Warps per CTA.  Many segments: small CTAs, so that few warps wait for one
     // another when a segment ends; few segments: large ones, so that a segment
     // is cut into few pieces.
-    const int most = pl->NW == 1 ? 16 : 12;
+    const int most = q4_sm_warps(pl->NW);
     pl->W = segs > 2 * sms ? 4 : segs > sms ? most / 2 : most;
-    const int slot = (s.H == 128 ? Q4<128>::kSlot : Q4<64>::kSlot);
-    pl->part_floats = (size_t)(16 * pl->NW + 4) + (size_t)8 * pl->NW * s.H;
-    pl->smem = (size_t)pl->W * (kSlots * slot + (16 * pl->NW + 4) * 4 +
-                                (size_t)8 * pl->NW * (s.H + 4) * 4);
-    pl->kernel = s.H == 128 ? (s.dtype == GQA_BF16 ? q4_pick<128, true>(pl->NW)
-                                                   : q4_pick<128, false>(pl->NW))
-                            : (s.dtype == GQA_BF16 ? q4_pick<64, true>(pl->NW)
-                                                   : q4_pick<64, false>(pl->NW));
+    if (s.H == 128)
+        q4_pick<128>(pl);
+    else
+        q4_pick<64>(pl);
     int dev = 0, resident = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return GQA_ERR_CUDA;
     {
@@ -1024,6 +1167,12 @@ gqa_status q4_plan(const gqa_shape& s, Q4Plan* pl) {
     }
     pl->grid = sms * resident;
     if ((size_t)pl->grid * 4 > kQ4FlagBytes) pl->grid = (int)(kQ4FlagBytes / 4);
+    // A CTA per segment where there are CTAs for all and even the longest segment the
+    // table allows is short: nothing is planned, cut or folded then.
+    const long long reach = s.window > 0 ? (s.window + s.T + 14) / 16 + 1 : s.max_blocks_per_seq;
+    pl->direct = segs <= pl->grid &&
+                 (reach < s.max_blocks_per_seq ? reach : s.max_blocks_per_seq) <= kQ4Direct * pl->W;
+    if (pl->direct) pl->grid = (int)segs;
     pl->workspace = kQ4FlagBytes + (size_t)pl->grid * 2 * pl->part_floats * 4;
     return GQA_OK;
 }
@@ -1072,6 +1221,8 @@ gqa_status launch_attention_fourbit(const gqa_shape& s, const void* q, const uin
     p.max_blocks = s.max_blocks_per_seq;
     p.num_blocks = s.num_blocks;
     p.window = s.window;
+    p.direct = pl.direct;
+    p.bf16 = s.dtype == GQA_BF16;
     const float scale = s.scale > 0.f ? s.scale : 1.f / sqrtf((float)s.H);
     p.scale_log2 = scale * 1.4426950408889634f;
     p.code_stride = (uint32_t)s.K * (uint32_t)(16 * s.H / 2);

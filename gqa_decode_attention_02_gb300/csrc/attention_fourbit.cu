@@ -7,35 +7,41 @@
 // other attention calls), K and V being code * group scale.
 //
 // What bounds it.  A position costs 2 * (H/2 + H/32) bytes per KV head (136 at
-// H = 128).  At 6.78 TB/s over 152 SMs a 16-token tile (2,176 bytes) arrives
-// every ~93 cycles per SM, in which its four schedulers issue ~370
-// instructions: the 16 words a lane holds of the tile must become f16 operands
-// within that, so instructions per code word, not bytes, are what is saved
-// first.  Everything below is chosen for that.
+// H = 128), so at the measured copy rate a 16-token tile (2,176 bytes) could arrive
+// every 95 cycles per SM; the copies alone, without the arithmetic, run at 97 % of
+// that rate.  The arithmetic takes longer: 64 sequences of 32,768 tokens (4 query
+// rows per KV head) need 148 cycles per tile and SM, 525 us, 64 % of the
+// copy rate, and 8 warps per SM are as fast as 16.  Taking parts out one by one
+// showed its shares, which add up rather than overlap: about 47 cycles for the 18
+// mma.sync (some 10 cycles of a scheduler each), 43 for turning the codes into
+// f16 operands, the rest for the softmax, the copies' addresses and the loop.  So
+// instructions per code word are what is saved first:
 //
 //  * No producer warp, no barriers in the loop: each warp copies its own tiles
-//    with 16-byte cp.async (9 instructions per two tiles) into a double buffer
-//    of its own and waits for its own copies only.
+//    with 16-byte cp.async into three slots of its own (two steps in flight, one
+//    computed) and waits for its own copies only.
 //  * Natural storage order, fragments by permutation.  Lane (g, q4) (g = lane /
 //    4) reads K dims H/4*q4 .. of its two tokens with one wide load each: one
 //    group per lane, one scale per token; V dims H/8*g .. of its four tokens:
 //    one group per lane again, and the output leaves as contiguous dims.  q is
 //    permuted to match once per segment.
-//  * Codes become f16 by or-ing a nibble under an exponent (0x6400: 1024 + n;
-//    nibbles one place up, 0x5400: 64 + n), subtracting the offset and
-//    multiplying by the scale: all exact (fourbit.cuh), so products are those
-//    of the cached values and sums are fp32.
+//  * Codes become f16 operands exactly, one or and one fma per pair (q4_values);
+//    the offset that this leaves is taken off by one more k-step of QK^T and one
+//    more row tile of PV, which also sums the probabilities.
 //  * S^T[16 tokens x 8 rows] and O^T[H x 8 rows] on mma.sync m16n8k16, tokens
-//    (dims) on M: up to 8 query rows cost 16 mma per tile.  Decode attention
-//    has T*G = 1..16 rows; tcgen05's M = 128 would be empty there, and its
-//    operands would have to pass through shared memory as f16.
+//    (dims) on M.  Up to three row tiles share one conversion; more rows run in
+//    chunks of 24 (chunks of 16: 72 us against 60 for 16 sequences of 40 rows).
+//    tcgen05 would take the mma off the schedulers but wants its operands in
+//    shared memory as f16, four times the codes' bytes, written there by the
+//    same warps; that trade was not built.
 //
 // Work split.  The batch's segments (sequence, KV head, row chunk) are laid end
 // to end in units (a segment's start-up units, then its tiles) and CTA c takes
 // the c-th equal range.  The warps of a CTA take tile pairs of a segment in
 // turn and meet in shared memory when it ends; a segment cut by a range
 // boundary goes through the workspace, the CTA that finishes last folding the
-// pieces in order (deterministic; nobody waits).
+// pieces in order (deterministic; nobody waits).  Where there is a CTA for every
+// segment and none is long, each CTA takes one whole segment.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -55,9 +61,10 @@ namespace {
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int kStepTiles = 2;    // tiles a warp computes per step
 constexpr int kSlots = 3;        // steps in a warp's buffer: one computed, two in flight
-// Start-up cost of a segment, in tiles per warp (256 ragged sequences, 8 rows, 4
-// warps: 2.1-3.1 us a segment, 0.24 us a tile; 24 rows: 7 us, 0.15 us).
-constexpr int q4_seg_units(int NW) { return NW == 1 ? 3 : NW == 2 ? 5 : 8; }
+// Start-up cost of a segment, in tiles per warp (256 ragged sequences, one row tile,
+// 4 warps: some 6 us a segment against 0.27 us a tile; with 3 units 255 us, 6 245, 8
+// 248.  Three row tiles: 7 us against 0.15-0.18 us).
+constexpr int q4_seg_units(int NW) { return NW == 1 ? 6 : NW == 2 ? 7 : 10; }
 constexpr int kQ4Direct = 10;     // longest segment of a planless launch, in tiles per warp
 constexpr int kQ4CutCost = 6;    // what cutting segments costs a CTA, in tiles per warp
 constexpr float kQ4None = -1e30f;  // maximum of no scores: finite, so references need no test

@@ -582,11 +582,12 @@ gqa_status gqa_kv_append_fourbit(const gqa_shape *shape, const void *k_new, cons
 /* Attention over a 4-bit cache, T >= 1: gqa_decode_attention /
  * gqa_verify_attention, or with tree_mask != NULL gqa_tree_verify_attention, with
  * K_b[j] and V_b[j] the cached values above.  H = 64 or 128, windows (not with
- * a tree mask), T * (N/K) <= 8192; more than 16 query rows per KV head run in
- * chunks of 16, each reading the KV head's blocks.  The products run on f16
+ * a tree mask), T * (N/K) <= 8192; more than 24 query rows per KV head run in
+ * chunks of at most 24, each reading the KV head's blocks.  The products run on f16
  * tensor-core operands with fp32 accumulation: cached values are exact in f16,
- * q rows in bf16 are scaled by a power of two first (exact down to 2^-31 of
- * the row's largest element), probabilities are rounded to f16.
+ * q rows are scaled by a power of two first (f16 then holds an element exactly
+ * down to 2^-20 of its row's largest, and to within 2^-31 of that below),
+ * probabilities are rounded to f16.
  * Workspace: gqa_attention_workspace_size(shape) bytes with that kv_dtype, zero-
  * filled before first use and left so, as for the other attention calls (the
  * two kinds may share one buffer).  GQA_FLAG_EARLY_KV acts as GQA_FLAG_PDL; the

@@ -1134,6 +1134,7 @@ std::map<std::tuple<int, const void*, int>, int> q4_resident;  // CTAs per SM
 gqa_status q4_plan(const gqa_shape& s, Q4Plan* pl) {
     const long long R = (long long)s.T * (s.N / s.K);
     if (R > kQ4MaxRows) return GQA_ERR_SHAPE;
+    if (s.K > (1 << 20)) return GQA_ERR_SHAPE;  // a block's code bytes in 32 bits
     // row chunks of up to 24 rows: every chunk converts the codes again
     pl->C = (int)((R + 8 * kQ4MaxTiles - 1) / (8 * kQ4MaxTiles));
     pl->Rc = (int)((R + pl->C - 1) / pl->C);
@@ -1176,7 +1177,8 @@ gqa_status q4_plan(const gqa_shape& s, Q4Plan* pl) {
     if ((size_t)pl->grid * 4 > kQ4FlagBytes) pl->grid = (int)(kQ4FlagBytes / 4);
     // A CTA per segment where there are CTAs for all and even the longest segment the
     // table allows is short: nothing is planned, cut or folded then.
-    const long long reach = s.window > 0 ? (s.window + s.T + 14) / 16 + 1 : s.max_blocks_per_seq;
+    const long long reach =
+        s.window > 0 ? ((long long)s.window + s.T + 14) / 16 + 1 : s.max_blocks_per_seq;
     pl->direct = segs <= pl->grid &&
                  (reach < s.max_blocks_per_seq ? reach : s.max_blocks_per_seq) <= kQ4Direct * pl->W;
     if (pl->direct) pl->grid = (int)segs;

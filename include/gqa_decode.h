@@ -591,7 +591,8 @@ gqa_status gqa_kv_append_fourbit(const gqa_shape *shape, const void *k_new, cons
  * Workspace: gqa_attention_workspace_size(shape) bytes with that kv_dtype, zero-
  * filled before first use and left so, as for the other attention calls (the
  * two kinds may share one buffer).  GQA_FLAG_EARLY_KV acts as GQA_FLAG_PDL; the
- * flags that force a kernel give GQA_ERR_SHAPE. */
+ * flags that force a kernel give GQA_ERR_SHAPE.  `out` must not overlap an
+ * input. */
 gqa_status gqa_attention_fourbit(const gqa_shape *shape, const void *q, const uint8_t *k_cache,
                                  const uint8_t *v_cache, const uint8_t *k_scale,
                                  const uint8_t *v_scale, const int32_t *block_tables,

@@ -289,6 +289,38 @@ def test_two_graphs_captured_on_one_stream_replay_together(gpu):
         assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("T", [1, 5])
+def test_blocks_whose_bytes_lie_beyond_32_bits(gpu, T):
+    """Block ids so high that code offsets pass 2^32: the same bits as the same rows
+    in a small cache, for attention, append and rows by slot."""
+    w = small(B=2, T=T, N=8, K=8, H=128, dtype="bf16", ctx=(700, 41), seed=21, append=True)
+    c, wd = four(w), to(w, gpu)
+    NB, high = w.num_blocks, 600_000
+    big = [torch.empty((high,) + x.shape[1:], dtype=torch.uint8, device=gpu) for x in c]
+    assert high * 8 * 1024 > 2 ** 32
+    for x, y in zip(big, c):
+        x[high - NB:] = t(y, gpu)
+    lowc = [t(x, gpu) for x in c]
+    used = torch.arange(w.max_blocks, device=gpu)[None] < (wd.context_lens[:, None] + 15) // 16
+    tables = torch.where(used, wd.block_tables + (high - NB), wd.block_tables)
+    fn = gq.append_decode_attention_quant if T == 1 else gq.append_verify_attention_quant
+    args = (wd.q[0], wd.k_new[0], wd.v_new[0])
+    a = fn(*args, *lowc, wd.block_tables, wd.context_lens, kv="int4")
+    b = fn(*args, *big, tables, wd.context_lens, kv="int4")
+    assert torch.equal(a, b)
+    for x, y in zip(big, lowc):
+        assert torch.equal(x[high - NB:], y)
+    slots = torch.arange((high - NB) * 16, high * 16, device=gpu, dtype=torch.int32)
+    sc = lambda z: dict(k_scale=z[2], v_scale=z[3], kv="int4")  # noqa: E731
+    rows = gq.kv_gather_slots(big[0], big[1], slots, **sc(big))
+    want = gq.kv_gather_slots(lowc[0], lowc[1], slots - (high - NB) * 16, **sc(lowc))
+    assert torch.equal(rows[0], want[0]) and torch.equal(rows[1], want[1])
+    gq.kv_append_slots(rows[1], rows[0], big[0], big[1], slots, **sc(big))
+    gq.kv_append_slots(want[1], want[0], lowc[0], lowc[1], slots - (high - NB) * 16, **sc(lowc))
+    for x, y in zip(big, lowc):
+        assert torch.equal(x[high - NB:], y)
+
+
 def test_device_errors_zero_the_sequence_and_leave_the_others(gpu):
     w = small(B=4, T=2, N=8, K=2, H=128, dtype="bf16", ctx=(40, 700, 33, 5), seed=8)
     c = four(w)

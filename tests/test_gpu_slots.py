@@ -314,3 +314,50 @@ def test_prompts_then_speculative_steps(gpu, kv, H, dtype):
     ids = [tb[b, j] for b in range(B) for j in range(h[b])] + [
         rg[(n[0] + i) % NB] for i in range(n[1])]
     assert sorted(ids) == list(range(NB)) and h[1] == 0
+
+
+def test_a_captured_step_replays_as_the_calls_do(gpu):
+    """Plan in place, append + attention and greedy acceptance in one CUDA graph: every
+    replay is the next step, with the same lengths, tables and outputs as the
+    calls made one by one."""
+    B, K, N, H, T, V, NB, mb = 5, 2, 8, 64, 4, 40, 60, 10
+    rng = np.random.default_rng(7)
+    gen = torch.Generator().manual_seed(7)
+
+    def fresh():
+        (kc, vc), (ks, vs) = caches("int4", NB, K, H, None, gpu, fill=0)
+        i32 = lambda x: t(np.asarray(x, np.int32), gpu)  # noqa: E731
+        return dict(c=[kc, vc, ks, vs], ctx=i32([0] * B), held=i32([0] * B), st=i32([0]),
+                    tables=i32(np.full((B, mb), -1)), ring=i32(order), state=i32([9, NB]),
+                    new=i32([T] * B), out=torch.empty(B, T, N, H, dtype=torch.float16, device=gpu),
+                    acc=i32([0] * B), nxt=i32([0] * B))
+
+    order = rng.permutation(NB)
+    q = torch.randn(B, T, N, H, generator=gen).half().to(gpu)
+    k, v = (torch.randn(B, T, K, H, generator=gen).half().to(gpu) for _ in range(2))
+    logits = torch.randn(B, T, V, generator=gen)
+    draft = logits[:, :-1].argmax(-1).to(torch.int32)
+    draft[::2, 1] += 1  # every other sequence loses its last two drafts each step
+    logits, draft = logits.to(gpu), draft.to(gpu)
+    aws = torch.zeros(1 << 16, dtype=torch.uint8, device=gpu)
+
+    def step(s):
+        gq.plan_blocks(s["ctx"], s["new"], s["tables"], s["held"], s["ring"], s["state"],
+                       in_place=True, status=s["st"])
+        gq.append_verify_attention_quant(q, k, v, *s["c"], s["tables"], s["ctx"], kv="int4",
+                                         out=s["out"], status=s["st"], pdl=True)
+        gq.accept_prefix(logits, draft, s["ctx"], accepted=s["acc"], next_token=s["nxt"],
+                         workspace=aws, status=s["st"])
+
+    a, b = fresh(), fresh()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(b)
+    for i in range(12):
+        step(a)
+        graph.replay()
+        torch.cuda.synchronize()
+        for n in ("ctx", "held", "state", "tables", "ring", "out", "acc"):
+            assert torch.equal(a[n], b[n]), (i, n)
+        assert int(a["st"].item()) == int(b["st"].item()) == 0
+    assert a["ctx"].tolist() == [24, 48, 24, 48, 24]

@@ -145,6 +145,22 @@ def test_attention_over_many_and_long_segments(gpu, B, N, K, ctx):
     check(out, ref, lim)
 
 
+@pytest.mark.parametrize("T,N,H", [(1, 3, 64), (1, 4, 128), (2, 8, 64), (3, 8, 64), (3, 8, 128)])
+def test_one_segment_over_the_whole_gpu(gpu, T, N, H):
+    """One KV head of one sequence: more pieces than a warp has lanes, 3 to 24 rows
+    each.  A page that no cache has, in one piece only, gives zeros."""
+    w = small(B=1, T=T, N=N, K=1, H=H, dtype="bf16", ctx=(90005,), seed=T * N + H)
+    c = four(w)
+    ref, lim = exact(w, c)
+    out, st = attend(w, c, gpu)
+    assert st == 0
+    check(out, ref, lim)
+    tables = w.block_tables.numpy().copy()
+    tables[0, 3500] = w.num_blocks
+    out, st = attend(w, c, gpu, tables=tables)
+    assert st == 8 and not out.any()
+
+
 @pytest.mark.parametrize("T,N,K,H,dtype", [(1, 32, 8, 128, "bf16"), (5, 40, 4, 64, "f16"),
                                            (3, 16, 2, 128, "f16")])
 @pytest.mark.parametrize("W", [1, 15, 17, 100, 1024])

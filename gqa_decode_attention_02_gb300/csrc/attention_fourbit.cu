@@ -12,9 +12,10 @@
 // that rate.  The arithmetic takes longer: 64 sequences of 32,768 tokens (4 query
 // rows per KV head) need 148 cycles per tile and SM, 525 us, 64 % of the
 // copy rate, and 8 warps per SM are as fast as 16.  Taking parts out one by one
-// showed its shares, which add up rather than overlap: about 47 cycles for the 18
-// mma.sync (some 10 cycles of a scheduler each), 43 for turning the codes into
-// f16 operands, the rest for the softmax, the copies' addresses and the loop.  So
+// showed its shares: about 47 cycles for the 18 mma.sync, 43 for turning the codes
+// into f16 operands, the rest for the softmax, the copies' addresses and the loop.
+// (In loops of their own an mma.sync takes 8 cycles of a scheduler, lop3 and hfma2
+// two each, two of each in turn 6.1: the pipes overlap only in part.)  So
 // instructions per code word are what is saved first:
 //
 //  * No producer warp, no barriers in the loop: each warp copies its own tiles

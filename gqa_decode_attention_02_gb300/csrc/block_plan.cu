@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kPlanThreads) block_plan_kernel(const PlanPara
         }
         off = scan(got, sums, &total);
     }
-    const bool full = count + total.give > C;  // more ids than blocks: keep them
+    const bool full = total.give > C - count;  // more ids than blocks: keep them
     if (full && lead && tid == 0) report(p.status, GQA_ERR_BLOCKS);
     // 3. Offsets to shared memory; small demands are met on the way.
     bool many_tokens = false;

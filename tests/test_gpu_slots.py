@@ -206,6 +206,22 @@ def test_plan_keeps_ids_the_ring_has_no_room_for(gpu):
     check_plan(a, tokens, gpu)
 
 
+def test_plan_with_more_returns_than_an_int_holds_beside_the_count(gpu):
+    """2^31 - 16384 ids claimed back by 16384 tables and a ring that is full."""
+    B, mb, NB = 16384, 131071, 1000003
+    i32 = lambda n, v: torch.full((n,), v, dtype=torch.int32, device=gpu)  # noqa: E731
+    ring = torch.arange(NB, dtype=torch.int32, device=gpu)
+    st = torch.zeros(1, dtype=torch.int32, device=gpu)
+    tables = torch.empty(B, mb, dtype=torch.int32, device=gpu)  # not read: nothing is returned
+    state = torch.tensor([7, NB], dtype=torch.int32, device=gpu)
+    plan = gq.plan_blocks(i32(B, 5), i32(B, -1), tables, i32(B, mb), ring, state, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == int(gq.Status.ERR_BLOCKS)
+    assert (plan.held == mb).all() and (plan.context_lens == 0).all()
+    assert plan.ring_state.tolist() == [7, NB]
+    assert torch.equal(ring, torch.arange(NB, dtype=torch.int32, device=gpu))
+
+
 def test_plan_reports_ids_that_are_no_blocks(gpu):
     a, tokens = plan_inputs(20, 6, finished=0.0)
     a[4][(a[5][0] + 1) % len(a[4])] = 10 ** 7

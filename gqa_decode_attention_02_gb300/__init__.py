@@ -608,6 +608,7 @@ def _attention4_shape(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block
 
 def _attention4(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, k_new, v_new,
                 out, scale, workspace, status, stream, pdl, early_kv, window, tree_mask, decode):
+    scale, window = float(scale or 0.0), int(window)  # (a tensor's value, not the tensor)
     try:
         dev = q.get_device()
         key = (dev, decode, window, scale, pdl, early_kv, q.shape, q.dtype, k_cache.shape,

@@ -265,9 +265,10 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
 
 def get_workspace4(nbytes: int, index: int, stream: int) -> torch.Tensor:
     """The workspace of a 4-bit attention call on the current stream (`stream`, of
-    GPU `index`): that stream's attention workspace.  Under graph capture a buffer of the graph's own, its ticket region
-    cleared by every replay: two graphs captured on one stream may then run at
-    the same time (a caller that passes its own workspace saves the clearing)."""
+    GPU `index`): that stream's attention workspace.  Under graph capture a buffer
+    of the graph's own, its ticket region cleared by every replay: two graphs
+    captured on one stream may then run at the same time (a caller that passes
+    its own workspace saves the clearing)."""
     if torch.cuda.is_current_stream_capturing():
         ws = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{index}")
         ws[:1 << 14].zero_()  # one int32 ticket per thread block

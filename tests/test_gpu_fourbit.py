@@ -393,6 +393,18 @@ def test_compaction_moves_the_branch(gpu, H):
         np.testing.assert_array_equal(got.cpu().numpy(), ref)
 
 
+def test_scale_given_as_a_tensor(gpu):
+    """Its value at each call counts, also after it changed in place."""
+    w = small(B=2, T=1, N=4, K=2, H=64, dtype="f16", ctx=(40, 17), seed=3)
+    wd, c = to(w, gpu), [t(x, gpu) for x in four(w)]
+    f = lambda s: gq.decode_attention_quant(wd.q[0], *c, wd.block_tables,  # noqa: E731
+                                            wd.context_lens, kv="int4", scale=s)
+    x = torch.tensor(0.25)
+    assert torch.equal(f(x), f(0.25))
+    x.fill_(0.5)
+    assert torch.equal(f(x), f(0.5)) and not torch.equal(f(0.5), f(0.25))
+
+
 def test_binding_refuses(gpu):
     w = small(B=2, T=1, N=8, K=2, H=128, dtype="bf16", ctx=(5, 40), seed=13)
     kc, vc, ks, vs = (t(x, gpu) for x in four(w))

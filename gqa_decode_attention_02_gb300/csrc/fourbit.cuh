@@ -49,20 +49,49 @@ __device__ __forceinline__ bool q4_scale_clips(uint32_t code) {
 __device__ __forceinline__ float q4_scale_value(uint32_t code) {
     return __half2float(__ushort_as_half((unsigned short)(code << 7)));
 }
-// Reciprocal of a scale value for q4_code; 0 for 0.
+// Reciprocal of a scale value for q4_word, at most 2^-23 of itself off; 0 for 0.
 __device__ __forceinline__ float q4_scale_inverse(float s) {
-    return s == 0.f ? 0.f : __frcp_rn(s);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    return s == 0.f ? 0.f : r;
 }
-// The 4-bit code of x under a scale of inverse r, as stored (c + 8).  By the same
-// distance argument x * r + 384, rounded to the 2^-15 that numbers near 384 have,
-// meets the midpoints between codes exactly where x / s does and stays off them
-// elsewhere; adding 1.5 * 2^23 then rounds to the integer, nearest even.
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t q4_pair(float lo, float hi) {
+    return (uint64_t)__float_as_uint(hi) << 32 | __float_as_uint(lo);
+}
+__device__ __forceinline__ uint64_t q4_fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t q4_add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+// The 4-bit codes of eight elements under a scale of inverse r, as stored (c + 8,
+// element e in bits 4e..).  x / s is a midpoint between codes exactly or at least
+// 2^-14 away from one (x has 11 significant bits, s four).  x * r + 384, rounded to
+// the 2^-15 that numbers near 384 have, is at most 2^-16 + 2^-20 off and meets the
+// midpoints exactly, so it falls as x / s does; adding 1.5 * 2^23 then rounds to the
+// integer, nearest even.  That leaves 0x4b400000 + c + 8 as the number's bits: the
+// words add up as they are, and what their upper parts sum to comes off once.
 // CLIP: keep within [-7, 7].
 template <bool CLIP>
-__device__ __forceinline__ uint32_t q4_code(float x, float r) {
-    float z = fmaf(x, r, 384.f);
-    if (CLIP) z = fminf(fmaxf(z, 377.f), 391.f);
-    return __float_as_uint(z + 12582536.f) & 15u;  // 1.5 * 2^23 - 384 + 8
+__device__ __forceinline__ uint32_t q4_word(const float (&x)[8], float r) {
+    uint32_t word = 0;
+    const uint64_t rr = q4_pair(r, r);
+#pragma unroll
+    for (int e = 6; e >= 0; e -= 2) {
+        uint64_t z = q4_fma2(q4_pair(x[e], x[e + 1]), rr, q4_pair(384.f, 384.f));
+        if (CLIP)
+            z = q4_pair(fminf(fmaxf(__uint_as_float((uint32_t)z), 377.f), 391.f),
+                        fminf(fmaxf(__uint_as_float((uint32_t)(z >> 32)), 377.f), 391.f));
+        // 1.5 * 2^23 - 384 + 8
+        z = q4_add2(z, q4_pair(12582536.f, 12582536.f));
+        word = word * 256u + (uint32_t)(z >> 32) * 16u + (uint32_t)z;
+    }
+    return word - 0x4b400000u * 0x11111111u;
 }
 
 }  // namespace gqa

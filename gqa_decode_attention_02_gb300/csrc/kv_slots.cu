@@ -11,12 +11,15 @@
 //
 // All of it is moving bytes: the floor is the 16-bit side plus the cache side
 // once.  A thread owns 8 consecutive elements (one 16-byte access on the 16-bit
-// side) of a key and a value row; four threads share a 4-bit group and H/8 a row, so
-// maxima take two (or log2(H/8)) shuffles inside the warp and every row is written
-// as one contiguous piece.  At 4 bits the arithmetic comes close to the bytes (a
-// warp handles 1 KB of rows): maxima are taken on the packed 16-bit patterns,
-// codes without a division (fourbit.cuh), and clipping is left to the warps whose
-// scales need it.
+// side) of a key and a value row, or 16 on the way to 4 bits; two threads share a
+// 4-bit group and H/8 an 8-bit row, so maxima take one (or log2(H/8)) shuffles
+// inside the warp and every row is written as one contiguous piece.  At 4 bits the
+// arithmetic comes close to the bytes: maxima are taken on the packed 16-bit
+// patterns, codes without a division and two to an instruction (fourbit.cuh), and
+// clipping is left to the warps whose scales need it.  36,060 rows of prompts
+// (8 heads of 128, bf16) at 4 bits, on the device: put 30 us and take 32 us for
+// 187 MB each, 6.2 and 5.8 TB/s of the 6.8 that a copy reaches.  (Take with two
+// parts a thread: no faster.)
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
@@ -89,7 +92,7 @@ __device__ __forceinline__ int slot_of(const SlotParams& p, uint32_t i, bool rep
     return blk * 16 + (pos & 15);
 }
 
-// Row and KV head of item it of H/8 parts each.
+// Row, KV head and part of item it, H/8 parts a row.
 template <int H>
 __device__ __forceinline__ void item_of(const SlotParams& p, uint32_t it, uint32_t* row,
                                         uint32_t* k, uint32_t* c) {
@@ -99,65 +102,76 @@ __device__ __forceinline__ void item_of(const SlotParams& p, uint32_t it, uint32
     *k = rk - *row * p.K;
 }
 
-// Largest magnitude of a group; a NaN element becomes zero.
-// Magnitudes of 16-bit floats compare as integers, two at a time.
+// Largest magnitude of a group, of which a thread has two quarters; a NaN element
+// becomes zero.  Magnitudes of 16-bit floats compare as integers, two at a time.
 template <bool BF16>
-__device__ __forceinline__ float group_max(uint4& w) {
+__device__ __forceinline__ float group_max(uint4 (&w)[2]) {
     constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;
-    auto top = [&](const uint4& v) {
-        const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                                    __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+    auto four = [&](const uint4& v) {
+        return __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                        __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+    };
+    auto top = [&]() {
+        const uint32_t m = __vmaxu2(four(w[0]), four(w[1]));
         return max(m & 0xffffu, m >> 16);
     };
-    uint32_t m = top(w);
+    uint32_t m = top();
     if (m > kInf) {  // rare: drop the NaN elements
         auto clean = [&](uint32_t x) {
             if ((x & 0x7fffu) > kInf) x &= 0xffff0000u;
             if ((x >> 16 & 0x7fffu) > kInf) x &= 0x0000ffffu;
             return x;
         };
-        w = make_uint4(clean(w.x), clean(w.y), clean(w.z), clean(w.w));
-        m = top(w);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            w[j] = make_uint4(clean(w[j].x), clean(w[j].y), clean(w[j].z), clean(w[j].w));
+        m = top();
     }
-#pragma unroll
-    for (int o = 1; o < kQ4Group / 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    return Elt<BF16>::lo(m);
+    return Elt<BF16>::lo(max(m, __shfl_xor_sync(0xffffffffu, m, 1)));
 }
 
-template <bool CLIP>
-__device__ __forceinline__ uint32_t code_word(const float (&x)[8], float r) {
-    uint32_t word = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) word |= q4_code<CLIP>(x[e], r) << (4 * e);
-    return word;
-}
+// A thread's 16-byte pieces of a row.  At 4 bits two: what a group costs once
+// (maximum, scale, addresses) is then shared by 16 elements (24 prompts of 200 to
+// 3,001 tokens, 8 heads of 128: 42 us with one piece, 30 with two).
+template <int KIND>
+constexpr int kPieces = KIND == kKvFourbit ? 2 : 1;
 
-// Eight elements of a row (part c of H/8) of KV head k into slot s.
+// The elements of part c of a row of KV head k into slot s.
 template <bool BF16, int KIND, int H>
-__device__ __forceinline__ void put8(const SlotParams& p, uint8_t* cache, void* scale, int s,
-                                     int k, int c, uint4 w) {
-    constexpr int P = H / 8;  // threads per row
+__device__ __forceinline__ void put(const SlotParams& p, uint8_t* cache, void* scale, int s, int k,
+                                    int c, uint4 (&w)[kPieces<KIND>]) {
+    constexpr int P = H / 8 / kPieces<KIND>;  // threads per row
     const size_t blk = (size_t)(s >> 4);
     const int row = s & 15;
     if constexpr (KIND == GQA_KV_SAME) {
         if (s >= 0)
-            reinterpret_cast<uint4*>(cache)[((blk * 16 + row) * p.K + k) * P + c] = w;
+            reinterpret_cast<uint4*>(cache)[((blk * 16 + row) * p.K + k) * P + c] = w[0];
         return;
     }
     float x[8];
     if constexpr (KIND == kKvFourbit) {
         const uint32_t sc = q4_scale_code(group_max<BF16>(w));
         const float r = q4_scale_inverse(q4_scale_value(sc));
-        widen8<BF16>(w, x);
-        const uint32_t word = __any_sync(0xffffffffu, q4_scale_clips(sc)) ? code_word<true>(x, r)
-                                                                          : code_word<false>(x, r);
+        uint2 word;
+        if (__any_sync(0xffffffffu, q4_scale_clips(sc))) {
+            widen8<BF16>(w[0], x);
+            word.x = q4_word<true>(x, r);
+            widen8<BF16>(w[1], x);
+            word.y = q4_word<true>(x, r);
+        } else {
+            widen8<BF16>(w[0], x);
+            word.x = q4_word<false>(x, r);
+            widen8<BF16>(w[1], x);
+            word.y = q4_word<false>(x, r);
+        }
         if (s >= 0) {
             const size_t r = (blk * p.K + k) * 16 + row;
-            reinterpret_cast<uint32_t*>(cache)[r * P + c] = word;
-            if ((c & 3) == 0) static_cast<uint8_t*>(scale)[r * (H / kQ4Group) + (c >> 2)] = (uint8_t)sc;
+            reinterpret_cast<uint2*>(cache)[r * P + c] = word;
+            if ((c & 1) == 0)
+                static_cast<uint8_t*>(scale)[r * (H / kQ4Group) + (c >> 1)] = (uint8_t)sc;
         }
     } else {
-        widen8<BF16>(w, x);
+        widen8<BF16>(w[0], x);
         float a = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(x[e]));
@@ -189,23 +203,28 @@ __device__ __forceinline__ void put8(const SlotParams& p, uint8_t* cache, void* 
 // Items: row i, KV head k, part c, keys and values of one item together.
 template <bool BF16, int KIND, int H>
 __global__ void __launch_bounds__(kSlotThreads) kv_put_kernel(const SlotParams p) {
+    constexpr int V = kPieces<KIND>;
     griddep_launch_dependents();
     griddep_wait();
-    const uint32_t items = p.rows * p.K * (H / 8), stride = gridDim.x * kSlotThreads;
+    const uint32_t items = p.rows * p.K * (H / 8 / V), stride = gridDim.x * kSlotThreads;
     // whole warps stay in the loop together (the shuffles); it < 2^31 + 2^24
     for (uint32_t it = blockIdx.x * kSlotThreads + threadIdx.x; it - (threadIdx.x & 31) < items;
          it += stride) {
         const bool on = it < items;
         uint32_t i, k, c;
-        item_of<H>(p, on ? it : items - 1, &i, &k, &c);
-        uint4 kw = make_uint4(0, 0, 0, 0), vw = kw;
-        if (on) {
-            kw = __ldg(p.k_new + it);
-            vw = __ldg(p.v_new + it);
+        item_of<H / V>(p, on ? it : items - 1, &i, &k, &c);
+        uint4 kw[V], vw[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            kw[j] = vw[j] = make_uint4(0, 0, 0, 0);
+            if (on) {
+                kw[j] = __ldg(p.k_new + (size_t)it * V + j);
+                vw[j] = __ldg(p.v_new + (size_t)it * V + j);
+            }
         }
         const int s = on ? slot_of(p, i, c == 0 && k == 0) : -1;
-        put8<BF16, KIND, H>(p, p.k_cache, p.k_scale, s, k, c, kw);
-        put8<BF16, KIND, H>(p, p.v_cache, p.v_scale, s, k, c, vw);
+        put<BF16, KIND, H>(p, p.k_cache, p.k_scale, s, k, c, kw);
+        put<BF16, KIND, H>(p, p.v_cache, p.v_scale, s, k, c, vw);
     }
 }
 

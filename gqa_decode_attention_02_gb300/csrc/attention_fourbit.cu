@@ -32,6 +32,9 @@
 //  * S^T[16 tokens x 8 rows] and O^T[H x 8 rows] on mma.sync m16n8k16, tokens
 //    (dims) on M.  Up to three row tiles share one conversion; more rows run in
 //    chunks of 24 (chunks of 16: 72 us against 60 for 16 sequences of 40 rows).
+//    Four tiles no longer fit the registers with two tiles of tokens: 32 rows over
+//    64 sequences of 8,192 tokens in 368 us against 387, over 4 of 500 in 24 against
+//    20; five: no gain anywhere.
 //    tcgen05 would take the mma off the schedulers but wants its operands in
 //    shared memory as f16, four times the codes' bytes, written there by the
 //    same warps; that trade was not built.

@@ -95,7 +95,6 @@ struct Q4Params {
     int max_blocks, num_blocks;
     int window;
     int direct;  // a CTA per segment (the host's rule)
-    int bf16;    // type of q and out
     float scale_log2;
     uint32_t code_stride, scale_stride;  // bytes of a block's codes, scales
     uint32_t ex[2];  // 0x64006400, 0x54005400 (see q4_values)
@@ -321,7 +320,7 @@ __device__ __forceinline__ void q4_values(uint32_t x, const Q4Scale& f, const ui
 // (nibbles 0|4, 1|5) and 2j+1 (2|6, 3|7).  Rows are scaled by a power of two that
 // puts their largest element in [64, 128): f16 then holds an element of either
 // type exactly down to 2^-20 of the largest, and to within 2^-31 of it below.
-template <int H, int NW>
+template <int H, int NW, bool BF16>
 struct Q4Rows {
     uint2 frag[NW][Q4<H>::kSteps][32];
     // -8 times a lane's part of its row's sum, as two f16 terms (22 bits; at most
@@ -349,8 +348,8 @@ struct Q4Rows {
     }
     __device__ __forceinline__ void make(const Q4Params& p, int u, uint32_t (&w)[H / 8]) {
         const int lane = threadIdx.x & 31, g = lane >> 2, q4 = lane & 3;
-        auto lo = [&](uint32_t x) { return p.bf16 ? Elt<true>::lo(x) : Elt<false>::lo(x); };
-        auto hi = [&](uint32_t x) { return p.bf16 ? Elt<true>::hi(x) : Elt<false>::hi(x); };
+        auto lo = [&](uint32_t x) { return Elt<BF16>::lo(x); };
+        auto hi = [&](uint32_t x) { return Elt<BF16>::hi(x); };
         float top = 0.f;
 #pragma unroll
         for (int i = 0; i < H / 8; ++i) top = fmaxf(top, fmaxf(fabsf(lo(w[i])), fabsf(hi(w[i]))));
@@ -382,12 +381,12 @@ struct Q4Rows {
 
 // A warp's state for one piece of a segment: NW tiles of 8 query rows.  Several
 // tiles share every converted code, and read the q fragments from shared memory.
-template <int H, int NW>
+template <int H, int NW, bool BF16>
 struct Q4Warp {
     using L = Q4<H>;
     static constexpr bool kKeepQ = NW == 1;  // q fragments in registers
     const Q4Params& p;
-    const Q4Rows<H, NW>* qr;
+    const Q4Rows<H, NW, BF16>* qr;
     const int lane, g, q4;
     const uint32_t ex[2];
     uint32_t kro, vro, sko, svo;  // this lane's offsets in a tile
@@ -404,7 +403,7 @@ struct Q4Warp {
     float m0[NW], m1[NW];
     bool bad;
 
-    __device__ Q4Warp(const Q4Params& p_, const Q4Rows<H, NW>* qr_)
+    __device__ Q4Warp(const Q4Params& p_, const Q4Rows<H, NW, BF16>* qr_)
         : p(p_), qr(qr_), lane(threadIdx.x & 31), g((threadIdx.x & 31) >> 2), q4(threadIdx.x & 3),
           ex{p_.ex[0], p_.ex[1]} {
         const int ta = token();
@@ -523,20 +522,31 @@ struct Q4Warp {
         }
     }
 
-    // O^T += V^T P^T of a tile.  The probabilities enter the product as f16 (half
-    // an ulp is 2^-11 of them, below the output's own rounding); their sum takes the
-    // rounded ones, so the weights still add up to one.
+    // O^T += V^T P^T of a tile.  The probabilities enter the product as f16, off by
+    // 2^-11 of themselves, an eighth of a bf16 output's half step.  An f16 output's half
+    // step is no more than that, so there what rounding left over enters as a second f16
+    // term (64 sequences of 8,192 tokens, f16, H = 128: 4 rows per KV head 160 us with it,
+    // 147 without; 24 rows 304 against 255).  The sum takes the same terms, so the
+    // weights still add up to one.
     template <bool FAST>
     __device__ __forceinline__ void values(const float (&sc)[NW][4], const uint8_t* tile, int tb) {
-        uint32_t pb[NW][2];
+        constexpr int kTerms = BF16 ? 1 : 2;
+        uint32_t pb[kTerms][NW][2];
 #pragma unroll
         for (int u = 0; u < NW; ++u) {
             const float e0 = fast_exp2(fmaf(sc[u][0], sl0[u], -m0[u]));
             const float e1 = fast_exp2(fmaf(sc[u][1], sl1[u], -m1[u]));
             const float e2 = fast_exp2(fmaf(sc[u][2], sl0[u], -m0[u]));
             const float e3 = fast_exp2(fmaf(sc[u][3], sl1[u], -m1[u]));
-            pb[u][0] = movm_t(Elt<false>::pack(e0, e1));
-            pb[u][1] = movm_t(Elt<false>::pack(e2, e3));
+            const uint32_t w0 = Elt<false>::pack(e0, e1), w1 = Elt<false>::pack(e2, e3);
+            pb[0][u][0] = movm_t(w0);
+            pb[0][u][1] = movm_t(w1);
+            if constexpr (kTerms == 2) {
+                pb[1][u][0] =
+                    movm_t(Elt<false>::pack(e0 - Elt<false>::lo(w0), e1 - Elt<false>::hi(w0)));
+                pb[1][u][1] =
+                    movm_t(Elt<false>::pack(e2 - Elt<false>::lo(w1), e3 - Elt<false>::hi(w1)));
+            }
         }
         uint32_t s[4];
 #pragma unroll
@@ -554,9 +564,11 @@ struct Q4Warp {
         const Q4Scale f01((s[0] << 7) | (s[1] << 23)), f23((s[2] << 7) | (s[3] << 23));
         constexpr uint32_t kOnes = 0x3c003c00u;
 #pragma unroll
-        for (int u = 0; u < NW; ++u)
-            q4_mma(sum[u], FAST ? as_u32(f01.s) : 0u, kOnes, FAST ? as_u32(f23.s) : 0u, kOnes,
-                   pb[u][0], pb[u][1]);
+        for (int z = 0; z < kTerms; ++z)
+#pragma unroll
+            for (int u = 0; u < NW; ++u)
+                q4_mma(sum[u], FAST ? as_u32(f01.s) : 0u, kOnes, FAST ? as_u32(f23.s) : 0u, kOnes,
+                       pb[z][u][0], pb[z][u][1]);
         uint32_t w[4][L::kVWords];
 #pragma unroll
         for (int i = 0; i < 4; ++i) q4_words(tile + vro + i * 4 * L::kRow, w[i]);
@@ -569,11 +581,13 @@ struct Q4Warp {
                 q4_values<FAST>(prmt(w[0][i], w[1][i], sel), f01, ex, va);
                 q4_values<FAST>(prmt(w[2][i], w[3][i], sel), f23, ex, vc);
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
+                for (int z = 0; z < kTerms; ++z)
 #pragma unroll
-                    for (int u = 0; u < NW; ++u)
-                        q4_mma(acc[u][4 * i + 2 * h + x], va[2 * x], va[2 * x + 1], vc[2 * x],
-                               vc[2 * x + 1], pb[u][0], pb[u][1]);
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int u = 0; u < NW; ++u)
+                            q4_mma(acc[u][4 * i + 2 * h + x], va[2 * x], va[2 * x + 1], vc[2 * x],
+                                   vc[2 * x + 1], pb[z][u][0], pb[z][u][1]);
             }
     }
 
@@ -685,15 +699,14 @@ __device__ __forceinline__ float q4_weight(float m, float M) {
     return fast_exp2(m - M);  // 0 for kQ4None unless all are
 }
 
-template <int H>
+template <int H, bool BF16>
 __device__ __forceinline__ void q4_store4(const Q4Params& p, int b, int kv, int r, int d,
                                           float4 v) {
     const int t = r / p.G, gg = r - t * p.G;
     uint16_t* dst = static_cast<uint16_t*>(p.out) +
                     (((size_t)b * p.T + t) * p.N + (size_t)kv * p.G + gg) * H + d;
     *reinterpret_cast<uint2*>(dst) =
-        p.bf16 ? make_uint2(Elt<true>::pack(v.x, v.y), Elt<true>::pack(v.z, v.w))
-               : make_uint2(Elt<false>::pack(v.x, v.y), Elt<false>::pack(v.z, v.w));
+        make_uint2(Elt<BF16>::pack(v.x, v.y), Elt<BF16>::pack(v.z, v.w));
 }
 
 // Partial of one piece in the workspace: max[8*NW], sum[8*NW], bad, pad, then
@@ -720,7 +733,7 @@ struct Q4Free {
 // that take a share of the pieces each, add up.  All orders are fixed by the sizes.
 // (Every thread going through its row's 20 maxima and sums itself: the fold of one
 // sequence of 100,003 tokens took 10 us, so 5, and the call 51 us, so 46.)
-template <int H, int NW>
+template <int H, int NW, bool BF16>
 __device__ __forceinline__ void fold_pieces(const Q4Params& p, int b, int kv, int rbase, int nrows,
                                          int first, int last, Q4Free<H> fr) {
     using Part = Q4Part<H, NW>;
@@ -815,7 +828,7 @@ __device__ __forceinline__ void fold_pieces(const Q4Params& p, int b, int kv, in
         }
         if (gi == 0 && x < items) {
             if (bad) o = make_float4(0.f, 0.f, 0.f, 0.f);
-            q4_store4<H>(p, b, kv, rbase + r, d, o);
+            q4_store4<H, BF16>(p, b, kv, rbase + r, d, o);
         }
         x += blockDim.x;
     }
@@ -824,7 +837,7 @@ __device__ __forceinline__ void fold_pieces(const Q4Params& p, int b, int kv, in
 // Warps an SM's registers hold at each row count.
 constexpr int q4_sm_warps(int NW) { return NW == 1 ? 16 : NW == 2 ? 12 : 8; }
 
-template <int H, int NW>
+template <int H, int NW, bool BF16>
 __global__ void __launch_bounds__(32 * q4_sm_warps(NW), 1) q4_attention_kernel(const Q4Params p) {
     using L = Q4<H>;
     using Part = Q4Part<H, NW>;
@@ -832,7 +845,7 @@ __global__ void __launch_bounds__(32 * q4_sm_warps(NW), 1) q4_attention_kernel(c
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int s_scan[16], s_long[16], s_b, s_base, s_last;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = blockDim.x >> 5;
-    auto* qr = reinterpret_cast<Q4Rows<H, NW>*>(smem + (size_t)W * kSlots * L::kSlot);
+    auto* qr = reinterpret_cast<Q4Rows<H, NW, BF16>*>(smem + (size_t)W * kSlots * L::kSlot);
     float* heads = reinterpret_cast<float*>(qr + 1);
     __shared__ uint32_t s_free[16];
     const Q4Free<H> fr = {smem, s_free};
@@ -1021,7 +1034,7 @@ __global__ void __launch_bounds__(32 * q4_sm_warps(NW), 1) q4_attention_kernel(c
     }
     if (warp < NW) qr->make(p, warp, qw);
     __syncthreads();
-    Q4Warp<H, NW> cs(p, qr);
+    Q4Warp<H, NW, BF16> cs(p, qr);
     uint32_t slot = 0;  // of the step being computed
     while (more) {
         cs.begin(cur);
@@ -1088,7 +1101,7 @@ __global__ void __launch_bounds__(32 * q4_sm_warps(NW), 1) q4_attention_kernel(c
                         o = make_float4(0.f, 0.f, 0.f, 0.f);
                     else
                         o = make_float4(o.x * iv, o.y * iv, o.z * iv, o.w * iv);
-                    q4_store4<H>(p, cs.b, cs.kv, cs.rbase + r, d, o);
+                    q4_store4<H, BF16>(p, cs.b, cs.kv, cs.rbase + r, d, o);
                 } else {
                     *reinterpret_cast<float4*>(part + Part::kHead + r * H + d) = o;
                     if (d == 0) {
@@ -1112,7 +1125,7 @@ __global__ void __launch_bounds__(32 * q4_sm_warps(NW), 1) q4_attention_kernel(c
                 __threadfence();
             }
             __syncthreads();
-            if (s_last) fold_pieces<H, NW>(p, cs.b, cs.kv, cs.rbase, nrows, first, last, fr);
+            if (s_last) fold_pieces<H, NW, BF16>(p, cs.b, cs.kv, cs.rbase, nrows, first, last, fr);
         }
         __syncthreads();  // the scratch is free again, the next piece's q rows are there
         if (lane == 0) cur = piece;
@@ -1129,21 +1142,22 @@ struct Q4Plan {
 };
 
 template <int H, int NW>
-void q4_pick(Q4Plan* pl) {
-    pl->kernel = reinterpret_cast<const void*>(&q4_attention_kernel<H, NW>);
+void q4_pick(Q4Plan* pl, bool bf16) {
+    pl->kernel = bf16 ? reinterpret_cast<const void*>(&q4_attention_kernel<H, NW, true>)
+                      : reinterpret_cast<const void*>(&q4_attention_kernel<H, NW, false>);
     pl->part_floats = Q4Part<H, NW>::kFloats;
     static_assert(8 * Q4<H>::kRowFloats * 4 <= Q4<H>::kSlot, "a row tile's scratch in a free slot");
     pl->smem = (size_t)pl->W * (kSlots * Q4<H>::kSlot + Q4Part<H, NW>::kHead * 4) +
-               sizeof(Q4Rows<H, NW>);
+               sizeof(Q4Rows<H, NW, true>);
 }
 template <int H>
-void q4_pick(Q4Plan* pl) {
+void q4_pick(Q4Plan* pl, bool bf16) {
     if (pl->NW == 1)
-        q4_pick<H, 1>(pl);
+        q4_pick<H, 1>(pl, bf16);
     else if (pl->NW == 2)
-        q4_pick<H, 2>(pl);
+        q4_pick<H, 2>(pl, bf16);
     else
-        q4_pick<H, 3>(pl);
+        q4_pick<H, 3>(pl, bf16);
 }
 
 std::mutex q4_mu;
@@ -1169,9 +1183,9 @@ gqa_status q4_plan(const gqa_shape& s, Q4Plan* pl) {
     const int most = q4_sm_warps(pl->NW);
     pl->W = segs > 2 * sms ? 4 : segs > sms ? most / 2 : most;
     if (s.H == 128)
-        q4_pick<128>(pl);
+        q4_pick<128>(pl, s.dtype == GQA_BF16);
     else
-        q4_pick<64>(pl);
+        q4_pick<64>(pl, s.dtype == GQA_BF16);
     int dev = 0, resident = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return GQA_ERR_CUDA;
     {
@@ -1249,7 +1263,6 @@ gqa_status launch_attention_fourbit(const gqa_shape& s, const void* q, const uin
     p.num_blocks = s.num_blocks;
     p.window = s.window;
     p.direct = pl.direct;
-    p.bf16 = s.dtype == GQA_BF16;
     const float scale = s.scale > 0.f ? s.scale : 1.f / sqrtf((float)s.H);
     p.scale_log2 = scale * 1.4426950408889634f;
     p.code_stride = (uint32_t)s.K * (uint32_t)(16 * s.H / 2);

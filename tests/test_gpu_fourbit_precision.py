@@ -1,0 +1,99 @@
+"""GPU attention over a 4-bit cache where its arithmetic is put to the test.
+
+Caches are made of codes and scales directly, the exact outputs in fp64 from the values
+c * s.  Notation of the bounds: ref the exact output, A = sum p |V| with the exact
+probabilities p, HALF the output type's half step relative to the value (2^-25 the
+smallest f16 half step), P what the products with V leave of a probability, relative to
+it.  Errors of the scores cost 2^-13 of A where sum |q k| scale log2(e) <= 40 (at most
+H/16 + 4 roundings of 2^-23 of that: 2^-14 of a probability; numerator and sum).
+"""
+import numpy as np
+import pytest
+import torch
+
+import gqa_decode_attention_02_gb300 as gq
+from oracle import fourbit as f4
+from test_gpu_fourbit import HALF, t
+
+pytestmark = pytest.mark.gpu
+P = {"f16": 2.0 ** -22, "bf16": 2.0 ** -11}  # of a probability, in the products with V
+DT = {"f16": torch.float16, "bf16": torch.bfloat16}
+GRID = f4.scale_values()
+
+
+def byte(s):
+    """The scale byte of a value on the grid."""
+    (i,) = np.flatnonzero(GRID[:226] == s)
+    return int(i)
+
+
+class Cache:
+    """One KV head of one sequence of n positions: codes [n, H] in -7..7 and scale
+    bytes [n, H/32] of keys and values, in shuffled blocks."""
+
+    def __init__(self, kc, ks, vc, vs, seed=0):
+        n, H = kc.shape
+        self.n, self.H, nb = n, H, (n + 15) // 16
+        self.perm = np.random.default_rng(seed).permutation(nb + 2)[:nb].astype(np.int32)
+        self.parts = []
+        for c, s in ((kc, ks), (vc, vs)):
+            nib = np.zeros((nb * 16, H), np.uint8)
+            nib[:n] = (c + 8).astype(np.uint8)
+            codes = np.full((nb + 2, 1, 16, H // 2), 0xFF, np.uint8)
+            scale = np.full((nb + 2, 1, 16, H // 32), 0xFF, np.uint8)
+            codes[self.perm, 0] = (nib[:, 0::2] | (nib[:, 1::2] << 4)).reshape(nb, 16, -1)
+            pad = np.full((nb * 16, H // 32), 0xFF, np.uint8)
+            pad[:n] = s
+            scale[self.perm, 0] = pad.reshape(nb, 16, -1)
+            self.parts.append((codes, scale))
+        self.k = kc * np.repeat(GRID[ks], 32, 1)
+        self.v = vc * np.repeat(GRID[vs], 32, 1)
+
+    def attend(self, q, dtype, dev, *, B=1, scale=None):
+        """q [N, H] (exact in dtype) for B sequences that share the blocks: [B, N, H]."""
+        (kc, ks), (vc, vs) = ([t(x, dev) for x in p] for p in self.parts)
+        qd = torch.from_numpy(q).to(DT[dtype])
+        assert (qd.double().numpy() == q).all()
+        qd = qd.to(dev)[None, None].expand(B, 1, -1, -1).contiguous()
+        tables = t(self.perm[None], dev).expand(B, -1).contiguous()
+        lens = torch.full((B,), self.n, dtype=torch.int32, device=dev)
+        st = torch.zeros(1, dtype=torch.int32, device=dev)
+        out = gq.decode_attention_quant(qd, kc, vc, ks, vs, tables, lens, kv="int4", scale=scale,
+                                        status=st)
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0
+        return out[:, 0].double().cpu().numpy()
+
+    def exact(self, q, scale=None):
+        """(ref, A, sum of exp(s - max s)) of every row."""
+        s = q @ self.k.T * (scale or self.H ** -0.5)
+        p = np.exp(s - s.max(-1, keepdims=True))
+        L = p.sum(-1, keepdims=True)
+        return p @ self.v / L, p @ np.abs(self.v) / L, L
+
+
+def check(out, ref, lim):
+    assert np.isfinite(out).all()
+    worst = np.abs(out - ref) / lim
+    assert (worst <= 1).all(), (int((worst > 1).sum()), float(worst.max()))
+
+
+@pytest.mark.parametrize("N,H", [(4, 64), (4, 128), (16, 64), (16, 128), (24, 128)])
+def test_f16_outputs_keep_the_probabilities(gpu, N, H):
+    """f16 outputs: what rounding a probability to f16 leaves is a second term of the
+    products, so 2^-22 of A remains of it and values that nearly cancel come out
+    within the output's own half step."""
+    rng = np.random.default_rng(N + H)
+    for n in (2, 3, 5, 16, 17, 33, 295):
+        codes = lambda: rng.integers(-7, 8, (n, H))  # noqa: E731
+        sb = lambda lo, hi: rng.integers(lo, hi, (n, H // 32))  # noqa: E731
+        vc = codes()
+        if n <= 3:
+            vc[1:] = -vc[:1]
+        c = Cache(codes(), sb(byte(2.0 ** -4), byte(2.0 ** -3)), vc, sb(byte(0.25), byte(0.5)))
+        q = torch.from_numpy(rng.standard_normal((N, H))).half().double().numpy()
+        ref, A, L = c.exact(q)
+        inner = A * (2.0 ** -13 + 2.0 ** -15 + 2.0 ** -22)
+        inner = inner + n * 2.0 ** -32 / L * 2 * np.abs(c.v).max()
+        out = c.attend(q, "f16", gpu)[0]
+        check(out, ref, inner + HALF["f16"] * (np.abs(ref) + inner) + 2.0 ** -25)

@@ -26,9 +26,8 @@
 //    group per lane, one scale per token; V dims H/8*g .. of its four tokens:
 //    one group per lane again, and the output leaves as contiguous dims.  q is
 //    permuted to match once per segment.
-//  * Codes become f16 operands exactly, one or and one fma per pair (q4_values);
-//    the offset that this leaves is taken off by one more k-step of QK^T and one
-//    more row tile of PV, which also sums the probabilities.
+//  * Codes become f16 operands exactly, one or and one fma per pair (q4_values).
+//    One more row tile of PV sums the probabilities.
 //  * S^T[16 tokens x 8 rows] and O^T[H x 8 rows] on mma.sync m16n8k16, tokens
 //    (dims) on M.  Up to three row tiles share one conversion; more rows run in
 //    chunks of 24 (chunks of 16: 72 us against 60 for 16 sequences of 40 rows).
@@ -275,14 +274,15 @@ __device__ __forceinline__ void q4_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
 
 // Scales of the two codes of a pair, times 2^-7, as f16x2 (exact: the smallest
 // scale is 2^-17, f16's last bit 2^-24), and what turns biased codes into values.
-// The 2^7 comes back with the score factors and the final rows.
+// The 2^7 comes back with the score factors and the final rows.  s has four
+// significant bits, so 129 s has eleven and 9 s eight: f16 holds both.
 constexpr float kQ4Unit = 128.f;
 struct Q4Scale {
-    __half2 s, n10, n6;  // s, -1024 s, -64 s
+    __half2 s, n10, n6;  // s, -1032 s, -72 s
     __device__ __forceinline__ explicit Q4Scale(uint32_t bits) {
         s = __hmul2(as_h2(bits), as_h2(0x20002000u));    // 2^-7
-        n10 = __hmul2(as_h2(bits), as_h2(0xc800c800u));  // -8
-        n6 = __hmul2(as_h2(bits), as_h2(0xb800b800u));   // -0.5
+        n10 = __hmul2(as_h2(bits), as_h2(0xc808c808u));  // -129 / 16
+        n6 = __hmul2(as_h2(bits), as_h2(0xb880b880u));   // -9 / 16
     }
 };
 
@@ -290,9 +290,11 @@ struct Q4Scale {
 // their scales.  Or-ed under an exponent a nibble n = c + 8 is 1024 + n (bits
 // 0-3 under 0x6400, ex[0]) or 64 + n (bits 4-7 under 0x5400, ex[1]; both come as
 // kernel parameters, or each of these lines is two instructions).
-// FAST: one fma each, (1024 + n) s - 1024 s = n s, every term exact (n s has 8
-// bits, the offset is a power of two; scales below 8192), and the 8 s too much
-// per code comes off elsewhere.  Otherwise c s, in two steps.
+// FAST: one fma each, (1024 + n) s - 1032 s = c s, every term and the result exact
+// (scales below 8192: 1032 s stays in range).  Otherwise in two steps.
+// (Another form, (1024 + n) s - 1024 s = n s with 8 s per code taken off the sums at the
+// end, loses what fp32 drops beside 8 sum(p s): f16 outputs of 113,000 positions were
+// 6.4e-5 off (rms, scales of 1/4), a hundred times their rounding; this form 6.6e-7.)
 template <bool FAST>
 __device__ __forceinline__ void q4_values(uint32_t x, const Q4Scale& f, const uint32_t (&ex)[2],
                                           uint32_t (&v)[4]) {
@@ -323,9 +325,6 @@ __device__ __forceinline__ void q4_values(uint32_t x, const Q4Scale& f, const ui
 template <int H, int NW, bool BF16>
 struct Q4Rows {
     uint2 frag[NW][Q4<H>::kSteps][32];
-    // -8 times a lane's part of its row's sum, as two f16 terms (22 bits; at most
-    // 8 * 32 * 128): meets the scales in one more k-step
-    uint32_t corr[NW][32];
     float factor[8 * NW];  // of the rows' scores, to the log2 domain
 
     // This lane's raw words of row 8u + g of virtual head k of sequence b.
@@ -358,15 +357,8 @@ struct Q4Rows {
         const int e = min(max(127 + 6 - (int)(__float_as_uint(top) >> 23), -112), 112);
         const float f = __uint_as_float((uint32_t)(127 + e) << 23);  // row times 2^e
         const float back = __uint_as_float((uint32_t)(127 - e) << 23);
-        float qsum = 0.f;
 #pragma unroll
-        for (int i = 0; i < H / 8; ++i) {
-            w[i] = Elt<false>::pack(lo(w[i]) * f, hi(w[i]) * f);
-            qsum += Elt<false>::lo(w[i]) + Elt<false>::hi(w[i]);
-        }
-        const float c8 = -8.f * qsum;
-        const float c8_hi = __half2float(__float2half_rn(c8));
-        corr[u][lane] = Elt<false>::pack(c8_hi, c8 - c8_hi);
+        for (int i = 0; i < H / 8; ++i) w[i] = Elt<false>::pack(lo(w[i]) * f, hi(w[i]) * f);
         // never 0, which a hidden position's -inf must not meet
         if (q4 == 0) factor[8 * u + g] = fmaxf(kQ4Unit * p.scale_log2 * back, 1.17549435e-38f);
 #pragma unroll
@@ -393,11 +385,10 @@ struct Q4Warp {
     uint32_t cko;                 // ... and of the 8 scale bytes it looks over
     int rbase, rend, b, kv, ctx;
     int edge_lo, edge_hi;  // tiles <= edge_lo or >= edge_hi hold hidden positions
-    uint32_t qf[kKeepQ ? NW : 1][L::kSteps][2], qc[NW];
+    uint32_t qf[kKeepQ ? NW : 1][L::kSteps][2];
     float acc[NW][L::kSteps][4];
-    // sums that ride along with the PV product as one more row tile: [0], [1]
-    // sum p s of this lane's group (what n = c + 8 adds, times 1/8) and [2], [3]
-    // sum p, each for rows 2*q4, 2*q4 + 1
+    // sum p, which rides along with the PV product as one more row tile (of ones): [0],
+    // [1] of rows 2*q4, 2*q4 + 1; [2], [3] the same
     float sum[NW][4];
     float sl0[NW], sl1[NW];  // score factor to the log2 domain, per row
     float m0[NW], m1[NW];
@@ -438,7 +429,6 @@ struct Q4Warp {
             m0[u] = m1[u] = kQ4None;
             sl0[u] = qr->factor[8 * u + 2 * q4];
             sl1[u] = qr->factor[8 * u + 2 * q4 + 1];
-            qc[u] = qr->corr[u][lane];
 #pragma unroll
             for (int e = 0; e < 4; ++e) sum[u][e] = 0.f;
 #pragma unroll
@@ -472,8 +462,7 @@ struct Q4Warp {
         }
     }
 
-    // Scores of NT tiles.  FAST: their codes come as n s; -8 s sum q is added by one
-    // more k-step (scales times the rows' corr).
+    // Scores of NT tiles.
     template <bool FAST, int NT>
     __device__ __forceinline__ void scores(float (&sc)[NT][NW][4], const uint8_t* tiles) {
         uint32_t wa[NT][L::kKWords], wb[NT][L::kKWords];
@@ -487,16 +476,11 @@ struct Q4Warp {
             q4_words(tile + kro + 8 * L::kRow, wb[j]);
         }
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const Q4Scale fa(sa[j]), fb(sb[j]);
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int u = 0; u < NW; ++u) {
+            for (int u = 0; u < NW; ++u)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sc[j][u][e] = 0.f;
-                if constexpr (FAST)
-                    q4_mma(sc[j][u], as_u32(fa.s), as_u32(fb.s), 0u, 0u, qc[u], 0u);
-            }
-        }
 #pragma unroll
         for (int i = 0; i < L::kKWords; ++i) {
             uint32_t va[NT][4], vb[NT][4];
@@ -525,8 +509,8 @@ struct Q4Warp {
     // O^T += V^T P^T of a tile.  The probabilities enter the product as f16, off by
     // 2^-11 of themselves, an eighth of a bf16 output's half step.  An f16 output's half
     // step is no more than that, so there what rounding left over enters as a second f16
-    // term (64 sequences of 8,192 tokens, f16, H = 128: 4 rows per KV head 160 us with it,
-    // 147 without; 24 rows 304 against 255).  The sum takes the same terms, so the
+    // term (64 sequences of 8,192 tokens, f16, H = 128: 4 rows per KV head 158 us with it,
+    // 146 without; 24 rows 285 against 238).  The sum takes the same terms, so the
     // weights still add up to one.
     template <bool FAST>
     __device__ __forceinline__ void values(const float (&sc)[NW][4], const uint8_t* tile, int tb) {
@@ -567,8 +551,7 @@ struct Q4Warp {
         for (int z = 0; z < kTerms; ++z)
 #pragma unroll
             for (int u = 0; u < NW; ++u)
-                q4_mma(sum[u], FAST ? as_u32(f01.s) : 0u, kOnes, FAST ? as_u32(f23.s) : 0u, kOnes,
-                       pb[z][u][0], pb[z][u][1]);
+                q4_mma(sum[u], kOnes, kOnes, kOnes, kOnes, pb[z][u][0], pb[z][u][1]);
         uint32_t w[4][L::kVWords];
 #pragma unroll
         for (int i = 0; i < 4; ++i) q4_words(tile + vro + i * 4 * L::kRow, w[i]);
@@ -672,25 +655,24 @@ struct Q4Warp {
             if (g == 0) {
                 head[r] = m0[u];
                 head[r + 1] = m1[u];
-                head[8 * NW + r] = sum[u][2];
-                head[8 * NW + r + 1] = sum[u][3];
+                head[8 * NW + r] = sum[u][0];
+                head[8 * NW + r + 1] = sum[u][1];
             }
         }
         if (lane == 0) head[16 * NW] = bad ? 1.f : 0.f;
     }
     template <int U>
     __device__ __forceinline__ void save_rows(float* rows) const {
-        const float c0 = -8.f * sum[U][0], c1 = -8.f * sum[U][1];  // n s to c s
         float* d0 = rows + 2 * q4 * L::kRowFloats + g * (H / 8);
         float* d1 = d0 + L::kRowFloats;
 #pragma unroll
         for (int i = 0; i < L::kSteps / 2; ++i) {
             reinterpret_cast<float4*>(d0)[i] =
-                make_float4(acc[U][2 * i][0] + c0, acc[U][2 * i][2] + c0,
-                            acc[U][2 * i + 1][0] + c0, acc[U][2 * i + 1][2] + c0);
+                make_float4(acc[U][2 * i][0], acc[U][2 * i][2], acc[U][2 * i + 1][0],
+                            acc[U][2 * i + 1][2]);
             reinterpret_cast<float4*>(d1)[i] =
-                make_float4(acc[U][2 * i][1] + c1, acc[U][2 * i][3] + c1,
-                            acc[U][2 * i + 1][1] + c1, acc[U][2 * i + 1][3] + c1);
+                make_float4(acc[U][2 * i][1], acc[U][2 * i][3], acc[U][2 * i + 1][1],
+                            acc[U][2 * i + 1][3]);
         }
     }
 };

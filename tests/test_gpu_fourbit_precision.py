@@ -97,3 +97,40 @@ def test_f16_outputs_keep_the_probabilities(gpu, N, H):
         inner = inner + n * 2.0 ** -32 / L * 2 * np.abs(c.v).max()
         out = c.attend(q, "f16", gpu)[0]
         check(out, ref, inner + HALF["f16"] * (np.abs(ref) + inner) + 2.0 ** -25)
+
+
+@pytest.mark.parametrize("N,H", [(4, 128), (4, 64), (16, 128), (24, 64)])
+def test_thousands_of_positions_in_one_warp(gpu, N, H):
+    """320 long segments: four warps each, so one adds up 10^4 positions and more.  Values
+    that nearly cancel, a group with one large channel (the others' codes 0 and +-1)
+    and a channel of zeros.  Scores are one product each (2^-22 of |score| <= 1 with
+    its scale factor, ex2 2^-22, P: 2^-20 of A, numerator and sum).  A product step
+    truncates each of 17 addends at 2^-23 of the largest with two bits to spare:
+    2^-21 of a partial sum at most, and partial sums stay within the range of the
+    cumulative sums of a warp's share (pairs of tiles, every fourth)."""
+    n, rng = 113_000, np.random.default_rng(H + N)
+    kc = np.zeros((n, H), np.int64)
+    kc[:, 0] = rng.integers(-7, 8, n)
+    ks = np.full((n, H // 32), byte(2.0 ** -4))
+    vc = rng.integers(-1, 2, (n, H))
+    vc[:, 32:] = rng.integers(-7, 8, (n, H - 32))
+    vc[:, 5] = rng.choice([-7, 7], n)
+    vc[:, 9] = 0
+    vs = np.full((n, H // 32), byte(0.25))
+    q = np.zeros((N, H))
+    q[:, 0] = rng.choice([-8.0, 8.0], N)
+    scale = 1.0 / 7
+    c = Cache(kc, ks, vc, vs)
+    ref, A, L = c.exact(q, scale)
+    out = c.attend(q, "f16", gpu, B=320, scale=scale)
+    share = np.arange(n) // 32 % 4
+    R = np.zeros((N, H))
+    for r in range(N):
+        s = c.k @ q[r] * scale
+        pv = np.exp(s - s.max())[:, None] * c.v
+        for w in range(4):
+            cum = np.cumsum(pv[share == w], 0)
+            R[r] = np.maximum(R[r], np.maximum(cum.max(0), 0) - np.minimum(cum.min(0), 0))
+    steps = n / 16 * 2.0 ** -21  # all warps'; the sum of p meets a warp's
+    inner = A * 2.0 ** -20 + steps * R / L + np.abs(ref) * steps / 4 + n * 2.0 ** -32 / L * 1.75
+    check(out, ref, inner + HALF["f16"] * (np.abs(ref) + inner) + 2.0 ** -25)

@@ -71,7 +71,13 @@ constexpr int q4_seg_units(int NW) { return NW == 1 ? 6 : NW == 2 ? 7 : 10; }
 constexpr int kQ4Direct = 10;     // longest segment of a planless launch, in tiles per warp
 constexpr int kQ4CutCost = 6;    // what cutting segments costs a CTA, in tiles per warp
 constexpr float kQ4None = -1e30f;  // maximum of no scores: finite, so references need no test
-constexpr float kQ4Gap = 8.0f;   // log2-domain slack before rescaling
+// A probability is 2^(score - reference).  The reference of a row is set 7 below its
+// largest score, and again once a score is 15 above it, so that the largest probability
+// is 2^7 .. 2^15, near the top of f16's range, and what f16 takes from small ones (2^-25
+// each) is 2^-32 of it.  (A reference at the maximum would lose positions 18 nats behind
+// it altogether, however many they are.)
+constexpr float kQ4Top = 7.0f;
+constexpr float kQ4Gap = 8.0f + kQ4Top;
 constexpr size_t kQ4FlagBytes = 262144; // tickets, one per CTA (as large as the other kernels' region)
 constexpr long long kQ4MaxRows = 8192;  // T*G
 constexpr int kQ4MaxTiles = 3;          // row tiles of 8 per warp
@@ -391,7 +397,7 @@ struct Q4Warp {
     // [1] of rows 2*q4, 2*q4 + 1; [2], [3] the same
     float sum[NW][4];
     float sl0[NW], sl1[NW];  // score factor to the log2 domain, per row
-    float m0[NW], m1[NW];
+    float m0[NW], m1[NW];    // references of the rows' probabilities
     bool bad;
 
     __device__ Q4Warp(const Q4Params& p_, const Q4Rows<H, NW, BF16>* qr_)
@@ -507,11 +513,11 @@ struct Q4Warp {
     }
 
     // O^T += V^T P^T of a tile.  The probabilities enter the product as f16, off by
-    // 2^-11 of themselves, an eighth of a bf16 output's half step.  An f16 output's half
-    // step is no more than that, so there what rounding left over enters as a second f16
-    // term (64 sequences of 8,192 tokens, f16, H = 128: 4 rows per KV head 158 us with it,
-    // 146 without; 24 rows 285 against 238).  The sum takes the same terms, so the
-    // weights still add up to one.
+    // 2^-11 of themselves (or 2^-25, see kQ4Top), an eighth of a bf16 output's half step.
+    // An f16 output's half step is no more than that, so there what rounding left over
+    // enters as a second f16 term (64 sequences of 8,192 tokens, f16, H = 128: 4 rows per
+    // KV head 158 us with it, 146 without; 24 rows 285 against 238).  The sum takes the
+    // same terms, so the weights still add up to one.
     template <bool FAST>
     __device__ __forceinline__ void values(const float (&sc)[NW][4], const uint8_t* tile, int tb) {
         constexpr int kTerms = BF16 ? 1 : 2;
@@ -574,8 +580,8 @@ struct Q4Warp {
             }
     }
 
-    // Running maximum over the scores of a step: rescale only when it grows by more
-    // than 2^kQ4Gap.
+    // References of the rows (kQ4Top below a running maximum) after the scores of a
+    // step: rescale only when one of them is more than kQ4Gap above.
     __device__ __forceinline__ void raise(const float (&sc)[kStepTiles][NW][4]) {
 #pragma unroll
         for (int u = 0; u < NW; ++u) {
@@ -594,6 +600,8 @@ struct Q4Warp {
                     x1 = fmaxf(x1, __shfl_xor_sync(FULL, x1, o));
                 }
                 const bool up0 = x0 > m0[u] + kQ4Gap, up1 = x1 > m1[u] + kQ4Gap;
+                x0 -= kQ4Top;
+                x1 -= kQ4Top;
                 const float f0 = up0 ? fast_exp2(m0[u] - x0) : 1.f;
                 const float f1 = up1 ? fast_exp2(m1[u] - x1) : 1.f;
                 if (up0) m0[u] = x0;

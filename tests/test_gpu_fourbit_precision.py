@@ -78,6 +78,38 @@ def check(out, ref, lim):
     assert (worst <= 1).all(), (int((worst > 1).sum()), float(worst.max()))
 
 
+@pytest.mark.parametrize("N,H,dtype", [(4, 64, "f16"), (4, 128, "bf16"), (16, 128, "f16"),
+                                       (24, 64, "bf16")])
+@pytest.mark.parametrize("gap", [16, 18, 20])
+def test_a_long_tail_behind_dominant_positions(gpu, N, H, dtype, gap):
+    """A few positions lead by `gap` nats and have no value (attention sinks): the
+    output is the tail's, whose probabilities are near 2^-23 .. 2^-29 of the
+    sinks'.  Probabilities enter the products as f16 against a reference that
+    leaves the largest at 2^7 at least: each of the tail is off by at most 2^-25 of
+    that, 2^-32 of a sink's.  320 segments: four warps each, sinks in the share of
+    every one."""
+    n, rng = 100_003, np.random.default_rng(gap)
+    kc = np.zeros((n, H), np.int64)
+    kc[:, 0] = rng.integers(-7, 8, n)
+    ks = np.full((n, H // 32), byte(2.0 ** -4))
+    vc, vs = rng.integers(1, 8, (n, H)), np.full((n, H // 32), byte(0.25))
+    vc *= rng.choice([-1, 1], H)
+    sinks = np.array([f * n // 4 // 128 * 128 + 32 * w for f in range(4) for w in range(4)])
+    kc[sinks], ks[sinks], vc[sinks] = 0, byte(gap / 8.0), 0
+    kc[sinks, 0] = 7
+    q = np.zeros((N, H))
+    q[:, 0] = 8.0
+    scale = 1.0 / 7  # a sink scores gap, the tail -0.5 .. 0.5
+    c = Cache(kc, ks, vc, vs)
+    ref, A, L = c.exact(q, scale)
+    assert (L < 20).all() and (np.abs(ref) > 5e-6).all()
+    lost = n * 2.0 ** -32 / L
+    inner = A * (2.0 ** -11 + 2.0 ** -13) + lost * (np.abs(c.v).max() + np.abs(ref))
+    lim = inner + HALF[dtype] * (np.abs(ref) + inner) + 2.0 ** -25
+    out = c.attend(q, dtype, gpu, B=320, scale=scale)
+    check(out, ref, lim)
+
+
 @pytest.mark.parametrize("N,H", [(4, 64), (4, 128), (16, 64), (16, 128), (24, 128)])
 def test_f16_outputs_keep_the_probabilities(gpu, N, H):
     """f16 outputs: what rounding a probability to f16 leaves is a second term of the

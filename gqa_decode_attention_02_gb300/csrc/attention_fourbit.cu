@@ -70,7 +70,8 @@ constexpr int kSlots = 3;        // steps in a warp's buffer: one computed, two 
 constexpr int q4_seg_units(int NW) { return NW == 1 ? 6 : NW == 2 ? 7 : 10; }
 constexpr int kQ4Direct = 10;     // longest segment of a planless launch, in tiles per warp
 constexpr int kQ4CutCost = 6;    // what cutting segments costs a CTA, in tiles per warp
-constexpr float kQ4None = -1e30f;  // maximum of no scores: finite, so references need no test
+// Reference where no score was seen: below all, and finite, so references need no test.
+constexpr float kQ4None = -3.402823466e38f;
 // A probability is 2^(score - reference).  The reference of a row is set 7 below its
 // largest score, and again once a score is 15 above it, so that the largest probability
 // is 2^7 .. 2^15, near the top of f16's range, and what f16 takes from small ones (2^-25
@@ -516,7 +517,7 @@ struct Q4Warp {
     // 2^-11 of themselves (or 2^-25, see kQ4Top), an eighth of a bf16 output's half step.
     // An f16 output's half step is no more than that, so there what rounding left over
     // enters as a second f16 term (64 sequences of 8,192 tokens, f16, H = 128: 4 rows per
-    // KV head 158 us with it, 146 without; 24 rows 285 against 238).  The sum takes the
+    // KV head 160 us with it, 144 without; 24 rows 281 against 244).  The sum takes the
     // same terms, so the weights still add up to one.
     template <bool FAST>
     __device__ __forceinline__ void values(const float (&sc)[NW][4], const uint8_t* tile, int tb) {
@@ -524,10 +525,15 @@ struct Q4Warp {
         uint32_t pb[kTerms][NW][2];
 #pragma unroll
         for (int u = 0; u < NW; ++u) {
-            const float e0 = fast_exp2(fmaf(sc[u][0], sl0[u], -m0[u]));
-            const float e1 = fast_exp2(fmaf(sc[u][1], sl1[u], -m1[u]));
-            const float e2 = fast_exp2(fmaf(sc[u][2], sl0[u], -m0[u]));
-            const float e3 = fast_exp2(fmaf(sc[u][3], sl1[u], -m1[u]));
+            // product and difference rounded one by one, as in raise(): where fp32 numbers
+            // are far apart an fma's would lie beyond the reference's 15.  (A mul.rn.f32x2
+            // before the add.rn.f32x2 gave an fma's results.)
+            auto x = [&](int e) { return __fmul_rn(sc[u][e], e & 1 ? sl1[u] : sl0[u]); };
+            const uint64_t m = q4_pair(-m0[u], -m1[u]);
+            const uint64_t x01 = q4_add2(q4_pair(x(0), x(1)), m);
+            const uint64_t x23 = q4_add2(q4_pair(x(2), x(3)), m);
+            const float e0 = fast_exp2(q4_lo(x01)), e1 = fast_exp2(q4_hi(x01));
+            const float e2 = fast_exp2(q4_lo(x23)), e3 = fast_exp2(q4_hi(x23));
             const uint32_t w0 = Elt<false>::pack(e0, e1), w1 = Elt<false>::pack(e2, e3);
             pb[0][u][0] = movm_t(w0);
             pb[0][u][1] = movm_t(w1);
@@ -591,15 +597,16 @@ struct Q4Warp {
                 x0 = fmaxf(x0, fmaxf(sc[j][u][0], sc[j][u][2]));
                 x1 = fmaxf(x1, fmaxf(sc[j][u][1], sc[j][u][3]));
             }
-            x0 *= sl0[u];
-            x1 *= sl1[u];
-            if (__any_sync(FULL, x0 > m0[u] + kQ4Gap || x1 > m1[u] + kQ4Gap)) {
+            x0 = __fmul_rn(x0, sl0[u]);
+            x1 = __fmul_rn(x1, sl1[u]);
+            auto above = [](float x, float m) { return __fsub_rn(x, m) > kQ4Gap; };
+            if (__any_sync(FULL, above(x0, m0[u]) || above(x1, m1[u]))) {
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) {
                     x0 = fmaxf(x0, __shfl_xor_sync(FULL, x0, o));
                     x1 = fmaxf(x1, __shfl_xor_sync(FULL, x1, o));
                 }
-                const bool up0 = x0 > m0[u] + kQ4Gap, up1 = x1 > m1[u] + kQ4Gap;
+                const bool up0 = above(x0, m0[u]), up1 = above(x1, m1[u]);
                 x0 -= kQ4Top;
                 x1 -= kQ4Top;
                 const float f0 = up0 ? fast_exp2(m0[u] - x0) : 1.f;

@@ -69,6 +69,10 @@ __device__ __forceinline__ uint64_t q4_add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
+__device__ __forceinline__ float q4_lo(uint64_t a) { return __uint_as_float((uint32_t)a); }
+__device__ __forceinline__ float q4_hi(uint64_t a) {
+    return __uint_as_float((uint32_t)(a >> 32));
+}
 // The 4-bit codes of eight elements under a scale of inverse r, as stored (c + 8,
 // element e in bits 4e..).  x / s is a midpoint between codes exactly or at least
 // 2^-14 away from one (x has 11 significant bits, s four).  x * r + 384, rounded to
@@ -85,8 +89,8 @@ __device__ __forceinline__ uint32_t q4_word(const float (&x)[8], float r) {
     for (int e = 6; e >= 0; e -= 2) {
         uint64_t z = q4_fma2(q4_pair(x[e], x[e + 1]), rr, q4_pair(384.f, 384.f));
         if (CLIP)
-            z = q4_pair(fminf(fmaxf(__uint_as_float((uint32_t)z), 377.f), 391.f),
-                        fminf(fmaxf(__uint_as_float((uint32_t)(z >> 32)), 377.f), 391.f));
+            z = q4_pair(fminf(fmaxf(q4_lo(z), 377.f), 391.f),
+                        fminf(fmaxf(q4_hi(z), 377.f), 391.f));
         // 1.5 * 2^23 - 384 + 8
         z = q4_add2(z, q4_pair(12582536.f, 12582536.f));
         word = word * 256u + (uint32_t)(z >> 32) * 16u + (uint32_t)z;

@@ -110,6 +110,30 @@ def test_a_long_tail_behind_dominant_positions(gpu, N, H, dtype, gap):
     check(out, ref, lim)
 
 
+@pytest.mark.parametrize("size", [2.0 ** 24, 2.0 ** 27, 2.0 ** 28, 2.0 ** 40, 2.0 ** 80, 2.0 ** 110])
+@pytest.mark.parametrize("N,H", [(4, 128), (16, 64)])
+def test_scores_of_any_size(gpu, N, H, size):
+    """Scores of millions and more, of both signs: the largest takes the row, whatever
+    the spacing of fp32 numbers near it.  (The best and the next key differ by a
+    quarter of the best's score, far above any rounding.)"""
+    n, rng = 700, np.random.default_rng(3)
+    kc = np.zeros((n, H), np.int64)
+    kc[:, 0] = rng.integers(1, 6, n)
+    ks, vs = np.full((n, H // 32), byte(1.0)), np.full((n, H // 32), byte(0.5))
+    vc = rng.integers(-7, 8, (n, H))
+    kc[413, 0], kc[77, 0] = 7, -7
+    q = np.zeros((N, H))
+    q[:, 0] = size
+    c = Cache(kc, ks, vc, vs)
+    out = c.attend(q, "bf16", gpu, B=3)
+    check(out, c.v[413][None], 2.0 ** -8 * np.abs(c.v[413]) + 2.0 ** -30)
+    kc[:, 0] = rng.integers(2, 7, n)  # every score far below zero
+    kc[413, 0], kc[77, 0], q[:, 0] = 1, 7, -size
+    c = Cache(kc, ks, vc, vs)
+    out = c.attend(q, "bf16", gpu, B=3)
+    check(out, c.v[413][None], 2.0 ** -8 * np.abs(c.v[413]) + 2.0 ** -30)
+
+
 @pytest.mark.parametrize("N,H", [(4, 64), (4, 128), (16, 64), (16, 128), (24, 128)])
 def test_f16_outputs_keep_the_probabilities(gpu, N, H):
     """f16 outputs: what rounding a probability to f16 leaves is a second term of the

@@ -155,6 +155,31 @@ def test_f16_outputs_keep_the_probabilities(gpu, N, H):
         check(out, ref, inner + HALF["f16"] * (np.abs(ref) + inner) + 2.0 ** -25)
 
 
+@pytest.mark.parametrize("N,H,dtype", [(3, 64, "bf16"), (4, 128, "f16"), (24, 128, "bf16")])
+def test_every_piece_of_a_split_segment_counts(gpu, N, H, dtype):
+    """Values that are waves along the sequence and average to almost nothing: leaving
+    out (or doubling) any stretch of 300 positions would move the output by several
+    times the bound, which is checked first."""
+    n, rng = 90_005, np.random.default_rng(N)
+    j, d = np.arange(n)[:, None], np.arange(H)[None]
+    wave = np.cos(2 * np.pi * (j * (1 + d // 2) / n + 0.25 * (d % 2)))
+    vc, vs = np.rint(7 * wave).astype(np.int64), np.full((n, H // 32), byte(0.125))
+    kc, ks = rng.integers(-7, 8, (n, H)), np.full((n, H // 32), byte(2.0 ** -6))
+    q = torch.from_numpy(rng.standard_normal((N, H))).to(DT[dtype]).double().numpy()
+    c = Cache(kc, ks, vc, vs)
+    ref, A, L = c.exact(q)
+    steps = n / 16 / 16 * 2.0 ** -21  # at least 16 warps share it
+    inner = A * (P[dtype] + 2.0 ** -13 + steps) + n * 2.0 ** -32 / L
+    lim = inner + HALF[dtype] * (np.abs(ref) + inner) + 2.0 ** -25
+    s = q @ c.k.T * H ** -0.5
+    p = np.exp(s - s.max(-1, keepdims=True))
+    for lo in range(0, n - 300, 300):
+        part, v = p[:, lo:lo + 300], c.v[lo:lo + 300]
+        moved = np.abs(part @ v - ref * part.sum(-1, keepdims=True)) / L
+        assert (moved / lim).max() > 3
+    check(c.attend(q, dtype, gpu)[0], ref, lim)
+
+
 @pytest.mark.parametrize("N,H", [(4, 128), (4, 64), (16, 128), (24, 64)])
 def test_thousands_of_positions_in_one_warp(gpu, N, H):
     """320 long segments: four warps each, so one adds up 10^4 positions and more.  Values

@@ -29,6 +29,8 @@
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "launch.h"
 #include "ptx.cuh"
 
@@ -38,6 +40,9 @@ namespace {
 constexpr int kPlanThreads = 1024;  // at most
 constexpr int kPlanMaxB = 16384;    // 12 bytes of shared memory per sequence
 constexpr int kPlanKeepB = 4096;    // ... 24 with its length and count and the long rows' list
+constexpr size_t plan_smem_bytes(bool keep, int B) {
+    return ((size_t)(keep ? 6 : 3) * B + 1) * sizeof(int);
+}
 constexpr int kPlanCluster = 8;
 constexpr int kPlanOneCta = 4096;   // tokens that one CTA handles alone
 constexpr int kPlanOwn = 8;         // table entries or tokens a thread writes alone
@@ -335,6 +340,23 @@ __global__ void __launch_bounds__(kPlanThreads) block_plan_kernel(const PlanPara
     }
 }
 
+// The kernel's shared-memory limit on the current device, once, to the most that any
+// batch takes: the limit belongs to the kernel, so a smaller one set for this call
+// would refuse a larger one of another thread.
+bool plan_ready(const void* kernel, bool keep) {
+    constexpr int kDevices = 64;
+    static std::atomic<bool> done[2][kDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev < kDevices && done[keep][dev].load(std::memory_order_acquire)) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)plan_smem_bytes(keep, keep ? kPlanKeepB : kPlanMaxB)) !=
+        cudaSuccess)
+        return false;
+    if (dev < kDevices) done[keep][dev].store(true, std::memory_order_release);
+    return true;
+}
+
 // Whether an output array overlaps the input that it replaces.
 bool updates_in_place(const PlanParams& p) {
     const int n[3] = {p.B, p.B, 2};
@@ -379,11 +401,7 @@ gqa_status launch_plan_blocks(int B, int max_blocks, int num_blocks, int tokens,
     const bool keep = B <= kPlanKeepB;
     const void* kernel = keep ? reinterpret_cast<const void*>(&block_plan_kernel<true>)
                               : reinterpret_cast<const void*>(&block_plan_kernel<false>);
-    const size_t smem = ((size_t)(keep ? 6 : 3) * B + 1) * sizeof(int);
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-            cudaSuccess)
-        return GQA_ERR_CUDA;
+    if (!plan_ready(kernel, keep)) return GQA_ERR_CUDA;
     // Outputs in buffers of their own need no barrier between the CTAs, so as many
     // run as there are tokens for (262,000 tokens: 64 CTAs 13 us, one cluster 22).
     p.in_place = updates_in_place(p);
@@ -395,7 +413,7 @@ gqa_status launch_plan_blocks(int B, int max_blocks, int num_blocks, int tokens,
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(B <= 256 && ctas == 1 ? 256 : kPlanThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = plan_smem_bytes(keep, B);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

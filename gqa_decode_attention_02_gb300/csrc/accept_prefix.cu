@@ -457,7 +457,7 @@ gqa_status launch_accept_prefix(int B, int T, int V, const float* logits, const 
                 : cudaLaunchKernelEx(&cfg, accept_grid_kernel<false>, logits, draft, parents,
                                      accepted, next_token, path, ctx_io, dev_status, tickets,
                                      parts, T, V, S, W);
-        return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GQA_OK : GQA_ERR_CUDA;
+        return launch_status(e);
     }
     // one cluster of up to 8 blocks per sequence; each block takes V/cs columns
     int cs = (int)((V + 1023) / 1024);
@@ -480,7 +480,7 @@ gqa_status launch_accept_prefix(int B, int T, int V, const float* logits, const 
                                  next_token, path, ctx_io, dev_status, T, V, cs)
             : cudaLaunchKernelEx(&cfg, accept_kernel<false>, logits, draft, parents, accepted,
                                  next_token, path, ctx_io, dev_status, T, V, cs);
-    return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GQA_OK : GQA_ERR_CUDA;
+    return launch_status(e);
 }
 
 }  // namespace gqa

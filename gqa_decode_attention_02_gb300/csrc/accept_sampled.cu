@@ -312,7 +312,7 @@ gqa_status launch_accept_sampled(int B, int T, int V, const float* q, const floa
                                  next_token, ctx_io, dev_status, T, V, cs)
             : cudaLaunchKernelEx(&cfg, accept_sampled_kernel<false>, q, p, draft, u, accepted,
                                  next_token, ctx_io, dev_status, T, V, cs);
-    return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GQA_OK : GQA_ERR_CUDA;
+    return launch_status(e);
 }
 
 }  // namespace gqa

@@ -2010,7 +2010,7 @@ gqa_status launch_attention(const gqa_shape& s, const AttnPlan& plan, const void
             return GQA_ERR_SHAPE;  // plan made for another call
         void* dargs[] = {&p};
         const cudaError_t e = cudaLaunchKernelExC(&cfg, direct_ptr(s.H, bf16), dargs);
-        return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GQA_OK : GQA_ERR_CUDA;
+        return launch_status(e);
     }
     const int nw = plan.tiles_per_warp;
     if ((tree_mask || s.window > 0 || plan.chunks > 1) && !plan.general)
@@ -2018,7 +2018,7 @@ gqa_status launch_attention(const gqa_shape& s, const AttnPlan& plan, const void
     const void* kern = pick_kernel(s.H, bf16, nw, plan.general, s.kv_dtype);
     void* args[] = {&tmk, &tmv, &p};
     const cudaError_t e = cudaLaunchKernelExC(&cfg, kern, args);
-    return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GQA_OK : GQA_ERR_CUDA;
+    return launch_status(e);
 }
 
 }  // namespace gqa

@@ -1278,7 +1278,7 @@ gqa_status launch_attention_fourbit(const gqa_shape& s, const void* q, const uin
     cfg.numAttrs = (s.flags & (GQA_FLAG_PDL | GQA_FLAG_EARLY_KV)) ? 1 : 0;
     void* args[] = {&p};
     const cudaError_t e = cudaLaunchKernelExC(&cfg, pl.kernel, args);
-    return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GQA_OK : GQA_ERR_CUDA;
+    return launch_status(e);
 }
 
 }  // namespace gqa

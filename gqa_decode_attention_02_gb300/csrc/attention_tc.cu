@@ -1092,7 +1092,7 @@ gqa_status launch_tc_attention(const gqa_shape& s, const void* q, const void* k_
                          : cudaLaunchKernelEx(&cfg, tc_attention_kernel<true, 128>, tmk, tmv, tmq, tmo, p))
             : (s.H == 64 ? cudaLaunchKernelEx(&cfg, tc_attention_kernel<false, 64>, tmk, tmv, tmq, tmo, p)
                          : cudaLaunchKernelEx(&cfg, tc_attention_kernel<false, 128>, tmk, tmv, tmq, tmo, p));
-    return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GQA_OK : GQA_ERR_CUDA;
+    return launch_status(e);
 }
 
 }  // namespace gqa

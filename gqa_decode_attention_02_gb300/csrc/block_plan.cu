@@ -425,7 +425,7 @@ gqa_status launch_plan_blocks(int B, int max_blocks, int num_blocks, int tokens,
     cfg.numAttrs = p.in_place ? 2 : pdl ? 1 : 0;
     void* args[] = {&p};
     const cudaError_t e = cudaLaunchKernelExC(&cfg, kernel, args);
-    return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GQA_OK : GQA_ERR_CUDA;
+    return launch_status(e);
 }
 
 }  // namespace gqa

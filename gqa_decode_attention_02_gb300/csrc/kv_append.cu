@@ -78,7 +78,7 @@ gqa_status launch_kv_append(const gqa_shape& s, const void* k_new, const void* v
         static_cast<const uint4*>(v_new), static_cast<uint4*>(k_cache),
         static_cast<uint4*>(v_cache), block_tables, context_lens, dev_status, s.B, s.T, row_vec,
         s.max_blocks_per_seq, s.num_blocks);
-    return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GQA_OK : GQA_ERR_CUDA;
+    return launch_status(e);
 }
 
 }  // namespace gqa

@@ -144,7 +144,7 @@ gqa_status launch_kv_compact(const gqa_shape& s, void* k_cache, void* v_cache, v
                               static_cast<uint32_t*>(v_scale))
                      : launch(kv_compact_kernel<true, uint16_t>, static_cast<uint16_t*>(k_scale),
                               static_cast<uint16_t*>(v_scale));
-    return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GQA_OK : GQA_ERR_CUDA;
+    return launch_status(e);
 }
 
 }  // namespace gqa

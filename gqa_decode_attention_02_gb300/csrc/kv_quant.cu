@@ -159,7 +159,7 @@ gqa_status launch_kv_append_quant(const gqa_shape& s, const void* k_new, const v
                     (void*)&context_lens, &dev_status, &B, &T, &K, &mb, &nb};
     const cudaError_t e = cudaLaunchKernelExC(
         &cfg, pick_append(s.dtype == GQA_BF16, s.kv_dtype, s.H), args);
-    return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? GQA_OK : GQA_ERR_CUDA;
+    return launch_status(e);
 }
 
 }  // namespace gqa

@@ -366,9 +366,8 @@ gqa_status launch_slots(const gqa_shape& s, const void* kernel, SlotParams p, lo
         p.rows = (uint32_t)n;
         cfg.gridDim = dim3((unsigned)(need < cap ? need : cap));
         void* args[] = {&p};
-        if (cudaLaunchKernelExC(&cfg, kernel, args) != cudaSuccess ||
-            cudaGetLastError() != cudaSuccess)
-            return GQA_ERR_CUDA;
+        const gqa_status st = launch_status(cudaLaunchKernelExC(&cfg, kernel, args));
+        if (st != GQA_OK) return st;
         rows -= n;
         if (p.k_new) {
             p.k_new += items;

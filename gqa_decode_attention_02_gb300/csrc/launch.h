@@ -135,6 +135,15 @@ gqa_status launch_plan_blocks(int B, int max_blocks, int num_blocks, int tokens,
                               int32_t* slots, int32_t* positions, bool pdl, int32_t* dev_status,
                               cudaStream_t stream);
 
+// What a call returns for its launch's result, which alone decides: the runtime keeps
+// the error of a refused call until it is asked for, so the last error may be an earlier
+// call's.  This one's is taken back.
+inline gqa_status launch_status(cudaError_t e) {
+    if (e == cudaSuccess) return GQA_OK;
+    cudaGetLastError();
+    return GQA_ERR_CUDA;
+}
+
 // Cached per-device SM count (0 on failure).
 int device_sm_count();
 

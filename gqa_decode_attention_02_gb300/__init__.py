@@ -113,26 +113,37 @@ def kv_append_quant(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tabl
     _lib._check("gqa_kv_append_quant", rc)
 
 
-def attention_engine(q, k_cache, block_tables, window=0, engine="auto") -> str:
+def _shape_of_call(q, k_cache, block_tables, scale, window, kv, flags=0):
+    """The shape of an attention call over a cache of kind kv."""
+    if kv not in _lib.KV_DTYPES:
+        raise ValueError(f"kv must be one of {sorted(_lib.KV_DTYPES)}, got {kv!r}")
+    if kv != "int4":
+        return _lib.make_shape(q, k_cache, block_tables, scale, window=window, flags=flags, kv=kv)
+    B, T, N, _ = q.shape
+    return _lib.make_shape4(q, k_cache, block_tables.shape[1], scale, B=B, T=T, N=N, flags=flags,
+                            window=window)
+
+
+def attention_engine(q, k_cache, block_tables, window=0, engine="auto", kv="same") -> str:
     """Which kernel serves an attention call of this shape: "warp" (the
     persistent mma.sync kernel), "direct" (mma.sync, one CTA per sequence and
-    KV head) or "tmem" (tcgen05 with tensor-memory accumulators);
-    gqa_attention_engine.  Host logic only, for a call without a tree mask (a
-    tree mask rules "direct" out)."""
+    KV head), "tmem" (tcgen05 with tensor-memory accumulators) or "fourbit" (that
+    of the 4-bit cache, kv="int4"); gqa_attention_engine.  Host logic only, for a
+    call without a tree mask (a tree mask rules "direct" out)."""
     if engine not in _lib.ENGINES:
         raise ValueError(f"engine must be one of {sorted(_lib.ENGINES)}, got {engine!r}")
-    shape = _lib.make_shape(q, k_cache, block_tables, None, window=window,
-                            flags=_lib.ENGINES[engine])
+    shape = _shape_of_call(q, k_cache, block_tables, None, window, kv, _lib.ENGINES[engine])
     e = _lib.lib().gqa_attention_engine(ctypes.byref(shape))
     if e == 0:
         raise _lib.GqaError("gqa_attention_engine", _lib.Status.ERR_SHAPE)
     return _lib.ENGINE_NAMES[e]
 
 
-def attention_workspace_size(q, k_cache, block_tables, scale=None, window=0) -> int:
-    """Workspace bytes of one attention call (a window never needs more than
-    full attention of the same shape)."""
-    return _lib.workspace_size(_lib.make_shape(q, k_cache, block_tables, scale, window=window))
+def attention_workspace_size(q, k_cache, block_tables, scale=None, window=0, kv="same") -> int:
+    """Workspace bytes of one attention call over a cache of kind kv ("same", "int8",
+    "e4m3", "int4"), on the current GPU (a window never needs more than full attention
+    of the same shape)."""
+    return _lib.workspace_size(_shape_of_call(q, k_cache, block_tables, scale, window, kv))
 
 
 def _attention(fn_name, q, k_cache, v_cache, block_tables, context_lens, out, scale,

@@ -61,7 +61,7 @@ FLAG_WARP_MMA = 4
 FLAG_TENSOR_MEMORY = 8
 FLAG_DIRECT = 16
 ENGINES = {"auto": 0, "warp": FLAG_WARP_MMA, "tmem": FLAG_TENSOR_MEMORY, "direct": FLAG_DIRECT}
-ENGINE_NAMES = {1: "warp", 2: "tmem", 3: "direct"}
+ENGINE_NAMES = {1: "warp", 2: "tmem", 3: "direct", 4: "fourbit"}
 
 
 EXPORTS = ("gqa_version", "gqa_status_string", "gqa_kv_append",
@@ -267,8 +267,9 @@ def get_workspace4(nbytes: int, index: int, stream: int) -> torch.Tensor:
     """The workspace of a 4-bit attention call on the current stream (`stream`, of
     GPU `index`): that stream's attention workspace.  Under graph capture a buffer
     of the graph's own, its ticket region cleared by every replay: two graphs
-    captured on one stream may then run at the same time (a caller that passes
-    its own workspace saves the clearing)."""
+    captured on one stream may then run at the same time.  (A workspace of the
+    caller's own, of attention_workspace_size(..., kv="int4") bytes and zeroed once,
+    saves the clearing; calls that may overlap need one each.)"""
     if torch.cuda.is_current_stream_capturing():
         ws = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{index}")
         ws[:1 << 14].zero_()  # one int32 ticket per thread block

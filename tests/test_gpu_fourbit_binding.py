@@ -1,0 +1,49 @@
+"""GPU checks of the binding of the 4-bit, slot and planner calls: a caller's own
+workspace, and tensors of the host after calls of the same sizes on the GPU."""
+import pytest
+import torch
+
+import gqa_decode_attention_02_gb300 as gq
+from helpers import small, to
+from test_gpu_fourbit import four, t
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("B,T,N,H,ctx", [(1, 1, 4, 64, (20,)), (3, 2, 8, 128, (9000, 40, 800)),
+                                         (40, 1, 8, 64, (3000,) * 40)])
+def test_a_workspace_of_the_size_asked_for(gpu, B, T, N, H, ctx):
+    """Cleared once, then used by every call, in graphs too: the same bits as with the
+    binding's own; a byte less is refused."""
+    w = small(B=B, T=T, N=N, K=2, H=H, dtype="f16", ctx=ctx, seed=B)
+    wd, c = to(w, gpu), [t(x, gpu) for x in four(w)]
+    q, bt, cl = wd.q[0], wd.block_tables, wd.context_lens
+    n = gq.attention_workspace_size(q, c[0], bt, kv="int4")
+    ws, out = torch.zeros(n, dtype=torch.uint8, device=gpu), torch.empty_like(q)
+    call = lambda **kw: gq.verify_attention_quant(q, *c, bt, cl, kv="int4", **kw)  # noqa: E731
+    want = call()
+    for _ in range(2):
+        assert torch.equal(call(workspace=ws), want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(workspace=ws, out=out)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    with pytest.raises(gq.GqaError) as e:
+        call(workspace=ws[: n - 1])
+    assert e.value.status == gq.Status.ERR_WORKSPACE
+
+
+def test_workspace_size_of_one_byte_caches(gpu):
+    w = small(B=2, T=1, N=8, K=2, H=128, dtype="f16", ctx=(40, 17))
+    q, bt = w.q[0].to(gpu), w.block_tables.to(gpu)
+    kc = torch.zeros(w.k_cache[0].shape, dtype=torch.uint8, device=gpu)
+    sc = torch.ones(kc.shape[0], 2, 16, device=gpu)
+    ws = torch.zeros(gq.attention_workspace_size(q, kc, bt, kv="int8"), dtype=torch.uint8,
+                     device=gpu)
+    a = gq.decode_attention_quant(q, kc, kc, sc, sc, bt, w.context_lens.to(gpu), workspace=ws)
+    b = gq.decode_attention_quant(q, kc, kc, sc, sc, bt, w.context_lens.to(gpu))
+    assert torch.equal(a, b)

@@ -753,7 +753,7 @@ def _slots_call(k, v, k_cache, v_cache, k_scale, v_scale, slots, kv, pdl):
     """(checked shape, device index) of a call by slot; rows k and v [M,K,H]."""
     try:
         dev = k.get_device()
-        key = (kv, pdl, k.shape, k.dtype, v.shape, v.dtype, k_cache.shape, k_cache.dtype,
+        key = (dev, kv, pdl, k.shape, k.dtype, v.shape, v.dtype, k_cache.shape, k_cache.dtype,
                v_cache.shape, v_cache.dtype, slots.shape, slots.dtype)
         fit = (k.is_contiguous() and v.is_contiguous() and k_cache.is_contiguous()
                and v_cache.is_contiguous() and slots.is_contiguous()
@@ -815,9 +815,9 @@ def kv_gather_slots(k_cache, v_cache, slots, *, k_scale=None, v_scale=None, kv="
         raise TypeError("k_cache and slots must be torch.Tensors")
     if k_cache.dim() != 4 or slots.dim() != 1:
         raise ValueError("k_cache must have 4 dims and slots 1")
+    if not k_cache.is_cuda:
+        raise ValueError("k_cache must be a CUDA tensor (the library has no CPU path)")
     if stream is not None or k_cache.get_device() != _lib.current_gpu():
-        if not k_cache.is_cuda:
-            raise ValueError("k_cache must be a CUDA tensor (the library has no CPU path)")
         with _lib.on_device(k_cache.device, stream):
             return kv_gather_slots(k_cache, v_cache, slots, k_scale=k_scale, v_scale=v_scale,
                                    kv=kv, dtype=dtype, k_out=k_out, v_out=v_out, status=status,
@@ -903,7 +903,7 @@ def plan_blocks(context_lens, new_lens, block_tables, held, free_ring, ring_stat
     outs = (context_lens_out, held_out, ring_state_out, cu_new, slots, positions)
     try:
         dev = context_lens.get_device()
-        key = ("plan", max_tokens, context_lens.shape, context_lens.dtype, new_lens.shape,
+        key = ("plan", dev, max_tokens, context_lens.shape, context_lens.dtype, new_lens.shape,
                new_lens.dtype, block_tables.shape, block_tables.dtype, held.shape, held.dtype,
                free_ring.shape, free_ring.dtype, ring_state.shape, ring_state.dtype,
                *[None if t is None else (t.shape, t.dtype) for t in outs])

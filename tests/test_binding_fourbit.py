@@ -6,6 +6,15 @@ import torch
 import gqa_decode_attention_02_gb300 as gq
 
 
+def test_tensors_of_the_host_are_refused():
+    k = torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    c, s = torch.zeros(1, 16, 2, 64, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
+    for f in (lambda: gq.kv_append_slots(k, k, c, c, s), lambda: gq.kv_gather_slots(c, c, s),
+              lambda: gq.plan_blocks(s, s, s[:, None], s, s, s)):
+        with pytest.raises(ValueError, match="must be a CUDA tensor"):
+            f()
+
+
 @pytest.mark.parametrize("H", [64, 128])
 def test_engine_of_a_four_bit_cache(cuda_lib, H):
     q = torch.zeros(2, 5, 8, H, dtype=torch.float16)

@@ -6,6 +6,7 @@ import torch
 import gqa_decode_attention_02_gb300 as gq
 from helpers import small, to
 from test_gpu_fourbit import four, t
+from test_gpu_slots import plan_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +48,19 @@ def test_workspace_size_of_one_byte_caches(gpu):
     a = gq.decode_attention_quant(q, kc, kc, sc, sc, bt, w.context_lens.to(gpu), workspace=ws)
     b = gq.decode_attention_quant(q, kc, kc, sc, sc, bt, w.context_lens.to(gpu))
     assert torch.equal(a, b)
+
+
+def test_tensors_of_the_host_after_a_call_on_the_gpu(gpu):
+    """The same sizes and types, checked before: refused all the same."""
+    k = torch.ones(3, 2, 64, dtype=torch.bfloat16)
+    c, s = torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16), torch.arange(3, dtype=torch.int32)
+    a, tokens = plan_inputs(4, 1)
+    host = [torch.from_numpy(x) for x in a]
+    put = lambda *x: gq.kv_append_slots(x[0], x[0], x[1], x[1].clone(), x[2])  # noqa: E731
+    put(k.to(gpu), c.to(gpu), s.to(gpu))
+    gq.plan_blocks(*[x.to(gpu) for x in host], max_tokens=tokens)
+    for f in (lambda: put(k, c, s), lambda: gq.kv_gather_slots(c, c, s),
+              lambda: gq.plan_blocks(*host, max_tokens=tokens),
+              lambda: put(k, c.to(gpu), s.to(gpu)), lambda: put(k.to(gpu), c.to(gpu), s)):
+        with pytest.raises(ValueError):
+            f()

@@ -898,6 +898,8 @@ def plan_blocks(context_lens, new_lens, block_tables, held, free_ring, ring_stat
         context_lens_out, held_out, ring_state_out = context_lens, held, ring_state
     if max_tokens is None:
         max_tokens = -1 if slots is None else slots.shape[0]
+    if max_tokens > 2 ** 31 - 1:
+        raise ValueError(f"max_tokens must be below 2**31, got {max_tokens}")
     if max_tokens < 0 and (slots is not None or positions is not None):
         raise ValueError("positions need slots or max_tokens")
     outs = (context_lens_out, held_out, ring_state_out, cu_new, slots, positions)

@@ -15,6 +15,14 @@ def test_tensors_of_the_host_are_refused():
             f()
 
 
+@pytest.mark.parametrize("n", [2 ** 31, 2 ** 32 + 5])
+def test_more_tokens_than_an_int_counts_are_refused(n):
+    """Not taken modulo 2^32."""
+    s = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="max_tokens"):
+        gq.plan_blocks(s, s, s[:, None], s, s, s, max_tokens=n)
+
+
 @pytest.mark.parametrize("H", [64, 128])
 def test_engine_of_a_four_bit_cache(cuda_lib, H):
     q = torch.zeros(2, 5, 8, H, dtype=torch.float16)

@@ -305,11 +305,14 @@ def verify_attention_quant(q, k_cache, v_cache, k_scale, v_scale, block_tables, 
 
 def _append_attention_quant(fn_name, q, k_new, v_new, k_cache, v_cache, k_scale, v_scale,
                             block_tables, context_lens, out, scale, workspace, status, stream,
-                            pdl, early_kv, kv, window):
+                            pdl, early_kv, kv, window, tree_mask=None):
     if kv == "int4":
         return _attention4(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
                            k_new, v_new, out, scale, workspace, status, stream, pdl, early_kv,
-                           window, None, "decode" in fn_name)
+                           window, tree_mask, "decode" in fn_name)
+    if tree_mask is not None:
+        raise ValueError('tree_mask needs kv="int4" here (one-byte caches: kv_append_quant, then '
+                         "verify_attention_quant)")
     _lib._need(q, "q", ndim=4)
     _lib._need(k_new, "k_new", q.dtype, 4)
     _lib._need(v_new, "v_new", q.dtype, 4)
@@ -355,14 +358,15 @@ def append_decode_attention_quant(q, k_new, v_new, k_cache, v_cache, k_scale, v_
 def append_verify_attention_quant(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale,
                                   block_tables, context_lens, *, kv="int8", out=None,
                                   scale=None, workspace=None, status=None, stream=None,
-                                  pdl=False, early_kv=False, window=0):
+                                  pdl=False, early_kv=False, window=0, tree_mask=None):
     """gqa_append_verify_attention_quant: the T new tokens appended to the
     one-byte cache and verify attention over it, in one call (two launches);
-    kv = "int4" gives gqa_append_attention_fourbit."""
+    kv = "int4" gives gqa_append_attention_fourbit, with tree_mask (as in
+    verify_attention_quant) tree verification."""
     return _append_attention_quant("gqa_append_verify_attention_quant", q, k_new, v_new,
                                    k_cache, v_cache, k_scale, v_scale, block_tables,
                                    context_lens, out, scale, workspace, status, stream, pdl,
-                                   early_kv, kv, window)
+                                   early_kv, kv, window, tree_mask)
 
 
 def accept_prefix(target_logits, draft_ids, context_lens=None, *, accepted=None,

@@ -5,6 +5,7 @@ import torch
 
 import gqa_decode_attention_02_gb300 as gq
 from helpers import small, to
+from test_gpu_attention import as_i64, random_trees
 from test_gpu_fourbit import four, t
 from test_gpu_slots import plan_inputs
 
@@ -64,3 +65,34 @@ def test_tensors_of_the_host_after_a_call_on_the_gpu(gpu):
               lambda: put(k, c.to(gpu), s.to(gpu)), lambda: put(k.to(gpu), c.to(gpu), s)):
         with pytest.raises(ValueError):
             f()
+
+
+@pytest.mark.parametrize("T,N,K,H,dtype", [(6, 16, 2, 128, "bf16"), (26, 8, 2, 64, "f16")])
+def test_append_and_tree_verification_in_one_call(gpu, T, N, K, H, dtype):
+    """gqa_append_attention_fourbit with a tree mask: the bits of the two calls, caches
+    included, eagerly and from a graph."""
+    ctx = (T, T + 1, 300, 1029)
+    w = small(B=4, T=T, N=N, K=K, H=H, dtype=dtype, ctx=ctx, seed=T, append=True)
+    wd, c = to(w, gpu), four(w)
+    mask = as_i64(random_trees(4, T, seed=T)).to(gpu)
+    q, kn, vn, bt, cl = wd.q[0], wd.k_new[0], wd.v_new[0], wd.block_tables, wd.context_lens
+    two, one, cap = ([t(x, gpu) for x in c] for _ in range(3))
+    gq.kv_append_quant(kn, vn, *two, bt, cl, kv="int4")
+    want = gq.verify_attention_quant(q, *two, bt, cl, kv="int4", tree_mask=mask)
+    chain = gq.verify_attention_quant(q, *two, bt, cl, kv="int4")
+    assert not torch.equal(want, chain)
+    fused = lambda c, **kw: gq.append_verify_attention_quant(  # noqa: E731
+        q, kn, vn, *c, bt, cl, kv="int4", tree_mask=mask, **kw)
+    assert torch.equal(fused(one, pdl=True), want)
+    out, graph = torch.empty_like(q), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fused(cap, out=out)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    for a, b, d in zip(two, one, cap):
+        assert torch.equal(a, b) and torch.equal(a, d)
+    with pytest.raises(ValueError, match="tree_mask"):
+        gq.append_verify_attention_quant(q, kn, vn, *two, bt, cl, kv="int8", tree_mask=mask)
+    with pytest.raises(gq.GqaError):  # not with a window
+        fused(one, window=8)

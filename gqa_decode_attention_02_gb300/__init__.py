@@ -531,10 +531,12 @@ def accept_sampled(target_probs, draft_probs, draft_ids, uniforms, context_lens=
 
 
 # ---- 4-bit cache, rows by slot, blocks of a step ------------------------------------------
-# These calls are a few microseconds of GPU work at batch sizes where the host's
-# part counts, so a combination of sizes and types is checked in full once: the
-# checked C shape is kept under everything the checks looked at, and a later call
-# of the same kind only makes sure that its tensors are contiguous and on one GPU.
+# 4-bit attention, rows by slot and the planner are a few microseconds of GPU work at
+# batch sizes where the host's part counts, so a combination of sizes and types is
+# checked in full once: the checked C shape is kept under everything the checks looked
+# at, and a later call of the same kind only makes sure that its tensors are contiguous
+# and on one GPU.  (Rows by slot: the number of rows is one of the sizes.  The 4-bit
+# append and compaction by block table check every call in full.)
 _checked: dict = {}
 
 

@@ -10,10 +10,11 @@
 // H = 128), so at the measured copy rate a 16-token tile (2,176 bytes) could arrive
 // every 95 cycles per SM; the copies alone, without the arithmetic, run at 97 % of
 // that rate.  The arithmetic takes longer: 64 sequences of 32,768 tokens (4 query
-// rows per KV head) need 148 cycles per tile and SM, 525 us, 64 % of the
-// copy rate, and 8 warps per SM are as fast as 16.  Taking parts out one by one
-// showed its shares: about 47 cycles for the 18 mma.sync, 43 for turning the codes
-// into f16 operands, the rest for the softmax, the copies' addresses and the loop.
+// rows per KV head) need 142 cycles per tile and SM, 504 us, 67 % of the
+// copy rate.  Taking parts out one by one, of a form with 18 mma.sync a tile (17 now)
+// and 148 cycles, showed its shares: about 47 cycles for the mma.sync, 43 for turning
+// the codes into f16 operands, the rest for the softmax, the copies' addresses and the
+// loop.
 // (In loops of their own an mma.sync takes 8 cycles of a scheduler, lop3 and hfma2
 // two each, two of each in turn 6.1: the pipes overlap only in part.)  So
 // instructions per code word are what is saved first:
@@ -30,7 +31,8 @@
 //    One more row tile of PV sums the probabilities.
 //  * S^T[16 tokens x 8 rows] and O^T[H x 8 rows] on mma.sync m16n8k16, tokens
 //    (dims) on M.  Up to three row tiles share one conversion; more rows run in
-//    chunks of 24 (chunks of 16: 72 us against 60 for 16 sequences of 40 rows).
+//    chunks of 24 (chunks of 16: 68 us against 59 for 16 sequences of 40 rows, 364
+//    against 244 for 64 of 8,192 tokens and 24 rows).
 //    Four tiles no longer fit the registers with two tiles of tokens: 32 rows over
 //    64 sequences of 8,192 tokens in 368 us against 387, over 4 of 500 in 24 against
 //    20; five: no gain anywhere.
@@ -65,11 +67,20 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr int kStepTiles = 2;    // tiles a warp computes per step
 constexpr int kSlots = 3;        // steps in a warp's buffer: one computed, two in flight
 // Start-up cost of a segment, in tiles per warp (256 ragged sequences, one row tile,
-// 4 warps: some 6 us a segment against 0.27 us a tile; with 3 units 255 us, 6 245, 8
-// 248.  Three row tiles: 7 us against 0.15-0.18 us).
+// 4 warps: some 6 us a segment against 0.27 us a tile; with 3 units 240 us, 6 228, 9
+// 234.  Three row tiles: 7 us against 0.15-0.18 us; 16 sequences of 40 rows with 5 units
+// 62 us, 10 59, 15 62).
 constexpr int q4_seg_units(int NW) { return NW == 1 ? 6 : NW == 2 ? 7 : 10; }
-constexpr int kQ4Direct = 10;     // longest segment of a planless launch, in tiles per warp
-constexpr int kQ4CutCost = 6;    // what cutting segments costs a CTA, in tiles per warp
+// Longest segment of a planless launch, in tiles per warp.  Such a launch against a
+// planned one (us, in a chain of calls in a graph): 295 tokens 5.8 against 6.8, 64 of
+// 16..1,024 9.1 against 10.4, 8 of 2,560 (the longest it takes at 16 warps) 21.5 against
+// 22.9; of 5,000 tokens 33.7 against 28.0, which is why it ends there.
+constexpr int kQ4Direct = 10;
+// What cutting segments costs a CTA, in tiles per warp.  Whole segments where the longest
+// passes an equal share by up to 0, 6 or 24 tiles a warp (us): 12 sequences of 16,000
+// tokens 68.5, 68.0, 86.3; 16 of 12,000..16,000 79.5, 79.1, 84.4; 30 of 8,000 78.4, 78.2,
+// 84.6; 8 of 5,000 27.9, 27.9, 35.2; but 16 of 16..5,000 31.1, 34.3, 34.1.
+constexpr int kQ4CutCost = 6;
 // Reference where no score was seen: below all, and finite, so references need no test.
 constexpr float kQ4None = -3.402823466e38f;
 // A probability is 2^(score - reference).  The reference of a row is set 7 below its
@@ -831,7 +842,13 @@ __device__ __forceinline__ void fold_pieces(const Q4Params& p, int b, int kv, in
     }
 }
 
-// Warps an SM's registers hold at each row count.
+// Warps an SM's registers hold at each row count: 128, 168 and 255 registers a thread.
+// At H = 128 some spill (one row tile 340 bytes, two 706, three 16), nearly all outside
+// the loop over the steps: 0.6 spilled accesses a tile.  One row tile with 12 warps (168
+// registers, next to no spills) and with 8 (none) against 16: 64 x 32,768 513 and 544 us
+// against 504, 256 ragged 232 and 253 against 228; shorter and f16 batches like 12 better
+// (32 x 8,192 79.5 us against 85.5; 64 x 8,192, f16, 152 against 160).  Two row tiles
+// with 8 warps (no spills): 64 x 8,192, 16 rows, 193 us against 203.
 constexpr int q4_sm_warps(int NW) { return NW == 1 ? 16 : NW == 2 ? 12 : 8; }
 
 template <int H, int NW, bool BF16>
@@ -923,8 +940,8 @@ __global__ void __launch_bounds__(32 * q4_sm_warps(NW), 1) q4_attention_kernel(c
         quota = total / grid + (total % grid != 0);
         quota = max(quota, 2 * kStepTiles * W);
         // Whole segments, one per CTA, where there is a CTA for each and the longest
-        // exceeds an equal share by less than cutting segments costs (about 6 tiles a
-        // warp: two more trips through L2 and a fold).
+        // exceeds an equal share by less than cutting segments costs (two more trips
+        // through L2 and a fold).
         whole = p.B * p.KC <= grid && longest <= quota + kQ4CutCost * W;
         const int c0 = (int)min((long long)total, (long long)blockIdx.x * quota);
         const int c1 = (int)min((long long)total, (long long)c0 + quota);
@@ -1176,7 +1193,10 @@ gqa_status q4_plan(const gqa_shape& s, Q4Plan* pl) {
     if (sms <= 0) return GQA_ERR_CUDA;
     // Warps per CTA.  Many segments: small CTAs, so that few warps wait for one
     // another when a segment ends; few segments: large ones, so that a segment
-    // is cut into few pieces.
+    // is cut into few pieces.  Between (one to two an SM), half of the most against all of
+    // them and against 4 (us): 160 segments of 1,024 tokens 17.9, 24.2, 18.8, of 8,192 58.7,
+    // 63.0, 55.7; 256 of 8,192 85.5, 90.6, 81.6, with a window of 1,024 17.8, -, 25.2; 74 of
+    // 4,096, H = 64, 33.3, 45.7, 39.8: never far from the best.
     const int most = q4_sm_warps(pl->NW);
     pl->W = segs > 2 * sms ? 4 : segs > sms ? most / 2 : most;
     if (s.H == 128)

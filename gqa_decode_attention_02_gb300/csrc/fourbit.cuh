@@ -14,7 +14,7 @@
 // number and the attention kernel adds no rounding of its own to K or V.
 // s is at most 9216 (7 * 9216 = 64512, the largest multiple of 7 below f16's
 // range whose scale has four bits); larger elements saturate.  Groups with
-// a / 7 below 2^-18 get s = 0 and read as zeros.
+// a / 7 of 2^-18 or less get s = 0 and read as zeros.
 //
 // Layout: codes [num_blocks][K][16][H/2] bytes -- the tile of a block and KV
 // head is contiguous, H/2 bytes a row, element 2i in the low half of byte i,

@@ -19,7 +19,9 @@
 // clipping is left to the warps whose scales need it.  36,060 rows of prompts
 // (8 heads of 128, bf16) at 4 bits, on the device: put 30 us and take 32 us for
 // 187 MB each, 6.2 and 5.8 TB/s of the 6.8 that a copy reaches.  (Take with two
-// parts a thread: no faster.)
+// parts a thread: no faster.)  16-bit caches: 45 and 46 us for 295 MB, 6.6 and 6.5 TB/s.
+// One-byte caches: take 37 us for 224 MB, 6.0 TB/s, put 74 us (int8) and 65 us (e4m3), 3.0
+// and 3.4 TB/s, bound by a division and a conversion per element.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 

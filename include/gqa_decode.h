@@ -586,8 +586,10 @@ gqa_status gqa_kv_append_fourbit(const gqa_shape *shape, const void *k_new, cons
  * chunks of at most 24, each reading the KV head's blocks.  The products run on f16
  * tensor-core operands with fp32 accumulation: cached values are exact in f16,
  * q rows are scaled by a power of two first (f16 then holds an element exactly
- * down to 2^-20 of its row's largest, and to within 2^-31 of that below),
- * probabilities are rounded to f16.
+ * down to 2^-20 of its row's largest, and to within 2^-31 of that below).
+ * Probabilities are f16 numbers below 2^15, the largest of a row at least 2^7: off by
+ * 2^-11 of themselves (f16 outputs: a second f16 term makes that 2^-22), or by 2^-32 of
+ * the largest where that is more.
  * Workspace: gqa_attention_workspace_size(shape) bytes with that kv_dtype, zero-
  * filled before first use and left so, as for the other attention calls (the
  * two kinds may share one buffer).  GQA_FLAG_EARLY_KV acts as GQA_FLAG_PDL; the
@@ -626,7 +628,8 @@ gqa_status gqa_kv_compact_fourbit(const gqa_shape *shape, uint8_t *k_cache, uint
  *              GQA_KV_E4M3 (fp32 scales [num_blocks][K][16]), GQA_KV_INT4 (above)
  *   slots      int32 [M]; -1: no row (append skips it, gather gives zeros)
  * gqa_kv_append_slots stores what the appends by block table store, bit for bit.
- * gqa_kv_gather_slots returns the cached values rounded once to dtype.  Slots of
+ * gqa_kv_gather_slots returns the cached values rounded to dtype (of one-byte caches:
+ * the fp32 product code * scale, rounded as such first).  Slots of
  * one append must differ (two rows of one slot: either, or a mix of the two).
  * Device errors: a slot that is neither -1 nor in [0, 16 * num_blocks) counts as
  * -1 (GQA_ERR_BLOCK_ID).  GQA_FLAG_PDL in shape->flags as elsewhere. */
@@ -666,7 +669,9 @@ gqa_status gqa_kv_gather_slots(const gqa_shape *shape, int64_t rows, const void 
  * A sequence is refused, left as it was and given no tokens (GQA_ERR_BLOCKS), if
  * the free ids or the max_tokens entries do not cover it and everything the
  * sequences before it asked for; one that asks for no ids is not refused for
- * lack of ids.  Other device errors: negative or oversized lengths, or held out
+ * lack of ids.  (The appends by block table write the T newest positions of every
+ * sequence: one that was refused, or added fewer than T, must not take part in them, or
+ * its last cached rows are overwritten.  An append by the slot map leaves it alone.)  Other device errors: negative or oversized lengths, or held out
  * of range (GQA_ERR_CONTEXT, left as it was); a ring state out of range, or more
  * ids returned than the ring has room for (GQA_ERR_BLOCKS, nothing taken /
  * nothing returned); an id outside [0, num_blocks) in the ring

@@ -24,6 +24,14 @@ CUDA kernels; calling any op without the built library raises.
         packed rows [M,K,H] into and out of a cache of any kind, by slot
     plan_blocks(context_lens, new_lens, block_tables, held, free_ring, ring_state)
         -> lengths, blocks and slots of a step, made on the GPU
+    kv_append_rotary(q, k_new, v_new, k_cache, v_cache, slots, positions, cos_sin) -> q
+        rotated by position; the keys rotated on their way into the cache
+    chunk_attention(q, k_cache, v_cache, block_tables, context_lens, cu_new) -> out
+        packed new tokens of requests of any lengths (prompts, parts of them, one token)
+    kv_block_bounds(k_cache, block_tables, context_lens, cu_new, bounds, bounds_scale),
+        select_blocks(q, bounds, bounds_scale, block_tables, context_lens, keep),
+        sparse_decode_attention(q, k_cache, v_cache, tables, lens): decoding that reads
+        the blocks of a long context that a query weighs most
 """
 from __future__ import annotations
 
@@ -40,6 +48,8 @@ __all__ = ["kv_append", "kv_append_quant", "decode_attention", "verify_attention
            "append_verify_attention_quant", "append_decode_attention",
            "append_verify_attention", "accept_prefix", "accept_sampled", "accept_tree",
            "kv_compact", "kv_append_slots", "kv_gather_slots", "plan_blocks", "BlockPlan",
+           "kv_append_rotary", "chunk_attention", "chunk_workspace_size", "kv_block_bounds",
+           "select_blocks", "BlockChoice", "sparse_decode_attention",
            "attention_workspace_size", "reset_workspaces", "GqaError", "Status", "Shape"]
 
 
@@ -971,3 +981,364 @@ def plan_blocks(context_lens, new_lens, block_tables, held, free_ring, ring_stat
     if rc:
         raise _lib.GqaError("gqa_plan_blocks", rc)
     return BlockPlan(context_lens_out, held_out, ring_state_out, cu_new, slots, positions)
+
+
+# ---- chunks of new tokens, rotated appends, decoding over chosen blocks ----------------------
+def _rows_stride(t, name, dtype=None):
+    """Elements between the rows of packed [M,heads,H], which may be a part of wider rows
+    (of a projection that makes q, k and v at once); the rows themselves are dense."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dims, got {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    M, X, H = t.shape
+    if (H > 1 and t.stride(2) != 1) or (X > 1 and t.stride(1) != H):
+        raise ValueError(f"{name}'s heads must be dense, got strides {t.stride()}")
+    stride = t.stride(0) if M > 1 else X * H
+    if stride < X * H or stride % 8:
+        raise ValueError(f"{name}'s rows must be a multiple of 8 elements apart and not overlap, "
+                         f"got {stride}")
+    return stride
+
+
+def _key_of(*tensors):
+    """What the checks of a call look at: of every tensor shape, strides, type and device."""
+    return tuple([None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+                  for t in tensors])
+
+
+def kv_append_rotary(q, k_new, v_new, k_cache, v_cache, slots, positions, cos_sin, *, q_out=None,
+                     k_scale=None, v_scale=None, kv="same", interleaved=False, status=None,
+                     stream=None, pdl=False):
+    """gqa_kv_append_rotary: queries q [M,N,H] and keys k_new [M,K,H] of M packed tokens
+    rotated by their positions (int32 [M]; -1: no token), the keys and v_new stored in
+    the slots of a cache of any kind as kv_append_slots stores them.  cos_sin fp32
+    [positions, R]: R/2 cosines, then R/2 sines (R a multiple of 16, at most H: the
+    first R elements of a row turn); pairs (i, i + R/2), or (2i, 2i + 1) with
+    interleaved=True.  q, k_new and v_new may be parts of one wider row each (a fused
+    projection's output).  Returns the rotated queries in q_out (may be q itself;
+    default: a new tensor), whose rows without a token stay as they are."""
+    try:
+        key = ("rotary", kv, interleaved, pdl, _key_of(q, k_new, v_new, k_cache, v_cache, slots,
+                                                       positions, cos_sin, q_out, k_scale, v_scale))
+        shape = _checked.get(key)
+    except (AttributeError, TypeError):
+        key = shape = None
+    if shape is None:
+        strides = (_rows_stride(q, "q"), _rows_stride(k_new, "k_new", q.dtype),
+                   _rows_stride(v_new, "v_new", q.dtype))
+        M, N, H = q.shape
+        if v_new.shape != k_new.shape or k_new.shape[0] != M or k_new.shape[2] != H:
+            raise ValueError(f"k_new and v_new must be [{M},K,{H}]")
+        for t, n in ((slots, "slots"), (positions, "positions")):
+            _lib._need(t, n, torch.int32, 1)
+            if t.shape[0] != M:
+                raise ValueError(f"{n} must have {M} entries, got {t.shape[0]}")
+        _lib._need(cos_sin, "cos_sin", torch.float32, 2)
+        if q_out is not None:
+            _lib._need(q_out, "q_out", q.dtype, 3)
+            if q_out.shape != q.shape:
+                raise ValueError(f"q_out must be {tuple(q.shape)}, got {tuple(q_out.shape)}")
+        made = _slots_shape(k_new, k_cache, v_cache, k_scale, v_scale, kv, pdl)
+        made.N = N
+        made.strides = strides
+        _lib.one_device(q, k_new, v_new, k_cache, v_cache, slots, positions, cos_sin, q_out,
+                        k_scale, v_scale)
+        shape = _remember(key, made)
+    dev = q.get_device()
+    if stream is not None or dev != _lib.current_gpu():
+        with _lib.on_device(torch.device("cuda", dev), stream):
+            return kv_append_rotary(q, k_new, v_new, k_cache, v_cache, slots, positions, cos_sin,
+                                    q_out=q_out, k_scale=k_scale, v_scale=v_scale, kv=kv,
+                                    interleaved=interleaved, status=status, pdl=pdl)
+    if q_out is None:
+        q_out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+    st = None
+    if status is not None:
+        st = _status_arg(status)
+        _lib.one_device(q, status)
+    rc = _lib.lib().gqa_kv_append_rotary(
+        shape[1], q.shape[0], q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+        *shape[0].strides, k_cache.data_ptr(), v_cache.data_ptr(),
+        None if k_scale is None else k_scale.data_ptr(),
+        None if v_scale is None else v_scale.data_ptr(), slots.data_ptr(), positions.data_ptr(),
+        cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(interleaved),
+        q_out.data_ptr(), st, _lib.raw_stream(dev))
+    if rc:
+        raise _lib.GqaError("gqa_kv_append_rotary", rc)
+    return q_out
+
+
+def _chunk_shape(q_heads, H, dtype, B, k_cache, v_cache, width, scale, window, flags):
+    _lib._need(k_cache, "k_cache", dtype, 4)
+    _lib._need(v_cache, "v_cache", dtype, 4)
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+    NB, bs, K, Hc = k_cache.shape
+    if Hc != H:
+        raise ValueError(f"head size mismatch: {H} vs {Hc}")
+    if dtype not in _lib._DTYPES:
+        raise ValueError(f"dtype {dtype} unsupported (fp16 / bf16)")
+    return _lib.Shape(B=B, T=1, N=q_heads, K=K, H=H, block_size=bs, num_blocks=NB,
+                      max_blocks_per_seq=width, dtype=_lib._DTYPES[dtype], scale=scale,
+                      flags=flags, window=window, kv_dtype=0)
+
+
+def chunk_workspace_size(shape) -> int:
+    """Workspace bytes of chunk_attention and sparse_decode_attention on the current GPU
+    (gqa_chunk_workspace_size): the same for every call of one head size."""
+    n = _lib.lib().gqa_chunk_workspace_size(ctypes.byref(shape))
+    if n == 0:
+        raise _lib.GqaError("gqa_chunk_workspace_size", _lib.Status.ERR_SHAPE)
+    return n
+
+
+def _chunk_launch(fn, shape, dev, like, workspace, status, call):
+    """The tail of a chunk call: workspace, status and the launch `call(ptr, bytes, status,
+    stream)` on the current stream of GPU dev."""
+    st = None
+    if status is not None:
+        st = _status_arg(status)
+        _lib.one_device(like, status)
+    cs = _lib.raw_stream(dev)
+    if workspace is None:
+        workspace = _lib.get_workspace4(shape.nbytes, dev, cs)
+    else:
+        _lib._need(workspace, "workspace", torch.uint8)
+        _lib.one_device(like, workspace)
+    rc = call(workspace.data_ptr(), workspace.numel(), st, cs)
+    if rc:
+        raise _lib.GqaError(fn, rc)
+
+
+def chunk_attention(q, k_cache, v_cache, block_tables, context_lens, cu_new, *, out=None,
+                    scale=None, window=0, workspace=None, status=None, stream=None, pdl=False):
+    """gqa_chunk_attention: q [M,N,H] holds the new tokens of B requests end to end, those of
+    request b in rows cu_new[b] .. cu_new[b+1] - 1 (int32 [B+1], as plan_blocks makes it), at
+    positions context_lens[b] - n .. context_lens[b] - 1; their keys and values are in the
+    cache [NB,16,K,H] already.  A token sees the positions up to its own, or the last
+    `window` of them.  q may be a part of wider rows.  Returns out [M,N,H] (dense), whose
+    rows from cu_new[B] on stay as they are (default out: zeros)."""
+    scale, window = float(scale or 0.0), int(window)
+    try:
+        key = ("chunk", scale, window, pdl, _key_of(q, k_cache, v_cache, block_tables,
+                                                    context_lens, cu_new, out))
+        shape = _checked.get(key)
+    except (AttributeError, TypeError):
+        key = shape = None
+    if shape is None:
+        stride = _rows_stride(q, "q")
+        M, N, H = q.shape
+        _lib._need(block_tables, "block_tables", torch.int32, 2)
+        B = block_tables.shape[0]
+        _need_tables(block_tables, context_lens, B)
+        _lib._need(cu_new, "cu_new", torch.int32, 1)
+        if cu_new.shape[0] != B + 1:
+            raise ValueError(f"cu_new must have {B + 1} entries, got {cu_new.shape[0]}")
+        if out is not None:
+            _lib._need(out, "out", q.dtype, 3)
+            if out.shape != q.shape:
+                raise ValueError(f"out must be {tuple(q.shape)}, got {tuple(out.shape)}")
+        made = _chunk_shape(N, H, q.dtype, B, k_cache, v_cache, block_tables.shape[1], scale,
+                            window, _lib.FLAG_PDL if pdl else 0)
+        dev = _lib.one_device(q, k_cache, v_cache, block_tables, context_lens, cu_new, out).index
+        made.stride = stride
+        with torch.cuda.device(dev):
+            made.nbytes = chunk_workspace_size(made)
+        shape = _remember(key, made)
+    dev = q.get_device()
+    if stream is not None or dev != _lib.current_gpu():
+        with _lib.on_device(torch.device("cuda", dev), stream):
+            return chunk_attention(q, k_cache, v_cache, block_tables, context_lens, cu_new,
+                                   out=out, scale=scale, window=window, workspace=workspace,
+                                   status=status, pdl=pdl)
+    if out is None:
+        out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+    f = _lib.lib().gqa_chunk_attention
+    _chunk_launch("gqa_chunk_attention", shape[0], dev, q, workspace, status,
+                  lambda ws, n, st, cs: f(shape[1], q.shape[0], q.data_ptr(), shape[0].stride,
+                                          k_cache.data_ptr(), v_cache.data_ptr(),
+                                          block_tables.data_ptr(), context_lens.data_ptr(),
+                                          cu_new.data_ptr(), out.data_ptr(), ws, n, st, cs))
+    return out
+
+
+def kv_block_bounds(k_cache, block_tables, context_lens, cu_new, bounds, bounds_scale, *,
+                    status=None, stream=None, pdl=False):
+    """gqa_kv_block_bounds: the largest and smallest key, per KV head and element and in 8
+    bits, of every block of k_cache [NB,16,K,H] that holds one of the newest cu_new[b+1] -
+    cu_new[b] tokens of a request: bounds int8 [NB,K,2,H] (0: largest, 1: smallest) and
+    bounds_scale fp32 [NB,K] are updated.  After every append."""
+    try:
+        key = ("bounds", pdl, _key_of(k_cache, block_tables, context_lens, cu_new, bounds,
+                                      bounds_scale))
+        shape = _checked.get(key)
+    except (AttributeError, TypeError):
+        key = shape = None
+    if shape is None:
+        _lib._need(k_cache, "k_cache", ndim=4)
+        NB, _, K, H = k_cache.shape
+        _lib._need(block_tables, "block_tables", torch.int32, 2)
+        B = block_tables.shape[0]
+        _need_tables(block_tables, context_lens, B)
+        _lib._need(cu_new, "cu_new", torch.int32, 1)
+        if cu_new.shape[0] != B + 1:
+            raise ValueError(f"cu_new must have {B + 1} entries, got {cu_new.shape[0]}")
+        _need_bounds(bounds, bounds_scale, K, H, NB)
+        made = _chunk_shape(K, H, k_cache.dtype, B, k_cache, k_cache, block_tables.shape[1], 0.0,
+                            0, _lib.FLAG_PDL if pdl else 0)
+        _lib.one_device(k_cache, block_tables, context_lens, cu_new, bounds, bounds_scale)
+        shape = _remember(key, made)
+    dev = k_cache.get_device()
+    if stream is not None or dev != _lib.current_gpu():
+        with _lib.on_device(torch.device("cuda", dev), stream):
+            return kv_block_bounds(k_cache, block_tables, context_lens, cu_new, bounds,
+                                   bounds_scale, status=status, pdl=pdl)
+    st = None
+    if status is not None:
+        st = _status_arg(status)
+        _lib.one_device(k_cache, status)
+    rc = _lib.lib().gqa_kv_block_bounds(
+        shape[1], k_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+        cu_new.data_ptr(), bounds.data_ptr(), bounds_scale.data_ptr(), st, _lib.raw_stream(dev))
+    if rc:
+        raise _lib.GqaError("gqa_kv_block_bounds", rc)
+
+
+def _need_bounds(bounds, scale, K, H, NB=None):
+    _lib._need(bounds, "bounds", torch.int8, 4)
+    _lib._need(scale, "bounds_scale", torch.float32, 2)
+    NB = bounds.shape[0] if NB is None else NB
+    if tuple(bounds.shape) != (NB, K, 2, H) or tuple(scale.shape) != (NB, K):
+        raise ValueError(f"bounds must be [{NB},{K},2,{H}] and bounds_scale [{NB},{K}], got "
+                         f"{tuple(bounds.shape)} and {tuple(scale.shape)}")
+
+
+class BlockChoice(typing.NamedTuple):
+    """What select_blocks returns."""
+    tables: torch.Tensor  # int32 [B,K,keep] cache blocks chosen, in order, then -1
+    lens: torch.Tensor    # int32 [B] tokens they hold
+    blocks: torch.Tensor  # int32 [B,K,keep] which block of the sequence each is, then -1
+
+
+def select_blocks(q, bounds, bounds_scale, block_tables, context_lens, keep, *, first=1, recent=2,
+                  tables=None, lens=None, blocks=None, workspace=None, status=None, stream=None,
+                  pdl=False) -> BlockChoice:
+    """gqa_select_blocks: for every KV head, the `keep` cache blocks of a sequence that its
+    queries q [B,1,N,H] may weigh most, by the bounds that kv_block_bounds holds: the
+    `first` and the `recent` newest blocks always (recent >= 1), the others by score; all
+    blocks where a sequence has no more.  The result is what sparse_decode_attention
+    reads."""
+    keep, first, recent = int(keep), int(first), int(recent)
+    try:
+        key = ("select", keep, first, recent, pdl,
+               _key_of(q, bounds, bounds_scale, block_tables, context_lens, tables, lens, blocks))
+        shape = _checked.get(key)
+    except (AttributeError, TypeError):
+        key = shape = None
+    if shape is None:
+        _lib._need(q, "q", ndim=4)
+        B, T, N, H = q.shape
+        if T != 1:
+            raise _lib.GqaError("gqa_select_blocks", _lib.Status.ERR_SHAPE)  # decode: T == 1
+        if q.dtype not in _lib._DTYPES:
+            raise ValueError(f"dtype {q.dtype} unsupported (fp16 / bf16)")
+        _lib._need(bounds, "bounds", torch.int8, 4)
+        NB, K = bounds.shape[:2]
+        _need_bounds(bounds, bounds_scale, K, H)
+        _need_tables(block_tables, context_lens, B)
+        for t, n, want in ((tables, "tables", (B, K, keep)), (lens, "lens", (B,)),
+                           (blocks, "blocks", (B, K, keep))):
+            if t is not None:
+                _lib._need(t, n, torch.int32, len(want))
+                if tuple(t.shape) != want:
+                    raise ValueError(f"{n} must be {list(want)}, got {tuple(t.shape)}")
+        made = _lib.Shape(B=B, T=1, N=N, K=K, H=H, block_size=16, num_blocks=NB,
+                          max_blocks_per_seq=block_tables.shape[1], dtype=_lib._DTYPES[q.dtype],
+                          scale=0.0, flags=_lib.FLAG_PDL if pdl else 0, window=0, kv_dtype=0)
+        _lib.one_device(q, bounds, bounds_scale, block_tables, context_lens, tables, lens, blocks)
+        made.nbytes = _lib.lib().gqa_select_workspace_size(ctypes.byref(made))
+        shape = _remember(key, made)
+    dev = q.get_device()
+    if stream is not None or dev != _lib.current_gpu():
+        with _lib.on_device(torch.device("cuda", dev), stream):
+            return select_blocks(q, bounds, bounds_scale, block_tables, context_lens, keep,
+                                 first=first, recent=recent, tables=tables, lens=lens,
+                                 blocks=blocks, workspace=workspace, status=status, pdl=pdl)
+    B, K = q.shape[0], bounds.shape[1]
+    if keep < 1:
+        raise _lib.GqaError("gqa_select_blocks", _lib.Status.ERR_SHAPE)
+    if tables is None:
+        tables = context_lens.new_empty((B, K, keep))
+    if lens is None:
+        lens = context_lens.new_empty(B)
+    if blocks is None:
+        blocks = context_lens.new_empty((B, K, keep))
+    st = None
+    if status is not None:
+        st = _status_arg(status)
+        _lib.one_device(q, status)
+    cs = _lib.raw_stream(dev)
+    if workspace is None:
+        workspace = _lib.get_scratch(shape[0].nbytes, dev, cs, "select")
+    else:
+        _lib._need(workspace, "workspace", torch.uint8)
+        _lib.one_device(q, workspace)
+    rc = _lib.lib().gqa_select_blocks(
+        shape[1], keep, first, recent, q.data_ptr(), bounds.data_ptr(), bounds_scale.data_ptr(),
+        block_tables.data_ptr(), context_lens.data_ptr(), tables.data_ptr(), lens.data_ptr(),
+        blocks.data_ptr(), workspace.data_ptr(), workspace.numel(), st, cs)
+    if rc:
+        raise _lib.GqaError("gqa_select_blocks", rc)
+    return BlockChoice(tables, lens, blocks)
+
+
+def sparse_decode_attention(q, k_cache, v_cache, tables, lens, *, out=None, scale=None,
+                            workspace=None, status=None, stream=None, pdl=False):
+    """gqa_sparse_decode_attention: decode attention (q [B,1,N,H], out the same) in which
+    every KV head reads blocks of its own: tables int32 [B,K,S] holds them, lens int32 [B]
+    how many tokens of them count (all but the last block whole), as select_blocks
+    returns both."""
+    scale = float(scale or 0.0)
+    try:
+        key = ("sparse", scale, pdl, _key_of(q, k_cache, v_cache, tables, lens, out))
+        shape = _checked.get(key)
+    except (AttributeError, TypeError):
+        key = shape = None
+    if shape is None:
+        _lib._need(q, "q", ndim=4)
+        B, T, N, H = q.shape
+        if T != 1:
+            raise _lib.GqaError("gqa_sparse_decode_attention", _lib.Status.ERR_SHAPE)
+        _lib._need(tables, "tables", torch.int32, 3)
+        _lib._need(lens, "lens", torch.int32, 1)
+        made = _chunk_shape(N, H, q.dtype, B, k_cache, v_cache, tables.shape[2], scale, 0,
+                            _lib.FLAG_PDL if pdl else 0)
+        if tuple(tables.shape[:2]) != (B, made.K) or lens.shape[0] != B:
+            raise ValueError(f"tables must be [{B},{made.K},S] and lens [{B}]")
+        if out is not None:
+            _lib._need(out, "out", q.dtype, 4)
+            if out.shape != q.shape:
+                raise ValueError(f"out must be {tuple(q.shape)}, got {tuple(out.shape)}")
+        dev = _lib.one_device(q, k_cache, v_cache, tables, lens, out).index
+        with torch.cuda.device(dev):
+            made.nbytes = chunk_workspace_size(made)
+        shape = _remember(key, made)
+    dev = q.get_device()
+    if stream is not None or dev != _lib.current_gpu():
+        with _lib.on_device(torch.device("cuda", dev), stream):
+            return sparse_decode_attention(q, k_cache, v_cache, tables, lens, out=out,
+                                           scale=scale, workspace=workspace, status=status,
+                                           pdl=pdl)
+    if out is None:
+        out = torch.empty_like(q)
+    f = _lib.lib().gqa_sparse_decode_attention
+    _chunk_launch("gqa_sparse_decode_attention", shape[0], dev, q, workspace, status,
+                  lambda ws, n, st, cs: f(shape[1], q.data_ptr(), k_cache.data_ptr(),
+                                          v_cache.data_ptr(), tables.data_ptr(), lens.data_ptr(),
+                                          out.data_ptr(), ws, n, st, cs))
+    return out

@@ -74,7 +74,9 @@ EXPORTS = ("gqa_version", "gqa_status_string", "gqa_kv_append",
            "gqa_tree_verify_attention_quant", "gqa_accept_tree", "gqa_kv_compact",
            "gqa_attention_engine", "gqa_kv_append_fourbit", "gqa_attention_fourbit",
            "gqa_append_attention_fourbit", "gqa_kv_compact_fourbit", "gqa_kv_append_slots",
-           "gqa_kv_gather_slots", "gqa_plan_blocks")
+           "gqa_kv_gather_slots", "gqa_plan_blocks", "gqa_kv_append_rotary",
+           "gqa_chunk_workspace_size", "gqa_chunk_attention", "gqa_sparse_decode_attention",
+           "gqa_kv_block_bounds", "gqa_select_workspace_size", "gqa_select_blocks")
 
 
 def lib() -> ctypes.CDLL:
@@ -143,10 +145,19 @@ def lib() -> ctypes.CDLL:
                 ("gqa_kv_compact_fourbit", [S] + [P] * 10),
                 ("gqa_kv_append_slots", [S, N] + [P] * 9),
                 ("gqa_kv_gather_slots", [S, N] + [P] * 9),
-                ("gqa_plan_blocks", [I] * 4 + [P] * 12 + [ctypes.c_uint, P, P])):
+                ("gqa_plan_blocks", [I] * 4 + [P] * 12 + [ctypes.c_uint, P, P]),
+                ("gqa_kv_append_rotary", [S, N] + [P] * 3 + [N] * 3 + [P] * 7 + [I] * 3 + [P] * 3),
+                ("gqa_chunk_attention", [S, N, P, N] + [P] * 7 + [Z, P, P]),
+                ("gqa_sparse_decode_attention", [S] + [P] * 7 + [Z, P, P]),
+                ("gqa_kv_block_bounds", [S] + [P] * 8),
+                ("gqa_select_blocks", [S] + [I] * 3 + [P] * 9 + [Z, P, P])):
             f = getattr(L, name)
             f.restype = I
             f.argtypes = args
+        for name in ("gqa_chunk_workspace_size", "gqa_select_workspace_size"):
+            f = getattr(L, name)
+            f.restype = Z
+            f.argtypes = [S]
         _lib = L
         return L
 
@@ -277,6 +288,17 @@ def get_workspace4(nbytes: int, index: int, stream: int) -> torch.Tensor:
     ws = _ws_cache.get((index, stream, "attention"))
     if ws is None or ws.numel() < nbytes:
         ws = get_workspace(nbytes, f"cuda:{index}")
+    return ws
+
+
+def get_scratch(nbytes: int, index: int, stream: int, kind: str) -> torch.Tensor:
+    """Scratch that needs no clearing, of a call on the current stream (`stream`, of GPU
+    `index`): kept per stream, or under graph capture a buffer of the graph's own."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=f"cuda:{index}")
+    ws = _ws_cache.get((index, stream, kind))
+    if ws is None or ws.numel() < nbytes:
+        ws = get_workspace(nbytes, f"cuda:{index}", kind=kind)
     return ws
 
 

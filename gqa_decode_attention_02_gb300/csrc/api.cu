@@ -167,11 +167,49 @@ gqa_status attention_entry(const gqa_shape* s, bool decode_only, bool fused, con
                                  static_cast<cudaStream_t>(stream));
 }
 
+// Shape of a call over a cache in q's dtype whose kernel is not a matter of flags.
+gqa_status check_plain(const gqa_shape* s) {
+    const gqa_status st = check_common(s);
+    if (st != GQA_OK) return st;
+    if (s->kv_dtype != GQA_KV_SAME) return GQA_ERR_DTYPE;
+    if (s->flags & (GQA_FLAG_WARP_MMA | GQA_FLAG_TENSOR_MEMORY | GQA_FLAG_DIRECT))
+        return GQA_ERR_SHAPE;
+    return s->N / s->K <= 8192 && s->B <= 16384 ? GQA_OK : GQA_ERR_SHAPE;
+}
+
+gqa_status chunk_entry(const gqa_shape* s, int64_t rows, int64_t q_stride, const void* q,
+                       const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                       bool head_tables, const int32_t* context_lens, const int32_t* cu_new,
+                       void* out, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                       void* stream) {
+    const gqa_status st = check_plain(s);
+    if (st != GQA_OK) return st;
+    if (rows < 0 || rows > (1ll << 31) - 1) return GQA_ERR_SHAPE;
+    const long long row = (long long)s->N * s->H;
+    if (row * 2 >= (1ll << 40) || q_stride < row || q_stride % 8 != 0 ||
+        q_stride * 2 >= (1ll << 40))
+        return GQA_ERR_SHAPE;
+    if (s->B == 0 || rows == 0) return GQA_OK;
+    if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !out ||
+        (!head_tables && !cu_new))
+        return GQA_ERR_NULL;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
+        return GQA_ERR_ALIGN;
+    const size_t flags = gqa::workspace_flags_bytes();
+    const size_t need = gqa::chunk_workspace_bytes(*s, flags);
+    if (need == 0) return GQA_ERR_CUDA;
+    if (!workspace || ws_bytes < need) return GQA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return GQA_ERR_ALIGN;
+    return gqa::launch_chunk_attention(*s, rows, q_stride, q, k_cache, v_cache, block_tables,
+                                       head_tables, context_lens, cu_new, out, workspace, flags,
+                                       dev_status, static_cast<cudaStream_t>(stream));
+}
+
 }  // namespace
 
 extern "C" {
 
-int gqa_version(void) { return 300; }
+int gqa_version(void) { return 400; }
 
 const char* gqa_status_string(int status) {
     switch (status) {
@@ -559,6 +597,101 @@ gqa_status gqa_kv_gather_slots(const gqa_shape* shape, int64_t rows, const void*
     return gqa::launch_kv_gather_slots(*shape, rows, k_cache, v_cache, k_scale, v_scale, slots,
                                        k_out, v_out, dev_status,
                                        static_cast<cudaStream_t>(stream));
+}
+
+gqa_status gqa_kv_append_rotary(const gqa_shape* shape, int64_t rows, const void* q,
+                                const void* k_new, const void* v_new, int64_t q_stride,
+                                int64_t k_stride, int64_t v_stride, void* k_cache, void* v_cache,
+                                void* k_scale, void* v_scale, const int32_t* slots,
+                                const int32_t* positions, const float* cos_sin, int table_rows,
+                                int rotary_dims, int interleaved, void* q_out,
+                                int32_t* dev_status, void* stream) {
+    const gqa_status st = check_slots(shape, rows, k_new, v_new, k_cache, v_cache, k_scale,
+                                      v_scale, slots);
+    if (st != GQA_OK) return st;
+    if (table_rows < 1 || rotary_dims < 16 || rotary_dims > shape->H || rotary_dims % 16 != 0)
+        return GQA_ERR_SHAPE;
+    const long long q_row = (long long)shape->N * shape->H, k_row = (long long)shape->K * shape->H;
+    if (q_stride < q_row || k_stride < k_row || v_stride < k_row || q_stride % 8 != 0 ||
+        k_stride % 8 != 0 || v_stride % 8 != 0)
+        return GQA_ERR_SHAPE;
+    if (rows == 0) return GQA_OK;
+    if (!q || !q_out || !positions || !cos_sin) return GQA_ERR_NULL;
+    if (!aligned16(q) || !aligned16(q_out) || !aligned16(cos_sin)) return GQA_ERR_ALIGN;
+    return gqa::launch_kv_append_rotary(*shape, rows, q, k_new, v_new, q_stride, k_stride,
+                                        v_stride, k_cache, v_cache, k_scale, v_scale, slots,
+                                        positions, cos_sin, table_rows, rotary_dims,
+                                        interleaved != 0, q_out, dev_status,
+                                        static_cast<cudaStream_t>(stream));
+}
+
+size_t gqa_chunk_workspace_size(const gqa_shape* shape) {
+    return check_plain(shape) == GQA_OK
+               ? gqa::chunk_workspace_bytes(*shape, gqa::workspace_flags_bytes())
+               : 0;
+}
+
+gqa_status gqa_chunk_attention(const gqa_shape* shape, int64_t rows, const void* q,
+                               int64_t q_stride, const void* k_cache, const void* v_cache,
+                               const int32_t* block_tables, const int32_t* context_lens,
+                               const int32_t* cu_new, void* out, void* workspace,
+                               size_t workspace_bytes, int32_t* dev_status, void* stream) {
+    return chunk_entry(shape, rows, q_stride, q, k_cache, v_cache, block_tables, false,
+                       context_lens, cu_new, out, workspace, workspace_bytes, dev_status, stream);
+}
+
+gqa_status gqa_sparse_decode_attention(const gqa_shape* shape, const void* q, const void* k_cache,
+                                       const void* v_cache, const int32_t* tables,
+                                       const int32_t* lens, void* out, void* workspace,
+                                       size_t workspace_bytes, int32_t* dev_status,
+                                       void* stream) {
+    if (shape && (shape->T != 1 || shape->window != 0)) return GQA_ERR_SHAPE;
+    return chunk_entry(shape, shape ? shape->B : 0, shape ? (int64_t)shape->N * shape->H : 0, q,
+                       k_cache, v_cache, tables, true, lens, nullptr, out, workspace,
+                       workspace_bytes, dev_status, stream);
+}
+
+gqa_status gqa_kv_block_bounds(const gqa_shape* shape, const void* k_cache,
+                               const int32_t* block_tables, const int32_t* context_lens,
+                               const int32_t* cu_new, int8_t* bounds, float* bounds_scale,
+                               int32_t* dev_status, void* stream) {
+    const gqa_status st = check_plain(shape);
+    if (st != GQA_OK || shape->B == 0) return st;
+    if (!k_cache || !block_tables || !context_lens || !cu_new || !bounds || !bounds_scale)
+        return GQA_ERR_NULL;
+    if (!aligned16(k_cache) || !aligned16(bounds)) return GQA_ERR_ALIGN;
+    return gqa::launch_block_bounds(*shape, k_cache, block_tables, context_lens, cu_new, bounds,
+                                    bounds_scale, dev_status, static_cast<cudaStream_t>(stream));
+}
+
+size_t gqa_select_workspace_size(const gqa_shape* shape) {
+    return check_plain(shape) == GQA_OK ? gqa::select_workspace_bytes(*shape) : 0;
+}
+
+gqa_status gqa_select_blocks(const gqa_shape* shape, int keep, int first, int recent,
+                             const void* q, const int8_t* bounds, const float* bounds_scale,
+                             const int32_t* block_tables, const int32_t* context_lens,
+                             int32_t* tables, int32_t* lens, int32_t* blocks, void* workspace,
+                             size_t workspace_bytes, int32_t* dev_status, void* stream) {
+    const gqa_status st = check_plain(shape);
+    if (st != GQA_OK) return st;
+    if (shape->T != 1 || shape->N / shape->K > 128) return GQA_ERR_SHAPE;
+    // (a table of the chosen blocks is a block table again)
+    if (keep < 1 || first < 0 || recent < 1 || (long long)first + recent > keep ||
+        (long long)keep * 16 > (1ll << 30) ||
+        (long long)shape->B * shape->K * keep > (1ll << 31) - 1)
+        return GQA_ERR_SHAPE;
+    if (shape->B == 0) return GQA_OK;
+    if (!q || !bounds || !bounds_scale || !block_tables || !context_lens || !tables || !lens ||
+        !blocks)
+        return GQA_ERR_NULL;
+    if (!aligned16(q) || !aligned16(bounds)) return GQA_ERR_ALIGN;
+    if (!workspace || workspace_bytes < gqa::select_workspace_bytes(*shape))
+        return GQA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return GQA_ERR_ALIGN;
+    return gqa::launch_select_blocks(*shape, keep, first, recent, q, bounds, bounds_scale,
+                                     block_tables, context_lens, tables, lens, blocks, workspace,
+                                     dev_status, static_cast<cudaStream_t>(stream));
 }
 
 gqa_status gqa_plan_blocks(int B, int max_blocks_per_seq, int num_blocks, int max_tokens,

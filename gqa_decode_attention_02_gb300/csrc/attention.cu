@@ -1787,6 +1787,20 @@ bool make_rows_map(CUtensorMap* m, const void* base, const gqa_shape& s, int hpc
     return r == CUDA_SUCCESS;
 }
 
+bool make_tensor_map(CUtensorMap* m, gqa_dtype dtype, int rank, const void* base,
+                     const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
+    auto fn = encode_fn();
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return fn && fn(m, dtype == GQA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                    (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t workspace_flags_bytes() { return (size_t)kMaxFlags * 4; }
+
 int device_sm_count() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;

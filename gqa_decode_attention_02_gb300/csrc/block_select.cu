@@ -1,0 +1,503 @@
+// block_select.cu -- which blocks of a long cache a query should read.
+//
+// CS336 lecture 10 §"Арифметическая интенсивность инференса" (decoding reads the whole
+// KV cache for every token and is bound by that) and §"PagedAttention" (the cache is
+// blocks of 16 tokens, found through a table): a query whose weights lie on few blocks
+// need read only those.  What stands for a block is, per KV head and element d, the
+// largest and the smallest key of its rows; for a query q
+//     sum_d max(q_d max_d, q_d min_d) >= <q, k>   for every key k of the block
+// bounds every score in it, at a thirtieth of the block's bytes:
+//   bounds  int8 [num_blocks][K][2][H]  (0: largest, 1: smallest), and a scale
+//           fp32 [num_blocks][K]: s = max |k| / 127 over the block's rows held,
+//           ceil(max_d / s) and floor(min_d / s) (outwards: still a bound, up to the
+//           divisions' rounding), within [-127, 127]
+// The query's rows become 8-bit codes as well, c = rn(q / t) with t = max |q| / 127, so
+// that the sums are whole numbers, at most 127 * 127 * 128 < 2^21 + 2^19, the same in any
+// order, exact in fp32; a block's score for a KV head is the largest over its G queries of
+//     (t * s) * sum_d max(c_d max_d, c_d min_d)       (both products rounded in fp32)
+// and equal scores go to the lower block: the choice does not depend on the schedule.
+#include <cuda_runtime.h>
+
+#include "launch.h"
+#include "ptx.cuh"
+
+namespace gqa {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kBoundThreads = 256;
+constexpr float kMaxFinite = 3.402823466e38f;
+
+// ---- bounds ------------------------------------------------------------------------
+struct BoundParams {
+    const uint4* k_cache;
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    const int32_t* cu_new;
+    int8_t* bounds;
+    float* scale;
+    int32_t* status;
+    int B, K, max_blocks, num_blocks;
+};
+
+// Largest and smallest magnitude-limited value: a NaN counts as 0, an infinity as the
+// largest finite number.
+template <bool BF16>
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+    constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;
+    auto one = [&](uint32_t x) {
+        const uint32_t m = x & 0x7fffu;
+        return m > kInf ? 0u : m == kInf ? (x & 0x8000u) | (kInf - 1) : x;
+    };
+    return one(w & 0xffffu) | one(w >> 16) << 16;
+}
+
+// A warp per block and KV head: 16 rows of H elements, 16 bytes a lane and row (H = 128:
+// two rows at a time).  The units of all sequences lie end to end, a warp takes every
+// W-th of them and looks up whose it is 32 sequences at a time.  Bound by reading the
+// keys once.
+template <bool BF16, int H>
+__global__ void __launch_bounds__(kBoundThreads) block_bounds_kernel(const BoundParams p) {
+    constexpr int P = H / 8, R = 32 / P;  // lanes per row, rows at a time
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31, c = lane % P, sub = lane / P;
+    const long long W = (long long)gridDim.x * (kBoundThreads / 32);
+    long long id = (long long)blockIdx.x * (kBoundThreads / 32) + (threadIdx.x >> 5);
+    const bool reporter = id == 0;
+    long long base = 0;  // units of the sequences before b0
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const int b = b0 + lane;
+        int ctx = 0, i0 = 0, n = 0;  // length; first touched block and how many
+        if (b < p.B) {
+            ctx = __ldg(p.context_lens + b);
+            const int add = __ldg(p.cu_new + b + 1) - __ldg(p.cu_new + b);
+            if (add < 0 || (add > 0 && (ctx < add || ctx > p.max_blocks * 16))) {
+                if (reporter) report(p.status, GQA_ERR_CONTEXT);
+            } else if (add > 0) {
+                i0 = (ctx - add) >> 4;
+                n = ((ctx + 15) >> 4) - i0;
+            }
+        }
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(kFull, incl, o);
+            if (lane >= o) incl += x;
+        }
+        const long long units = (long long)__shfl_sync(kFull, incl, 31) * p.K;
+        for (; id < base + units; id += W) {
+            const int u = (int)((id - base) / p.K), k = (int)((id - base) % p.K);
+            const int src = __popc(__ballot_sync(kFull, incl <= u));
+            const int at = __shfl_sync(kFull, i0, src) + u - __shfl_sync(kFull, incl - n, src);
+            const int held = min(16, __shfl_sync(kFull, ctx, src) - at * 16);
+            const int blk = __ldg(p.block_tables + (size_t)(b0 + src) * p.max_blocks + at);
+            if (blk < 0 || blk >= p.num_blocks) {
+                if (lane == 0) report(p.status, GQA_ERR_BLOCK_ID);
+                continue;
+            }
+            const uint4* rows = p.k_cache + ((size_t)blk * 16 * p.K + k) * P + c;
+            uint4 w[16 / R];
+#pragma unroll
+            for (int j = 0; j < 16 / R; ++j) {
+                const int r = j * R + sub;  // (rows past the last repeat the first)
+                w[j] = __ldg(rows + (size_t)(r < held ? r : 0) * p.K * P);
+            }
+            uint32_t m2 = 0;  // largest magnitudes
+#pragma unroll
+            for (int j = 0; j < 16 / R; ++j)
+                m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(w[j].x & 0x7fff7fffu, w[j].y & 0x7fff7fffu),
+                                           __vmaxu2(w[j].z & 0x7fff7fffu, w[j].w & 0x7fff7fffu)));
+            uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+            if (m >= (BF16 ? 0x7f80u : 0x7c00u)) {  // rare
+                m = 0;
+#pragma unroll
+                for (int j = 0; j < 16 / R; ++j) {
+                    w[j] = make_uint4(finite2<BF16>(w[j].x), finite2<BF16>(w[j].y),
+                                      finite2<BF16>(w[j].z), finite2<BF16>(w[j].w));
+                    const uint32_t a[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        m = max(m, max(a[e] & 0x7fffu, a[e] >> 16 & 0x7fffu));
+                }
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+            float top[8], low[8];
+#pragma unroll
+            for (int j = 0; j < 16 / R; ++j) {
+                const uint32_t a[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float x = e & 1 ? Elt<BF16>::hi(a[e >> 1]) : Elt<BF16>::lo(a[e >> 1]);
+                    top[e] = j ? fmaxf(top[e], x) : x;
+                    low[e] = j ? fminf(low[e], x) : x;
+                }
+            }
+#pragma unroll
+            for (int o = P; o < 32; o <<= 1)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    top[e] = fmaxf(top[e], __shfl_xor_sync(kFull, top[e], o));
+                    low[e] = fminf(low[e], __shfl_xor_sync(kFull, low[e], o));
+                }
+            const float s = __fdiv_rn(Elt<BF16>::lo(m), 127.f);
+            if (sub < 2) {  // lanes of the first row write the largest, of the second the smallest
+                uint32_t word[2] = {0u, 0u};
+                if (s > 0.f) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float y = sub ? floorf(__fdiv_rn(low[e], s)) : ceilf(__fdiv_rn(top[e], s));
+                        const int code = (int)fminf(fmaxf(y, -127.f), 127.f);
+                        word[e >> 2] |= (uint32_t)(code & 0xff) << (8 * (e & 3));
+                    }
+                }
+                const size_t row = (size_t)blk * p.K + k;
+                reinterpret_cast<uint2*>(p.bounds)[(row * 2 + sub) * P + c] =
+                    make_uint2(word[0], word[1]);
+                if (lane == 0) p.scale[row] = s;
+            }
+        }
+        base += units;
+    }
+}
+
+// ---- scores ------------------------------------------------------------------------
+constexpr int kScoreThreads = 128;
+struct SelectParams {
+    const void* q;
+    const int8_t* bounds;
+    const float* scale;
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    int32_t* tables;
+    int32_t* lens;
+    int32_t* blocks;
+    float* scores;  // [B][K][max_blocks]
+    int32_t* status;
+    int B, N, K, G, max_blocks, num_blocks;
+    int keep, first, recent, splits;
+};
+
+__device__ __forceinline__ int blocks_of(const SelectParams& p, int ctx) {
+    return ctx >= 1 && ctx <= p.max_blocks * 16 ? (ctx + 15) >> 4 : 0;
+}
+// D += A(16 x 32, row) * B(32 x 8, col), 8-bit integers
+__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                       uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A CTA per sequence, KV head and part of its blocks.  The score is one product of a
+// block's row [largest | smallest] with [max(c, 0) | min(c, 0)] of each query, 16 blocks
+// by 8 queries at a time.  A product's k positions are in the order in which 16-byte
+// loads bring them, the same for both sides.  Bound by reading the bounds.
+template <bool BF16, int H>
+__global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const SelectParams p) {
+    constexpr int V = 2 * H / 16;  // 16-byte pieces of a row
+    extern __shared__ uint4 codes[];  // [ceil(G / 8) * 8][V], then the scales
+    griddep_launch_dependents();
+    griddep_wait();
+    const int part = blockIdx.x % p.splits, bk = blockIdx.x / p.splits;
+    const int b = bk / p.K, k = bk - b * p.K;
+    const int ctx = __ldg(p.context_lens + b), nb = blocks_of(p, ctx);
+    if (nb <= p.keep) return;  // all of them
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int G8 = (p.G + 7) / 8 * 8;
+    float* qs = reinterpret_cast<float*>(codes + (size_t)G8 * V);
+    for (int g = warp; g < G8; g += kScoreThreads / 32) {
+        constexpr int E = H / 32;  // elements of a lane
+        float x[E], a = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            x[e] = 0.f;
+            if (g < p.G) {
+                const uint16_t* src = static_cast<const uint16_t*>(p.q) +
+                                      ((size_t)b * p.N + (size_t)k * p.G + g) * H + lane * E;
+                const uint32_t w = (uint32_t)finite2<BF16>(src[e]);
+                x[e] = Elt<BF16>::lo(w);
+            }
+            a = fmaxf(a, fabsf(x[e]));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(kFull, a, o));
+        const float t = __fdiv_rn(a, 127.f);
+        int8_t* row = reinterpret_cast<int8_t*>(codes + (size_t)g * V);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int code = t > 0.f ? __float2int_rn(fminf(fmaxf(__fdiv_rn(x[e], t), -127.f), 127.f)) : 0;
+            row[lane * E + e] = (int8_t)max(code, 0);
+            row[H + lane * E + e] = (int8_t)min(code, 0);
+        }
+        if (lane == 0) qs[g] = t;
+    }
+    __syncthreads();
+    const int32_t* table = p.block_tables + (size_t)b * p.max_blocks;
+    float* out = p.scores + (size_t)bk * p.max_blocks;
+    const int tiles = (nb + 15) / 16, g = lane >> 2, t = lane & 3;
+    for (int tile = part * (kScoreThreads / 32) + warp; tile < tiles;
+         tile += p.splits * (kScoreThreads / 32)) {
+        const int i = tile * 16 + (lane & 15);
+        int id = i < nb ? __ldg(table + i) : 0;
+        const bool bad = id < 0 || id >= p.num_blocks;
+        if (bad) id = 0;
+        if (bad && k == 0 && lane < 16) report(p.status, GQA_ERR_BLOCK_ID);
+        const unsigned bads = __ballot_sync(kFull, bad);
+        const int ida = __shfl_sync(kFull, id, g), idb = __shfl_sync(kFull, id, g + 8);
+        const uint4* ra = reinterpret_cast<const uint4*>(p.bounds) + ((size_t)ida * p.K + k) * V;
+        const uint4* rb = reinterpret_cast<const uint4*>(p.bounds) + ((size_t)idb * p.K + k) * V;
+        uint4 wa[V / 4], wb[V / 4];
+#pragma unroll
+        for (int x = 0; x < V / 4; ++x) {
+            wa[x] = __ldg(ra + 4 * x + t);
+            wb[x] = __ldg(rb + 4 * x + t);
+        }
+        const float sa = __ldg(p.scale + (size_t)ida * p.K + k);
+        const float sb = __ldg(p.scale + (size_t)idb * p.K + k);
+        float va = -INFINITY, vb = -INFINITY;
+        for (int n0 = 0; n0 < G8; n0 += 8) {
+            int d[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int x = 0; x < V / 4; ++x) {
+                const uint4 w = codes[(size_t)(n0 + g) * V + 4 * x + t];
+                mma_s8(d, wa[x].x, wb[x].x, wa[x].y, wb[x].y, w.x, w.y);
+                mma_s8(d, wa[x].z, wb[x].z, wa[x].w, wb[x].w, w.z, w.w);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int n = n0 + 2 * t + e;
+                if (n < p.G) {  // (a product past fp32's range counts as its largest number)
+                    const float u = qs[n];
+                    va = fmaxf(va, __fmul_rn(fminf(__fmul_rn(u, sa), kMaxFinite), (float)d[e]));
+                    vb = fmaxf(vb, __fmul_rn(fminf(__fmul_rn(u, sb), kMaxFinite), (float)d[2 + e]));
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            va = fmaxf(va, __shfl_xor_sync(kFull, va, o));
+            vb = fmaxf(vb, __shfl_xor_sync(kFull, vb, o));
+        }
+        if (t == 0) {
+            const int ia = tile * 16 + g;
+            if (ia < nb) out[ia] = bads >> g & 1 ? -INFINITY : va;
+            if (ia + 8 < nb) out[ia + 8] = bads >> (g + 8) & 1 ? -INFINITY : vb;
+        }
+    }
+}
+
+// ---- the choice --------------------------------------------------------------------
+constexpr int kPickThreads = 512;
+constexpr int kPickHeld = 11520;  // scores held in shared memory; more are read again
+
+// Order-preserving bits of a score (-0 as 0; a NaN, which a scale that holds one gives,
+// below every number).
+__device__ __forceinline__ uint32_t score_key(float x) {
+    if (x != x) return 0u;
+    const uint32_t u = __float_as_uint(x + 0.f);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// A CTA per sequence and KV head: the key of the last block to take by four passes over
+// eight bits each (a histogram of the candidates that share the bits found so far), then
+// the blocks above it and as many of those at it as are left, in order.
+__global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectParams p) {
+    __shared__ int hist[256];
+    __shared__ int sums[2][kPickThreads / 32];
+    __shared__ uint32_t s_prefix;
+    __shared__ int s_left;
+    extern __shared__ uint32_t keys[];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int bk = blockIdx.x, b = bk / p.K, k = bk - b * p.K, tid = threadIdx.x;
+    const int lane = tid & 31, warp = tid >> 5;
+    const int ctx = __ldg(p.context_lens + b), nb = blocks_of(p, ctx);
+    const int32_t* table = p.block_tables + (size_t)b * p.max_blocks;
+    int32_t* tables = p.tables + (size_t)bk * p.keep;
+    int32_t* blocks = p.blocks + (size_t)bk * p.keep;
+    const int held = min(nb, p.keep);
+    if (k == 0 && tid == 0) {
+        p.lens[b] = nb ? (held - 1) * 16 + ctx - (nb - 1) * 16 : 0;
+        if (nb == 0) report(p.status, GQA_ERR_CONTEXT);
+    }
+    for (int i = held + tid; i < p.keep; i += kPickThreads) tables[i] = blocks[i] = -1;
+    if (nb <= p.keep) {
+        for (int i = tid; i < nb; i += kPickThreads) {
+            tables[i] = __ldg(table + i);
+            blocks[i] = i;
+        }
+        return;
+    }
+    // blocks [lo, hi) compete for `left` places
+    const int lo = p.first, hi = nb - p.recent, count = hi - lo;
+    int left = p.keep - p.first - p.recent;
+    for (int i = tid; i < p.first + p.recent; i += kPickThreads) {
+        const int at = i < p.first ? i : hi + i - p.first;
+        const int to = i < p.first ? i : p.keep - p.recent + i - p.first;
+        tables[to] = __ldg(table + at);
+        blocks[to] = at;
+    }
+    if (left == 0) return;
+    const float* scores = p.scores + (size_t)bk * p.max_blocks + lo;
+    const bool in_smem = count <= kPickHeld;
+    if (in_smem)
+        for (int i = tid; i < count; i += kPickThreads) keys[i] = score_key(__ldcg(scores + i));
+    auto key = [&](int i) { return in_smem ? keys[i] : score_key(__ldcg(scores + i)); };
+    uint32_t prefix = 0;
+    for (int shift = 24; shift >= 0; shift -= 8) {
+        if (tid < 256) hist[tid] = 0;
+        __syncthreads();
+        const uint32_t known = shift == 24 ? 0u : ~0u << (shift + 8);
+        for (int i = tid; i < count; i += kPickThreads) {
+            const uint32_t u = key(i);
+            if ((u & known) == prefix) atomicAdd(&hist[u >> shift & 255u], 1);
+        }
+        __syncthreads();
+        if (warp == 0) {  // bin of the left-th largest: lane l has bins 255 - 8 l ..
+            int n[8], own = 0;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) own += n[x] = hist[255 - 8 * lane - x];
+            int incl = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(kFull, incl, o);
+                if (lane >= o) incl += y;
+            }
+            if (incl - own < left && left <= incl) {
+                int above = incl - own, x = 0;
+                while (above + n[x] < left) above += n[x++];
+                s_prefix = prefix | (uint32_t)(255 - 8 * lane - x) << shift;
+                s_left = left - above;
+            }
+        }
+        __syncthreads();
+        prefix = s_prefix;
+        left = s_left;
+    }
+    // a run of blocks per thread: how many lie above the key and at it, before it too
+    const int run = (count + kPickThreads - 1) / kPickThreads;
+    const int from = min(count, tid * run), to = min(count, from + run);
+    int above = 0, equal = 0;
+    for (int i = from; i < to; ++i) {
+        const uint32_t u = key(i);
+        above += u > prefix;
+        equal += u == prefix;
+    }
+    int ia = above, ie = equal;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(kFull, ia, o), y = __shfl_up_sync(kFull, ie, o);
+        if (lane >= o) {
+            ia += x;
+            ie += y;
+        }
+    }
+    if (lane == 31) {
+        sums[0][warp] = ia;
+        sums[1][warp] = ie;
+    }
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) {
+        ia += sums[0][w];
+        ie += sums[1][w];
+    }
+    int a = ia - above, e = ie - equal;
+    for (int i = from; i < to; ++i) {
+        const uint32_t u = key(i);
+        const bool take = u > prefix || (u == prefix && e < left);
+        if (take) {
+            const int at = p.first + a + min(e, left);
+            tables[at] = __ldg(table + lo + i);
+            blocks[at] = lo + i;
+        }
+        a += u > prefix;
+        e += u == prefix;
+    }
+}
+
+}  // namespace
+
+gqa_status launch_block_bounds(const gqa_shape& s, const void* k_cache,
+                               const int32_t* block_tables, const int32_t* context_lens,
+                               const int32_t* cu_new, int8_t* bounds, float* bounds_scale,
+                               int32_t* dev_status, cudaStream_t stream) {
+    const int sms = device_sm_count();
+    if (sms <= 0) return GQA_ERR_CUDA;
+    BoundParams p = {static_cast<const uint4*>(k_cache), block_tables, context_lens, cu_new,
+                     bounds, bounds_scale, dev_status, s.B, s.K, s.max_blocks_per_seq,
+                     s.num_blocks};
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kBoundThreads);
+    cfg.gridDim = dim3((unsigned)(sms * 4));
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = (s.flags & (GQA_FLAG_PDL | GQA_FLAG_EARLY_KV)) ? 1 : 0;
+    return launch_status(
+        s.dtype == GQA_BF16
+            ? (s.H == 64 ? cudaLaunchKernelEx(&cfg, block_bounds_kernel<true, 64>, p)
+                         : cudaLaunchKernelEx(&cfg, block_bounds_kernel<true, 128>, p))
+            : (s.H == 64 ? cudaLaunchKernelEx(&cfg, block_bounds_kernel<false, 64>, p)
+                         : cudaLaunchKernelEx(&cfg, block_bounds_kernel<false, 128>, p)));
+}
+
+size_t select_workspace_bytes(const gqa_shape& s) {
+    return (size_t)s.B * s.K * s.max_blocks_per_seq * sizeof(float);
+}
+
+gqa_status launch_select_blocks(const gqa_shape& s, int keep, int first, int recent,
+                                const void* q, const int8_t* bounds, const float* bounds_scale,
+                                const int32_t* block_tables, const int32_t* context_lens,
+                                int32_t* tables, int32_t* lens, int32_t* blocks, void* workspace,
+                                int32_t* dev_status, cudaStream_t stream) {
+    const int sms = device_sm_count();
+    if (sms <= 0) return GQA_ERR_CUDA;
+    SelectParams p = {q, bounds, bounds_scale, block_tables, context_lens, tables, lens, blocks,
+                      static_cast<float*>(workspace), dev_status, s.B, s.N, s.K, s.N / s.K,
+                      s.max_blocks_per_seq, s.num_blocks, keep, first, recent, 1};
+    const long long bk = (long long)s.B * s.K;
+    const long long tiles = (s.max_blocks_per_seq + 15) / 16;
+    long long splits = (sms * 16 + bk - 1) / bk;
+    const long long most = (tiles + kScoreThreads / 32 - 1) / (kScoreThreads / 32);
+    if (splits > most) splits = most;
+    p.splits = (int)splits;
+    const size_t smem = (size_t)(p.G + 7) / 8 * 8 * (2 * s.H + sizeof(float));
+    if (smem > 48 * 1024 || bk * splits > (1ll << 31) - 1) return GQA_ERR_SHAPE;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cudaError_t e = cudaSuccess;
+    if (s.max_blocks_per_seq > keep) {
+        cfg.numAttrs = (s.flags & (GQA_FLAG_PDL | GQA_FLAG_EARLY_KV)) ? 1 : 0;
+        cfg.gridDim = dim3((unsigned)(bk * splits));
+        cfg.blockDim = dim3(kScoreThreads);
+        cfg.dynamicSmemBytes = smem;
+        e = s.dtype == GQA_BF16
+                ? (s.H == 64 ? cudaLaunchKernelEx(&cfg, block_score_kernel<true, 64>, p)
+                             : cudaLaunchKernelEx(&cfg, block_score_kernel<true, 128>, p))
+                : (s.H == 64 ? cudaLaunchKernelEx(&cfg, block_score_kernel<false, 64>, p)
+                             : cudaLaunchKernelEx(&cfg, block_score_kernel<false, 128>, p));
+        if (e != cudaSuccess) return launch_status(e);
+        cfg.numAttrs = 1;  // it waits for the scores itself
+    } else {
+        cfg.numAttrs = (s.flags & (GQA_FLAG_PDL | GQA_FLAG_EARLY_KV)) ? 1 : 0;
+    }
+    cfg.gridDim = dim3((unsigned)bk);
+    cfg.blockDim = dim3(kPickThreads);
+    // (static and dynamic together within what needs no opt-in)
+    cfg.dynamicSmemBytes =
+        sizeof(uint32_t) * (size_t)(s.max_blocks_per_seq < kPickHeld ? s.max_blocks_per_seq
+                                                                           : kPickHeld);
+    return launch_status(cudaLaunchKernelEx(&cfg, block_pick_kernel, p));
+}
+
+}  // namespace gqa

@@ -4,6 +4,8 @@
 //   kv_append_slots    packed rows [M][K][H] of any number of requests into a
 //                      cache of any kind, by a slot per row (block * 16 + row)
 //   kv_gather_slots    the way back: rows [M][K][H] in the dtype of the shape
+//   kv_append_rotary   kv_append_slots of keys rotated by position on the way, and
+//                      the queries rotated with them
 //
 // CS336 lecture 10 §"PagedAttention" (fixed-size blocks; a token's place is its
 // block and its row); the quantization is that of kv_quant.cu (one byte) and
@@ -313,6 +315,199 @@ __global__ void __launch_bounds__(kSlotThreads) kv_take_kernel(const SlotParams 
     }
 }
 
+// ---- rotation by position ------------------------------------------------------------
+// The first R of a row's H elements turn in pairs (x1, x2), elements (i, i + R/2), or
+// (2i, 2i + 1) interleaved, by the angle of the token's position, whose cosine c and
+// sine s a table [positions][R] holds (cosines, then sines, fp32; a caller makes it in as
+// many bits as far positions need):
+//     x1' = x1 c - x2 s,  x2' = x2 c + x1 s
+// Each product and the sum are rounded in fp32 one by one (no fma: the result does not
+// depend on how a compiler joins them), then to the 16-bit type; what is stored is then
+// what kv_append_slots stores of that row.  A thread makes 8 elements and reads their
+// partners itself (the same 128-byte lines, by a lane of the same warp: no second trip to
+// memory, and q may be rotated in place, since a warp reads all it needs before it
+// writes).  Bound by moving q, k and v once each way.
+struct RotaryParams {
+    const uint4* q;
+    uint4* q_out;
+    const float* table;
+    const int32_t* positions;
+    long long q_stride, k_stride, v_stride;  // of rows, in 16-byte pieces
+    uint32_t N, hg;                          // query heads, groups of kHeads of them
+    uint32_t hmul, hshift;                   // i / hg, as kmul
+    uint32_t q_items;                        // threads of the queries' part, whole warps
+    int far, R;                              // positions in the table; elements that turn
+};
+constexpr int kHeads = 4;  // query heads that share a thread's cosines and sines
+
+// Table row of row i, or -1.
+__device__ __forceinline__ int position_of(const SlotParams& p, const RotaryParams& r, uint32_t i,
+                                           bool reporter) {
+    const int at = __ldg(r.positions + i);
+    if (at >= 0 && at < r.far) return at;
+    if (at != -1 && reporter) report(p.status, GQA_ERR_CONTEXT);
+    return -1;
+}
+
+// Cosines and sines of the eight elements of part c (interleaved: of their four pairs).
+template <bool PAIRS>
+struct Angles {
+    float c[PAIRS ? 4 : 8], s[PAIRS ? 4 : 8];
+    __device__ __forceinline__ void load(const RotaryParams& r, int at, int part) {
+        const int half = r.R / 2;
+        const int e = PAIRS ? 4 * part : 8 * part < half ? 8 * part : 8 * part - half;
+        const float4* t = reinterpret_cast<const float4*>(r.table + (size_t)at * r.R + e);
+        const float4* u = reinterpret_cast<const float4*>(r.table + (size_t)at * r.R + half + e);
+#pragma unroll
+        for (int i = 0; i < (PAIRS ? 1 : 2); ++i) {
+            const float4 a = __ldg(t + i), b = __ldg(u + i);
+            c[4 * i] = a.x;
+            c[4 * i + 1] = a.y;
+            c[4 * i + 2] = a.z;
+            c[4 * i + 3] = a.w;
+            s[4 * i] = b.x;
+            s[4 * i + 1] = b.y;
+            s[4 * i + 2] = b.z;
+            s[4 * i + 3] = b.w;
+        }
+    }
+};
+// Part of the row that holds the partners of part c.
+__device__ __forceinline__ int partner(const RotaryParams& r, int c) {
+    const int h = r.R / 16;
+    return c < h ? c + h : c - h;
+}
+template <bool BF16, bool PAIRS>
+__device__ __forceinline__ uint4 turn(const RotaryParams& r, const Angles<PAIRS>& a, int part,
+                                      uint4 own, uint4 other) {
+    float x[8], y[8], z[8];
+    widen8<BF16>(own, x);
+    if constexpr (PAIRS) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            z[2 * i] = __fsub_rn(__fmul_rn(x[2 * i], a.c[i]), __fmul_rn(x[2 * i + 1], a.s[i]));
+            z[2 * i + 1] = __fadd_rn(__fmul_rn(x[2 * i + 1], a.c[i]), __fmul_rn(x[2 * i], a.s[i]));
+        }
+    } else {
+        widen8<BF16>(other, y);
+        const bool first = 16 * part < r.R;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float u = __fmul_rn(x[i], a.c[i]), v = __fmul_rn(y[i], a.s[i]);
+            z[i] = first ? __fsub_rn(u, v) : __fadd_rn(u, v);
+        }
+    }
+    return make_uint4(Elt<BF16>::pack(z[0], z[1]), Elt<BF16>::pack(z[2], z[3]),
+                      Elt<BF16>::pack(z[4], z[5]), Elt<BF16>::pack(z[6], z[7]));
+}
+
+// Threads 0 .. q_items - 1: kHeads query heads of a row and part; then keys and values as
+// in kv_put_kernel.
+template <bool BF16, int KIND, int H, bool PAIRS>
+__global__ void __launch_bounds__(kSlotThreads)
+    kv_put_rotary_kernel(const SlotParams p, const RotaryParams r) {
+    constexpr int V = kPieces<KIND>, P = H / 8;
+    griddep_launch_dependents();
+    griddep_wait();
+    const uint32_t q_work = p.rows * r.hg * P;
+    const uint32_t items = r.q_items + p.rows * p.K * (P / V), stride = gridDim.x * kSlotThreads;
+    for (uint32_t it = blockIdx.x * kSlotThreads + threadIdx.x; it - (threadIdx.x & 31) < items;
+         it += stride) {
+        if (it < r.q_items) {  // (whole warps)
+            const bool on = it < q_work;
+            const uint32_t j = on ? it : q_work - 1, rk = j / P, c = j % P;
+            const uint32_t row = (__umulhi(rk, r.hmul) + rk) >> r.hshift, g = rk - row * r.hg;
+            const int at = on ? position_of(p, r, row, c == 0 && g == 0) : -1;
+            uint4 own[kHeads], other[kHeads];
+            const bool turns = (int)(8 * c) < r.R;
+            const uint4* src = r.q + (size_t)row * r.q_stride;
+            const int pc = turns && !PAIRS ? partner(r, (int)c) : (int)c;
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h) {
+                const uint32_t n = g * kHeads + h;
+                if (at >= 0 && n < r.N) {
+                    own[h] = src[n * P + c];
+                    if (!PAIRS) other[h] = src[n * P + pc];
+                }
+            }
+            __syncwarp();  // a row's parts are read before any is written (in place)
+            if (at < 0) continue;
+            Angles<PAIRS> a;
+            if (turns) a.load(r, at, (int)c);
+            uint4* dst = r.q_out + (size_t)row * r.N * P;
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h) {
+                const uint32_t n = g * kHeads + h;
+                if (n < r.N)
+                    dst[n * P + c] = turns ? turn<BF16, PAIRS>(r, a, (int)c, own[h], other[h])
+                                           : own[h];
+            }
+            continue;
+        }
+        const uint32_t j = it - r.q_items;
+        const bool on = it < items;
+        uint32_t i, k, c;
+        item_of<H / V>(p, on ? j : p.rows * p.K * (P / V) - 1, &i, &k, &c);
+        const int at = on ? position_of(p, r, i, false) : -1;
+        const int s = at >= 0 ? slot_of(p, i, c == 0 && k == 0) : -1;
+        const uint4* ks = p.k_new + (size_t)i * r.k_stride + k * P;
+        const uint4* vs = p.v_new + (size_t)i * r.v_stride + k * P;
+        uint4 kw[V], vw[V];
+#pragma unroll
+        for (int x = 0; x < V; ++x) {
+            const int part = (int)c * V + x;
+            kw[x] = vw[x] = make_uint4(0, 0, 0, 0);
+            if (s < 0) continue;
+            kw[x] = __ldg(ks + part);
+            vw[x] = __ldg(vs + part);
+            if (8 * part < r.R) {
+                Angles<PAIRS> a;
+                a.load(r, at, part);
+                const uint4 other = PAIRS ? kw[x] : __ldg(ks + partner(r, part));
+                kw[x] = turn<BF16, PAIRS>(r, a, part, kw[x], other);
+            }
+        }
+        put<BF16, KIND, H>(p, p.k_cache, p.k_scale, s, k, c, kw);
+        put<BF16, KIND, H>(p, p.v_cache, p.v_scale, s, k, c, vw);
+    }
+}
+
+template <bool BF16, int H, bool PAIRS>
+const void* rotary_kernel(int kind) {
+    switch (kind) {
+        case GQA_KV_SAME:
+            return reinterpret_cast<const void*>(
+                &kv_put_rotary_kernel<BF16, GQA_KV_SAME, H, PAIRS>);
+        case GQA_KV_INT8:
+            return reinterpret_cast<const void*>(
+                &kv_put_rotary_kernel<BF16, GQA_KV_INT8, H, PAIRS>);
+        case GQA_KV_E4M3:
+            return reinterpret_cast<const void*>(
+                &kv_put_rotary_kernel<BF16, GQA_KV_E4M3, H, PAIRS>);
+        default:
+            return reinterpret_cast<const void*>(&kv_put_rotary_kernel<BF16, kKvFourbit, H, PAIRS>);
+    }
+}
+const void* pick_rotary_kernel(const gqa_shape& s, bool pairs) {
+    const bool bf16 = s.dtype == GQA_BF16;
+    if (s.H == 128)
+        return bf16 ? (pairs ? rotary_kernel<true, 128, true>(s.kv_dtype)
+                             : rotary_kernel<true, 128, false>(s.kv_dtype))
+                    : (pairs ? rotary_kernel<false, 128, true>(s.kv_dtype)
+                             : rotary_kernel<false, 128, false>(s.kv_dtype));
+    return bf16 ? (pairs ? rotary_kernel<true, 64, true>(s.kv_dtype)
+                         : rotary_kernel<true, 64, false>(s.kv_dtype))
+                : (pairs ? rotary_kernel<false, 64, true>(s.kv_dtype)
+                         : rotary_kernel<false, 64, false>(s.kv_dtype));
+}
+
+// i / d = (umulhi(i, mul) + i) >> shift for i < 2^31
+void divisor(uint32_t d, uint32_t* mul, uint32_t* shift) {
+    *shift = 0;
+    while ((1ull << *shift) < d) ++*shift;
+    *mul = (uint32_t)(((1ull << 32) * ((1ull << *shift) - d)) / d + 1);
+}
+
 template <bool PUT, bool BF16, int KIND, int H>
 const void* slot_kernel() {
     return PUT ? reinterpret_cast<const void*>(&kv_put_kernel<BF16, KIND, H>)
@@ -348,8 +543,7 @@ gqa_status launch_slots(const gqa_shape& s, const void* kernel, SlotParams p, lo
     p.K = (uint32_t)s.K;
     p.max_blocks = s.max_blocks_per_seq;
     p.num_blocks = s.num_blocks;
-    while ((1ll << p.kshift) < s.K) ++p.kshift;
-    p.kmul = (uint32_t)(((1ull << 32) * ((1ull << p.kshift) - (uint64_t)s.K)) / (uint64_t)s.K + 1);
+    divisor((uint32_t)s.K, &p.kmul, &p.kshift);
     if (per_row >= (1ll << 31)) return GQA_ERR_SHAPE;
     long long most = ((1ll << 31) - 1) / per_row;
     if (!p.slots) most = most / s.T * s.T;  // whole sequences
@@ -423,6 +617,77 @@ gqa_status launch_kv_gather_slots(const gqa_shape& s, long long rows, const void
     p.slots = slots;
     p.status = dev_status;
     return launch_slots(s, pick_slot_kernel<false>(s), p, rows, stream);
+}
+
+gqa_status launch_kv_append_rotary(const gqa_shape& s, long long rows, const void* q,
+                                   const void* k_new, const void* v_new, long long q_stride,
+                                   long long k_stride, long long v_stride, void* k_cache,
+                                   void* v_cache, void* k_scale, void* v_scale,
+                                   const int32_t* slots, const int32_t* positions,
+                                   const float* table, int table_rows, int rotary_dims,
+                                   bool interleaved, void* q_out, int32_t* dev_status,
+                                   cudaStream_t stream) {
+    if (rows == 0) return GQA_OK;
+    SlotParams p = {};
+    p.k_new = static_cast<const uint4*>(k_new);
+    p.v_new = static_cast<const uint4*>(v_new);
+    p.k_cache = static_cast<uint8_t*>(k_cache);
+    p.v_cache = static_cast<uint8_t*>(v_cache);
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.slots = slots;
+    p.status = dev_status;
+    p.K = (uint32_t)s.K;
+    p.num_blocks = s.num_blocks;
+    divisor(p.K, &p.kmul, &p.kshift);
+    RotaryParams r = {};
+    r.q = static_cast<const uint4*>(q);
+    r.q_out = static_cast<uint4*>(q_out);
+    r.table = table;
+    r.positions = positions;
+    r.q_stride = q_stride / 8;
+    r.k_stride = k_stride / 8;
+    r.v_stride = v_stride / 8;
+    r.N = (uint32_t)s.N;
+    r.hg = (r.N + kHeads - 1) / kHeads;
+    divisor(r.hg, &r.hmul, &r.hshift);
+    r.far = table_rows;
+    r.R = rotary_dims;
+    const int sms = device_sm_count();
+    if (sms <= 0) return GQA_ERR_CUDA;
+    const int V = s.kv_dtype == GQA_KV_INT4 ? 2 : 1;
+    const long long q_row = (long long)r.hg * (s.H / 8), k_row = (long long)s.K * (s.H / 8 / V);
+    const long long per_row = q_row + k_row;
+    if (per_row >= (1ll << 30)) return GQA_ERR_SHAPE;
+    const long long most = ((1ll << 31) - 64) / per_row;  // fewer than 2^31 threads a launch
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kSlotThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = (s.flags & (GQA_FLAG_PDL | GQA_FLAG_EARLY_KV)) ? 1 : 0;
+    const void* kernel = pick_rotary_kernel(s, interleaved);
+    while (rows > 0) {
+        const long long n = rows < most ? rows : most;
+        const long long q_items = (n * q_row + 31) / 32 * 32, items = q_items + n * k_row;
+        const long long need = (items + kSlotThreads - 1) / kSlotThreads, cap = (long long)sms * 32;
+        p.rows = (uint32_t)n;
+        r.q_items = (uint32_t)q_items;
+        cfg.gridDim = dim3((unsigned)(need < cap ? need : cap));
+        void* args[] = {&p, &r};
+        const gqa_status st = launch_status(cudaLaunchKernelExC(&cfg, kernel, args));
+        if (st != GQA_OK) return st;
+        rows -= n;
+        r.q += n * r.q_stride;
+        r.q_out += n * s.N * (s.H / 8);
+        p.k_new += n * r.k_stride;
+        p.v_new += n * r.v_stride;
+        p.slots += n;
+        r.positions += n;
+    }
+    return GQA_OK;
 }
 
 }  // namespace gqa

@@ -87,6 +87,11 @@ bool make_cache_map(CUtensorMap* m, const void* base, const gqa_shape& s);
 // Elements outside the tensor read as zero and are not written.
 bool make_rows_map(CUtensorMap* m, const void* base, const gqa_shape& s, int hpc, int tpc);
 
+// A TMA view of a tensor of 16-bit elements, 128-byte swizzled (rank <= 5; strides in bytes,
+// of every dimension but the first).
+bool make_tensor_map(CUtensorMap* m, gqa_dtype dtype, int rank, const void* base,
+                     const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box);
+
 // The direct warp-level kernel (one CTA per (sequence, KV head)): which
 // shapes it can serve, and which it serves by default.  Host logic only.
 bool direct_attention_supported(const gqa_shape& s, bool masked);
@@ -126,6 +131,30 @@ gqa_status launch_kv_gather_slots(const gqa_shape& s, long long rows, const void
                                   const int32_t* slots, void* k_out, void* v_out,
                                   int32_t* dev_status, cudaStream_t stream);
 
+// kv_append_slots of keys rotated by position, and the queries rotated with them (see
+// gqa_kv_append_rotary); strides of rows in elements.
+gqa_status launch_kv_append_rotary(const gqa_shape& s, long long rows, const void* q,
+                                   const void* k_new, const void* v_new, long long q_stride,
+                                   long long k_stride, long long v_stride, void* k_cache,
+                                   void* v_cache, void* k_scale, void* v_scale,
+                                   const int32_t* slots, const int32_t* positions,
+                                   const float* table, int table_rows, int rotary_dims,
+                                   bool interleaved, void* q_out, int32_t* dev_status,
+                                   cudaStream_t stream);
+
+// 8-bit bounds of the blocks that hold new tokens, and the blocks that a query should
+// read by them (see gqa_kv_block_bounds and gqa_select_blocks).
+gqa_status launch_block_bounds(const gqa_shape& s, const void* k_cache,
+                               const int32_t* block_tables, const int32_t* context_lens,
+                               const int32_t* cu_new, int8_t* bounds, float* bounds_scale,
+                               int32_t* dev_status, cudaStream_t stream);
+size_t select_workspace_bytes(const gqa_shape& s);
+gqa_status launch_select_blocks(const gqa_shape& s, int keep, int first, int recent,
+                                const void* q, const int8_t* bounds, const float* bounds_scale,
+                                const int32_t* block_tables, const int32_t* context_lens,
+                                int32_t* tables, int32_t* lens, int32_t* blocks, void* workspace,
+                                int32_t* dev_status, cudaStream_t stream);
+
 // Block tables, slots and lengths of a step (see gqa_plan_blocks).
 gqa_status launch_plan_blocks(int B, int max_blocks, int num_blocks, int tokens,
                               const int32_t* context_lens, const int32_t* new_lens,
@@ -135,6 +164,18 @@ gqa_status launch_plan_blocks(int B, int max_blocks, int num_blocks, int tokens,
                               int32_t* slots, int32_t* positions, bool pdl, int32_t* dev_status,
                               cudaStream_t stream);
 
+// Attention of ragged chunks of new tokens (see gqa_chunk_attention): q rows `q_stride`
+// elements apart; cu_new == nullptr: one row per sequence; head_tables: block tables
+// [B][K][max_blocks], one per KV head.  The workspace is flags_bytes of zeroed tickets and
+// then partial results, as for the other attention kernels (0 bytes: no GPU).
+size_t chunk_workspace_bytes(const gqa_shape& s, size_t flags_bytes);
+gqa_status launch_chunk_attention(const gqa_shape& s, long long rows, long long q_stride,
+                                  const void* q, const void* k_cache, const void* v_cache,
+                                  const int32_t* block_tables, bool head_tables,
+                                  const int32_t* context_lens, const int32_t* cu_new, void* out,
+                                  void* workspace, size_t flags_bytes, int32_t* dev_status,
+                                  cudaStream_t stream);
+
 // What a call returns for its launch's result, which alone decides: the runtime keeps
 // the error of a refused call until it is asked for, so the last error may be an earlier
 // call's.  This one's is taken back.
@@ -143,6 +184,9 @@ inline gqa_status launch_status(cudaError_t e) {
     cudaGetLastError();
     return GQA_ERR_CUDA;
 }
+
+// Bytes of the ticket region at the start of every attention workspace.
+size_t workspace_flags_bytes();
 
 // Cached per-device SM count (0 on failure).
 int device_sm_count();

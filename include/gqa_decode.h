@@ -23,6 +23,12 @@
  *                        into and out of a cache of any kind, by slot
  *   gqa_plan_blocks      block tables, slot maps and lengths of a step from the
  *                        requests' lengths
+ *   gqa_kv_append_rotary queries and keys rotated by position, the keys and values
+ *                        into a cache of any kind, by slot
+ *   gqa_chunk_attention  attention of the new tokens of requests of any lengths
+ *                        (prompts, parts of prompts, single tokens) over the cache
+ *   gqa_kv_block_bounds, gqa_select_blocks, gqa_sparse_decode_attention  decoding
+ *                        that reads only the blocks that a query may weigh most
  *
  * Sources (web pages, cited by title and section):
  *   "CS336, лекции 10 и 12: инференс и оценка моделей" (CS336 lectures 10/12,
@@ -685,6 +691,127 @@ gqa_status gqa_plan_blocks(int B, int max_blocks_per_seq, int num_blocks, int ma
                            int32_t *ring_state_out, int32_t *cu_new, int32_t *slots,
                            int32_t *positions, unsigned int flags, int32_t *dev_status,
                            void *stream);
+
+/* Rotated append.  The calls above take q and k as attention uses them; where a model
+ * turns them by position, this call does it on the way into the cache.
+ *   rows       M >= 0 packed tokens, as in gqa_kv_append_slots
+ *   q [M][N][H], k_new, v_new [M][K][H] in dtype; the rows of each are q_stride,
+ *              k_stride, v_stride elements apart (at least a row, multiples of 8), so
+ *              that they may lie side by side in a projection's output
+ *   positions  int32 [M]: of token i, or -1: no token, nothing of the row is read or
+ *              written
+ *   cos_sin    fp32 [table_rows][rotary_dims]: of each position rotary_dims / 2
+ *              cosines, then as many sines (made by the caller, in as many bits as
+ *              far positions need).  rotary_dims = R: a multiple of 16, 16 .. H
+ *   interleaved  0: element i < R/2 turns with element i + R/2; else 2i with 2i + 1
+ *   q_out      [M][N][H], dense; may be q itself where q is dense
+ * For a pair (x1, x2) with cosine c and sine s: x1 c - x2 s and x2 c + x1 s, each
+ * product and the sum rounded in fp32, then to dtype; elements from R on stay as they
+ * are.  The cache then gets what gqa_kv_append_slots stores of the rounded rows (k
+ * turned, v not), bit for bit, at slots[i]; -1: q only.  shape: N, K, H, num_blocks,
+ * dtype, kv_dtype and the scales as there; the other fields only have to be valid.
+ * cos_sin, q, k_new, v_new, q_out and the caches 16-byte aligned; k_new, v_new, q
+ * (unless it is q_out) and the tables must not overlap what is written.
+ * Device errors: a position that is neither -1 nor in [0, table_rows) counts as -1
+ * (GQA_ERR_CONTEXT); slots as in gqa_kv_append_slots. */
+gqa_status gqa_kv_append_rotary(const gqa_shape *shape, int64_t rows, const void *q,
+                                const void *k_new, const void *v_new, int64_t q_stride,
+                                int64_t k_stride, int64_t v_stride, void *k_cache,
+                                void *v_cache, void *k_scale, void *v_scale,
+                                const int32_t *slots, const int32_t *positions,
+                                const float *cos_sin, int table_rows, int rotary_dims,
+                                int interleaved, void *q_out, int32_t *dev_status,
+                                void *stream);
+
+/* Attention of chunks of new tokens.  CS336 lecture 10 §"Арифметическая интенсивность
+ * инференса" (the prompt's tokens at once, bound by arithmetic; then a token at a time):
+ * prompts, parts of prompts behind a cached prefix and single tokens in one call.
+ *   rows         M >= 0 rows of q and out
+ *   q            [M][N][H], rows q_stride elements apart (at least N * H, a multiple of
+ *                8); out [M][N][H], dense
+ *   cu_new       int32 [B+1]: sequence b's n = cu_new[b+1] - cu_new[b] >= 0 new tokens
+ *                are rows cu_new[b] .. cu_new[b+1] - 1 (gqa_plan_blocks makes it)
+ *   context_lens int32 [B] tokens held INCLUDING the new ones, which sit at positions
+ *                context_lens[b] - n ..; their keys and values are in the cache already
+ *                (gqa_kv_append_slots, gqa_kv_append_rotary)
+ * Row i at position a sees positions 0 .. a, or with shape->window = W > 0 the last W of
+ * them; blocks wholly below the earliest token's window are never read.  Otherwise as
+ * gqa_verify_attention, for a cache in q's dtype: the softmax in fp32, probabilities
+ * rounded to dtype for the product with V, fp32 sums.  Rows outside every sequence's are
+ * neither read for a result nor written.  A NaN or infinity in V at a position that
+ * the token's own 128 neighbours see and the token does not may reach its output; those
+ * that no token of the call's sequence sees do not.
+ * Requires B <= 16384, N / K <= 8192, H in {64, 128}; shape->T is not used (1);
+ * GQA_FLAG_EARLY_KV acts as GQA_FLAG_PDL, the flags that force a kernel give
+ * GQA_ERR_SHAPE.  out must not overlap an input.  Workspace: at least
+ * gqa_chunk_workspace_size(shape) bytes, which depends on H alone; zero-filled
+ * before first use and left so, and it may be one that the other attention calls use.
+ * The context is split over thread blocks as there; the result does not depend on
+ * the schedule.
+ * Device errors: context_lens[b] < n or > 16 * max_blocks_per_seq: the sequence's rows
+ * are zeros (GQA_ERR_CONTEXT); cu_new[b] < 0, > cu_new[b+1] or cu_new[b+1] > M: the
+ * sequence is left out (GQA_ERR_CONTEXT); a block id in use out of range: zeros for
+ * the rows that would read it (GQA_ERR_BLOCK_ID). */
+size_t gqa_chunk_workspace_size(const gqa_shape *shape);
+gqa_status gqa_chunk_attention(const gqa_shape *shape, int64_t rows, const void *q,
+                               int64_t q_stride, const void *k_cache, const void *v_cache,
+                               const int32_t *block_tables, const int32_t *context_lens,
+                               const int32_t *cu_new, void *out, void *workspace,
+                               size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/* Decoding over chosen blocks.  Decoding is bound by reading the cache (the same
+ * section); a query whose weights lie on few blocks of a long context need read only
+ * those.  Three calls, for a cache in q's dtype:
+ *
+ * gqa_kv_block_bounds keeps, of every cache block and KV head, the largest and the
+ * smallest key of the rows held, element by element, in 8 bits:
+ *   bounds        int8 [num_blocks][K][2][H], 0: ceil(max_d / s), 1: floor(min_d / s),
+ *                 within [-127, 127] (0 where s is 0)
+ *   bounds_scale  fp32 [num_blocks][K]: s = max |k| / 127 (divisions in IEEE fp32); a
+ *                 NaN element counts as 0, an infinite one as dtype's largest number
+ * It makes anew those of the blocks that hold one of the newest cu_new[b+1] - cu_new[b]
+ * tokens of a sequence (cu_new: int32 [B+1]), so one call after every append keeps
+ * them all.  (Where acceptance has shortened a sequence they may still count rows that
+ * were dropped, until the next append to that block.)  Device errors: lengths as in
+ * gqa_chunk_attention, a bad block id: that sequence or block is left as it was.
+ *
+ * gqa_select_blocks chooses, for every sequence and KV head, `keep` of its blocks (all of
+ * them if it has no more): the `first` ones and the `recent` newest ones always, the
+ * others by score, equal scores by the lower block.  With c = rn(q / t), t = max |q| / 127
+ * of each of the head's G = N / K queries, a block's score is the largest over them of
+ *   (t * s) * sum_d max(c_d max_d, c_d min_d)
+ * (whole numbers; the two products rounded in fp32): a bound of what a key of the
+ * block can score.  (Of q too a NaN counts as 0, an infinity as the largest number.)
+ *   q            [B][1][N][H] in dtype; N / K <= 128
+ *   tables       int32 [B][K][keep]: the cache blocks chosen, in the sequence's order
+ *   blocks       int32 [B][K][keep]: which block of the sequence each is; both -1 past
+ *                the last one
+ *   lens         int32 [B]: the tokens that the chosen blocks hold
+ *   workspace    gqa_select_workspace_size(shape) bytes of scratch, not cleared
+ * Requires 1 <= recent, 0 <= first, first + recent <= keep, shape->T = 1, B <= 16384.
+ * Device errors: a length < 1 or too long gives lens 0 and -1 (GQA_ERR_CONTEXT); a bad
+ * block id scores lowest (GQA_ERR_BLOCK_ID) and shows in tables if it is chosen all
+ * the same.
+ *
+ * gqa_sparse_decode_attention is gqa_decode_attention with a block table per KV head:
+ * tables int32 [B][K][S] (S = shape->max_blocks_per_seq) and lens int32 [B] as chosen, the
+ * last block in part.  Requirements, workspace (gqa_chunk_workspace_size) and device
+ * errors as gqa_chunk_attention with one token per sequence; no window. */
+gqa_status gqa_kv_block_bounds(const gqa_shape *shape, const void *k_cache,
+                               const int32_t *block_tables, const int32_t *context_lens,
+                               const int32_t *cu_new, int8_t *bounds, float *bounds_scale,
+                               int32_t *dev_status, void *stream);
+size_t gqa_select_workspace_size(const gqa_shape *shape);
+gqa_status gqa_select_blocks(const gqa_shape *shape, int keep, int first, int recent,
+                             const void *q, const int8_t *bounds, const float *bounds_scale,
+                             const int32_t *block_tables, const int32_t *context_lens,
+                             int32_t *tables, int32_t *lens, int32_t *blocks, void *workspace,
+                             size_t workspace_bytes, int32_t *dev_status, void *stream);
+gqa_status gqa_sparse_decode_attention(const gqa_shape *shape, const void *q,
+                                       const void *k_cache, const void *v_cache,
+                                       const int32_t *tables, const int32_t *lens, void *out,
+                                       void *workspace, size_t workspace_bytes,
+                                       int32_t *dev_status, void *stream);
 
 #ifdef __cplusplus
 }

@@ -54,13 +54,18 @@ constexpr int kStep = 128;     // positions of a KV tile
 constexpr int kBlocks = kStep / 16;
 constexpr int kSoftWarp = 4;   // first softmax warp
 constexpr int kThreadsCh = 384;
+// Registers per thread: the softmax warps hold 128 scores each.  Together no more than the
+// launch's 384 x 168.
+constexpr int kRegsIssue = 88, kRegsSoft = 208;
+static_assert(128 * kRegsIssue + 256 * kRegsSoft <= kThreadsCh * 168, "register split");
 constexpr int kStart = 2;      // units of an item's start-up and end
-constexpr int kQuota = 4;      // units per CTA at least
+constexpr int kQuota = 6;      // units per CTA at least
+constexpr int kWhole = 4;      // KV tiles up to which an item is never split
 constexpr float kSlack = 8.f;  // log2 slack before O is rescaled
-constexpr int kSeqCache = 128;
+constexpr int kSeqCache = 64;
 constexpr int kBadRing = 8;    // items in flight at most (the ring holds 8 tiles)
 constexpr int kMaxSeqs = 16384;
-constexpr uint32_t kColS = 0, kColO = 256;  // tensor-memory columns, 128 per tile
+constexpr uint32_t kColS = 0, kColO = 256;  // tensor-memory columns, 128 per slot
 
 template <int H>
 struct Ch {
@@ -88,13 +93,13 @@ struct ChunkParams {
 
 struct ChunkSmem {
     uint64_t full[8], empty[8];
-    uint64_t q_full, q_free;
-    uint64_t s_ready[2], p_ready[2], o_ready[2], o_free[2], group[2];
-    uint64_t done;
+    // per slot (a row tile in the works: its Q, S, O and softmax warps)
+    uint64_t q_full[2], q_free[2], s_ready[2], p_ready[2], o_ready[2], o_free[2], group[2];
+    uint64_t done[2];
     long long c0, c1, base;  // range of units; first unit of the first item
     long long quota;
-    int b0, vh0, qi0;
-    uint32_t tmem;
+    int b0, vh0, qi0, whole;
+    uint32_t tmem, lock;
     volatile int abort_flag;
     volatile int bad[kBadRing];
     int ticket[2];
@@ -152,13 +157,16 @@ struct Piece {
     Seq s;
     int b, vh, f;  // first token
     int lo, hi, t0, t1;
+    int slot;         // of the first row tile (with two: 0, the other's is 1)
     long long first;  // unit of tile lo
+    __device__ __forceinline__ bool split() const { return t0 != lo || t1 != hi; }
 };
-// Tokens of row tile i, and its KV tiles within the piece.
+// Tokens [f, e) of the row tile in a slot, and its KV tiles [a, b) within the piece.
 struct Sub {
     int f, e, a, b;
 };
-__device__ __forceinline__ Sub sub_of(const ChunkParams& p, const Piece& pc, int i) {
+__device__ __forceinline__ Sub sub_of(const ChunkParams& p, const Piece& pc, int slot) {
+    const int i = slot ^ pc.slot;  // which row tile (a lone one's other slot: past the tokens)
     Sub x;
     x.f = pc.f + i * p.tpc;
     x.e = min(pc.s.n, x.f + p.tpc);
@@ -170,19 +178,21 @@ __device__ __forceinline__ Sub sub_of(const ChunkParams& p, const Piece& pc, int
     return x;
 }
 
-// The pieces of the CTA's range in order; every role walks the same.
+// The pieces of the CTA's range in order; every role walks the same.  Items of up to
+// `whole` KV tiles belong to the CTA in whose range they begin.  Lone row tiles take the
+// two slots in turn, so that one's end and the next one's start overlap.
 struct Walk {
-    long long pos, c1, base;
-    int b, vh, qi, nq;
+    long long pos, c0, c1, base;
+    int b, vh, qi, nq, turn;
     Seq s;
     __device__ void init(const ChunkSmem& sm, const ChunkParams& p) {
-        pos = sm.c0;
+        pos = c0 = sm.c0;
         c1 = sm.c1;
         base = sm.base;
         b = sm.b0;
         vh = sm.vh0;
         qi = sm.qi0;
-        nq = 0;
+        nq = turn = 0;
         if (pos < c1) {
             s = cached_seq(sm, p, b);
             nq = items_of(p, s);
@@ -200,7 +210,15 @@ struct Walk {
             const int lo = tile_lo(p, s, f), hi = tile_hi(s, min(s.n, f + 2 * p.tpc));
             const long long first = base + kStart, end = first + (hi - lo);
             if (pos < end) {
-                const long long from = max(pos, first), to = min(c1, end);
+                long long from = max(pos, first), to = min(c1, end);
+                if (hi - lo <= sm.whole) {
+                    if (base < c0) {  // another CTA's
+                        pos = end;
+                        continue;
+                    }
+                    from = first;
+                    to = end;
+                }
                 pos = to;
                 if (to <= from) break;  // only start-up units
                 pc.s = s;
@@ -212,6 +230,11 @@ struct Walk {
                 pc.first = first;
                 pc.t0 = lo + (int)(from - first);
                 pc.t1 = lo + (int)(to - first);
+                pc.slot = 0;
+                if (f + p.tpc >= s.n) {
+                    pc.slot = turn;
+                    turn ^= 1;
+                }
                 return true;
             }
             base = end;
@@ -239,6 +262,11 @@ __device__ __forceinline__ long long scan_ll(long long v, int lane) {
     }
     return v;
 }
+// a / b for a >= 0, b > 0 (32 bits where they do)
+__device__ __forceinline__ long long div_ll(long long a, long long b) {
+    if ((a | b) >> 32 == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
+}
 
 // Rows [r0, r0 + n) of the output become zeros (whole warp).
 template <int H>
@@ -248,91 +276,131 @@ __device__ void zero_rows(const ChunkParams& p, int r0, int n) {
     for (long long i = threadIdx.x & 31; i < count; i += 32) o[i] = make_uint4(0, 0, 0, 0);
 }
 
-// All threads: units of every sequence (in `cost`, shared memory), then this CTA's
-// range and the item it starts in.
+// Units of one virtual head of sequences first .. first + 31, a lane each (whole warp);
+// CTA 0 also reports and clears those out of range.
+template <int H>
+__device__ long long warp_units(const ChunkParams& p, int first, Seq& s) {
+    const int lane = threadIdx.x & 31, b = first + lane;
+    s = {0, 0, 0, 0};
+    if (b < p.B) s = read_seq(p, b);
+    const int nq = items_of(p, s);
+    long long c = 0;
+    if (nq <= 4)
+        for (int qi = 0; qi < nq; ++qi) c += item_units(p, s, qi);
+    unsigned many = __ballot_sync(kAll, nq > 4);
+    while (many) {
+        const int src = __ffs(many) - 1;
+        many &= many - 1;
+        Seq t;
+        t.n = __shfl_sync(kAll, s.n, src);
+        t.ctx = __shfl_sync(kAll, s.ctx, src);
+        const int m = __shfl_sync(kAll, nq, src);
+        long long x = 0;
+        for (int qi = lane; qi < m; qi += 32) x += item_units(p, t, qi);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kAll, x, o);
+        if (lane == src) c = x;
+    }
+    if (blockIdx.x == 0 && __any_sync(kAll, s.code != 0)) {
+        if (s.code) report(p.status, GQA_ERR_CONTEXT);
+        unsigned zero = __ballot_sync(kAll, s.code == 1);
+        while (zero) {
+            const int at = first + __ffs(zero) - 1;
+            zero &= zero - 1;
+            const int r0 = p.cu_new ? __ldg(p.cu_new + at) : at;
+            const int r1 = p.cu_new ? __ldg(p.cu_new + at + 1) : at + 1;
+            zero_rows<H>(p, r0, r1 - r0);
+        }
+    }
+    return c;
+}
+
+// Warps 0 .. 3: units of every sequence (`cost`, shared memory, where there are more than
+// a lane each), then warp 0: this CTA's range and the item it starts in.
 template <int H>
 __device__ void chunk_plan(const ChunkParams& p, ChunkSmem& sm, long long* cost) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int first = warp * 32; first < p.B; first += kThreadsCh) {
-        const int b = first + lane;
-        Seq s = {0, 0, 0, 0};
-        if (b < p.B) s = read_seq(p, b);
-        const int nq = items_of(p, s);
-        long long c = 0;
-        if (nq <= 8)
-            for (int qi = 0; qi < nq; ++qi) c += item_units(p, s, qi);
-        unsigned many = __ballot_sync(kAll, nq > 8);
-        while (many) {
-            const int src = __ffs(many) - 1;
-            many &= many - 1;
-            Seq t;
-            t.n = __shfl_sync(kAll, s.n, src);
-            t.ctx = __shfl_sync(kAll, s.ctx, src);
-            const int m = __shfl_sync(kAll, nq, src);
-            long long x = 0;
-            for (int qi = lane; qi < m; qi += 32) x += item_units(p, t, qi);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kAll, x, o);
-            if (lane == src) c = x;
-        }
-        if (b < p.B) cost[b] = c;
-        if (blockIdx.x == 0) {
-            if (s.code) report(p.status, GQA_ERR_CONTEXT);
-            unsigned zero = __ballot_sync(kAll, s.code == 1);
-            while (zero) {
-                const int src = __ffs(zero) - 1;
-                zero &= zero - 1;
-                const int at = first + src;
-                const int r0 = p.cu_new ? __ldg(p.cu_new + at) : at;
-                const int r1 = p.cu_new ? __ldg(p.cu_new + at + 1) : at + 1;
-                zero_rows<H>(p, r0, r1 - r0);
-            }
-        }
-    }
-    __syncthreads();
-    if (warp != 0) return;
-    const int per = (p.B + 31) / 32;
-    const int lo = min(p.B, lane * per), hi = min(p.B, lo + per);
+    const bool few = p.B <= 32;
+    Seq s;
     long long local = 0;
-    for (int b = lo; b < hi; ++b) local += cost[b];
+    int lo = lane, hi = min(p.B, lane + 1);  // this lane's sequences
+    if (few) {
+        if (warp != 0) return;
+        local = warp_units<H>(p, 0, s);
+    } else {
+        for (int first = warp * 32; first < p.B; first += kThreadsCh) {
+            const long long c = warp_units<H>(p, first, s);
+            if (first + lane < p.B) cost[first + lane] = c;
+        }
+        __syncthreads();
+        if (warp != 0) return;
+        const int per = (p.B + 31) / 32;
+        lo = min(p.B, lane * per);
+        hi = min(p.B, lo + per);
+        for (int b = lo; b < hi; ++b) local += cost[b];
+    }
     const long long incl = scan_ll(local, lane), excl = incl - local;
     const long long total = shfl_ll(incl, 31) * p.KC;
-    const long long quota = max((total + gridDim.x - 1) / gridDim.x, (long long)kQuota);
+    const long long quota =
+        max(div_ll(total + gridDim.x - 1, gridDim.x), (long long)kQuota);
     const long long c0 = blockIdx.x * quota, c1 = min(total, c0 + quota);
     const bool mine = c0 < c1 && excl * p.KC <= c0 && c0 < incl * p.KC;
     const unsigned owners = __ballot_sync(kAll, mine);
     int b0 = 0;
-    long long base = 0;
+    long long base = 0, one = 0;  // first unit of b0; units of a virtual head of it
     if (mine) {
         base = excl * p.KC;
         b0 = lo;
-        while (c0 >= base + cost[b0] * p.KC) base += cost[b0++] * p.KC;
+        one = local;
+        if (!few) {
+            while (c0 >= base + cost[b0] * p.KC) base += cost[b0++] * p.KC;
+            one = cost[b0];
+        }
     }
     const int owner = owners ? __ffs(owners) - 1 : 0;
     b0 = __shfl_sync(kAll, b0, owner);
     base = shfl_ll(base, owner);
+    one = shfl_ll(one, owner);
     if (lane == 0) {
         sm.c0 = c0;
         sm.c1 = max(c0, c1);
         sm.quota = quota;
+        sm.whole = (int)max((long long)kWhole, min(quota >> 4, (long long)1 << 20));
         sm.b0 = b0;
+        sm.base = 0;
+        sm.vh0 = sm.qi0 = 0;
+    }
+    __syncwarp();
+    // lengths of the sequences from b0 on
+    if (few && b0 == 0) {
+        if (lane < p.B) {
+            sm.rows[lane] = p.cu_new ? __ldg(p.cu_new + lane) : lane;
+            sm.ctxs[lane] = s.ctx;
+        }
+        if (lane == 0) sm.rows[p.B] = p.cu_new ? __ldg(p.cu_new + p.B) : p.B;
+    } else {
+        for (int i = lane; i <= kSeqCache; i += 32) {
+            const int b = min(b0 + i, p.B);
+            sm.rows[i] = p.cu_new ? __ldg(p.cu_new + b) : b;
+            if (i < kSeqCache) sm.ctxs[i] = b < p.B ? __ldg(p.context_lens + b) : 0;
+        }
     }
     if (owners) {
         // the virtual head, then the item in it (a run of items per lane)
-        const Seq s = read_seq(p, b0);
-        const int nq = items_of(p, s);
-        const int vh = (int)((c0 - base) / cost[b0]);
-        base += vh * cost[b0];
+        const Seq t = read_seq(p, b0);
+        const int nq = items_of(p, t);
+        const int vh = (int)div_ll(c0 - base, one);
+        base += vh * one;
         const int run = (nq + 31) / 32;
         const int qlo = min(nq, lane * run), qhi = min(nq, qlo + run);
         long long x = 0;
-        for (int qi = qlo; qi < qhi; ++qi) x += item_units(p, s, qi);
+        for (int qi = qlo; qi < qhi; ++qi) x += item_units(p, t, qi);
         const long long xi = scan_ll(x, lane), xe = xi - x;
         if (base + xe <= c0 && c0 < base + xi) {
             long long at = base + xe;
             int qi = qlo;
             while (true) {
-                const int u = item_units(p, s, qi);
+                const int u = item_units(p, t, qi);
                 if (c0 < at + u) break;
                 at += u;
                 ++qi;
@@ -341,11 +409,6 @@ __device__ void chunk_plan(const ChunkParams& p, ChunkSmem& sm, long long* cost)
             sm.qi0 = qi;
             sm.base = at;
         }
-    }
-    for (int i = lane; i <= kSeqCache; i += 32) {
-        const int b = min(b0 + i, p.B);
-        sm.rows[i] = p.cu_new ? __ldg(p.cu_new + b) : b;
-        if (i < kSeqCache) sm.ctxs[i] = b < p.B ? __ldg(p.context_lens + b) : 0;
     }
 }
 
@@ -357,17 +420,13 @@ __device__ void chunk_load(const CUtensorMap* tmk, const CUtensorMap* tmv, const
                            uint8_t* ring, ChunkSmem& sm) {
     using C = Ch<H>;
     const int lane = threadIdx.x & 31;
-    if (lane == 0) {
-        tma_prefetch_desc(tmk);
-        tma_prefetch_desc(tmv);
-    }
     Walk wk;
     wk.init(sm, p);
     Piece pc;
     int it = 0, item = 0;
     bool aborted = false;
     while (!aborted && wk.next(sm, p, pc)) {
-        const int kv = pc.vh / p.cpt;
+        const int kv = p.cpt > 1 ? pc.vh / p.cpt : pc.vh;
         const int32_t* table = p.block_tables + pc.b * p.table_b + kv * p.table_k;
         // blocks that the item's rows see: none below the window, none past its last token
         const int pos0 = pc.s.ctx - pc.s.n + pc.f;
@@ -427,143 +486,259 @@ __device__ void chunk_load(const CUtensorMap* tmk, const CUtensorMap* tmv, const
 }
 
 // ---------------------------------------------------------------------------
-// Warp 2, one lane: the Q tiles of every piece, once the products of the last one have
-// read theirs.  Rows past the sequence's last token are the next sequence's (or zeros
-// past the tensor): their results are not stored.
+// Warp 2, one lane: the Q tiles of every piece, each slot's once the products of the
+// last one have read theirs.  Rows past the sequence's last token are the next
+// sequence's (or zeros past the tensor): their results are not stored.
 template <int H>
 __device__ void chunk_queries(const CUtensorMap* tmq, const ChunkParams& p, uint8_t* qbuf,
                               ChunkSmem& sm) {
     using C = Ch<H>;
     if ((threadIdx.x & 31) != 0) return;
-    tma_prefetch_desc(tmq);
     Walk wk;
     wk.init(sm, p);
     Piece pc;
-    int k = 0;
+    int k[2] = {0, 0};
     bool aborted = false;
-    while (wk.next(sm, p, pc)) {
-        if (k >= 1 && !mbar_wait(smem_addr(&sm.q_free), (k - 1) & 1)) give_up(sm, p);
-        aborted = sm.abort_flag != 0;
-        if (aborted) break;
-        const int kv = pc.vh / p.cpt, h0 = (pc.vh % p.cpt) * p.hpc;
-        const int tiles = pc.f + p.tpc < pc.s.n ? 2 : 1;
-        mbar_arrive_expect_tx(smem_addr(&sm.q_full),
-                              (uint32_t)(tiles * C::kHalves * 128 * p.tpc * p.hpc));
-        for (int i = 0; i < tiles; ++i)
+    while (!aborted && wk.next(sm, p, pc)) {
+        const int kv = p.cpt > 1 ? pc.vh / p.cpt : pc.vh, h0 = (pc.vh - kv * p.cpt) * p.hpc;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const Sub sub = sub_of(p, pc, i);
+            if (sub.a >= sub.b || aborted) continue;
+            if (k[i] >= 1 && !mbar_wait(smem_addr(&sm.q_free[i]), (k[i] - 1) & 1)) give_up(sm, p);
+            aborted = sm.abort_flag != 0;
+            if (aborted) continue;
+            const uint32_t bar = smem_addr(&sm.q_full[i]);
+            mbar_arrive_expect_tx(bar, (uint32_t)(C::kHalves * 128 * p.tpc * p.hpc));
             for (int h = 0; h < C::kHalves; ++h)
-                tma_load_4d(smem_addr(qbuf) + i * C::kTile + h * (kRows * 128), tmq,
-                            smem_addr(&sm.q_full), 64 * h, h0, kv, pc.s.r0 + pc.f + i * p.tpc);
-        ++k;
+                tma_load_4d(smem_addr(qbuf) + i * C::kTile + h * (kRows * 128), tmq, bar, 64 * h,
+                            h0, kv, pc.s.r0 + sub.f);
+            ++k[i];
+        }
     }
-    if (aborted && k >= 1) mbar_wait(smem_addr(&sm.q_full), (k - 1) & 1);
+    if (aborted)
+        for (int i = 0; i < 2; ++i)
+            if (k[i] >= 1) mbar_wait(smem_addr(&sm.q_full[i]), (k[i] - 1) & 1);
 }
 
 // ---------------------------------------------------------------------------
-// Warp 0, one lane: every MMA.
-template <bool BF16, int H>
+// Warps 0 and 3, one lane each: the MMAs of slot I.  QK of a KV tile, PV of it once its
+// probabilities are written, QK of the next one behind it.  An issuer's wait costs some
+// 100 cycles even when there is nothing to wait for, and the tensor cores' queue is a few
+// MMAs deep: two issuers hide each other's waits.  They take turns by a lock, a PV and the
+// QK behind it at a time: interleaved, both slots' products would end together, then
+// both softmaxes run while the tensor cores rest (measured 2.4 us per pair of tiles).  A
+// turn ends four MMAs before its products do, about what handing it over takes.
+__device__ __forceinline__ bool take_turn(ChunkSmem& sm) {
+    const uint32_t lock = smem_addr(&sm.lock);
+    unsigned long long t0 = 0;
+    for (int n = 0;; ++n) {
+        uint32_t old;
+        asm volatile("atom.acquire.cta.shared::cta.exch.b32 %0, [%1], 1;"
+                     : "=r"(old)
+                     : "r"(lock)
+                     : "memory");
+        if (old == 0) return true;
+        if ((n & 63) == 63) {  // a bounded wait
+            if (t0 == 0)
+                t0 = global_ns();
+            else if (global_ns() - t0 > kWaitLimitNs)
+                return false;
+        }
+    }
+}
+__device__ __forceinline__ void end_turn(ChunkSmem& sm) {
+    asm volatile("st.release.cta.shared::cta.b32 [%0], 0;" ::"r"(smem_addr(&sm.lock)) : "memory");
+}
+
+template <bool BF16, int H, int I>
 __device__ void chunk_mma(const ChunkParams& p, uint8_t* ring, uint8_t* qbuf, ChunkSmem& sm) {
     using C = Ch<H>;
     if ((threadIdx.x & 31) != 0) return;
     constexpr uint32_t id_s = umma_idesc_ct(BF16, kRows, kStep, false);
     constexpr uint32_t id_o = umma_idesc_ct(BF16, kRows, H, true);
-    const uint32_t tmem = sm.tmem;
-    const uint64_t dq = umma_desc_sw128(smem_addr(qbuf), 16, 1024);
-    const uint64_t dk = umma_desc_sw128(smem_addr(ring), 16, C::kGroup);
-    const uint64_t dv = umma_desc_sw128(smem_addr(ring), 1024, C::kGroup);
-    auto landed = [&](int n) {
-        return mbar_wait(smem_addr(&sm.full[n % C::kSlots]), (n / C::kSlots) & 1);
-    };
-    auto qk = [&](int i, int n) {  // S_i = Q_i K^T, K in ring tile n
-        const uint64_t a = dq + (uint64_t)(i * (C::kTile >> 4));
-        const uint64_t b = dk + (uint64_t)((n % C::kSlots) * (C::kTile >> 4));
-#pragma unroll
-        for (int kk = 0; kk < H / 16; ++kk)
-            umma_ss(tmem + kColS + i * 128,
-                    a + (uint64_t)(((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4),
-                    b + (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id_s, kk > 0);
-        umma_commit(smem_addr(&sm.s_ready[i]));
-    };
-    auto pv = [&](int i, int n, bool add) {  // O_i += P_i V, V in ring tile n
-        const uint64_t b = dv + (uint64_t)((n % C::kSlots) * (C::kTile >> 4));
-        umma_ts(tmem + kColO + i * 128, tmem + kColS + i * 128, b, id_o, add);
-#pragma unroll
-        for (int ks = 1; ks < kBlocks; ++ks)
-            umma_ts(tmem + kColO + i * 128, tmem + kColS + i * 128 + 8 * ks,
-                    b + (uint64_t)((ks * 2 * C::kGroup) >> 4), id_o, true);
-        umma_commit(smem_addr(&sm.o_ready[i]));
+    const uint32_t tS = sm.tmem + kColS + I * 128, tO = sm.tmem + kColO + I * 128;
+    const uint64_t dq = umma_desc_sw128(smem_addr(qbuf) + I * C::kTile, 16, 1024);
+    const uint64_t dk0 = umma_desc_sw128(smem_addr(ring), 16, C::kGroup);
+    const uint64_t dv0 = umma_desc_sw128(smem_addr(ring), 1024, C::kGroup);
+    const uint32_t full = smem_addr(&sm.full[0]), empty = smem_addr(&sm.empty[0]);
+    int r = 0;         // ring slot of the next tile
+    uint32_t ph = 0;   // and its phase
+    uint32_t steps = 0, pieces = 0;
+    auto advance = [&]() {
+        if (++r == C::kSlots) {
+            r = 0;
+            ph ^= 1;
+        }
     };
     Walk wk;
     wk.init(sm, p);
     Piece pc;
-    int n = 0, k = 0;  // ring tiles and pieces so far
-    int steps[2] = {0, 0}, used[2] = {0, 0};
     bool ok = true;
-    while (ok && wk.next(sm, p, pc)) {
-        const Sub sub[2] = {sub_of(p, pc, 0), sub_of(p, pc, 1)};
-        ok = mbar_wait(smem_addr(&sm.q_full), k & 1) && !sm.abort_flag && landed(n);
-        if (!ok) break;
-        tc_fence_after();
+    auto qk = [&](bool last) {  // S = Q K^T, K in ring slot r
+        const uint64_t dk = dk0 + (uint32_t)(r * (C::kTile >> 4));
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (sub[i].a < sub[i].b && sub[i].a == pc.t0) qk(i, n);
-        umma_commit(smem_addr(&sm.empty[n % C::kSlots]));
-        if (pc.t0 + 1 == pc.t1) umma_commit(smem_addr(&sm.q_free));
-        for (int j = pc.t0; j < pc.t1 && ok; ++j, n += 2) {
-            ok = landed(n + 1);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (!ok) break;
-                if (j >= sub[i].a && j < sub[i].b) {
-                    ok = mbar_wait(smem_addr(&sm.p_ready[i]), steps[i] & 1);
-                    ++steps[i];
-                    if (j == sub[i].a) {
-                        if (used[i] > 0)
-                            ok = ok && mbar_wait(smem_addr(&sm.o_free[i]), (used[i] - 1) & 1);
-                        ++used[i];
-                    }
-                    if (!ok || sm.abort_flag) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    pv(i, n + 1, j > sub[i].a);
-                }
-                if (j + 1 >= sub[i].a && j + 1 < sub[i].b) {
-                    ok = landed(n + 2);
-                    if (ok) qk(i, n + 2);
-                }
-            }
-            if (!ok) break;
-            umma_commit(smem_addr(&sm.empty[(n + 1) % C::kSlots]));
-            if (j + 1 < pc.t1) {
-                umma_commit(smem_addr(&sm.empty[(n + 2) % C::kSlots]));
-                if (j + 2 == pc.t1) umma_commit(smem_addr(&sm.q_free));
-            }
+        for (int kk = 0; kk < H / 16; ++kk) {
+            if (kk == H / 16 - 4) end_turn(sm);
+            umma_ss(tS, dq + (uint64_t)(((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4),
+                    dk + (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id_s, kk > 0);
         }
-        ++k;
+        umma_commit(smem_addr(&sm.s_ready[I]));
+        umma_commit(empty + 8 * r);
+        if (last) umma_commit(smem_addr(&sm.q_free[I]));
+        advance();
+    };
+    while (ok && wk.next(sm, p, pc)) {
+        const Sub sub = sub_of(p, pc, I);
+        bool begun = false;  // QK of tile j has been issued
+        for (int j = pc.t0; j < pc.t1 && ok; ++j) {
+            if (j < sub.a || j >= sub.b) {  // not seen by this slot's rows
+                for (int kv = 0; kv < 2 && ok; ++kv) {
+                    ok = mbar_wait(full + 8 * r, ph);
+                    mbar_arrive(empty + 8 * r);
+                    advance();
+                }
+                continue;
+            }
+            if (j == sub.a) ok = mbar_wait(smem_addr(&sm.q_full[I]), pieces & 1);
+            if (!begun) {
+                ok = ok && mbar_wait(full + 8 * r, ph) && take_turn(sm);
+                if (!ok) break;
+                qk(j + 1 == sub.b);
+            }
+            begun = false;
+            ok = mbar_wait(full + 8 * r, ph) && mbar_wait(smem_addr(&sm.p_ready[I]), steps & 1);
+            ++steps;
+            if (j == sub.a && pieces > 0)  // O of the last piece has been read
+                ok = ok && mbar_wait(smem_addr(&sm.o_free[I]), (pieces - 1) & 1);
+            ok = ok && !sm.abort_flag && take_turn(sm);
+            if (!ok) break;
+            tc_fence_after();
+            const int rk = r + 1 == C::kSlots ? 0 : r + 1;
+            begun = j + 1 < sub.b && mbar_try_wait(full + 8 * rk, rk ? ph : ph ^ 1);
+            {
+                const uint64_t dv = dv0 + (uint32_t)(r * (C::kTile >> 4));
+                umma_ts(tO, tS, dv, id_o, j > sub.a);
+#pragma unroll
+                for (int ks = 1; ks < kBlocks; ++ks) {
+                    if (ks == kBlocks - 4 && !begun) end_turn(sm);
+                    umma_ts(tO, tS + 8 * ks, dv + (uint64_t)((ks * 2 * C::kGroup) >> 4), id_o, true);
+                }
+                umma_commit(smem_addr(&sm.o_ready[I]));
+                umma_commit(empty + 8 * r);
+                advance();
+            }
+            if (begun) qk(j + 2 == sub.b);
+        }
+        if (sub.a < sub.b) ++pieces;
     }
     if (!ok) give_up(sm, p);
-    umma_commit(smem_addr(&sm.done));  // every MMA ends before tensor memory is freed
-    if (!mbar_wait(smem_addr(&sm.done), 0)) give_up(sm, p);
+    umma_commit(smem_addr(&sm.done[I]));  // every MMA ends before tensor memory is freed
+    if (!mbar_wait(smem_addr(&sm.done[I]), 0)) give_up(sm, p);
 }
 
 // ---------------------------------------------------------------------------
-// Softmax of row tile i, a thread per row.
+__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
+    return (uint64_t)__float_as_uint(hi) << 32 | __float_as_uint(lo);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float lo2(uint64_t a) { return __uint_as_float((uint32_t)a); }
+__device__ __forceinline__ float hi2(uint64_t a) { return __uint_as_float((uint32_t)(a >> 32)); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Folds the pieces' rows of a slot's tile (its 128 threads): running maximum and sum
+// over the pieces in order, four dims of a row at a time.  E of them a thread and C pieces
+// at once, so that their reads overlap.
+template <bool BF16, int H, int E, int C, class Part, class Row>
+__device__ __forceinline__ void fold(int tid, int count, int pieces, const Part& part_of,
+                                     const Row& out_row) {
+    const int total = count * (H / 4);
+    for (int x0 = tid; x0 < total; x0 += kRows * E) {
+        float M[E], L[E], acc[E][4];
+        int r[E], d[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int x = min(x0 + e * kRows, total - 1);
+            r[e] = x % count;
+            d[e] = x / count;
+            M[e] = -INFINITY;
+            L[e] = acc[e][0] = acc[e][1] = acc[e][2] = acc[e][3] = 0.f;
+        }
+        bool bad = false;
+        for (int c0 = 0; c0 < pieces; c0 += C) {
+            float m[C][E], l[C][E];
+            float4 v[C][E];
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const float* q = part_of(min(c0 + c, pieces - 1));
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    m[c][e] = __ldcg(q + kRows * H + r[e]);
+                    l[c][e] = __ldcg(q + kRows * (H + 1) + r[e]);
+                    v[c][e] = __ldcg(reinterpret_cast<const float4*>(q) + d[e] * kRows + r[e]);
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    bad |= l[c][e] < 0.f;
+                    if (c0 + c >= pieces || !(l[c][e] > 0.f)) continue;  // nothing seen in it
+                    const float top = fmaxf(M[e], m[c][e]);
+                    const float f = fast_exp2(M[e] - top), w = fast_exp2(m[c][e] - top);
+                    M[e] = top;
+                    L[e] = fmaf(L[e], f, w * l[c][e]);
+                    acc[e][0] = fmaf(acc[e][0], f, w * v[c][e].x);
+                    acc[e][1] = fmaf(acc[e][1], f, w * v[c][e].y);
+                    acc[e][2] = fmaf(acc[e][2], f, w * v[c][e].z);
+                    acc[e][3] = fmaf(acc[e][3], f, w * v[c][e].w);
+                }
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            if (x0 + e * kRows >= total) break;
+            uint2 y = make_uint2(0u, 0u);
+            if (!bad && L[e] > 0.f) {
+                const float inv = 1.f / L[e];
+                y = make_uint2(Elt<BF16>::pack(acc[e][0] * inv, acc[e][1] * inv),
+                               Elt<BF16>::pack(acc[e][2] * inv, acc[e][3] * inv));
+            }
+            *reinterpret_cast<uint2*>(out_row(r[e]) + 4 * d[e]) = y;
+        }
+    }
+}
+
+// Softmax of the row tiles in slot i, a thread per row.
 template <bool BF16, int H>
 __device__ void chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm) {
     using C = Ch<H>;
     using E = Elt<BF16>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int i = (warp - kSoftWarp) >> 2;           // row tile
+    const int i = (warp - kSoftWarp) >> 2;           // slot
     const int row = 32 * (warp & 3) + lane;          // tensor-memory lane
-    const int tid = row;                             // within the tile's 128 threads
+    const int tid = row;                             // within the slot's 128 threads
+    const int row_t = row / p.hpc, row_h = row % p.hpc;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tS = sm.tmem + kColS + i * 128 + lanes, tO = sm.tmem + kColO + i * 128 + lanes;
     const uint32_t bS = smem_addr(&sm.s_ready[i]), bP = smem_addr(&sm.p_ready[i]),
                    bO = smem_addr(&sm.o_ready[i]), bF = smem_addr(&sm.o_free[i]),
                    bG = smem_addr(&sm.group[i]);
+    const uint64_t scale2 = pair2(p.scale_log2, p.scale_log2);
     int meets = 0;
-    auto meet = [&]() {  // the tile's 128 threads
+    auto meet = [&]() {  // the slot's 128 threads
         mbar_arrive(bG);
         const bool ok = mbar_wait(bG, meets & 1);
         ++meets;
@@ -579,14 +754,14 @@ __device__ void chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
         const int ring0 = n0;
         n0 += 2 * (pc.t1 - pc.t0);
         const Sub sub = sub_of(p, pc, i);
-        if (sub.f >= sub.e) continue;  // no tokens for this row tile
-        const int h0 = (pc.vh % p.cpt) * p.hpc;
+        if (sub.f >= sub.e) continue;  // no tokens for this slot
+        const int kv = p.cpt > 1 ? pc.vh / p.cpt : pc.vh, h0 = (pc.vh - kv * p.cpt) * p.hpc;
         const int heads = min(p.hpc, p.G - h0);
         const int count = (sub.e - sub.f - 1) * p.hpc + heads;  // rows in use
         const bool active = row < count;
         const bool warp_on = 32 * (warp & 3) < count;
         const int at = pc.s.ctx - pc.s.n;  // position of the first new token
-        const int lim = at + sub.f + (active ? row / p.hpc : 0);
+        const int lim = at + sub.f + (active ? row_t : 0);
         const int low = p.window > 0 ? lim - p.window + 1 : 0;
         // positions that the item's rows see at all
         const int see_lo = p.window > 0 ? max(0, at + pc.f - p.window + 1) : 0;
@@ -605,23 +780,24 @@ __device__ void chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
                 const int from = low - tok, to = lim + 1 - tok;  // columns seen
                 if (!__all_sync(kAll, from <= 0 && to >= kStep)) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < 4; ++c) {
+                        const int a = from - 32 * c, b = to - 32 * c;
+                        const uint32_t seen = (b >= 32 ? ~0u : b <= 0 ? 0u : ~(~0u << b)) &
+                                              (a <= 0 ? ~0u : a >= 32 ? 0u : ~0u << a);
 #pragma unroll
                         for (int x = 0; x < 32; ++x)
-                            if (32 * c + x < from || 32 * c + x >= to) s[c][x] = 0xff800000u;
+                            if (!(seen >> x & 1u)) s[c][x] = 0xff800000u;
+                    }
                 }
                 float mx[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    float a = __uint_as_float(s[c][0]), b = __uint_as_float(s[c][1]);
+                    mx[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
 #pragma unroll
-                    for (int x = 2; x < 32; x += 2) {
-                        a = fmaxf(a, __uint_as_float(s[c][x]));
-                        b = fmaxf(b, __uint_as_float(s[c][x + 1]));
-                    }
-                    mx[c] = fmaxf(a, b);
+                    for (int x = 2; x < 32; x += 2)
+                        mx[c] = max3(mx[c], __uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1]));
                 }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+                const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
                 const bool need = top > m + kSlack;
                 if (__any_sync(kAll, need)) {
                     const float f = need && m != -INFINITY ? fast_exp2(m - top) : 1.f;
@@ -647,21 +823,24 @@ __device__ void chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
                     }
                 }
                 const float ref = m == -INFINITY ? 0.f : -m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t ref2 = pair2(ref, ref);
+                uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t w[16];
 #pragma unroll
                     for (int x = 0; x < 16; ++x) {
-                        w[x] = E::pack(
-                            fast_exp2(fmaf(__uint_as_float(s[c][2 * x]), p.scale_log2, ref)),
-                            fast_exp2(fmaf(__uint_as_float(s[c][2 * x + 1]), p.scale_log2, ref)));
-                        sum[x & 1] += E::lo(w[x]);
-                        sum[2 + (x & 1)] += E::hi(w[x]);
+                        const uint64_t y = fma2(pair2(__uint_as_float(s[c][2 * x]),
+                                                      __uint_as_float(s[c][2 * x + 1])),
+                                                scale2, ref2);
+                        const float a = fast_exp2(lo2(y)), b = fast_exp2(hi2(y));
+                        w[x] = E::pack(a, b);
+                        sum[x & 1] = add2(sum[x & 1], pair2(a, b));
                     }
                     tmem_st16(tS + 16 * c, w);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                const uint64_t both = add2(sum[0], sum[1]);
+                l += lo2(both) + hi2(both);
                 tmem_wait_st();
             }
             // V rows that no row of the item sees hold anything: zeros, since 0 * NaN counts
@@ -694,65 +873,60 @@ __device__ void chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
             if (!ok) break;
             tc_fence_after();
         }
-        // (set before the tiles landed; without one, nothing has been waited for)
-        const bool bad = some && sm.bad[item % kBadRing] != 0;
-        const int first_cta = (int)(pc.first / sm.quota);
-        const int last_cta = (int)((pc.first + (pc.hi - pc.lo) - 1) / sm.quota);
-        const size_t head0 = (size_t)(pc.vh / p.cpt) * p.G + h0;  // query head of the tile's first
-        uint16_t* const out = static_cast<uint16_t*>(p.out);
-        auto out_row = [&](int r) {
-            return out + (((size_t)pc.s.r0 + sub.f + r / p.hpc) * p.N + head0 + r % p.hpc) * H;
-        };
-        if (first_cta == last_cta) {
-            if (warp_on) {
-                const float inv = bad || !(l > 0.f) ? 0.f : 1.f / l;
-                uint16_t* dst = active ? out_row(row) : nullptr;
-#pragma unroll 1
+        // O_i, 32 dims at a time, the next ones on their way while these are stored
+        auto drain = [&](const auto& store) {
+            if (warp_on && some) {
+                uint32_t o[2][32];
+                tmem_ld32(tO, o[0]);
+#pragma unroll
                 for (int c = 0; c < H / 32; ++c) {
-                    uint32_t o[32];
-                    tmem_ld32(tO + 32 * c, o);
                     tmem_wait_ld();
-                    uint32_t w[16];
-#pragma unroll
-                    for (int x = 0; x < 16; ++x)
-                        w[x] = inv == 0.f ? 0u
-                                          : E::pack(__uint_as_float(o[2 * x]) * inv,
-                                                    __uint_as_float(o[2 * x + 1]) * inv);
-                    if (active)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            reinterpret_cast<uint4*>(dst + 32 * c)[x] =
-                                make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+                    if (c + 1 < H / 32) tmem_ld32(tO + 32 * (c + 1), o[(c + 1) & 1]);
+                    if (active) store(c, o[c & 1]);
                 }
             }
             tc_fence_before();
             if (some) mbar_arrive(bF);
+        };
+        // (set before the tiles landed; without one, nothing has been waited for)
+        const bool bad = some && sm.bad[item % kBadRing] != 0;
+        uint16_t* const out = static_cast<uint16_t*>(p.out) +
+                              (((size_t)pc.s.r0 + sub.f) * p.N + (size_t)kv * p.G + h0) * H;
+        if (!pc.split()) {
+            const float inv = bad || !(l > 0.f) ? 0.f : 1.f / l;
+            uint4* dst = reinterpret_cast<uint4*>(out + ((size_t)row_t * p.N + row_h) * H);
+            drain([&](int c, const uint32_t (&o)[32]) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        w[y] = inv == 0.f ? 0u
+                                          : E::pack(__uint_as_float(o[8 * x + 2 * y]) * inv,
+                                                    __uint_as_float(o[8 * x + 2 * y + 1]) * inv);
+                    dst[4 * c + x] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            });
             continue;
         }
         // a piece of an item that several CTAs share: [H/4][128 rows][4] values, maxima, sums
-        const int me = blockIdx.x, pieces = last_cta - first_cta + 1;
+        const int me = blockIdx.x;
+        const int first_cta = (int)div_ll(pc.first, sm.quota);
+        const int last_cta = (int)div_ll(pc.first + (pc.hi - pc.lo) - 1, sm.quota);
+        const int tile = i ^ pc.slot, pieces = last_cta - first_cta + 1;
         {
-            float* part = p.partials + ((size_t)(me * 2 + (me == first_cta)) * 2 + i) * C::kPart;
-            if (warp_on && some) {
-#pragma unroll 1
-                for (int c = 0; c < H / 32; ++c) {
-                    uint32_t o[32];
-                    tmem_ld32(tO + 32 * c, o);
-                    tmem_wait_ld();
-                    if (active)
+            float* part = p.partials + ((size_t)(me * 2 + (me == first_cta)) * 2 + tile) * C::kPart;
+            drain([&](int c, const uint32_t (&o)[32]) {
 #pragma unroll
-                        for (int x = 0; x < 8; ++x)
-                            __stcg(reinterpret_cast<uint4*>(part) + (8 * c + x) * kRows + row,
-                                   make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]));
-                }
-            }
-            tc_fence_before();
-            if (some) mbar_arrive(bF);
+                for (int x = 0; x < 8; ++x)
+                    __stcg(reinterpret_cast<uint4*>(part) + (8 * c + x) * kRows + row,
+                           make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]));
+            });
             __stcg(part + kRows * H + row, m);
             __stcg(part + kRows * (H + 1) + row, bad ? -1.f : l);  // a bad block shows as -1
         }
         __threadfence();
-        int32_t* const flag = p.flags + 2 * first_cta + i;
+        int32_t* const flag = p.flags + 2 * first_cta + tile;
         ok = meet();
         if (ok && tid == 0) {
             unsigned v;
@@ -764,42 +938,19 @@ __device__ void chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
         }
         ok = __all_sync(kAll, ok && meet());
         if (!ok) break;
-        const bool last = sm.ticket[i] == pieces - 1;
-        if (last) {
+        if (sm.ticket[i] == pieces - 1) {
             __threadfence();
             auto part_of = [&](int c) {
-                return p.partials + ((size_t)(c * 2 + (c == first_cta)) * 2 + i) * C::kPart;
+                return p.partials +
+                       ((size_t)((first_cta + c) * 2 + (c == 0)) * 2 + tile) * C::kPart;
             };
-            for (int x = tid; x < count * (H / 4); x += kRows) {
-                const int r = x % count, d = x / count;
-                float M = -INFINITY;
-                bool any_bad = false;
-                for (int c = first_cta; c <= last_cta; ++c) {
-                    const float* q = part_of(c) + kRows * H + r;
-                    M = fmaxf(M, __ldcg(q));
-                    any_bad |= __ldcg(q + kRows) < 0.f;
-                }
-                float acc[4] = {0.f, 0.f, 0.f, 0.f}, L = 0.f;
-                for (int c = first_cta; c <= last_cta; ++c) {
-                    const float* q = part_of(c);
-                    const float lc = __ldcg(q + kRows * (H + 1) + r);
-                    if (!(lc > 0.f)) continue;  // nothing seen in this piece
-                    const float w = fast_exp2(__ldcg(q + kRows * H + r) - M);
-                    const float4 v = __ldcg(reinterpret_cast<const float4*>(q) + d * kRows + r);
-                    L = fmaf(w, lc, L);
-                    acc[0] = fmaf(w, v.x, acc[0]);
-                    acc[1] = fmaf(w, v.y, acc[1]);
-                    acc[2] = fmaf(w, v.z, acc[2]);
-                    acc[3] = fmaf(w, v.w, acc[3]);
-                }
-                const bool zero = any_bad || !(L > 0.f);
-                const float inv = zero ? 0.f : 1.f / L;
-                uint2 y = make_uint2(0u, 0u);
-                if (!zero)
-                    y = make_uint2(E::pack(acc[0] * inv, acc[1] * inv),
-                                   E::pack(acc[2] * inv, acc[3] * inv));
-                *reinterpret_cast<uint2*>(out_row(r) + 4 * d) = y;
-            }
+            auto out_row = [&](int r) {
+                return out + ((size_t)(r / p.hpc) * p.N + r % p.hpc) * H;
+            };
+            if (count * (H / 4) <= 2 * kRows)
+                fold<BF16, H, 2, 4>(tid, count, pieces, part_of, out_row);
+            else
+                fold<BF16, H, 8, 2>(tid, count, pieces, part_of, out_row);
             if (tid == 0) *flag = 0;  // as the next call wants it
         }
         // (no thread writes the ticket again before every thread has read it)
@@ -822,46 +973,55 @@ __global__ void __launch_bounds__(kThreadsCh, 1)
     ChunkSmem& sm = *reinterpret_cast<ChunkSmem*>(ring + C::kSlots * C::kTile);
     const int warp = threadIdx.x >> 5;
     griddep_launch_dependents();
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 32) {
         for (int s = 0; s < 8; ++s) {
             mbar_init(smem_addr(&sm.full[s]), 1);
-            mbar_init(smem_addr(&sm.empty[s]), 1);
+            mbar_init(smem_addr(&sm.empty[s]), 2);
         }
-        mbar_init(smem_addr(&sm.q_full), 1);
-        mbar_init(smem_addr(&sm.q_free), 1);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&sm.q_full[i]), 1);
+            mbar_init(smem_addr(&sm.q_free[i]), 1);
             mbar_init(smem_addr(&sm.s_ready[i]), 1);
             mbar_init(smem_addr(&sm.p_ready[i]), kRows);
             mbar_init(smem_addr(&sm.o_ready[i]), 1);
             mbar_init(smem_addr(&sm.o_free[i]), kRows);
             mbar_init(smem_addr(&sm.group[i]), kRows);
+            mbar_init(smem_addr(&sm.done[i]), 1);
         }
-        mbar_init(smem_addr(&sm.done), 1);
         sm.abort_flag = 0;
-        sm.base = 0;
-        sm.vh0 = sm.qi0 = 0;
+        sm.lock = 0;
         fence_mbar_init();
     }
-    if (warp == 0) tmem_alloc(smem_addr(&sm.tmem), 512);
+    if (threadIdx.x == 64) {
+        tma_prefetch_desc(&tmk);
+        tma_prefetch_desc(&tmv);
+        tma_prefetch_desc(&tmq);
+    }
+    if (warp == 2) tmem_alloc(smem_addr(&sm.tmem), 512);
     griddep_wait();  // everything read or written follows earlier kernels
-    __syncthreads();  // (the plan's scratch is the ring; the range's start is set above)
     chunk_plan<H>(p, sm, reinterpret_cast<long long*>(ring));
-    fence_proxy_async_shared();  // the scratch before the copies that overwrite it
+    fence_proxy_async_shared();  // the plan's scratch before the copies that overwrite it
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 0)
-        chunk_mma<BF16, H>(p, ring, qbuf, sm);
-    else if (warp == 1)
-        chunk_load<H>(&tmk, &tmv, p, ring, sm);
-    else if (warp == 2)
-        chunk_queries<H>(&tmq, p, qbuf, sm);
-    else if (warp >= kSoftWarp)
+    if (warp < kSoftWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+        if (warp == 0)
+            chunk_mma<BF16, H, 0>(p, ring, qbuf, sm);
+        else if (warp == 1)
+            chunk_load<H>(&tmk, &tmv, p, ring, sm);
+        else if (warp == 2)
+            chunk_queries<H>(&tmq, p, qbuf, sm);
+        else
+            chunk_mma<BF16, H, 1>(p, ring, qbuf, sm);
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
         chunk_softmax<BF16, H>(p, ring, sm);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 0) tmem_dealloc(sm.tmem, 512);
+    if (warp == 2) tmem_dealloc(sm.tmem, 512);
 }
 
 template <int H>

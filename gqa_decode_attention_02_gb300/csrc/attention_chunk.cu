@@ -62,8 +62,7 @@ constexpr int kStart = 2;      // units of an item's start-up and end
 constexpr int kQuota = 6;      // units per CTA at least
 constexpr int kWhole = 4;      // KV tiles up to which an item is never split
 constexpr float kSlack = 8.f;  // log2 slack before O is rescaled
-constexpr int kSeqCache = 64;
-constexpr int kBadRing = 8;    // items in flight at most (the ring holds 8 tiles)
+constexpr int kPieces = 8;      // pieces between the scheduler and the last role
 constexpr int kMaxSeqs = 16384;
 constexpr uint32_t kColS = 0, kColO = 256;  // tensor-memory columns, 128 per slot
 
@@ -91,19 +90,30 @@ struct ChunkParams {
     float scale_log2;
 };
 
+// KV tiles [t0, t1) of an item, as the scheduler hands them to the other roles (t0 < 0: no
+// more).  Per slot: its row tile's KV tiles [a, b) within the piece, rows in use (0: none),
+// first row of q and out and its position.
+struct Piece {
+    int t0, t1;
+    int a[2], b[2], count[2], row0[2], pos[2], tile[2];
+    int kv, h0;              // KV head, first query head in its group
+    int see_lo, see_hi;      // positions that the item's rows see
+    int first_cta, last_cta; // CTAs that share the item
+    long long table;         // its row of the block tables
+};
 struct ChunkSmem {
     uint64_t full[8], empty[8];
+    uint64_t piece_full[kPieces], piece_free[kPieces];
     // per slot (a row tile in the works: its Q, S, O and softmax warps)
-    uint64_t q_full[2], q_free[2], s_ready[2], p_ready[2], o_ready[2], o_free[2], group[2];
-    uint64_t done[2];
+    uint64_t q_full[2], q_free[2], s_ready[2], p_ready[2], o_ready[2], o_free[2], group[2], done[2];
     long long c0, c1, base;  // range of units; first unit of the first item
     long long quota;
     int b0, vh0, qi0, whole;
     uint32_t tmem, lock;
     volatile int abort_flag;
-    volatile int bad[kBadRing];
+    volatile int bad[kPieces];
     int ticket[2];
-    int ctxs[kSeqCache], rows[kSeqCache + 1];
+    Piece pieces[kPieces];
 };
 
 // A sequence's new rows, or none where its lengths are out of range.
@@ -127,11 +137,6 @@ __device__ __forceinline__ Seq read_seq(const ChunkParams& p, int b) {
                              __ldg(p.context_lens + b))
                     : seq_of(p, b, b + 1, __ldg(p.context_lens + b));
 }
-__device__ __forceinline__ Seq cached_seq(const ChunkSmem& sm, const ChunkParams& p, int b) {
-    const int i = b - sm.b0;
-    if (i < kSeqCache) return seq_of(p, sm.rows[i], sm.rows[i + 1], sm.ctxs[i]);
-    return read_seq(p, b);
-}
 __device__ __forceinline__ int items_of(const ChunkParams& p, const Seq& s) {
     return (s.n + 2 * p.tpc - 1) / (2 * p.tpc);
 }
@@ -152,66 +157,53 @@ __device__ __forceinline__ void give_up(ChunkSmem& sm, const ChunkParams& p) {
     sm.abort_flag = 1;
 }
 
-// KV tiles [t0, t1) of an item, of those [lo, hi) that it has.
-struct Piece {
-    Seq s;
-    int b, vh, f;  // first token
-    int lo, hi, t0, t1;
-    int slot;         // of the first row tile (with two: 0, the other's is 1)
-    long long first;  // unit of tile lo
-    __device__ __forceinline__ bool split() const { return t0 != lo || t1 != hi; }
-};
-// Tokens [f, e) of the row tile in a slot, and its KV tiles [a, b) within the piece.
-struct Sub {
-    int f, e, a, b;
-};
-__device__ __forceinline__ Sub sub_of(const ChunkParams& p, const Piece& pc, int slot) {
-    const int i = slot ^ pc.slot;  // which row tile (a lone one's other slot: past the tokens)
-    Sub x;
-    x.f = pc.f + i * p.tpc;
-    x.e = min(pc.s.n, x.f + p.tpc);
-    x.a = x.b = pc.t0;
-    if (x.f < x.e) {
-        x.a = max(pc.t0, tile_lo(p, pc.s, x.f));
-        x.b = max(x.a, min(pc.t1, tile_hi(pc.s, x.e)));
-    }
-    return x;
+// a / b for a >= 0, b > 0 (32 bits where they do)
+__device__ __forceinline__ long long div_ll(long long a, long long b) {
+    if ((a | b) >> 32 == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
 }
 
-// The pieces of the CTA's range in order; every role walks the same.  Items of up to
-// `whole` KV tiles belong to the CTA in whose range they begin.  Lone row tiles take the
-// two slots in turn, so that one's end and the next one's start overlap.
+// The pieces of the CTA's range in order.  Items of up to `whole` KV tiles belong to the CTA
+// in whose range they begin.  Lone row tiles take the two slots in turn, so that one's
+// end and the next one's start overlap.
 struct Walk {
-    long long pos, c0, c1, base;
-    int b, vh, qi, nq, turn;
-    Seq s;
+    long long pos, c0, c1, base, quota;
+    int b, vh, qi, nq, turn, whole;
+    Seq s, ahead;  // of sequences b and b + 1
+    __device__ void load(const ChunkParams& p) {
+        s = ahead;
+        nq = items_of(p, s);
+        if (b + 1 < p.B) ahead = read_seq(p, b + 1);
+    }
     __device__ void init(const ChunkSmem& sm, const ChunkParams& p) {
         pos = c0 = sm.c0;
         c1 = sm.c1;
         base = sm.base;
+        quota = sm.quota;
+        whole = sm.whole;
         b = sm.b0;
         vh = sm.vh0;
         qi = sm.qi0;
         nq = turn = 0;
         if (pos < c1) {
-            s = cached_seq(sm, p, b);
-            nq = items_of(p, s);
+            ahead = read_seq(p, b);
+            load(p);
         }
     }
-    __device__ bool next(const ChunkSmem& sm, const ChunkParams& p, Piece& pc) {
+    __device__ bool next(const ChunkParams& p, Piece& pc) {
         while (pos < c1) {
             if (nq == 0) {
                 if (++b >= p.B) break;
-                s = cached_seq(sm, p, b);
-                nq = items_of(p, s);
+                load(p);
                 continue;
             }
-            const int f = qi * 2 * p.tpc;
-            const int lo = tile_lo(p, s, f), hi = tile_hi(s, min(s.n, f + 2 * p.tpc));
+            const int f = qi * 2 * p.tpc, e = min(s.n, f + 2 * p.tpc), mid = min(e, f + p.tpc);
+            const int lo = tile_lo(p, s, f), hi = tile_hi(s, e);
             const long long first = base + kStart, end = first + (hi - lo);
             if (pos < end) {
                 long long from = max(pos, first), to = min(c1, end);
-                if (hi - lo <= sm.whole) {
+                const bool small = hi - lo <= whole;
+                if (small) {
                     if (base < c0) {  // another CTA's
                         pos = end;
                         continue;
@@ -221,20 +213,34 @@ struct Walk {
                 }
                 pos = to;
                 if (to <= from) break;  // only start-up units
-                pc.s = s;
-                pc.b = b;
-                pc.vh = vh;
-                pc.f = f;
-                pc.lo = lo;
-                pc.hi = hi;
-                pc.first = first;
                 pc.t0 = lo + (int)(from - first);
                 pc.t1 = lo + (int)(to - first);
-                pc.slot = 0;
-                if (f + p.tpc >= s.n) {
-                    pc.slot = turn;
-                    turn ^= 1;
+                const int kv = p.cpt > 1 ? vh / p.cpt : vh;
+                pc.kv = kv;
+                pc.h0 = (vh - kv * p.cpt) * p.hpc;
+                pc.table = b * p.table_b + kv * p.table_k;
+                const int at = s.ctx - s.n;  // position of the first new token
+                pc.see_lo = p.window > 0 ? max(0, at + f - p.window + 1) : 0;
+                pc.see_hi = at + e;
+                const bool cut = to - from != hi - lo;
+                pc.first_cta = cut ? (int)div_ll(first, quota) : -1;
+                pc.last_cta = cut ? (int)div_ll(end - 1, quota) : -1;
+                const int heads = min(p.hpc, p.G - pc.h0);
+                const bool lone = mid == e;
+                for (int i = 0; i < 2; ++i) {
+                    const int tile = lone ? i ^ turn : i;
+                    const int tf = tile ? mid : f, te = tile ? e : mid;
+                    pc.tile[i] = tile;
+                    pc.row0[i] = s.r0 + tf;
+                    pc.pos[i] = at + tf;
+                    pc.count[i] = tf < te ? (te - tf - 1) * p.hpc + heads : 0;
+                    pc.a[i] = pc.b[i] = pc.t0;
+                    if (tf < te) {
+                        pc.a[i] = max(pc.t0, tile_lo(p, s, tf));
+                        pc.b[i] = max(pc.a[i], min(pc.t1, tile_hi(s, te)));
+                    }
                 }
+                if (lone) turn ^= 1;
                 return true;
             }
             base = end;
@@ -262,12 +268,6 @@ __device__ __forceinline__ long long scan_ll(long long v, int lane) {
     }
     return v;
 }
-// a / b for a >= 0, b > 0 (32 bits where they do)
-__device__ __forceinline__ long long div_ll(long long a, long long b) {
-    if ((a | b) >> 32 == 0) return (uint32_t)a / (uint32_t)b;
-    return a / b;
-}
-
 // Rows [r0, r0 + n) of the output become zeros (whole warp).
 template <int H>
 __device__ void zero_rows(const ChunkParams& p, int r0, int n) {
@@ -371,20 +371,6 @@ __device__ void chunk_plan(const ChunkParams& p, ChunkSmem& sm, long long* cost)
         sm.vh0 = sm.qi0 = 0;
     }
     __syncwarp();
-    // lengths of the sequences from b0 on
-    if (few && b0 == 0) {
-        if (lane < p.B) {
-            sm.rows[lane] = p.cu_new ? __ldg(p.cu_new + lane) : lane;
-            sm.ctxs[lane] = s.ctx;
-        }
-        if (lane == 0) sm.rows[p.B] = p.cu_new ? __ldg(p.cu_new + p.B) : p.B;
-    } else {
-        for (int i = lane; i <= kSeqCache; i += 32) {
-            const int b = min(b0 + i, p.B);
-            sm.rows[i] = p.cu_new ? __ldg(p.cu_new + b) : b;
-            if (i < kSeqCache) sm.ctxs[i] = b < p.B ? __ldg(p.context_lens + b) : 0;
-        }
-    }
     if (owners) {
         // the virtual head, then the item in it (a run of items per lane)
         const Seq t = read_seq(p, b0);
@@ -413,6 +399,14 @@ __device__ void chunk_plan(const ChunkParams& p, ChunkSmem& sm, long long* cost)
 }
 
 // ---------------------------------------------------------------------------
+// Waits for piece k of the CTA; false after a time-out or an abort.
+__device__ __forceinline__ bool piece_ready(ChunkSmem& sm, int k) {
+    return mbar_wait(smem_addr(&sm.piece_full[k % kPieces]), (k / kPieces) & 1) && !sm.abort_flag;
+}
+__device__ __forceinline__ void piece_done(ChunkSmem& sm, int k) {
+    mbar_arrive(smem_addr(&sm.piece_free[k % kPieces]));
+}
+
 // Warp 1: K and V tiles into the ring, K(j) then V(j).  A lane per cache block; block
 // ids are read 32 at a time, the next ones while these are in use.
 template <int H>
@@ -420,25 +414,29 @@ __device__ void chunk_load(const CUtensorMap* tmk, const CUtensorMap* tmv, const
                            uint8_t* ring, ChunkSmem& sm) {
     using C = Ch<H>;
     const int lane = threadIdx.x & 31;
-    Walk wk;
-    wk.init(sm, p);
-    Piece pc;
-    int it = 0, item = 0;
+    int it = 0, r = 0;
+    uint32_t ph = 1;  // phase whose end frees slot r (none at first)
     bool aborted = false;
-    while (!aborted && wk.next(sm, p, pc)) {
-        const int kv = p.cpt > 1 ? pc.vh / p.cpt : pc.vh;
-        const int32_t* table = p.block_tables + pc.b * p.table_b + kv * p.table_k;
+    for (int k = 0;; ++k) {
+        aborted = __any_sync(kAll, !piece_ready(sm, k));
+        if (aborted) break;
+        const Piece& pc = sm.pieces[k % kPieces];
+        const int t0 = pc.t0, t1 = pc.t1, kv = pc.kv;
+        if (t0 < 0) break;
+        const int32_t* table = p.block_tables + pc.table;
         // blocks that the item's rows see: none below the window, none past its last token
-        const int pos0 = pc.s.ctx - pc.s.n + pc.f;
-        const int blo = p.window > 0 ? max(0, pos0 - p.window + 1) / 16 : 0;
-        const int bhi = (pc.s.ctx - pc.s.n + min(pc.s.n, pc.f + 2 * p.tpc) - 1) / 16 + 1;
-        if (lane == 0) sm.bad[item % kBadRing] = 0;
+        const int blo = pc.see_lo / 16, bhi = (pc.see_hi + 15) / 16;
+        __syncwarp();
+        if (lane == 0) {
+            sm.bad[k % kPieces] = 0;
+            piece_done(sm, k);
+        }
         auto load_ids = [&](int from) {
             const int i = from + lane;
             return i >= blo && i < bhi ? __ldg(table + i) : 0;
         };
-        int win = pc.t0 * kBlocks, ids = load_ids(win), nxt = load_ids(win + 32);
-        for (int j = pc.t0; j < pc.t1 && !aborted; ++j) {
+        int win = t0 * kBlocks, ids = load_ids(win), nxt = load_ids(win + 32);
+        for (int j = t0; j < t1 && !aborted; ++j) {
             if (j * kBlocks - win == 32) {
                 win += 32;
                 ids = nxt;
@@ -447,38 +445,40 @@ __device__ void chunk_load(const CUtensorMap* tmk, const CUtensorMap* tmv, const
             const int id = __shfl_sync(kAll, ids, (j * kBlocks - win + lane) & 31);
             const int blk = j * kBlocks + lane;
             const bool mine = lane < kBlocks && blk >= blo && blk < bhi;
-            const unsigned on = __ballot_sync(kAll, mine);
             const bool bad = __any_sync(kAll, mine && (id < 0 || id >= p.num_blocks));
-            const uint32_t bytes = __popc(on) * (16 * H * 2);
+            // (a block that no row sees: past the tensor's end, which reads as zeros)
+            const int at = mine ? 2 * id : 2 * p.num_blocks;
 #pragma unroll 1
-            for (int kvsel = 0; kvsel < 2; ++kvsel, ++it) {
-                const int s = it % C::kSlots;
-                const uint32_t bar = smem_addr(&sm.full[s]);
+            for (int kvsel = 0; kvsel < 2; ++kvsel) {
+                const uint32_t bar = smem_addr(&sm.full[r]);
                 if (lane == 0) {
-                    bool ok = true;
-                    if (it >= C::kSlots)
-                        ok = mbar_wait(smem_addr(&sm.empty[s]), (it / C::kSlots - 1) & 1);
+                    bool ok = it < C::kSlots || mbar_wait(smem_addr(&sm.empty[r]), ph);
                     if (!ok) give_up(sm, p);
                     aborted = !ok || sm.abort_flag;
                     if (!aborted) {
                         if (bad) {
                             report(p.status, GQA_ERR_BLOCK_ID);
-                            sm.bad[item % kBadRing] = 1;
+                            sm.bad[k % kPieces] = 1;
                             __threadfence_block();
                             mbar_arrive(bar);
                         } else {
-                            mbar_arrive_expect_tx(bar, bytes);
+                            mbar_arrive_expect_tx(bar, (uint32_t)C::kTile);
                         }
                     }
                 }
                 aborted = __shfl_sync(kAll, aborted, 0);
                 if (aborted) break;
-                if (mine && !bad)
-                    tma_load_5d(smem_addr(ring + (size_t)s * C::kTile) + lane * 2 * C::kGroup,
-                                kvsel ? tmv : tmk, bar, 0, 0, 0, 2 * id, kv);
+                if (lane < kBlocks && !bad)
+                    tma_load_5d(smem_addr(ring + (size_t)r * C::kTile) + lane * 2 * C::kGroup,
+                                kvsel ? tmv : tmk, bar, 0, 0, 0, at, kv);
+                ++it;
+                if (++r == C::kSlots) {
+                    r = 0;
+                    ph ^= 1;
+                }
             }
         }
-        ++item;
+        if (aborted) break;
     }
     if (lane == 0 && aborted)  // copies in flight land before the CTA ends
         for (int j = max(0, it - C::kSlots); j < it; ++j)
@@ -486,43 +486,61 @@ __device__ void chunk_load(const CUtensorMap* tmk, const CUtensorMap* tmv, const
 }
 
 // ---------------------------------------------------------------------------
-// Warp 2, one lane: the Q tiles of every piece, each slot's once the products of the
-// last one have read theirs.  Rows past the sequence's last token are the next
-// sequence's (or zeros past the tensor): their results are not stored.
+// Warp 2, one lane: the pieces, two ahead of the queries it loads, and the Q tiles of each,
+// a slot's once the products of the last one have read theirs.  Rows past the
+// sequence's last token are the next sequence's (or zeros past the tensor): their
+// results are not stored.
 template <int H>
-__device__ void chunk_queries(const CUtensorMap* tmq, const ChunkParams& p, uint8_t* qbuf,
-                              ChunkSmem& sm) {
+__device__ void chunk_schedule(const CUtensorMap* tmq, const ChunkParams& p, uint8_t* qbuf,
+                               ChunkSmem& sm) {
     using C = Ch<H>;
     if ((threadIdx.x & 31) != 0) return;
     Walk wk;
     wk.init(sm, p);
-    Piece pc;
-    int k[2] = {0, 0};
-    bool aborted = false;
-    while (!aborted && wk.next(sm, p, pc)) {
-        const int kv = p.cpt > 1 ? pc.vh / p.cpt : pc.vh, h0 = (pc.vh - kv * p.cpt) * p.hpc;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const Sub sub = sub_of(p, pc, i);
-            if (sub.a >= sub.b || aborted) continue;
-            if (k[i] >= 1 && !mbar_wait(smem_addr(&sm.q_free[i]), (k[i] - 1) & 1)) give_up(sm, p);
-            aborted = sm.abort_flag != 0;
-            if (aborted) continue;
+    int out = 0, in = 0;  // pieces handed out; pieces whose queries are on their way
+    uint32_t loads[2] = {0, 0};
+    bool more = true, ok = true;
+    while (ok) {
+        if (more && out < in + 3) {
+            const int e = out % kPieces;
+            if (out >= kPieces)
+                ok = mbar_wait(smem_addr(&sm.piece_free[e]), (out / kPieces - 1) & 1);
+            if (!ok) break;
+            more = wk.next(p, sm.pieces[e]);
+            if (!more) sm.pieces[e].t0 = -1;
+            mbar_arrive(smem_addr(&sm.piece_full[e]));
+            if (more) ++out;
+            continue;
+        }
+        if (in == out) break;
+        const Piece& pc = sm.pieces[in % kPieces];
+#pragma unroll 1
+        for (int i = 0; i < 2 && ok; ++i) {
+            if (pc.a[i] >= pc.b[i]) continue;
+            if (loads[i] > 0) ok = mbar_wait(smem_addr(&sm.q_free[i]), (loads[i] - 1) & 1);
+            if (!ok || sm.abort_flag) {
+                ok = false;
+                break;
+            }
             const uint32_t bar = smem_addr(&sm.q_full[i]);
             mbar_arrive_expect_tx(bar, (uint32_t)(C::kHalves * 128 * p.tpc * p.hpc));
+#pragma unroll 1
             for (int h = 0; h < C::kHalves; ++h)
                 tma_load_4d(smem_addr(qbuf) + i * C::kTile + h * (kRows * 128), tmq, bar, 64 * h,
-                            h0, kv, pc.s.r0 + sub.f);
-            ++k[i];
+                            pc.h0, pc.kv, pc.row0[i]);
+            ++loads[i];
         }
+        ++in;
     }
-    if (aborted)
-        for (int i = 0; i < 2; ++i)
-            if (k[i] >= 1) mbar_wait(smem_addr(&sm.q_full[i]), (k[i] - 1) & 1);
+    if (!ok) {
+        give_up(sm, p);
+        for (int i = 0; i < 2; ++i)  // copies in flight land before the CTA ends
+            if (loads[i] > 0) mbar_wait(smem_addr(&sm.q_full[i]), (loads[i] - 1) & 1);
+    }
 }
 
 // ---------------------------------------------------------------------------
-// Warps 0 and 3, one lane each: the MMAs of slot I.  QK of a KV tile, PV of it once its
+// Warps 0 and 3, one lane each: the MMAs of a slot.  QK of a KV tile, PV of it once its
 // probabilities are written, QK of the next one behind it.  An issuer's wait costs some
 // 100 cycles even when there is nothing to wait for, and the tensor cores' queue is a few
 // MMAs deep: two issuers hide each other's waits.  They take turns by a lock, a PV and the
@@ -551,8 +569,9 @@ __device__ __forceinline__ void end_turn(ChunkSmem& sm) {
     asm volatile("st.release.cta.shared::cta.b32 [%0], 0;" ::"r"(smem_addr(&sm.lock)) : "memory");
 }
 
-template <bool BF16, int H, int I>
-__device__ void chunk_mma(const ChunkParams& p, uint8_t* ring, uint8_t* qbuf, ChunkSmem& sm) {
+template <bool BF16, int H>
+__device__ void chunk_mma(const ChunkParams& p, uint8_t* ring, uint8_t* qbuf, ChunkSmem& sm,
+                          int I) {
     using C = Ch<H>;
     if ((threadIdx.x & 31) != 0) return;
     constexpr uint32_t id_s = umma_idesc_ct(BF16, kRows, kStep, false);
@@ -571,9 +590,6 @@ __device__ void chunk_mma(const ChunkParams& p, uint8_t* ring, uint8_t* qbuf, Ch
             ph ^= 1;
         }
     };
-    Walk wk;
-    wk.init(sm, p);
-    Piece pc;
     bool ok = true;
     auto qk = [&](bool last) {  // S = Q K^T, K in ring slot r
         const uint64_t dk = dk0 + (uint32_t)(r * (C::kTile >> 4));
@@ -588,11 +604,16 @@ __device__ void chunk_mma(const ChunkParams& p, uint8_t* ring, uint8_t* qbuf, Ch
         if (last) umma_commit(smem_addr(&sm.q_free[I]));
         advance();
     };
-    while (ok && wk.next(sm, p, pc)) {
-        const Sub sub = sub_of(p, pc, I);
+    for (int k = 0; ok; ++k) {
+        ok = piece_ready(sm, k);
+        if (!ok) break;
+        const Piece& pc = sm.pieces[k % kPieces];
+        const int t0 = pc.t0, t1 = pc.t1, ja = pc.a[I], jb = pc.b[I];
+        if (t0 < 0) break;
+        piece_done(sm, k);
         bool begun = false;  // QK of tile j has been issued
-        for (int j = pc.t0; j < pc.t1 && ok; ++j) {
-            if (j < sub.a || j >= sub.b) {  // not seen by this slot's rows
+        for (int j = t0; j < t1 && ok; ++j) {
+            if (j < ja || j >= jb) {  // not seen by this slot's rows
                 for (int kv = 0; kv < 2 && ok; ++kv) {
                     ok = mbar_wait(full + 8 * r, ph);
                     mbar_arrive(empty + 8 * r);
@@ -600,25 +621,25 @@ __device__ void chunk_mma(const ChunkParams& p, uint8_t* ring, uint8_t* qbuf, Ch
                 }
                 continue;
             }
-            if (j == sub.a) ok = mbar_wait(smem_addr(&sm.q_full[I]), pieces & 1);
+            if (j == ja) ok = mbar_wait(smem_addr(&sm.q_full[I]), pieces & 1);
             if (!begun) {
                 ok = ok && mbar_wait(full + 8 * r, ph) && take_turn(sm);
                 if (!ok) break;
-                qk(j + 1 == sub.b);
+                qk(j + 1 == jb);
             }
             begun = false;
             ok = mbar_wait(full + 8 * r, ph) && mbar_wait(smem_addr(&sm.p_ready[I]), steps & 1);
             ++steps;
-            if (j == sub.a && pieces > 0)  // O of the last piece has been read
+            if (j == ja && pieces > 0)  // O of the last piece has been read
                 ok = ok && mbar_wait(smem_addr(&sm.o_free[I]), (pieces - 1) & 1);
             ok = ok && !sm.abort_flag && take_turn(sm);
             if (!ok) break;
             tc_fence_after();
             const int rk = r + 1 == C::kSlots ? 0 : r + 1;
-            begun = j + 1 < sub.b && mbar_try_wait(full + 8 * rk, rk ? ph : ph ^ 1);
+            begun = j + 1 < jb && mbar_try_wait(full + 8 * rk, rk ? ph : ph ^ 1);
             {
                 const uint64_t dv = dv0 + (uint32_t)(r * (C::kTile >> 4));
-                umma_ts(tO, tS, dv, id_o, j > sub.a);
+                umma_ts(tO, tS, dv, id_o, j > ja);
 #pragma unroll
                 for (int ks = 1; ks < kBlocks; ++ks) {
                     if (ks == kBlocks - 4 && !begun) end_turn(sm);
@@ -628,9 +649,9 @@ __device__ void chunk_mma(const ChunkParams& p, uint8_t* ring, uint8_t* qbuf, Ch
                 umma_commit(empty + 8 * r);
                 advance();
             }
-            if (begun) qk(j + 2 == sub.b);
+            if (begun) qk(j + 2 == jb);
         }
-        if (sub.a < sub.b) ++pieces;
+        if (ja < jb) ++pieces;
     }
     if (!ok) give_up(sm, p);
     umma_commit(smem_addr(&sm.done[I]));  // every MMA ends before tensor memory is freed
@@ -683,9 +704,11 @@ __device__ __forceinline__ void fold(int tid, int count, int pieces, const Part&
             float4 v[C][E];
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const float* q = part_of(min(c0 + c, pieces - 1));
+                const float* q = part_of(c0 + c);
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
+                    l[c][e] = 0.f;
+                    if (c0 + c >= pieces || x0 + e * kRows >= total) continue;
                     m[c][e] = __ldcg(q + kRows * H + r[e]);
                     l[c][e] = __ldcg(q + kRows * (H + 1) + r[e]);
                     v[c][e] = __ldcg(reinterpret_cast<const float4*>(q) + d[e] * kRows + r[e]);
@@ -696,7 +719,7 @@ __device__ __forceinline__ void fold(int tid, int count, int pieces, const Part&
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     bad |= l[c][e] < 0.f;
-                    if (c0 + c >= pieces || !(l[c][e] > 0.f)) continue;  // nothing seen in it
+                    if (!(l[c][e] > 0.f)) continue;  // nothing seen in it
                     const float top = fmaxf(M[e], m[c][e]);
                     const float f = fast_exp2(M[e] - top), w = fast_exp2(m[c][e] - top);
                     M[e] = top;
@@ -730,7 +753,15 @@ __device__ void chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
     const int i = (warp - kSoftWarp) >> 2;           // slot
     const int row = 32 * (warp & 3) + lane;          // tensor-memory lane
     const int tid = row;                             // within the slot's 128 threads
-    const int row_t = row / p.hpc, row_h = row % p.hpc;
+    const int row_t = row / p.hpc;
+    // Outputs are stored by quads of threads, each 64 bytes of a row of the quad at a time:
+    // the four rows, in 16-byte pieces from the tile's first
+    uint32_t quad[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const int r = (row & ~3) + x;
+        quad[x] = ((uint32_t)(r / p.hpc) * p.N + r % p.hpc) * (H / 8) + (lane & 3);
+    }
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tS = sm.tmem + kColS + i * 128 + lanes, tO = sm.tmem + kColO + i * 128 + lanes;
     const uint32_t bS = smem_addr(&sm.s_ready[i]), bP = smem_addr(&sm.p_ready[i]),
@@ -744,30 +775,31 @@ __device__ void chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
         ++meets;
         return ok;
     };
-    Walk wk;
-    wk.init(sm, p);
-    Piece pc;
-    int step = 0, item = -1, n0 = 0;
+    int step = 0, n0 = 0;
     bool ok = true;
-    while (ok && wk.next(sm, p, pc)) {
-        ++item;
+    for (int k = 0; ok; ++k) {
+        ok = __all_sync(kAll, piece_ready(sm, k));
+        if (!ok) break;
+        const Piece& pc = sm.pieces[k % kPieces];
+        const int t0 = pc.t0, ja = pc.a[i], jb = pc.b[i], count = pc.count[i];
+        if (t0 < 0) break;
         const int ring0 = n0;
-        n0 += 2 * (pc.t1 - pc.t0);
-        const Sub sub = sub_of(p, pc, i);
-        if (sub.f >= sub.e) continue;  // no tokens for this slot
-        const int kv = p.cpt > 1 ? pc.vh / p.cpt : pc.vh, h0 = (pc.vh - kv * p.cpt) * p.hpc;
-        const int heads = min(p.hpc, p.G - h0);
-        const int count = (sub.e - sub.f - 1) * p.hpc + heads;  // rows in use
+        n0 += 2 * (pc.t1 - t0);
+        auto release = [&]() {
+            __syncwarp();
+            if (lane == 0) piece_done(sm, k);
+        };
+        if (count == 0) {  // no tokens for this slot
+            release();
+            continue;
+        }
         const bool active = row < count;
         const bool warp_on = 32 * (warp & 3) < count;
-        const int at = pc.s.ctx - pc.s.n;  // position of the first new token
-        const int lim = at + sub.f + (active ? row_t : 0);
+        const int lim = pc.pos[i] + (active ? row_t : 0);
         const int low = p.window > 0 ? lim - p.window + 1 : 0;
-        // positions that the item's rows see at all
-        const int see_lo = p.window > 0 ? max(0, at + pc.f - p.window + 1) : 0;
-        const int see_hi = at + min(pc.s.n, pc.f + 2 * p.tpc);
+        const int see_lo = pc.see_lo, see_hi = pc.see_hi;
         float m = -INFINITY, l = 0.f;
-        for (int j = sub.a; j < sub.b; ++j, ++step) {
+        for (int j = ja; j < jb; ++j, ++step) {
             ok = __all_sync(kAll, mbar_wait(bS, step & 1));
             if (!ok) break;
             const int tok = j * kStep;
@@ -784,9 +816,11 @@ __device__ void chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
                         const int a = from - 32 * c, b = to - 32 * c;
                         const uint32_t seen = (b >= 32 ? ~0u : b <= 0 ? 0u : ~(~0u << b)) &
                                               (a <= 0 ? ~0u : a >= 32 ? 0u : ~0u << a);
+                        if (__any_sync(kAll, seen != ~0u)) {
 #pragma unroll
-                        for (int x = 0; x < 32; ++x)
-                            if (!(seen >> x & 1u)) s[c][x] = 0xff800000u;
+                            for (int x = 0; x < 32; ++x)
+                                if (!(seen >> x & 1u)) s[c][x] = 0xff800000u;
+                        }
                     }
                 }
                 float mx[4];
@@ -801,7 +835,7 @@ __device__ void chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
                 const bool need = top > m + kSlack;
                 if (__any_sync(kAll, need)) {
                     const float f = need && m != -INFINITY ? fast_exp2(m - top) : 1.f;
-                    if (j > sub.a && __any_sync(kAll, f != 1.f)) {  // the last PV has ended
+                    if (j > ja && __any_sync(kAll, f != 1.f)) {  // the last PV has ended
                         ok = __all_sync(kAll, mbar_wait(bO, (step - 1) & 1));
                         if (!ok) break;
                         tc_fence_after();
@@ -843,21 +877,23 @@ __device__ void chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
                 l += lo2(both) + hi2(both);
                 tmem_wait_st();
             }
-            // V rows that no row of the item sees hold anything: zeros, since 0 * NaN counts
+            // V rows of a block that rows of the item see in part: the others hold anything
+            // and become zeros, since 0 * NaN counts (whole blocks came as zeros)
             const int v0 = max(0, see_lo - tok), v1 = min(kStep, see_hi - tok);
-            if (v0 > 0 || v1 < kStep) {
-                const int nv = ring0 + 2 * (j - pc.t0) + 1;
+            const int z0 = v0 & 15, z = z0 + (-v1 & 15);  // rows before v0 and from v1 on
+            if (z > 0) {
+                const int nv = ring0 + 2 * (j - t0) + 1;
                 ok = __all_sync(kAll, mbar_wait(smem_addr(&sm.full[nv % C::kSlots]),
                                                 (nv / C::kSlots) & 1));
                 if (!ok) break;
                 const uint32_t vb = smem_addr(ring + (size_t)(nv % C::kSlots) * C::kTile);
                 // (every 16 bytes of a row, wherever the swizzle puts them)
-                for (int x = tid; x < kStep * (H / 8); x += kRows) {
-                    const int r = x / (H / 8), c = x % (H / 8);
-                    if (r < v0 || r >= v1)
-                        st_shared_v4(vb + (r >> 3) * C::kGroup + (c >> 3) * 1024 + (r & 7) * 128 +
-                                         (c & 7) * 16,
-                                     make_uint4(0, 0, 0, 0));
+                for (int x = tid; x < z * (H / 8); x += kRows) {
+                    const int k = x / (H / 8), c = x % (H / 8);
+                    const int r = k < z0 ? v0 - 1 - k : v1 + k - z0;
+                    st_shared_v4(vb + (r >> 3) * C::kGroup + (c >> 3) * 1024 + (r & 7) * 128 +
+                                     (c & 7) * 16,
+                                 make_uint4(0, 0, 0, 0));
                 }
                 fence_proxy_async_shared();
             }
@@ -867,56 +903,73 @@ __device__ void chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
         ok = __all_sync(kAll, ok);
         if (!ok) break;
         // ---- the tile's rows ------------------------------------------------------
-        const bool some = sub.a < sub.b;  // any KV tile in this piece
+        const bool some = ja < jb;  // any KV tile in this piece
         if (some) {
             ok = __all_sync(kAll, mbar_wait(bO, (step - 1) & 1));
             if (!ok) break;
             tc_fence_after();
         }
-        // O_i, 32 dims at a time, the next ones on their way while these are stored
+        // O_i, 32 dims at a time (a loop: code that runs once a piece is code that is not in
+        // the instruction cache)
         auto drain = [&](const auto& store) {
             if (warp_on && some) {
-                uint32_t o[2][32];
-                tmem_ld32(tO, o[0]);
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < H / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + 32 * c, o);
                     tmem_wait_ld();
-                    if (c + 1 < H / 32) tmem_ld32(tO + 32 * (c + 1), o[(c + 1) & 1]);
-                    if (active) store(c, o[c & 1]);
+                    store(c, o);
                 }
             }
             tc_fence_before();
             if (some) mbar_arrive(bF);
         };
         // (set before the tiles landed; without one, nothing has been waited for)
-        const bool bad = some && sm.bad[item % kBadRing] != 0;
+        const bool bad = some && sm.bad[k % kPieces] != 0;
         uint16_t* const out = static_cast<uint16_t*>(p.out) +
-                              (((size_t)pc.s.r0 + sub.f) * p.N + (size_t)kv * p.G + h0) * H;
-        if (!pc.split()) {
+                              ((size_t)pc.row0[i] * p.N + (size_t)pc.kv * p.G + pc.h0) * H;
+        const int first_cta = pc.first_cta, last_cta = pc.last_cta;
+        const int tile = pc.tile[i], pieces = last_cta - first_cta + 1;
+        release();
+        if (first_cta < 0) {
             const float inv = bad || !(l > 0.f) ? 0.f : 1.f / l;
-            uint4* dst = reinterpret_cast<uint4*>(out + ((size_t)row_t * p.N + row_h) * H);
+            uint4* dst = reinterpret_cast<uint4*>(out);
             drain([&](int c, const uint32_t (&o)[32]) {
+                uint32_t w[4][4];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    uint32_t w[4];
+                for (int x = 0; x < 16; ++x)
+                    w[x >> 2][x & 3] = inv == 0.f ? 0u
+                                                  : E::pack(__uint_as_float(o[2 * x]) * inv,
+                                                            __uint_as_float(o[2 * x + 1]) * inv);
+                // piece x of this thread's row <-> piece (lane & 3) of the quad's row x
 #pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        w[y] = inv == 0.f ? 0u
-                                          : E::pack(__uint_as_float(o[8 * x + 2 * y]) * inv,
-                                                    __uint_as_float(o[8 * x + 2 * y + 1]) * inv);
-                    dst[4 * c + x] = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int y = 0; y < 4; ++y) {
+#pragma unroll
+                    for (int x = 0; x < 4; x += 2) {
+                        const uint32_t u = __shfl_xor_sync(kAll, lane & 1 ? w[x][y] : w[x + 1][y], 1);
+                        w[x][y] = lane & 1 ? u : w[x][y];
+                        w[x + 1][y] = lane & 1 ? w[x + 1][y] : u;
+                    }
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint32_t u = __shfl_xor_sync(kAll, lane & 2 ? w[x][y] : w[x + 2][y], 2);
+                        w[x][y] = lane & 2 ? u : w[x][y];
+                        w[x + 2][y] = lane & 2 ? w[x + 2][y] : u;
+                    }
                 }
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    if ((row & ~3) + x < count)
+                        dst[quad[x] + 4 * c] = make_uint4(w[x][0], w[x][1], w[x][2], w[x][3]);
             });
             continue;
         }
         // a piece of an item that several CTAs share: [H/4][128 rows][4] values, maxima, sums
         const int me = blockIdx.x;
-        const int first_cta = (int)div_ll(pc.first, sm.quota);
-        const int last_cta = (int)div_ll(pc.first + (pc.hi - pc.lo) - 1, sm.quota);
-        const int tile = i ^ pc.slot, pieces = last_cta - first_cta + 1;
         {
             float* part = p.partials + ((size_t)(me * 2 + (me == first_cta)) * 2 + tile) * C::kPart;
             drain([&](int c, const uint32_t (&o)[32]) {
+                if (!active) return;
 #pragma unroll
                 for (int x = 0; x < 8; ++x)
                     __stcg(reinterpret_cast<uint4*>(part) + (8 * c + x) * kRows + row,
@@ -947,10 +1000,7 @@ __device__ void chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
             auto out_row = [&](int r) {
                 return out + ((size_t)(r / p.hpc) * p.N + r % p.hpc) * H;
             };
-            if (count * (H / 4) <= 2 * kRows)
-                fold<BF16, H, 2, 4>(tid, count, pieces, part_of, out_row);
-            else
-                fold<BF16, H, 8, 2>(tid, count, pieces, part_of, out_row);
+            fold<BF16, H, 4, 4>(tid, count, pieces, part_of, out_row);
             if (tid == 0) *flag = 0;  // as the next call wants it
         }
         // (no thread writes the ticket again before every thread has read it)
@@ -977,6 +1027,8 @@ __global__ void __launch_bounds__(kThreadsCh, 1)
         for (int s = 0; s < 8; ++s) {
             mbar_init(smem_addr(&sm.full[s]), 1);
             mbar_init(smem_addr(&sm.empty[s]), 2);
+            mbar_init(smem_addr(&sm.piece_full[s]), 1);
+            mbar_init(smem_addr(&sm.piece_free[s]), 3 + 8);  // issuers, loader, softmax warps
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&sm.q_full[i]), 1);
@@ -1006,14 +1058,12 @@ __global__ void __launch_bounds__(kThreadsCh, 1)
     tc_fence_after();
     if (warp < kSoftWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-        if (warp == 0)
-            chunk_mma<BF16, H, 0>(p, ring, qbuf, sm);
-        else if (warp == 1)
+        if (warp == 1)
             chunk_load<H>(&tmk, &tmv, p, ring, sm);
         else if (warp == 2)
-            chunk_queries<H>(&tmq, p, qbuf, sm);
+            chunk_schedule<H>(&tmq, p, qbuf, sm);
         else
-            chunk_mma<BF16, H, 1>(p, ring, qbuf, sm);
+            chunk_mma<BF16, H>(p, ring, qbuf, sm, warp == 0 ? 0 : 1);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
         chunk_softmax<BF16, H>(p, ring, sm);

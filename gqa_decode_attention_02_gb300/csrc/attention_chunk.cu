@@ -81,7 +81,7 @@ struct ChunkParams {
     const int32_t* context_lens;
     const int32_t* cu_new;  // nullptr: sequence b has the one row b
     int32_t* status;
-    int32_t* flags;         // tickets: two per CTA that holds a first piece
+    int32_t* flags;         // tickets: of the item whose first piece a CTA holds
     float* partials;        // [grid][2][2][kPart]: slot 0 a later piece, slot 1 a first one
     int B, M, N, K, G;
     int tpc, hpc, cpt, KC;  // tokens and heads of a row tile; head chunks per KV head
@@ -105,13 +105,19 @@ struct ChunkSmem {
     uint64_t full[8], empty[8];
     uint64_t piece_full[kPieces], piece_free[kPieces];
     // per slot (a row tile in the works: its Q, S, O and softmax warps)
-    uint64_t q_full[2], q_free[2], s_ready[2], p_ready[2], o_ready[2], o_free[2], group[2], done[2];
+    uint64_t q_full[2], q_free[2], s_ready[2], p_ready[2], o_ready[2], o_free[2], done[2];
+    uint64_t all;  // the softmax threads
     long long c0, c1, base;  // range of units; first unit of the first item
     long long quota;
     int b0, vh0, qi0, whole;
     uint32_t tmem, lock;
     volatile int abort_flag;
     volatile int bad[kPieces];
+    // the items that the CTA shares: 0 as a later piece of one, 1 as the first
+    struct {
+        int first_cta, pieces, kv, h0;
+    } shared[2];
+    int shared_rows[2][2], shared_count[2][2];  // per row tile
     int ticket[2];
     Piece pieces[kPieces];
 };
@@ -680,19 +686,19 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
-// Folds the pieces' rows of a slot's tile (its 128 threads): running maximum and sum
+// Folds the pieces' rows of a row tile (256 threads): running maximum and sum
 // over the pieces in order, four dims of a row at a time.  E of them a thread and C pieces
 // at once, so that their reads overlap.
 template <bool BF16, int H, int E, int C, class Part, class Row>
 __device__ __forceinline__ void fold(int tid, int count, int pieces, const Part& part_of,
                                      const Row& out_row) {
     const int total = count * (H / 4);
-    for (int x0 = tid; x0 < total; x0 += kRows * E) {
+    for (int x0 = tid; x0 < total; x0 += 2 * kRows * E) {
         float M[E], L[E], acc[E][4];
         int r[E], d[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const int x = min(x0 + e * kRows, total - 1);
+            const int x = min(x0 + e * 2 * kRows, total - 1);
             r[e] = x % count;
             d[e] = x / count;
             M[e] = -INFINITY;
@@ -708,7 +714,7 @@ __device__ __forceinline__ void fold(int tid, int count, int pieces, const Part&
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     l[c][e] = 0.f;
-                    if (c0 + c >= pieces || x0 + e * kRows >= total) continue;
+                    if (c0 + c >= pieces || x0 + e * 2 * kRows >= total) continue;
                     m[c][e] = __ldcg(q + kRows * H + r[e]);
                     l[c][e] = __ldcg(q + kRows * (H + 1) + r[e]);
                     v[c][e] = __ldcg(reinterpret_cast<const float4*>(q) + d[e] * kRows + r[e]);
@@ -732,7 +738,7 @@ __device__ __forceinline__ void fold(int tid, int count, int pieces, const Part&
         }
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            if (x0 + e * kRows >= total) break;
+            if (x0 + e * 2 * kRows >= total) break;
             uint2 y = make_uint2(0u, 0u);
             if (!bad && L[e] > 0.f) {
                 const float inv = 1.f / L[e];
@@ -746,7 +752,7 @@ __device__ __forceinline__ void fold(int tid, int count, int pieces, const Part&
 
 // Softmax of the row tiles in slot i, a thread per row.
 template <bool BF16, int H>
-__device__ void chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm) {
+__device__ bool chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm) {
     using C = Ch<H>;
     using E = Elt<BF16>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -765,16 +771,8 @@ __device__ void chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tS = sm.tmem + kColS + i * 128 + lanes, tO = sm.tmem + kColO + i * 128 + lanes;
     const uint32_t bS = smem_addr(&sm.s_ready[i]), bP = smem_addr(&sm.p_ready[i]),
-                   bO = smem_addr(&sm.o_ready[i]), bF = smem_addr(&sm.o_free[i]),
-                   bG = smem_addr(&sm.group[i]);
+                   bO = smem_addr(&sm.o_ready[i]), bF = smem_addr(&sm.o_free[i]);
     const uint64_t scale2 = pair2(p.scale_log2, p.scale_log2);
-    int meets = 0;
-    auto meet = [&]() {  // the slot's 128 threads
-        mbar_arrive(bG);
-        const bool ok = mbar_wait(bG, meets & 1);
-        ++meets;
-        return ok;
-    };
     int step = 0, n0 = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -805,24 +803,30 @@ __device__ void chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
             const int tok = j * kStep;
             if (warp_on) {
                 tc_fence_after();
-                uint32_t s[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, s[c]);
-                tmem_wait_ld();
                 const int from = low - tok, to = lim + 1 - tok;  // columns seen
                 if (!__all_sync(kAll, from <= 0 && to >= kStep)) {
-#pragma unroll
+                    // some are not: -inf there, in tensor memory (a loop of its own, so
+                    // that the code of the tiles seen whole stays short)
+#pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         const int a = from - 32 * c, b = to - 32 * c;
                         const uint32_t seen = (b >= 32 ? ~0u : b <= 0 ? 0u : ~(~0u << b)) &
                                               (a <= 0 ? ~0u : a >= 32 ? 0u : ~0u << a);
-                        if (__any_sync(kAll, seen != ~0u)) {
+                        if (__all_sync(kAll, seen == ~0u)) continue;
+                        uint32_t x[32];
+                        tmem_ld32(tS + 32 * c, x);
+                        tmem_wait_ld();
 #pragma unroll
-                            for (int x = 0; x < 32; ++x)
-                                if (!(seen >> x & 1u)) s[c][x] = 0xff800000u;
-                        }
+                        for (int e = 0; e < 32; ++e)
+                            if (!(seen >> e & 1u)) x[e] = 0xff800000u;
+                        tmem_st32(tS + 32 * c, x);
                     }
+                    tmem_wait_st();
                 }
+                uint32_t s[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, s[c]);
+                tmem_wait_ld();
                 float mx[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -909,32 +913,40 @@ __device__ void chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
             if (!ok) break;
             tc_fence_after();
         }
-        // O_i, 32 dims at a time (a loop: code that runs once a piece is code that is not in
-        // the instruction cache)
-        auto drain = [&](const auto& store) {
-            if (warp_on && some) {
-#pragma unroll 1
-                for (int c = 0; c < H / 32; ++c) {
-                    uint32_t o[32];
-                    tmem_ld32(tO + 32 * c, o);
-                    tmem_wait_ld();
-                    store(c, o);
-                }
-            }
-            tc_fence_before();
-            if (some) mbar_arrive(bF);
-        };
         // (set before the tiles landed; without one, nothing has been waited for)
         const bool bad = some && sm.bad[k % kPieces] != 0;
-        uint16_t* const out = static_cast<uint16_t*>(p.out) +
-                              ((size_t)pc.row0[i] * p.N + (size_t)pc.kv * p.G + pc.h0) * H;
-        const int first_cta = pc.first_cta, last_cta = pc.last_cta;
-        const int tile = pc.tile[i], pieces = last_cta - first_cta + 1;
+        const int first_cta = pc.first_cta, tile = pc.tile[i];
+        uint4* const out = reinterpret_cast<uint4*>(
+            static_cast<uint16_t*>(p.out) +
+            ((size_t)pc.row0[i] * p.N + (size_t)pc.kv * p.G + pc.h0) * H);
+        const int w = (int)blockIdx.x == first_cta;  // an item's first piece ends its CTA's range
+        if (first_cta >= 0 && tid == 0)
+            sm.shared[w] = {first_cta, pc.last_cta - first_cta + 1, pc.kv, pc.h0};
+        if (first_cta >= 0 && tid == 0) {
+            sm.shared_rows[w][tile] = pc.row0[i];
+            sm.shared_count[w][tile] = count;
+        }
         release();
-        if (first_cta < 0) {
-            const float inv = bad || !(l > 0.f) ? 0.f : 1.f / l;
-            uint4* dst = reinterpret_cast<uint4*>(out);
-            drain([&](int c, const uint32_t (&o)[32]) {
+        // a piece of an item that several CTAs share: [H/4][128 rows][4] values, maxima, sums
+        float* const part =
+            p.partials + ((size_t)((int)blockIdx.x * 2 + w) * 2 + tile) * C::kPart;
+        const float inv = first_cta >= 0 ? 1.f : bad || !(l > 0.f) ? 0.f : 1.f / l;
+        // O_i, 32 dims at a time (a loop: code that runs once a piece is not in the
+        // instruction cache)
+        if (warp_on && some) {
+#pragma unroll 1
+            for (int c = 0; c < H / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(tO + 32 * c, o);
+                tmem_wait_ld();
+                if (first_cta >= 0) {
+                    if (active)
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            __stcg(reinterpret_cast<uint4*>(part) + (8 * c + x) * kRows + row,
+                                   make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]));
+                    continue;
+                }
                 uint32_t w[4][4];
 #pragma unroll
                 for (int x = 0; x < 16; ++x)
@@ -960,53 +972,70 @@ __device__ void chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
                     if ((row & ~3) + x < count)
-                        dst[quad[x] + 4 * c] = make_uint4(w[x][0], w[x][1], w[x][2], w[x][3]);
-            });
-            continue;
+                        out[quad[x] + 4 * c] = make_uint4(w[x][0], w[x][1], w[x][2], w[x][3]);
+            }
         }
-        // a piece of an item that several CTAs share: [H/4][128 rows][4] values, maxima, sums
-        const int me = blockIdx.x;
-        {
-            float* part = p.partials + ((size_t)(me * 2 + (me == first_cta)) * 2 + tile) * C::kPart;
-            drain([&](int c, const uint32_t (&o)[32]) {
-                if (!active) return;
-#pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    __stcg(reinterpret_cast<uint4*>(part) + (8 * c + x) * kRows + row,
-                           make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]));
-            });
+        tc_fence_before();
+        if (some) mbar_arrive(bF);
+        if (first_cta >= 0) {
             __stcg(part + kRows * H + row, m);
             __stcg(part + kRows * (H + 1) + row, bad ? -1.f : l);  // a bad block shows as -1
         }
-        __threadfence();
-        int32_t* const flag = p.flags + 2 * first_cta + tile;
-        ok = meet();
-        if (ok && tid == 0) {
+    }
+    if (!ok) give_up(sm, p);
+    return ok;
+}
+
+// The softmax warps, when every piece of the CTA is done: for the items that it shares with
+// others (the one that its range begins in, the one that it ends in), a ticket; the CTA
+// that draws an item's last one folds the pieces.
+template <bool BF16, int H>
+__device__ void chunk_shared(const ChunkParams& p, ChunkSmem& sm) {
+    using C = Ch<H>;
+    const int tid = threadIdx.x - 32 * kSoftWarp;
+    __threadfence();  // partial results before the ticket
+    int meets = 0;
+    auto meet = [&]() {  // the softmax threads
+        mbar_arrive(smem_addr(&sm.all));
+        const bool ok = mbar_wait(smem_addr(&sm.all), meets & 1);
+        ++meets;
+        return ok;
+    };
+    if (!meet()) return give_up(sm, p);
+#pragma unroll 1
+    for (int w = 0; w < 2; ++w) {
+        const int first_cta = sm.shared[w].first_cta, pieces = sm.shared[w].pieces;
+        if (pieces == 0) continue;
+        if (tid == 0) {
             unsigned v;
             asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
                          : "=r"(v)
-                         : "l"(flag)
+                         : "l"(p.flags + first_cta)
                          : "memory");
-            sm.ticket[i] = (int)v;
+            sm.ticket[w] = (int)v;
+            if ((int)v == pieces - 1) p.flags[first_cta] = 0;  // as the next call wants it
         }
-        ok = __all_sync(kAll, ok && meet());
-        if (!ok) break;
-        if (sm.ticket[i] == pieces - 1) {
-            __threadfence();
+        if (!meet()) return give_up(sm, p);
+        if (sm.ticket[w] != pieces - 1) continue;
+        __threadfence();
+#pragma unroll 1
+        for (int tile = 0; tile < 2; ++tile) {
+            const int count = sm.shared_count[w][tile];
+            if (count == 0) continue;
             auto part_of = [&](int c) {
                 return p.partials +
                        ((size_t)((first_cta + c) * 2 + (c == 0)) * 2 + tile) * C::kPart;
             };
+            uint16_t* const out =
+                static_cast<uint16_t*>(p.out) +
+                ((size_t)sm.shared_rows[w][tile] * p.N + (size_t)sm.shared[w].kv * p.G +
+                 sm.shared[w].h0) * H;
             auto out_row = [&](int r) {
                 return out + ((size_t)(r / p.hpc) * p.N + r % p.hpc) * H;
             };
             fold<BF16, H, 4, 4>(tid, count, pieces, part_of, out_row);
-            if (tid == 0) *flag = 0;  // as the next call wants it
         }
-        // (no thread writes the ticket again before every thread has read it)
-        ok = __all_sync(kAll, meet());
     }
-    if (!ok) give_up(sm, p);
 }
 
 template <bool BF16, int H>
@@ -1037,11 +1066,13 @@ __global__ void __launch_bounds__(kThreadsCh, 1)
             mbar_init(smem_addr(&sm.p_ready[i]), kRows);
             mbar_init(smem_addr(&sm.o_ready[i]), 1);
             mbar_init(smem_addr(&sm.o_free[i]), kRows);
-            mbar_init(smem_addr(&sm.group[i]), kRows);
             mbar_init(smem_addr(&sm.done[i]), 1);
         }
         sm.abort_flag = 0;
         sm.lock = 0;
+        mbar_init(smem_addr(&sm.all), 2 * kRows);
+        sm.shared[0].pieces = sm.shared[1].pieces = 0;
+        for (int i = 0; i < 4; ++i) sm.shared_count[i >> 1][i & 1] = 0;
         fence_mbar_init();
     }
     if (threadIdx.x == 64) {
@@ -1066,7 +1097,7 @@ __global__ void __launch_bounds__(kThreadsCh, 1)
             chunk_mma<BF16, H>(p, ring, qbuf, sm, warp == 0 ? 0 : 1);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
-        chunk_softmax<BF16, H>(p, ring, sm);
+        if (chunk_softmax<BF16, H>(p, ring, sm)) chunk_shared<BF16, H>(p, sm);
     }
     tc_fence_before();
     __syncthreads();
@@ -1107,7 +1138,7 @@ bool query_map(CUtensorMap* m, const void* q, const gqa_shape& s, long long rows
 
 size_t chunk_workspace_bytes(const gqa_shape& s, size_t flags_bytes) {
     const int sms = device_sm_count();
-    if (sms < 1 || (size_t)sms * 2 * sizeof(int32_t) > flags_bytes) return 0;
+    if (sms < 1 || (size_t)sms * sizeof(int32_t) > flags_bytes) return 0;
     return flags_bytes + (size_t)sms * 4 * kRows * (s.H + 2) * sizeof(float);
 }
 

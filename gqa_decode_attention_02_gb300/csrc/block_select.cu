@@ -52,6 +52,25 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w) {
     return one(w & 0xffffu) | one(w >> 16) << 16;
 }
 
+template <bool BF16>
+__device__ __forceinline__ uint32_t larger2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    if constexpr (BF16)
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else
+        asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t smaller2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    if constexpr (BF16)
+        asm("min.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else
+        asm("min.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // A warp per block and KV head: 16 rows of H elements, 16 bytes a lane and row (H = 128:
 // two rows at a time).  The units of all sequences lie end to end, a warp takes every
 // W-th of them and looks up whose it is 32 sequences at a time.  Bound by reading the
@@ -123,23 +142,22 @@ __global__ void __launch_bounds__(kBoundThreads) block_bounds_kernel(const Bound
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
-            float top[8], low[8];
+            uint32_t top[4], low[4];  // two elements a word
 #pragma unroll
             for (int j = 0; j < 16 / R; ++j) {
                 const uint32_t a[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float x = e & 1 ? Elt<BF16>::hi(a[e >> 1]) : Elt<BF16>::lo(a[e >> 1]);
-                    top[e] = j ? fmaxf(top[e], x) : x;
-                    low[e] = j ? fminf(low[e], x) : x;
+                for (int e = 0; e < 4; ++e) {
+                    top[e] = j ? larger2<BF16>(top[e], a[e]) : a[e];
+                    low[e] = j ? smaller2<BF16>(low[e], a[e]) : a[e];
                 }
             }
 #pragma unroll
             for (int o = P; o < 32; o <<= 1)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    top[e] = fmaxf(top[e], __shfl_xor_sync(kFull, top[e], o));
-                    low[e] = fminf(low[e], __shfl_xor_sync(kFull, low[e], o));
+                for (int e = 0; e < 4; ++e) {
+                    top[e] = larger2<BF16>(top[e], __shfl_xor_sync(kFull, top[e], o));
+                    low[e] = smaller2<BF16>(low[e], __shfl_xor_sync(kFull, low[e], o));
                 }
             const float s = __fdiv_rn(Elt<BF16>::lo(m), 127.f);
             if (sub < 2) {  // lanes of the first row write the largest, of the second the smallest
@@ -147,8 +165,10 @@ __global__ void __launch_bounds__(kBoundThreads) block_bounds_kernel(const Bound
                 if (s > 0.f) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float y = sub ? floorf(__fdiv_rn(low[e], s)) : ceilf(__fdiv_rn(top[e], s));
-                        const int code = (int)fminf(fmaxf(y, -127.f), 127.f);
+                        const uint32_t x = sub ? low[e >> 1] : top[e >> 1];
+                        const float y = __fdiv_rn(e & 1 ? Elt<BF16>::hi(x) : Elt<BF16>::lo(x), s);
+                        const float z = sub ? floorf(y) : ceilf(y);
+                        const int code = (int)fminf(fmaxf(z, -127.f), 127.f);
                         word[e >> 2] |= (uint32_t)(code & 0xff) << (8 * (e & 3));
                     }
                 }

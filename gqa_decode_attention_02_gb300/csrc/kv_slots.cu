@@ -323,10 +323,9 @@ __global__ void __launch_bounds__(kSlotThreads) kv_take_kernel(const SlotParams 
 //     x1' = x1 c - x2 s,  x2' = x2 c + x1 s
 // Each product and the sum are rounded in fp32 one by one (no fma: the result does not
 // depend on how a compiler joins them), then to the 16-bit type; what is stored is then
-// what kv_append_slots stores of that row.  A thread makes 8 elements and reads their
-// partners itself (the same 128-byte lines, by a lane of the same warp: no second trip to
-// memory, and q may be rotated in place, since a warp reads all it needs before it
-// writes).  Bound by moving q, k and v once each way.
+// what kv_append_slots stores of that row.  A thread makes 8 elements; their partners are
+// another lane's of the warp (the lanes of a row are neighbours) and come by shuffles, so q
+// may be rotated in place.  Bound by moving q, k and v once each way.
 struct RotaryParams {
     const uint4* q;
     uint4* q_out;
@@ -377,6 +376,10 @@ __device__ __forceinline__ int partner(const RotaryParams& r, int c) {
     const int h = r.R / 16;
     return c < h ? c + h : c - h;
 }
+__device__ __forceinline__ uint4 shuffle(uint4 v, uint32_t from) {
+    return make_uint4(__shfl_sync(0xffffffffu, v.x, from), __shfl_sync(0xffffffffu, v.y, from),
+                      __shfl_sync(0xffffffffu, v.z, from), __shfl_sync(0xffffffffu, v.w, from));
+}
 template <bool BF16, bool PAIRS>
 __device__ __forceinline__ uint4 turn(const RotaryParams& r, const Angles<PAIRS>& a, int part,
                                       uint4 own, uint4 other) {
@@ -418,29 +421,27 @@ __global__ void __launch_bounds__(kSlotThreads)
             const uint32_t j = on ? it : q_work - 1, rk = j / P, c = j % P;
             const uint32_t row = (__umulhi(rk, r.hmul) + rk) >> r.hshift, g = rk - row * r.hg;
             const int at = on ? position_of(p, r, row, c == 0 && g == 0) : -1;
-            uint4 own[kHeads], other[kHeads];
+            uint4 own[kHeads];
             const bool turns = (int)(8 * c) < r.R;
             const uint4* src = r.q + (size_t)row * r.q_stride;
-            const int pc = turns && !PAIRS ? partner(r, (int)c) : (int)c;
+            const uint32_t lane = threadIdx.x & 31;
+            const uint32_t from = turns && !PAIRS ? lane - c + partner(r, (int)c) : lane;
 #pragma unroll
             for (int h = 0; h < kHeads; ++h) {
                 const uint32_t n = g * kHeads + h;
-                if (at >= 0 && n < r.N) {
-                    own[h] = src[n * P + c];
-                    if (!PAIRS) other[h] = src[n * P + pc];
-                }
+                own[h] = make_uint4(0, 0, 0, 0);
+                if (at >= 0 && n < r.N) own[h] = src[n * P + c];
             }
-            __syncwarp();  // a row's parts are read before any is written (in place)
-            if (at < 0) continue;
             Angles<PAIRS> a;
-            if (turns) a.load(r, at, (int)c);
+            if (turns && at >= 0) a.load(r, at, (int)c);
             uint4* dst = r.q_out + (size_t)row * r.N * P;
 #pragma unroll
             for (int h = 0; h < kHeads; ++h) {
                 const uint32_t n = g * kHeads + h;
-                if (n < r.N)
-                    dst[n * P + c] = turns ? turn<BF16, PAIRS>(r, a, (int)c, own[h], other[h])
-                                           : own[h];
+                const uint4 other = PAIRS ? own[h] : shuffle(own[h], from);
+                if (at >= 0 && n < r.N)
+                    dst[n * P + c] =
+                        turns ? turn<BF16, PAIRS>(r, a, (int)c, own[h], other) : own[h];
             }
             continue;
         }
@@ -457,13 +458,20 @@ __global__ void __launch_bounds__(kSlotThreads)
         for (int x = 0; x < V; ++x) {
             const int part = (int)c * V + x;
             kw[x] = vw[x] = make_uint4(0, 0, 0, 0);
-            if (s < 0) continue;
-            kw[x] = __ldg(ks + part);
-            vw[x] = __ldg(vs + part);
-            if (8 * part < r.R) {
+            uint4 other = kw[x];
+            if (s >= 0) {
+                kw[x] = __ldg(ks + part);
+                vw[x] = __ldg(vs + part);
+                // (16 elements a thread: the partner may be either part of its thread)
+                if (!PAIRS && V == 2 && 8 * part < r.R) other = __ldg(ks + partner(r, part));
+            }
+            if (!PAIRS && V == 1) {
+                const uint32_t lane = threadIdx.x & 31;
+                other = shuffle(kw[x], 8 * part < r.R ? lane - c + partner(r, part) : lane);
+            }
+            if (s >= 0 && 8 * part < r.R) {
                 Angles<PAIRS> a;
                 a.load(r, at, part);
-                const uint4 other = PAIRS ? kw[x] : __ldg(ks + partner(r, part));
                 kw[x] = turn<BF16, PAIRS>(r, a, part, kw[x], other);
             }
         }

@@ -72,27 +72,28 @@ __device__ __forceinline__ uint32_t smaller2(uint32_t a, uint32_t b) {
 }
 
 // A warp per block and KV head: 16 rows of H elements, 16 bytes a lane and row (H = 128:
-// two rows at a time).  The units of all sequences lie end to end, a warp takes every
-// W-th of them and looks up whose it is 32 sequences at a time.  Bound by reading the
-// keys once.
+// two rows at a time).  The units of 256 sequences at a time lie end to end (a prefix
+// sum of the CTA), a warp takes every W-th of them.  Bound by reading the keys once.
 template <bool BF16, int H>
-__global__ void __launch_bounds__(kBoundThreads) block_bounds_kernel(const BoundParams p) {
+__global__ void __launch_bounds__(kBoundThreads, 4) block_bounds_kernel(const BoundParams p) {
     constexpr int P = H / 8, R = 32 / P;  // lanes per row, rows at a time
+    __shared__ int s_end[kBoundThreads], s_first[kBoundThreads], s_ctx[kBoundThreads];
+    __shared__ int s_warp[kBoundThreads / 32];
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31, c = lane % P, sub = lane / P;
+    const uint32_t K = (uint32_t)p.K;
     const long long W = (long long)gridDim.x * (kBoundThreads / 32);
     long long id = (long long)blockIdx.x * (kBoundThreads / 32) + (threadIdx.x >> 5);
-    const bool reporter = id == 0;
     long long base = 0;  // units of the sequences before b0
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const int b = b0 + lane;
+    for (int b0 = 0; b0 < p.B; b0 += kBoundThreads) {
+        const int b = b0 + (int)threadIdx.x;
         int ctx = 0, i0 = 0, n = 0;  // length; first touched block and how many
         if (b < p.B) {
             ctx = __ldg(p.context_lens + b);
             const int add = __ldg(p.cu_new + b + 1) - __ldg(p.cu_new + b);
             if (add < 0 || (add > 0 && (ctx < add || ctx > p.max_blocks * 16))) {
-                if (reporter) report(p.status, GQA_ERR_CONTEXT);
+                if (blockIdx.x == 0) report(p.status, GQA_ERR_CONTEXT);
             } else if (add > 0) {
                 i0 = (ctx - add) >> 4;
                 n = ((ctx + 15) >> 4) - i0;
@@ -104,12 +105,28 @@ __global__ void __launch_bounds__(kBoundThreads) block_bounds_kernel(const Bound
             const int x = __shfl_up_sync(kFull, incl, o);
             if (lane >= o) incl += x;
         }
-        const long long units = (long long)__shfl_sync(kFull, incl, 31) * p.K;
+        if (b0 > 0) __syncthreads();  // the last sequences' entries have been read
+        if (lane == 31) s_warp[threadIdx.x >> 5] = incl;
+        __syncthreads();
+        int blocks = 0;
+#pragma unroll
+        for (int w = 0; w < kBoundThreads / 32; ++w) {
+            if (w < (int)(threadIdx.x >> 5)) incl += s_warp[w];
+            blocks += s_warp[w];
+        }
+        s_end[threadIdx.x] = incl;
+        s_first[threadIdx.x] = i0 - (incl - n);
+        s_ctx[threadIdx.x] = ctx;
+        __syncthreads();
+        const long long units = (long long)blocks * K;
         for (; id < base + units; id += W) {
-            const int u = (int)((id - base) / p.K), k = (int)((id - base) % p.K);
-            const int src = __popc(__ballot_sync(kFull, incl <= u));
-            const int at = __shfl_sync(kFull, i0, src) + u - __shfl_sync(kFull, incl - n, src);
-            const int held = min(16, __shfl_sync(kFull, ctx, src) - at * 16);
+            const uint32_t v = (uint32_t)(id - base), u = v / K, k = v - u * K;
+            int src = 0;  // whose it is
+#pragma unroll
+            for (int o = kBoundThreads / 2; o > 0; o >>= 1)
+                if (s_end[src + o - 1] <= (int)u) src += o;
+            const int at = s_first[src] + (int)u;
+            const int held = min(16, s_ctx[src] - at * 16);
             const int blk = __ldg(p.block_tables + (size_t)(b0 + src) * p.max_blocks + at);
             if (blk < 0 || blk >= p.num_blocks) {
                 if (lane == 0) report(p.status, GQA_ERR_BLOCK_ID);
@@ -259,10 +276,16 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const Select
     const int32_t* table = p.block_tables + (size_t)b * p.max_blocks;
     float* out = p.scores + (size_t)bk * p.max_blocks;
     const int tiles = (nb + 15) / 16, g = lane >> 2, t = lane & 3;
-    for (int tile = part * (kScoreThreads / 32) + warp; tile < tiles;
-         tile += p.splits * (kScoreThreads / 32)) {
-        const int i = tile * 16 + (lane & 15);
-        int id = i < nb ? __ldg(table + i) : 0;
+    const int stride = p.splits * (kScoreThreads / 32);
+    int tile = part * (kScoreThreads / 32) + warp;
+    auto load_id = [&](int x) {
+        const int i = x * 16 + (lane & 15);
+        return i < nb ? __ldg(table + i) : 0;
+    };
+    int ahead = load_id(tile);
+    for (; tile < tiles; tile += stride) {
+        int id = ahead;
+        ahead = load_id(tile + stride);
         const bool bad = id < 0 || id >= p.num_blocks;
         if (bad) id = 0;
         if (bad && k == 0 && lane < 16) report(p.status, GQA_ERR_BLOCK_ID);
@@ -311,8 +334,7 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const Select
 }
 
 // ---- the choice --------------------------------------------------------------------
-constexpr int kPickThreads = 512;
-constexpr int kPickHeld = 11520;  // scores held in shared memory; more are read again
+constexpr int kPickHeld = 9600;  // scores held in shared memory; more are read again
 
 // Order-preserving bits of a score (-0 as 0; a NaN, which a scale that holds one gives,
 // below every number).
@@ -322,18 +344,22 @@ __device__ __forceinline__ uint32_t score_key(float x) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// A CTA per sequence and KV head: the key of the last block to take by four passes over
-// eight bits each (a histogram of the candidates that share the bits found so far), then
-// the blocks above it and as many of those at it as are left, in order.
-__global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectParams p) {
-    __shared__ int hist[256];
-    __shared__ int sums[2][kPickThreads / 32];
-    __shared__ uint32_t s_prefix;
+// A CTA per sequence and KV head: the key of the last block to take by passes over eleven
+// bits each (a histogram of the candidates that share the bits found so far), from the
+// first bit in which any two candidates differ -- the leading ones, sign and exponent, are
+// mostly alike, and a histogram of them would be one bin --; then the blocks above it and as
+// many of those at it as are left, in order.
+__global__ void __launch_bounds__(1024) block_pick_kernel(const SelectParams p) {
+    constexpr int kBits = 11, kBins = 1 << kBits;
+    __shared__ int hist[kBins];
+    __shared__ int sums[2][32];
+    __shared__ uint32_t s_or, s_and, s_prefix;
     __shared__ int s_left;
     extern __shared__ uint32_t keys[];
     griddep_launch_dependents();
     griddep_wait();
-    const int bk = blockIdx.x, b = bk / p.K, k = bk - b * p.K, tid = threadIdx.x;
+    const int bk = blockIdx.x, b = bk / p.K, k = bk - b * p.K;
+    const int tid = threadIdx.x, threads = blockDim.x;
     const int lane = tid & 31, warp = tid >> 5;
     const int ctx = __ldg(p.context_lens + b), nb = blocks_of(p, ctx);
     const int32_t* table = p.block_tables + (size_t)b * p.max_blocks;
@@ -344,9 +370,9 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectPa
         p.lens[b] = nb ? (held - 1) * 16 + ctx - (nb - 1) * 16 : 0;
         if (nb == 0) report(p.status, GQA_ERR_CONTEXT);
     }
-    for (int i = held + tid; i < p.keep; i += kPickThreads) tables[i] = blocks[i] = -1;
+    for (int i = held + tid; i < p.keep; i += threads) tables[i] = blocks[i] = -1;
     if (nb <= p.keep) {
-        for (int i = tid; i < nb; i += kPickThreads) {
+        for (int i = tid; i < nb; i += threads) {
             tables[i] = __ldg(table + i);
             blocks[i] = i;
         }
@@ -355,7 +381,7 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectPa
     // blocks [lo, hi) compete for `left` places
     const int lo = p.first, hi = nb - p.recent, count = hi - lo;
     int left = p.keep - p.first - p.recent;
-    for (int i = tid; i < p.first + p.recent; i += kPickThreads) {
+    for (int i = tid; i < p.first + p.recent; i += threads) {
         const int at = i < p.first ? i : hi + i - p.first;
         const int to = i < p.first ? i : p.keep - p.recent + i - p.first;
         tables[to] = __ldg(table + at);
@@ -364,42 +390,66 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectPa
     if (left == 0) return;
     const float* scores = p.scores + (size_t)bk * p.max_blocks + lo;
     const bool in_smem = count <= kPickHeld;
-    if (in_smem)
-        for (int i = tid; i < count; i += kPickThreads) keys[i] = score_key(__ldcg(scores + i));
+    if (tid == 0) {
+        s_or = 0u;
+        s_and = ~0u;
+    }
+    __syncthreads();
+    uint32_t any = 0u, all = ~0u;
+    for (int i = tid; i < count; i += threads) {
+        const uint32_t u = score_key(__ldcg(scores + i));
+        if (in_smem) keys[i] = u;
+        any |= u;
+        all &= u;
+    }
+    any = __reduce_or_sync(kFull, any);
+    all = __reduce_and_sync(kFull, all);
+    if (lane == 0) {
+        atomicOr(&s_or, any);
+        atomicAnd(&s_and, all);
+    }
+    __syncthreads();
     auto key = [&](int i) { return in_smem ? keys[i] : score_key(__ldcg(scores + i)); };
-    uint32_t prefix = 0;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
+    int bits = 32 - __clz(s_or ^ s_and);  // low bits in which keys differ
+    uint32_t prefix = bits == 32 ? 0u : s_and >> bits << bits;
+    while (bits > 0) {
+        const int take = min(bits, kBits), shift = bits - take, bins = 1 << take;
+        for (int i = tid; i < bins; i += threads) hist[i] = 0;
         __syncthreads();
-        const uint32_t known = shift == 24 ? 0u : ~0u << (shift + 8);
-        for (int i = tid; i < count; i += kPickThreads) {
+        const uint32_t known = bits == 32 ? 0u : ~0u << bits;
+        for (int i = tid; i < count; i += threads) {
             const uint32_t u = key(i);
-            if ((u & known) == prefix) atomicAdd(&hist[u >> shift & 255u], 1);
+            if ((u & known) == prefix) atomicAdd(&hist[u >> shift & (bins - 1)], 1);
         }
         __syncthreads();
-        if (warp == 0) {  // bin of the left-th largest: lane l has bins 255 - 8 l ..
-            int n[8], own = 0;
+        // bin of the left-th largest: thread t < 512 has the `per` bins from the top's t-th
+        const int per = (bins + 511) / 512, t0 = bins - 1 - tid * per;
+        int own = 0;
+        if (tid < 512)
+            for (int x = 0; x < per; ++x)
+                if (t0 - x >= 0) own += hist[t0 - x];
+        int incl = own;
 #pragma unroll
-            for (int x = 0; x < 8; ++x) own += n[x] = hist[255 - 8 * lane - x];
-            int incl = own;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(kFull, incl, o);
-                if (lane >= o) incl += y;
-            }
-            if (incl - own < left && left <= incl) {
-                int above = incl - own, x = 0;
-                while (above + n[x] < left) above += n[x++];
-                s_prefix = prefix | (uint32_t)(255 - 8 * lane - x) << shift;
-                s_left = left - above;
-            }
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kFull, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) sums[0][warp] = incl;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) incl += sums[0][w];
+        if (tid < 512 && incl - own < left && left <= incl) {
+            int above = incl - own, x = 0;
+            while (above + hist[t0 - x] < left) above += hist[t0 - x++];
+            s_prefix = prefix | (uint32_t)(t0 - x) << shift;
+            s_left = left - above;
         }
         __syncthreads();
         prefix = s_prefix;
         left = s_left;
+        bits = shift;
     }
     // a run of blocks per thread: how many lie above the key and at it, before it too
-    const int run = (count + kPickThreads - 1) / kPickThreads;
+    const int run = (count + threads - 1) / threads;
     const int from = min(count, tid * run), to = min(count, from + run);
     int above = 0, equal = 0;
     for (int i = from; i < to; ++i) {
@@ -416,6 +466,7 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectPa
             ie += y;
         }
     }
+    __syncthreads();
     if (lane == 31) {
         sums[0][warp] = ia;
         sums[1][warp] = ie;
@@ -428,8 +479,7 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectPa
     int a = ia - above, e = ie - equal;
     for (int i = from; i < to; ++i) {
         const uint32_t u = key(i);
-        const bool take = u > prefix || (u == prefix && e < left);
-        if (take) {
+        if (u > prefix || (u == prefix && e < left)) {
             const int at = p.first + a + min(e, left);
             tables[at] = __ldg(table + lo + i);
             blocks[at] = lo + i;
@@ -512,7 +562,8 @@ gqa_status launch_select_blocks(const gqa_shape& s, int keep, int first, int rec
         cfg.numAttrs = (s.flags & (GQA_FLAG_PDL | GQA_FLAG_EARLY_KV)) ? 1 : 0;
     }
     cfg.gridDim = dim3((unsigned)bk);
-    cfg.blockDim = dim3(kPickThreads);
+    // as many threads as let every row be resident at once, within 512 .. 1024
+    cfg.blockDim = dim3(bk <= 2 * sms ? 1024 : 512);
     // (static and dynamic together within what needs no opt-in)
     cfg.dynamicSmemBytes =
         sizeof(uint32_t) * (size_t)(s.max_blocks_per_seq < kPickHeld ? s.max_blocks_per_seq

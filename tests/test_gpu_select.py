@@ -138,7 +138,7 @@ def test_ties_go_to_the_lowest_block(gpu, keep):
     check_select(gpu, (q, -codes.abs(), scale, tables, ctx), keep, 0, 1)  # scores below zero
 
 
-@pytest.mark.parametrize("n", [11519 * 16, 11520 * 16 + 48, 30000 * 16])
+@pytest.mark.parametrize("n", [9599 * 16, 9600 * 16 + 48, 30000 * 16])
 def test_more_blocks_than_shared_memory_holds(gpu, n):
     args = make_select(1, 4, 1, 64, BF16, [n], seed=1)
     check_select(gpu, args, 300, 1, 2)

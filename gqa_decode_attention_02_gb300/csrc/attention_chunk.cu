@@ -58,8 +58,9 @@ constexpr int kThreadsCh = 384;
 // launch's 384 x 168.
 constexpr int kRegsIssue = 88, kRegsSoft = 208;
 static_assert(128 * kRegsIssue + 256 * kRegsSoft <= kThreadsCh * 168, "register split");
-constexpr int kStart = 2;      // units of an item's start-up and end
-constexpr int kQuota = 6;      // units per CTA at least
+// Units of work: a KV tile of an item with one row tile (its bytes: 1.5 us) or two (its
+// MMAs: 1.8 us), an item's start and end; and per CTA at least.
+constexpr int kLone = 5, kPair = 6, kStart = 10, kQuota = 30;
 constexpr int kWhole = 4;      // KV tiles up to which an item is never split
 constexpr float kSlack = 8.f;  // log2 slack before O is rescaled
 constexpr int kPieces = 8;      // pieces between the scheduler and the last role
@@ -154,8 +155,8 @@ __device__ __forceinline__ int tile_hi(const Seq& s, int e) {
     return (s.ctx - s.n + e - 1) / kStep + 1;
 }
 __device__ __forceinline__ int item_units(const ChunkParams& p, const Seq& s, int qi) {
-    const int f = qi * 2 * p.tpc;
-    return tile_hi(s, min(s.n, f + 2 * p.tpc)) - tile_lo(p, s, f) + kStart;
+    const int f = qi * 2 * p.tpc, e = min(s.n, f + 2 * p.tpc);
+    return (tile_hi(s, e) - tile_lo(p, s, f)) * (f + p.tpc < e ? kPair : kLone) + kStart;
 }
 
 __device__ __forceinline__ void give_up(ChunkSmem& sm, const ChunkParams& p) {
@@ -205,22 +206,25 @@ struct Walk {
             }
             const int f = qi * 2 * p.tpc, e = min(s.n, f + 2 * p.tpc), mid = min(e, f + p.tpc);
             const int lo = tile_lo(p, s, f), hi = tile_hi(s, e);
-            const long long first = base + kStart, end = first + (hi - lo);
+            // (a KV tile is the CTA's in whose range its first unit lies)
+            const int each = mid < e ? kPair : kLone;
+            const long long first = base + kStart, end = first + (long long)(hi - lo) * each;
             if (pos < end) {
-                long long from = max(pos, first), to = min(c1, end);
-                const bool small = hi - lo <= whole;
-                if (small) {
+                int from = lo, to = hi;
+                if (hi - lo <= whole) {
                     if (base < c0) {  // another CTA's
                         pos = end;
                         continue;
                     }
-                    from = first;
-                    to = end;
+                    pos = end;
+                } else {
+                    if (pos > first) from += (int)div_ll(pos - first + each - 1, each);
+                    if (c1 < end) to = c1 > first ? lo + (int)div_ll(c1 - first + each - 1, each) : lo;
+                    pos = min(c1, end);
                 }
-                pos = to;
-                if (to <= from) break;  // only start-up units
-                pc.t0 = lo + (int)(from - first);
-                pc.t1 = lo + (int)(to - first);
+                if (to <= from) continue;
+                pc.t0 = from;
+                pc.t1 = to;
                 const int kv = p.cpt > 1 ? vh / p.cpt : vh;
                 pc.kv = kv;
                 pc.h0 = (vh - kv * p.cpt) * p.hpc;
@@ -230,7 +234,7 @@ struct Walk {
                 pc.see_hi = at + e;
                 const bool cut = to - from != hi - lo;
                 pc.first_cta = cut ? (int)div_ll(first, quota) : -1;
-                pc.last_cta = cut ? (int)div_ll(end - 1, quota) : -1;
+                pc.last_cta = cut ? (int)div_ll(end - each, quota) : -1;
                 const int heads = min(p.hpc, p.G - pc.h0);
                 const bool lone = mid == e;
                 for (int i = 0; i < 2; ++i) {
@@ -371,7 +375,7 @@ __device__ void chunk_plan(const ChunkParams& p, ChunkSmem& sm, long long* cost)
         sm.c0 = c0;
         sm.c1 = max(c0, c1);
         sm.quota = quota;
-        sm.whole = (int)max((long long)kWhole, min(quota >> 4, (long long)1 << 20));
+        sm.whole = (int)max((long long)kWhole, min(quota / (32 * kPair), (long long)1 << 20));
         sm.b0 = b0;
         sm.base = 0;
         sm.vh0 = sm.qi0 = 0;
@@ -686,70 +690,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
-// Folds the pieces' rows of a row tile (256 threads): running maximum and sum
-// over the pieces in order, four dims of a row at a time.  E of them a thread and C pieces
-// at once, so that their reads overlap.
-template <bool BF16, int H, int E, int C, class Part, class Row>
-__device__ __forceinline__ void fold(int tid, int count, int pieces, const Part& part_of,
-                                     const Row& out_row) {
-    const int total = count * (H / 4);
-    for (int x0 = tid; x0 < total; x0 += 2 * kRows * E) {
-        float M[E], L[E], acc[E][4];
-        int r[E], d[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int x = min(x0 + e * 2 * kRows, total - 1);
-            r[e] = x % count;
-            d[e] = x / count;
-            M[e] = -INFINITY;
-            L[e] = acc[e][0] = acc[e][1] = acc[e][2] = acc[e][3] = 0.f;
-        }
-        bool bad = false;
-        for (int c0 = 0; c0 < pieces; c0 += C) {
-            float m[C][E], l[C][E];
-            float4 v[C][E];
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const float* q = part_of(c0 + c);
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    l[c][e] = 0.f;
-                    if (c0 + c >= pieces || x0 + e * 2 * kRows >= total) continue;
-                    m[c][e] = __ldcg(q + kRows * H + r[e]);
-                    l[c][e] = __ldcg(q + kRows * (H + 1) + r[e]);
-                    v[c][e] = __ldcg(reinterpret_cast<const float4*>(q) + d[e] * kRows + r[e]);
-                }
-            }
-#pragma unroll
-            for (int c = 0; c < C; ++c)
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    bad |= l[c][e] < 0.f;
-                    if (!(l[c][e] > 0.f)) continue;  // nothing seen in it
-                    const float top = fmaxf(M[e], m[c][e]);
-                    const float f = fast_exp2(M[e] - top), w = fast_exp2(m[c][e] - top);
-                    M[e] = top;
-                    L[e] = fmaf(L[e], f, w * l[c][e]);
-                    acc[e][0] = fmaf(acc[e][0], f, w * v[c][e].x);
-                    acc[e][1] = fmaf(acc[e][1], f, w * v[c][e].y);
-                    acc[e][2] = fmaf(acc[e][2], f, w * v[c][e].z);
-                    acc[e][3] = fmaf(acc[e][3], f, w * v[c][e].w);
-                }
-        }
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            if (x0 + e * 2 * kRows >= total) break;
-            uint2 y = make_uint2(0u, 0u);
-            if (!bad && L[e] > 0.f) {
-                const float inv = 1.f / L[e];
-                y = make_uint2(Elt<BF16>::pack(acc[e][0] * inv, acc[e][1] * inv),
-                               Elt<BF16>::pack(acc[e][2] * inv, acc[e][3] * inv));
-            }
-            *reinterpret_cast<uint2*>(out_row(r[e]) + 4 * d[e]) = y;
-        }
-    }
-}
-
 // Softmax of the row tiles in slot i, a thread per row.
 template <bool BF16, int H>
 __device__ bool chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm) {
@@ -927,32 +867,36 @@ __device__ bool chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
             sm.shared_count[w][tile] = count;
         }
         release();
-        // a piece of an item that several CTAs share: [H/4][128 rows][4] values, maxima, sums
+        // O_i in q's dtype, or, of a piece of an item that several CTAs share, as it is,
+        // [128 rows][H], then the rows' references and sums.  64 bytes of a row at a time, in a
+        // loop (code that runs once a piece is not in the instruction cache), stored by
+        // quads of threads.
+        const bool whole = first_cta < 0;
         float* const part =
             p.partials + ((size_t)((int)blockIdx.x * 2 + w) * 2 + tile) * C::kPart;
-        const float inv = first_cta >= 0 ? 1.f : bad || !(l > 0.f) ? 0.f : 1.f / l;
-        // O_i, 32 dims at a time (a loop: code that runs once a piece is not in the
-        // instruction cache)
+        const float inv = bad || !(l > 0.f) ? 0.f : 1.f / l;
+        uint4* const dst = whole ? out : reinterpret_cast<uint4*>(part);
         if (warp_on && some) {
 #pragma unroll 1
-            for (int c = 0; c < H / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32(tO + 32 * c, o);
-                tmem_wait_ld();
-                if (first_cta >= 0) {
-                    if (active)
-#pragma unroll
-                        for (int x = 0; x < 8; ++x)
-                            __stcg(reinterpret_cast<uint4*>(part) + (8 * c + x) * kRows + row,
-                                   make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]));
-                    continue;
-                }
+            for (int c = 0; c < (whole ? H / 32 : H / 16); ++c) {
                 uint32_t w[4][4];
+                if (whole) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + 32 * c, o);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int x = 0; x < 16; ++x)
-                    w[x >> 2][x & 3] = inv == 0.f ? 0u
-                                                  : E::pack(__uint_as_float(o[2 * x]) * inv,
-                                                            __uint_as_float(o[2 * x + 1]) * inv);
+                    for (int x = 0; x < 16; ++x)
+                        w[x >> 2][x & 3] = inv == 0.f
+                                               ? 0u
+                                               : E::pack(__uint_as_float(o[2 * x]) * inv,
+                                                         __uint_as_float(o[2 * x + 1]) * inv);
+                } else {
+                    uint32_t o[16];
+                    tmem_ld16(tO + 16 * c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) w[x >> 2][x & 3] = o[x];
+                }
                 // piece x of this thread's row <-> piece (lane & 3) of the quad's row x
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
@@ -970,14 +914,17 @@ __device__ bool chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
                     }
                 }
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    if ((row & ~3) + x < count)
-                        out[quad[x] + 4 * c] = make_uint4(w[x][0], w[x][1], w[x][2], w[x][3]);
+                for (int x = 0; x < 4; ++x) {
+                    const int r = (row & ~3) + x;
+                    const uint32_t at = whole ? quad[x] : (uint32_t)(r * (H / 4) + (lane & 3));
+                    if (r < count)
+                        __stcg(dst + at + 4 * c, make_uint4(w[x][0], w[x][1], w[x][2], w[x][3]));
+                }
             }
         }
         tc_fence_before();
         if (some) mbar_arrive(bF);
-        if (first_cta >= 0) {
+        if (!whole) {
             __stcg(part + kRows * H + row, m);
             __stcg(part + kRows * (H + 1) + row, bad ? -1.f : l);  // a bad block shows as -1
         }
@@ -990,7 +937,7 @@ __device__ bool chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
 // others (the one that its range begins in, the one that it ends in), a ticket; the CTA
 // that draws an item's last one folds the pieces.
 template <bool BF16, int H>
-__device__ void chunk_shared(const ChunkParams& p, ChunkSmem& sm) {
+__device__ void chunk_shared(const ChunkParams& p, ChunkSmem& sm, float* weight) {
     using C = Ch<H>;
     const int tid = threadIdx.x - 32 * kSoftWarp;
     __threadfence();  // partial results before the ticket
@@ -1018,23 +965,90 @@ __device__ void chunk_shared(const ChunkParams& p, ChunkSmem& sm) {
         if (!meet()) return give_up(sm, p);
         if (sm.ticket[w] != pieces - 1) continue;
         __threadfence();
-#pragma unroll 1
-        for (int tile = 0; tile < 2; ++tile) {
-            const int count = sm.shared_count[w][tile];
-            if (count == 0) continue;
-            auto part_of = [&](int c) {
-                return p.partials +
-                       ((size_t)((first_cta + c) * 2 + (c == 0)) * 2 + tile) * C::kPart;
-            };
-            uint16_t* const out =
-                static_cast<uint16_t*>(p.out) +
-                ((size_t)sm.shared_rows[w][tile] * p.N + (size_t)sm.shared[w].kv * p.G +
-                 sm.shared[w].h0) * H;
-            auto out_row = [&](int r) {
-                return out + ((size_t)(r / p.hpc) * p.N + r % p.hpc) * H;
-            };
-            fold<BF16, H, 4, 4>(tid, count, pieces, part_of, out_row);
+        auto part_of = [&](int c, int tile) {
+            return p.partials + ((size_t)((first_cta + c) * 2 + (c == 0)) * 2 + tile) * C::kPart;
+        };
+        // weights of the pieces' rows, a thread per row of both tiles (in the shared memory
+        // that tiles were in)
+        {
+            const float* const rows = part_of(0, tid / kRows) + kRows * H + tid % kRows;
+            const float* const rest = part_of(1, tid / kRows) + kRows * H + tid % kRows;
+            const bool on = tid % kRows < sm.shared_count[w][tid / kRows];
+            float M = -INFINITY, L = 0.f;
+            bool bad = false;
+#pragma unroll 4
+            for (int c = 0; c < pieces; ++c) {
+                const float* q = c ? rest + (size_t)(c - 1) * 4 * C::kPart : rows;
+                const float mc = on ? __ldcg(q) : 0.f, lc = on ? __ldcg(q + kRows) : 0.f;
+                bad |= lc < 0.f;
+                const bool seen = lc > 0.f;  // else nothing in this piece
+                const float top = seen ? fmaxf(M, mc) : M;
+                const float f = M == -INFINITY ? 0.f : fast_exp2(M - top);
+                L = fmaf(L, f, seen ? lc * fast_exp2(mc - top) : 0.f);
+                M = top;
+                weight[c * 2 * kRows + tid] = seen ? mc : -INFINITY;
+            }
+            const float inv = bad || !(L > 0.f) ? 0.f : 1.f / L;
+            for (int c = 0; c < pieces; ++c) {
+                float& x = weight[c * 2 * kRows + tid];
+                x = x == -INFINITY ? 0.f : fast_exp2(x - M) * inv;
+            }
         }
+        if (!meet()) return give_up(sm, p);
+        // four dims of a row at a time, in the pieces' order: four of them a thread and four
+        // pieces at once, so that their reads overlap
+        constexpr int V = H / 4, kEach = 4, kAtOnce = 4;
+        const int n0 = sm.shared_count[w][0], total = (n0 + sm.shared_count[w][1]) * V;
+#pragma unroll 1
+        for (int x0 = tid; x0 < total; x0 += 2 * kRows * kEach) {
+            float acc[kEach][4] = {};
+            int row[kEach];  // of both tiles
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                const int r = (x0 + e * 2 * kRows) / V;
+                row[e] = r < n0 ? r : r - n0 + kRows;
+            }
+#pragma unroll 1
+            for (int c0 = 0; c0 < pieces; c0 += kAtOnce) {
+                float4 v[kAtOnce][kEach];
+                float f[kAtOnce][kEach];
+#pragma unroll
+                for (int c = 0; c < kAtOnce; ++c)
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e) {
+                        f[c][e] = 0.f;
+                        if (x0 + e * 2 * kRows < total && c0 + c < pieces)
+                            f[c][e] = weight[(c0 + c) * 2 * kRows + row[e]];
+                        v[c][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (f[c][e] != 0.f)  // (else nothing may be there)
+                            v[c][e] = __ldcg(reinterpret_cast<const float4*>(
+                                                 part_of(c0 + c, row[e] / kRows)) +
+                                             row[e] % kRows * V + x0 % V);
+                    }
+#pragma unroll
+                for (int c = 0; c < kAtOnce; ++c)
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e) {
+                        acc[e][0] = fmaf(f[c][e], v[c][e].x, acc[e][0]);
+                        acc[e][1] = fmaf(f[c][e], v[c][e].y, acc[e][1]);
+                        acc[e][2] = fmaf(f[c][e], v[c][e].z, acc[e][2]);
+                        acc[e][3] = fmaf(f[c][e], v[c][e].w, acc[e][3]);
+                    }
+            }
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                if (x0 + e * 2 * kRows >= total) continue;
+                const int r = row[e] % kRows;
+                uint16_t* const out =
+                    static_cast<uint16_t*>(p.out) +
+                    ((size_t)(sm.shared_rows[w][row[e] / kRows] + r / p.hpc) * p.N +
+                     (size_t)sm.shared[w].kv * p.G + sm.shared[w].h0 + r % p.hpc) * H;
+                reinterpret_cast<uint2*>(out)[x0 % V] =
+                    make_uint2(Elt<BF16>::pack(acc[e][0], acc[e][1]),
+                               Elt<BF16>::pack(acc[e][2], acc[e][3]));
+            }
+        }
+        if (!meet()) return give_up(sm, p);  // the weights have been read
     }
 }
 
@@ -1097,7 +1111,8 @@ __global__ void __launch_bounds__(kThreadsCh, 1)
             chunk_mma<BF16, H>(p, ring, qbuf, sm, warp == 0 ? 0 : 1);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
-        if (chunk_softmax<BF16, H>(p, ring, sm)) chunk_shared<BF16, H>(p, sm);
+        if (chunk_softmax<BF16, H>(p, ring, sm))
+            chunk_shared<BF16, H>(p, sm, reinterpret_cast<float*>(qbuf));
     }
     tc_fence_before();
     __syncthreads();
@@ -1110,6 +1125,11 @@ constexpr size_t chunk_smem() {
     return 1024 + (size_t)(2 + Ch<H>::kSlots) * Ch<H>::kTile + sizeof(ChunkSmem);
 }
 static_assert(chunk_smem<128>() <= 227 * 1024 && chunk_smem<64>() <= 227 * 1024, "shared memory");
+constexpr int kMaxCtas = 152;  // pieces whose weights the fold holds
+static_assert(kMaxCtas * 2 * kRows * sizeof(float) <= (size_t)(2 + Ch<64>::kSlots) * Ch<64>::kTile &&
+                  kMaxCtas * 2 * kRows * sizeof(float) <=
+                      (size_t)(2 + Ch<128>::kSlots) * Ch<128>::kTile,
+              "the fold's weights fit where tiles were");
 static_assert(kMaxSeqs * sizeof(long long) <= (size_t)Ch<64>::kSlots * Ch<64>::kTile &&
                   kMaxSeqs * sizeof(long long) <= (size_t)Ch<128>::kSlots * Ch<128>::kTile,
               "the plan's scratch fits in the ring");
@@ -1198,11 +1218,12 @@ gqa_status launch_chunk_attention(const gqa_shape& s, long long rows, long long 
     if (!block_map(&tmk, k_cache, s) || !block_map(&tmv, v_cache, s) ||
         !query_map(&tmq, q, s, rows, q_stride, p.hpc, p.tpc))
         return GQA_ERR_CUDA;
-    const int sms = device_sm_count();
+    const int sms = std::min(device_sm_count(), kMaxCtas);
     if (sms < 1) return GQA_ERR_CUDA;
     // no more CTAs than units can be (every item at the tables' width)
     const long long items = (rows + 2 * p.tpc - 1) / (2 * p.tpc) + s.B;
-    const long long most = items * p.KC * ((s.max_blocks_per_seq + kBlocks - 1) / kBlocks + kStart);
+    const long long most =
+        items * p.KC * (((s.max_blocks_per_seq + kBlocks - 1) / kBlocks) * (long long)kPair + kStart);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)std::max<long long>(
         1, std::min<long long>(sms, (most + kQuota - 1) / kQuota)));

@@ -61,7 +61,9 @@ static_assert(128 * kRegsIssue + 256 * kRegsSoft <= kThreadsCh * 168, "register 
 // Units of work: a KV tile of an item with one row tile (its bytes: 1.5 us) or two (its
 // MMAs: 1.8 us), an item's start and end; and per CTA at least.
 constexpr int kLone = 5, kPair = 6, kStart = 10, kQuota = 30;
-constexpr int kWhole = 4;      // KV tiles up to which an item is never split
+// A range boundary this near to an item's start or end moves there: a smaller piece is not
+// worth its fold (some 5 us with one row tile of few rows, 20 with two full ones).
+constexpr int kNearLone = 2 * kLone, kNearPair = 8 * kPair;
 constexpr float kSlack = 8.f;  // log2 slack before O is rescaled
 constexpr int kPieces = 8;      // pieces between the scheduler and the last role
 constexpr int kMaxSeqs = 16384;
@@ -110,7 +112,7 @@ struct ChunkSmem {
     uint64_t all;  // the softmax threads
     long long c0, c1, base;  // range of units; first unit of the first item
     long long quota;
-    int b0, vh0, qi0, whole;
+    int b0, vh0, qi0;
     uint32_t tmem, lock;
     volatile int abort_flag;
     volatile int bad[kPieces];
@@ -170,12 +172,11 @@ __device__ __forceinline__ long long div_ll(long long a, long long b) {
     return a / b;
 }
 
-// The pieces of the CTA's range in order.  Items of up to `whole` KV tiles belong to the CTA
-// in whose range they begin.  Lone row tiles take the two slots in turn, so that one's
-// end and the next one's start overlap.
+// The pieces of the CTA's range in order.  Lone row tiles take the two slots in turn, so
+// that one's end and the next one's start overlap.
 struct Walk {
-    long long pos, c0, c1, base, quota;
-    int b, vh, qi, nq, turn, whole;
+    long long c0, c1, base, quota;
+    int b, vh, qi, nq, turn;
     Seq s, ahead;  // of sequences b and b + 1
     __device__ void load(const ChunkParams& p) {
         s = ahead;
@@ -183,22 +184,23 @@ struct Walk {
         if (b + 1 < p.B) ahead = read_seq(p, b + 1);
     }
     __device__ void init(const ChunkSmem& sm, const ChunkParams& p) {
-        pos = c0 = sm.c0;
+        c0 = sm.c0;
         c1 = sm.c1;
         base = sm.base;
         quota = sm.quota;
-        whole = sm.whole;
         b = sm.b0;
         vh = sm.vh0;
         qi = sm.qi0;
         nq = turn = 0;
-        if (pos < c1) {
+        if (c0 < c1) {
             ahead = read_seq(p, b);
             load(p);
+        } else {
+            base = c1;  // nothing for this CTA
         }
     }
     __device__ bool next(const ChunkParams& p, Piece& pc) {
-        while (pos < c1) {
+        while (base < c1) {
             if (nq == 0) {
                 if (++b >= p.B) break;
                 load(p);
@@ -207,22 +209,18 @@ struct Walk {
             const int f = qi * 2 * p.tpc, e = min(s.n, f + 2 * p.tpc), mid = min(e, f + p.tpc);
             const int lo = tile_lo(p, s, f), hi = tile_hi(s, e);
             // (a KV tile is the CTA's in whose range its first unit lies)
-            const int each = mid < e ? kPair : kLone;
+            const int each = mid < e ? kPair : kLone, near = mid < e ? kNearPair : kNearLone;
             const long long first = base + kStart, end = first + (long long)(hi - lo) * each;
-            if (pos < end) {
-                int from = lo, to = hi;
-                if (hi - lo <= whole) {
-                    if (base < c0) {  // another CTA's
-                        pos = end;
-                        continue;
-                    }
-                    pos = end;
-                } else {
-                    if (pos > first) from += (int)div_ll(pos - first + each - 1, each);
-                    if (c1 < end) to = c1 > first ? lo + (int)div_ll(c1 - first + each - 1, each) : lo;
-                    pos = min(c1, end);
-                }
-                if (to <= from) continue;
+            int from = lo, to = hi;
+            if (c0 > first + near)
+                from = end - c0 <= near ? hi : lo + (int)div_ll(c0 - first + each - 1, each);
+            if (c1 < end) {
+                if (c1 <= first + near)
+                    to = lo;
+                else if (end - c1 > near)
+                    to = lo + (int)div_ll(c1 - first + each - 1, each);
+            }
+            if (from < to) {
                 pc.t0 = from;
                 pc.t1 = to;
                 const int kv = p.cpt > 1 ? vh / p.cpt : vh;
@@ -232,9 +230,10 @@ struct Walk {
                 const int at = s.ctx - s.n;  // position of the first new token
                 pc.see_lo = p.window > 0 ? max(0, at + f - p.window + 1) : 0;
                 pc.see_hi = at + e;
+                // the CTAs whose ranges begin in the item, but for its ends
                 const bool cut = to - from != hi - lo;
-                pc.first_cta = cut ? (int)div_ll(first, quota) : -1;
-                pc.last_cta = cut ? (int)div_ll(end - each, quota) : -1;
+                pc.first_cta = cut ? (int)div_ll(first + near, quota) : -1;
+                pc.last_cta = cut ? (int)div_ll(end - near - 1, quota) : -1;
                 const int heads = min(p.hpc, p.G - pc.h0);
                 const bool lone = mid == e;
                 for (int i = 0; i < 2; ++i) {
@@ -251,7 +250,6 @@ struct Walk {
                     }
                 }
                 if (lone) turn ^= 1;
-                return true;
             }
             base = end;
             if (++qi == nq) {
@@ -261,8 +259,8 @@ struct Walk {
                     nq = 0;
                 }
             }
+            if (from < to) return true;
         }
-        pos = c1;
         return false;
     }
 };
@@ -375,7 +373,6 @@ __device__ void chunk_plan(const ChunkParams& p, ChunkSmem& sm, long long* cost)
         sm.c0 = c0;
         sm.c1 = max(c0, c1);
         sm.quota = quota;
-        sm.whole = (int)max((long long)kWhole, min(quota / (32 * kPair), (long long)1 << 20));
         sm.b0 = b0;
         sm.base = 0;
         sm.vh0 = sm.qi0 = 0;
@@ -949,21 +946,19 @@ __device__ void chunk_shared(const ChunkParams& p, ChunkSmem& sm, float* weight)
         return ok;
     };
     if (!meet()) return give_up(sm, p);
+    if (tid % kRows == 0 && sm.shared[tid / kRows].pieces > 0) {
+        const int w = tid / kRows;
+        int32_t* const flag = p.flags + sm.shared[w].first_cta;
+        unsigned v;
+        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(v) : "l"(flag) : "memory");
+        sm.ticket[w] = (int)v;
+        if ((int)v == sm.shared[w].pieces - 1) *flag = 0;  // as the next call wants it
+    }
+    if (!meet()) return give_up(sm, p);
 #pragma unroll 1
     for (int w = 0; w < 2; ++w) {
         const int first_cta = sm.shared[w].first_cta, pieces = sm.shared[w].pieces;
-        if (pieces == 0) continue;
-        if (tid == 0) {
-            unsigned v;
-            asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
-                         : "=r"(v)
-                         : "l"(p.flags + first_cta)
-                         : "memory");
-            sm.ticket[w] = (int)v;
-            if ((int)v == pieces - 1) p.flags[first_cta] = 0;  // as the next call wants it
-        }
-        if (!meet()) return give_up(sm, p);
-        if (sm.ticket[w] != pieces - 1) continue;
+        if (pieces == 0 || sm.ticket[w] != pieces - 1) continue;
         __threadfence();
         auto part_of = [&](int c, int tile) {
             return p.partials + ((size_t)((first_cta + c) * 2 + (c == 0)) * 2 + tile) * C::kPart;

@@ -125,6 +125,18 @@ struct ChunkSmem {
     Piece pieces[kPieces];
 };
 
+// Waits for the phase of a barrier with the given parity; false after kTries polls, each of
+// which lasts tens of cycles to some microseconds (a second at least).  A count instead
+// of ptx.cuh's clock: this kernel waits in forty places, and its code has to stay in the
+// instruction cache.
+constexpr uint32_t kTries = 1u << 26;
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+    for (uint32_t n = 0; n < kTries; ++n)
+        if (mbar_try_wait(bar, parity)) return true;
+    return false;
+}
+
 // A sequence's new rows, or none where its lengths are out of range.
 struct Seq {
     int n, ctx, r0;
@@ -167,7 +179,7 @@ __device__ __forceinline__ void give_up(ChunkSmem& sm, const ChunkParams& p) {
 }
 
 // a / b for a >= 0, b > 0 (32 bits where they do)
-__device__ __forceinline__ long long div_ll(long long a, long long b) {
+__device__ __noinline__ long long div_ll(long long a, long long b) {
     if ((a | b) >> 32 == 0) return (uint32_t)a / (uint32_t)b;
     return a / b;
 }
@@ -408,7 +420,7 @@ __device__ void chunk_plan(const ChunkParams& p, ChunkSmem& sm, long long* cost)
 // ---------------------------------------------------------------------------
 // Waits for piece k of the CTA; false after a time-out or an abort.
 __device__ __forceinline__ bool piece_ready(ChunkSmem& sm, int k) {
-    return mbar_wait(smem_addr(&sm.piece_full[k % kPieces]), (k / kPieces) & 1) && !sm.abort_flag;
+    return wait_for(smem_addr(&sm.piece_full[k % kPieces]), (k / kPieces) & 1) && !sm.abort_flag;
 }
 __device__ __forceinline__ void piece_done(ChunkSmem& sm, int k) {
     mbar_arrive(smem_addr(&sm.piece_free[k % kPieces]));
@@ -459,7 +471,7 @@ __device__ void chunk_load(const CUtensorMap* tmk, const CUtensorMap* tmv, const
             for (int kvsel = 0; kvsel < 2; ++kvsel) {
                 const uint32_t bar = smem_addr(&sm.full[r]);
                 if (lane == 0) {
-                    bool ok = it < C::kSlots || mbar_wait(smem_addr(&sm.empty[r]), ph);
+                    bool ok = it < C::kSlots || wait_for(smem_addr(&sm.empty[r]), ph);
                     if (!ok) give_up(sm, p);
                     aborted = !ok || sm.abort_flag;
                     if (!aborted) {
@@ -489,7 +501,7 @@ __device__ void chunk_load(const CUtensorMap* tmk, const CUtensorMap* tmv, const
     }
     if (lane == 0 && aborted)  // copies in flight land before the CTA ends
         for (int j = max(0, it - C::kSlots); j < it; ++j)
-            mbar_wait(smem_addr(&sm.full[j % C::kSlots]), (j / C::kSlots) & 1);
+            wait_for(smem_addr(&sm.full[j % C::kSlots]), (j / C::kSlots) & 1);
 }
 
 // ---------------------------------------------------------------------------
@@ -511,7 +523,7 @@ __device__ void chunk_schedule(const CUtensorMap* tmq, const ChunkParams& p, uin
         if (more && out < in + 3) {
             const int e = out % kPieces;
             if (out >= kPieces)
-                ok = mbar_wait(smem_addr(&sm.piece_free[e]), (out / kPieces - 1) & 1);
+                ok = wait_for(smem_addr(&sm.piece_free[e]), (out / kPieces - 1) & 1);
             if (!ok) break;
             more = wk.next(p, sm.pieces[e]);
             if (!more) sm.pieces[e].t0 = -1;
@@ -524,7 +536,7 @@ __device__ void chunk_schedule(const CUtensorMap* tmq, const ChunkParams& p, uin
 #pragma unroll 1
         for (int i = 0; i < 2 && ok; ++i) {
             if (pc.a[i] >= pc.b[i]) continue;
-            if (loads[i] > 0) ok = mbar_wait(smem_addr(&sm.q_free[i]), (loads[i] - 1) & 1);
+            if (loads[i] > 0) ok = wait_for(smem_addr(&sm.q_free[i]), (loads[i] - 1) & 1);
             if (!ok || sm.abort_flag) {
                 ok = false;
                 break;
@@ -542,7 +554,7 @@ __device__ void chunk_schedule(const CUtensorMap* tmq, const ChunkParams& p, uin
     if (!ok) {
         give_up(sm, p);
         for (int i = 0; i < 2; ++i)  // copies in flight land before the CTA ends
-            if (loads[i] > 0) mbar_wait(smem_addr(&sm.q_full[i]), (loads[i] - 1) & 1);
+            if (loads[i] > 0) wait_for(smem_addr(&sm.q_full[i]), (loads[i] - 1) & 1);
     }
 }
 
@@ -556,21 +568,16 @@ __device__ void chunk_schedule(const CUtensorMap* tmq, const ChunkParams& p, uin
 // turn ends four MMAs before its products do, about what handing it over takes.
 __device__ __forceinline__ bool take_turn(ChunkSmem& sm) {
     const uint32_t lock = smem_addr(&sm.lock);
-    unsigned long long t0 = 0;
-    for (int n = 0;; ++n) {
+#pragma unroll 1
+    for (uint32_t n = 0; n < kTries; ++n) {  // a bounded wait
         uint32_t old;
         asm volatile("atom.acquire.cta.shared::cta.exch.b32 %0, [%1], 1;"
                      : "=r"(old)
                      : "r"(lock)
                      : "memory");
         if (old == 0) return true;
-        if ((n & 63) == 63) {  // a bounded wait
-            if (t0 == 0)
-                t0 = global_ns();
-            else if (global_ns() - t0 > kWaitLimitNs)
-                return false;
-        }
     }
+    return false;
 }
 __device__ __forceinline__ void end_turn(ChunkSmem& sm) {
     asm volatile("st.release.cta.shared::cta.b32 [%0], 0;" ::"r"(smem_addr(&sm.lock)) : "memory");
@@ -622,23 +629,23 @@ __device__ void chunk_mma(const ChunkParams& p, uint8_t* ring, uint8_t* qbuf, Ch
         for (int j = t0; j < t1 && ok; ++j) {
             if (j < ja || j >= jb) {  // not seen by this slot's rows
                 for (int kv = 0; kv < 2 && ok; ++kv) {
-                    ok = mbar_wait(full + 8 * r, ph);
+                    ok = wait_for(full + 8 * r, ph);
                     mbar_arrive(empty + 8 * r);
                     advance();
                 }
                 continue;
             }
-            if (j == ja) ok = mbar_wait(smem_addr(&sm.q_full[I]), pieces & 1);
+            if (j == ja) ok = wait_for(smem_addr(&sm.q_full[I]), pieces & 1);
             if (!begun) {
-                ok = ok && mbar_wait(full + 8 * r, ph) && take_turn(sm);
+                ok = ok && wait_for(full + 8 * r, ph) && take_turn(sm);
                 if (!ok) break;
                 qk(j + 1 == jb);
             }
             begun = false;
-            ok = mbar_wait(full + 8 * r, ph) && mbar_wait(smem_addr(&sm.p_ready[I]), steps & 1);
+            ok = wait_for(full + 8 * r, ph) && wait_for(smem_addr(&sm.p_ready[I]), steps & 1);
             ++steps;
             if (j == ja && pieces > 0)  // O of the last piece has been read
-                ok = ok && mbar_wait(smem_addr(&sm.o_free[I]), (pieces - 1) & 1);
+                ok = ok && wait_for(smem_addr(&sm.o_free[I]), (pieces - 1) & 1);
             ok = ok && !sm.abort_flag && take_turn(sm);
             if (!ok) break;
             tc_fence_after();
@@ -662,7 +669,7 @@ __device__ void chunk_mma(const ChunkParams& p, uint8_t* ring, uint8_t* qbuf, Ch
     }
     if (!ok) give_up(sm, p);
     umma_commit(smem_addr(&sm.done[I]));  // every MMA ends before tensor memory is freed
-    if (!mbar_wait(smem_addr(&sm.done[I]), 0)) give_up(sm, p);
+    if (!wait_for(smem_addr(&sm.done[I]), 0)) give_up(sm, p);
 }
 
 // ---------------------------------------------------------------------------
@@ -735,7 +742,7 @@ __device__ bool chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
         const int see_lo = pc.see_lo, see_hi = pc.see_hi;
         float m = -INFINITY, l = 0.f;
         for (int j = ja; j < jb; ++j, ++step) {
-            ok = __all_sync(kAll, mbar_wait(bS, step & 1));
+            ok = __all_sync(kAll, wait_for(bS, step & 1));
             if (!ok) break;
             const int tok = j * kStep;
             if (warp_on) {
@@ -777,7 +784,7 @@ __device__ bool chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
                 if (__any_sync(kAll, need)) {
                     const float f = need && m != -INFINITY ? fast_exp2(m - top) : 1.f;
                     if (j > ja && __any_sync(kAll, f != 1.f)) {  // the last PV has ended
-                        ok = __all_sync(kAll, mbar_wait(bO, (step - 1) & 1));
+                        ok = __all_sync(kAll, wait_for(bO, (step - 1) & 1));
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll 1
@@ -824,7 +831,7 @@ __device__ bool chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
             const int z0 = v0 & 15, z = z0 + (-v1 & 15);  // rows before v0 and from v1 on
             if (z > 0) {
                 const int nv = ring0 + 2 * (j - t0) + 1;
-                ok = __all_sync(kAll, mbar_wait(smem_addr(&sm.full[nv % C::kSlots]),
+                ok = __all_sync(kAll, wait_for(smem_addr(&sm.full[nv % C::kSlots]),
                                                 (nv / C::kSlots) & 1));
                 if (!ok) break;
                 const uint32_t vb = smem_addr(ring + (size_t)(nv % C::kSlots) * C::kTile);
@@ -846,7 +853,7 @@ __device__ bool chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
         // ---- the tile's rows ------------------------------------------------------
         const bool some = ja < jb;  // any KV tile in this piece
         if (some) {
-            ok = __all_sync(kAll, mbar_wait(bO, (step - 1) & 1));
+            ok = __all_sync(kAll, wait_for(bO, (step - 1) & 1));
             if (!ok) break;
             tc_fence_after();
         }
@@ -941,7 +948,7 @@ __device__ void chunk_shared(const ChunkParams& p, ChunkSmem& sm, float* weight)
     int meets = 0;
     auto meet = [&]() {  // the softmax threads
         mbar_arrive(smem_addr(&sm.all));
-        const bool ok = mbar_wait(smem_addr(&sm.all), meets & 1);
+        const bool ok = wait_for(smem_addr(&sm.all), meets & 1);
         ++meets;
         return ok;
     };

@@ -1005,12 +1005,6 @@ def _rows_stride(t, name, dtype=None):
     return stride
 
 
-def _key_of(*tensors):
-    """What the checks of a call look at: of every tensor shape, strides, type and device."""
-    return tuple([None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
-                  for t in tensors])
-
-
 def kv_append_rotary(q, k_new, v_new, k_cache, v_cache, slots, positions, cos_sin, *, q_out=None,
                      k_scale=None, v_scale=None, kv="same", interleaved=False, status=None,
                      stream=None, pdl=False):
@@ -1023,9 +1017,24 @@ def kv_append_rotary(q, k_new, v_new, k_cache, v_cache, slots, positions, cos_si
     projection's output).  Returns the rotated queries in q_out (may be q itself;
     default: a new tensor), whose rows without a token stay as they are."""
     try:
-        key = ("rotary", kv, interleaved, pdl, _key_of(q, k_new, v_new, k_cache, v_cache, slots,
-                                                       positions, cos_sin, q_out, k_scale, v_scale))
-        shape = _checked.get(key)
+        dev = q.get_device()
+        key = ("rotary", dev, kv, interleaved, pdl, q.shape, q.stride(), q.dtype, k_new.shape,
+               k_new.stride(), k_new.dtype, v_new.shape, v_new.stride(), v_new.dtype,
+               k_cache.shape, k_cache.dtype, v_cache.shape, v_cache.dtype, slots.shape,
+               slots.dtype, positions.shape, positions.dtype, cos_sin.shape, cos_sin.dtype)
+        fit = (k_cache.is_contiguous() and v_cache.is_contiguous() and slots.is_contiguous()
+               and positions.is_contiguous() and cos_sin.is_contiguous()
+               and dev == k_new.get_device() == v_new.get_device() == k_cache.get_device()
+               == v_cache.get_device() == slots.get_device() == positions.get_device()
+               == cos_sin.get_device())
+        if q_out is not None:
+            key += (q_out.shape, q_out.dtype)
+            fit = fit and q_out.is_contiguous() and dev == q_out.get_device()
+        if k_scale is not None or v_scale is not None:
+            key += ("scale", k_scale.shape, k_scale.dtype, v_scale.shape, v_scale.dtype)
+            fit = (fit and k_scale.is_contiguous() and v_scale.is_contiguous()
+                   and dev == k_scale.get_device() == v_scale.get_device())
+        shape = _checked.get(key) if fit else None
     except (AttributeError, TypeError):
         key = shape = None
     if shape is None:
@@ -1046,10 +1055,9 @@ def kv_append_rotary(q, k_new, v_new, k_cache, v_cache, slots, positions, cos_si
         made = _slots_shape(k_new, k_cache, v_cache, k_scale, v_scale, kv, pdl)
         made.N = N
         made.strides = strides
-        _lib.one_device(q, k_new, v_new, k_cache, v_cache, slots, positions, cos_sin, q_out,
-                        k_scale, v_scale)
+        dev = _lib.one_device(q, k_new, v_new, k_cache, v_cache, slots, positions, cos_sin, q_out,
+                              k_scale, v_scale).index
         shape = _remember(key, made)
-    dev = q.get_device()
     if stream is not None or dev != _lib.current_gpu():
         with _lib.on_device(torch.device("cuda", dev), stream):
             return kv_append_rotary(q, k_new, v_new, k_cache, v_cache, slots, positions, cos_sin,
@@ -1097,9 +1105,8 @@ def chunk_workspace_size(shape) -> int:
     return n
 
 
-def _chunk_launch(fn, shape, dev, like, workspace, status, call):
-    """The tail of a chunk call: workspace, status and the launch `call(ptr, bytes, status,
-    stream)` on the current stream of GPU dev."""
+def _chunk_tail(shape, dev, like, workspace, status):
+    """(workspace, its bytes, status, stream) of a chunk call on the current stream of GPU dev."""
     st = None
     if status is not None:
         st = _status_arg(status)
@@ -1110,9 +1117,7 @@ def _chunk_launch(fn, shape, dev, like, workspace, status, call):
     else:
         _lib._need(workspace, "workspace", torch.uint8)
         _lib.one_device(like, workspace)
-    rc = call(workspace.data_ptr(), workspace.numel(), st, cs)
-    if rc:
-        raise _lib.GqaError(fn, rc)
+    return workspace.data_ptr(), workspace.numel(), st, cs
 
 
 def chunk_attention(q, k_cache, v_cache, block_tables, context_lens, cu_new, *, out=None,
@@ -1125,9 +1130,20 @@ def chunk_attention(q, k_cache, v_cache, block_tables, context_lens, cu_new, *, 
     rows from cu_new[B] on stay as they are (default out: zeros)."""
     scale, window = float(scale or 0.0), int(window)
     try:
-        key = ("chunk", scale, window, pdl, _key_of(q, k_cache, v_cache, block_tables,
-                                                    context_lens, cu_new, out))
-        shape = _checked.get(key)
+        dev = q.get_device()
+        key = ("chunk", dev, scale, window, pdl, q.shape, q.stride(), q.dtype, k_cache.shape,
+               k_cache.dtype, v_cache.shape, v_cache.dtype, block_tables.shape,
+               block_tables.dtype, context_lens.shape, context_lens.dtype, cu_new.shape,
+               cu_new.dtype)
+        fit = (k_cache.is_contiguous() and v_cache.is_contiguous()
+               and block_tables.is_contiguous() and context_lens.is_contiguous()
+               and cu_new.is_contiguous() and dev == k_cache.get_device()
+               == v_cache.get_device() == block_tables.get_device()
+               == context_lens.get_device() == cu_new.get_device())
+        if out is not None:
+            key += (out.shape, out.dtype)
+            fit = fit and out.is_contiguous() and dev == out.get_device()
+        shape = _checked.get(key) if fit else None
     except (AttributeError, TypeError):
         key = shape = None
     if shape is None:
@@ -1146,11 +1162,10 @@ def chunk_attention(q, k_cache, v_cache, block_tables, context_lens, cu_new, *, 
         made = _chunk_shape(N, H, q.dtype, B, k_cache, v_cache, block_tables.shape[1], scale,
                             window, _lib.FLAG_PDL if pdl else 0)
         dev = _lib.one_device(q, k_cache, v_cache, block_tables, context_lens, cu_new, out).index
-        made.stride = stride
+        made.stride, made.rows = stride, M
         with torch.cuda.device(dev):
             made.nbytes = chunk_workspace_size(made)
         shape = _remember(key, made)
-    dev = q.get_device()
     if stream is not None or dev != _lib.current_gpu():
         with _lib.on_device(torch.device("cuda", dev), stream):
             return chunk_attention(q, k_cache, v_cache, block_tables, context_lens, cu_new,
@@ -1158,12 +1173,13 @@ def chunk_attention(q, k_cache, v_cache, block_tables, context_lens, cu_new, *, 
                                    status=status, pdl=pdl)
     if out is None:
         out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
-    f = _lib.lib().gqa_chunk_attention
-    _chunk_launch("gqa_chunk_attention", shape[0], dev, q, workspace, status,
-                  lambda ws, n, st, cs: f(shape[1], q.shape[0], q.data_ptr(), shape[0].stride,
-                                          k_cache.data_ptr(), v_cache.data_ptr(),
-                                          block_tables.data_ptr(), context_lens.data_ptr(),
-                                          cu_new.data_ptr(), out.data_ptr(), ws, n, st, cs))
+    ws, n, st, cs = _chunk_tail(shape[0], dev, q, workspace, status)
+    rc = _lib.lib().gqa_chunk_attention(
+        shape[1], shape[0].rows, q.data_ptr(), shape[0].stride, k_cache.data_ptr(),
+        v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), cu_new.data_ptr(),
+        out.data_ptr(), ws, n, st, cs)
+    if rc:
+        raise _lib.GqaError("gqa_chunk_attention", rc)
     return out
 
 
@@ -1174,9 +1190,16 @@ def kv_block_bounds(k_cache, block_tables, context_lens, cu_new, bounds, bounds_
     cu_new[b] tokens of a request: bounds int8 [NB,K,2,H] (0: largest, 1: smallest) and
     bounds_scale fp32 [NB,K] are updated.  After every append."""
     try:
-        key = ("bounds", pdl, _key_of(k_cache, block_tables, context_lens, cu_new, bounds,
-                                      bounds_scale))
-        shape = _checked.get(key)
+        dev = k_cache.get_device()
+        key = ("bounds", dev, pdl, k_cache.shape, k_cache.dtype, block_tables.shape,
+               block_tables.dtype, context_lens.shape, context_lens.dtype, cu_new.shape,
+               cu_new.dtype, bounds.shape, bounds.dtype, bounds_scale.shape, bounds_scale.dtype)
+        fit = (k_cache.is_contiguous() and block_tables.is_contiguous()
+               and context_lens.is_contiguous() and cu_new.is_contiguous()
+               and bounds.is_contiguous() and bounds_scale.is_contiguous()
+               and dev == block_tables.get_device() == context_lens.get_device()
+               == cu_new.get_device() == bounds.get_device() == bounds_scale.get_device())
+        shape = _checked.get(key) if fit else None
     except (AttributeError, TypeError):
         key = shape = None
     if shape is None:
@@ -1191,9 +1214,9 @@ def kv_block_bounds(k_cache, block_tables, context_lens, cu_new, bounds, bounds_
         _need_bounds(bounds, bounds_scale, K, H, NB)
         made = _chunk_shape(K, H, k_cache.dtype, B, k_cache, k_cache, block_tables.shape[1], 0.0,
                             0, _lib.FLAG_PDL if pdl else 0)
-        _lib.one_device(k_cache, block_tables, context_lens, cu_new, bounds, bounds_scale)
+        dev = _lib.one_device(k_cache, block_tables, context_lens, cu_new, bounds,
+                              bounds_scale).index
         shape = _remember(key, made)
-    dev = k_cache.get_device()
     if stream is not None or dev != _lib.current_gpu():
         with _lib.on_device(torch.device("cuda", dev), stream):
             return kv_block_bounds(k_cache, block_tables, context_lens, cu_new, bounds,
@@ -1235,9 +1258,19 @@ def select_blocks(q, bounds, bounds_scale, block_tables, context_lens, keep, *, 
     reads."""
     keep, first, recent = int(keep), int(first), int(recent)
     try:
-        key = ("select", keep, first, recent, pdl,
-               _key_of(q, bounds, bounds_scale, block_tables, context_lens, tables, lens, blocks))
-        shape = _checked.get(key)
+        dev = q.get_device()
+        key = ("select", dev, keep, first, recent, pdl, q.shape, q.dtype, bounds.shape,
+               bounds.dtype, bounds_scale.shape, bounds_scale.dtype, block_tables.shape,
+               block_tables.dtype, context_lens.shape, context_lens.dtype)
+        fit = (q.is_contiguous() and bounds.is_contiguous() and bounds_scale.is_contiguous()
+               and block_tables.is_contiguous() and context_lens.is_contiguous()
+               and dev == bounds.get_device() == bounds_scale.get_device()
+               == block_tables.get_device() == context_lens.get_device())
+        for t in (tables, lens, blocks):
+            if t is not None:
+                fit = fit and t.is_contiguous() and dev == t.get_device()
+            key += (None,) if t is None else (t.shape, t.dtype)
+        shape = _checked.get(key) if fit else None
     except (AttributeError, TypeError):
         key = shape = None
     if shape is None:
@@ -1260,24 +1293,24 @@ def select_blocks(q, bounds, bounds_scale, block_tables, context_lens, keep, *, 
         made = _lib.Shape(B=B, T=1, N=N, K=K, H=H, block_size=16, num_blocks=NB,
                           max_blocks_per_seq=block_tables.shape[1], dtype=_lib._DTYPES[q.dtype],
                           scale=0.0, flags=_lib.FLAG_PDL if pdl else 0, window=0, kv_dtype=0)
-        _lib.one_device(q, bounds, bounds_scale, block_tables, context_lens, tables, lens, blocks)
+        dev = _lib.one_device(q, bounds, bounds_scale, block_tables, context_lens, tables, lens,
+                              blocks).index
         made.nbytes = _lib.lib().gqa_select_workspace_size(ctypes.byref(made))
         shape = _remember(key, made)
-    dev = q.get_device()
     if stream is not None or dev != _lib.current_gpu():
         with _lib.on_device(torch.device("cuda", dev), stream):
             return select_blocks(q, bounds, bounds_scale, block_tables, context_lens, keep,
                                  first=first, recent=recent, tables=tables, lens=lens,
                                  blocks=blocks, workspace=workspace, status=status, pdl=pdl)
-    B, K = q.shape[0], bounds.shape[1]
     if keep < 1:
         raise _lib.GqaError("gqa_select_blocks", _lib.Status.ERR_SHAPE)
+    B, K = shape[0].B, shape[0].K
     if tables is None:
-        tables = context_lens.new_empty((B, K, keep))
-    if lens is None:
-        lens = context_lens.new_empty(B)
+        tables = context_lens.new_empty((B, K, keep)) if blocks is None else torch.empty_like(blocks)
     if blocks is None:
-        blocks = context_lens.new_empty((B, K, keep))
+        blocks = torch.empty_like(tables)
+    if lens is None:
+        lens = torch.empty_like(context_lens)
     st = None
     if status is not None:
         st = _status_arg(status)
@@ -1305,8 +1338,17 @@ def sparse_decode_attention(q, k_cache, v_cache, tables, lens, *, out=None, scal
     returns both."""
     scale = float(scale or 0.0)
     try:
-        key = ("sparse", scale, pdl, _key_of(q, k_cache, v_cache, tables, lens, out))
-        shape = _checked.get(key)
+        dev = q.get_device()
+        key = ("sparse", dev, scale, pdl, q.shape, q.dtype, k_cache.shape, k_cache.dtype,
+               v_cache.shape, v_cache.dtype, tables.shape, tables.dtype, lens.shape, lens.dtype)
+        fit = (q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+               and tables.is_contiguous() and lens.is_contiguous()
+               and dev == k_cache.get_device() == v_cache.get_device() == tables.get_device()
+               == lens.get_device())
+        if out is not None:
+            key += (out.shape, out.dtype)
+            fit = fit and out.is_contiguous() and dev == out.get_device()
+        shape = _checked.get(key) if fit else None
     except (AttributeError, TypeError):
         key = shape = None
     if shape is None:
@@ -1328,7 +1370,6 @@ def sparse_decode_attention(q, k_cache, v_cache, tables, lens, *, out=None, scal
         with torch.cuda.device(dev):
             made.nbytes = chunk_workspace_size(made)
         shape = _remember(key, made)
-    dev = q.get_device()
     if stream is not None or dev != _lib.current_gpu():
         with _lib.on_device(torch.device("cuda", dev), stream):
             return sparse_decode_attention(q, k_cache, v_cache, tables, lens, out=out,
@@ -1336,9 +1377,10 @@ def sparse_decode_attention(q, k_cache, v_cache, tables, lens, *, out=None, scal
                                            pdl=pdl)
     if out is None:
         out = torch.empty_like(q)
-    f = _lib.lib().gqa_sparse_decode_attention
-    _chunk_launch("gqa_sparse_decode_attention", shape[0], dev, q, workspace, status,
-                  lambda ws, n, st, cs: f(shape[1], q.data_ptr(), k_cache.data_ptr(),
-                                          v_cache.data_ptr(), tables.data_ptr(), lens.data_ptr(),
-                                          out.data_ptr(), ws, n, st, cs))
+    ws, n, st, cs = _chunk_tail(shape[0], dev, q, workspace, status)
+    rc = _lib.lib().gqa_sparse_decode_attention(
+        shape[1], q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), tables.data_ptr(),
+        lens.data_ptr(), out.data_ptr(), ws, n, st, cs)
+    if rc:
+        raise _lib.GqaError("gqa_sparse_decode_attention", rc)
     return out

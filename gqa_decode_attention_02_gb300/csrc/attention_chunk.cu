@@ -60,7 +60,7 @@ constexpr int kRegsIssue = 88, kRegsSoft = 208;
 static_assert(128 * kRegsIssue + 256 * kRegsSoft <= kThreadsCh * 168, "register split");
 // Units of work: a KV tile of an item with one row tile (its bytes: 1.5 us) or two (its
 // MMAs: 1.8 us), an item's start and end; and per CTA at least.
-constexpr int kLone = 5, kPair = 6, kStart = 10, kQuota = 30;
+constexpr int kLone = 5, kPair = 6, kStart = 10, kQuota = 20;
 // A range boundary this near to an item's start or end moves there: a smaller piece is not
 // worth its fold (some 5 us with one row tile of few rows, 20 with two full ones).
 constexpr int kNearLone = 2 * kLone, kNearPair = 8 * kPair;

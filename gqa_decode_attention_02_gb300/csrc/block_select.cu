@@ -344,6 +344,11 @@ __device__ __forceinline__ uint32_t score_key(float x) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// Sum of the first `warp` of a CTA's per-warp counts (whole warp).
+__device__ __forceinline__ int before_warp(const int* sums, int warp, int lane, int warps) {
+    return __reduce_add_sync(kFull, lane < warp && lane < warps ? sums[lane] : 0);
+}
+
 // A CTA per sequence and KV head: the key of the last block to take by passes over eleven
 // bits each (a histogram of the candidates that share the bits found so far), from the
 // first bit in which any two candidates differ -- the leading ones, sign and exponent, are
@@ -436,7 +441,7 @@ __global__ void __launch_bounds__(1024) block_pick_kernel(const SelectParams p) 
         }
         if (lane == 31) sums[0][warp] = incl;
         __syncthreads();
-        for (int w = 0; w < warp; ++w) incl += sums[0][w];
+        incl += before_warp(sums[0], warp, lane, threads / 32);
         if (tid < 512 && incl - own < left && left <= incl) {
             int above = incl - own, x = 0;
             while (above + hist[t0 - x] < left) above += hist[t0 - x++];
@@ -472,10 +477,8 @@ __global__ void __launch_bounds__(1024) block_pick_kernel(const SelectParams p) 
         sums[1][warp] = ie;
     }
     __syncthreads();
-    for (int w = 0; w < warp; ++w) {
-        ia += sums[0][w];
-        ie += sums[1][w];
-    }
+    ia += before_warp(sums[0], warp, lane, threads / 32);
+    ie += before_warp(sums[1], warp, lane, threads / 32);
     int a = ia - above, e = ie - equal;
     for (int i = from; i < to; ++i) {
         const uint32_t u = key(i);

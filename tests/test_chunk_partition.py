@@ -7,7 +7,7 @@ import random
 
 import pytest
 
-LONE, PAIR, START, QUOTA = 5, 6, 10, 30
+LONE, PAIR, START, QUOTA = 5, 6, 10, 20
 NEAR = {LONE: 2 * LONE, PAIR: 8 * PAIR}
 
 

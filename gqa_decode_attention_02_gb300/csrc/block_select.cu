@@ -18,6 +18,8 @@
 // and equal scores go to the lower block: the choice does not depend on the schedule.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "launch.h"
 #include "ptx.cuh"
 
@@ -352,14 +354,15 @@ __device__ __forceinline__ int before_warp(const int* sums, int warp, int lane, 
 // A CTA per sequence and KV head: the key of the last block to take by passes over eleven
 // bits each (a histogram of the candidates that share the bits found so far), from the
 // first bit in which any two candidates differ -- the leading ones, sign and exponent, are
-// mostly alike, and a histogram of them would be one bin --; then the blocks above it and as
-// many of those at it as are left, in order.
-__global__ void __launch_bounds__(1024) block_pick_kernel(const SelectParams p) {
+// mostly alike, and a histogram of them would be one bin --, or, once no more than 32 are
+// left, by comparing those with one another; then the blocks above it and as many of those
+// at it as are left, in order.
+__global__ void __launch_bounds__(1024, 2) block_pick_kernel(const SelectParams p) {
     constexpr int kBits = 11, kBins = 1 << kBits;
     __shared__ int hist[kBins];
     __shared__ int sums[2][32];
-    __shared__ uint32_t s_or, s_and, s_prefix;
-    __shared__ int s_left;
+    __shared__ uint32_t s_or, s_and, s_prefix, s_few[32];
+    __shared__ int s_left, s_bin, s_count;
     extern __shared__ uint32_t keys[];
     griddep_launch_dependents();
     griddep_wait();
@@ -447,11 +450,33 @@ __global__ void __launch_bounds__(1024) block_pick_kernel(const SelectParams p) 
             while (above + hist[t0 - x] < left) above += hist[t0 - x++];
             s_prefix = prefix | (uint32_t)(t0 - x) << shift;
             s_left = left - above;
+            s_bin = hist[t0 - x];
+            s_count = 0;
         }
         __syncthreads();
         prefix = s_prefix;
         left = s_left;
         bits = shift;
+        if (bits == 0 || s_bin > 32) continue;
+        const uint32_t same = ~0u << bits;
+        for (int i = tid; i < count; i += threads) {
+            const uint32_t u = key(i);
+            if ((u & same) == prefix) s_few[atomicAdd(&s_count, 1)] = u;
+        }
+        __syncthreads();
+        const int few = s_bin;
+        const uint32_t mine = lane < few ? s_few[lane] : 0u;
+        int more = 0, equal = 0;
+        for (int i = 0; i < few; ++i) {
+            const uint32_t u = __shfl_sync(kFull, mine, i);
+            more += u > mine;
+            equal += u == mine;
+        }
+        // (every warp finds the same)
+        const unsigned at = __ballot_sync(kFull, lane < few && more < left && left <= more + equal);
+        prefix = __shfl_sync(kFull, mine, __ffs(at) - 1);
+        left -= __shfl_sync(kFull, more, __ffs(at) - 1);
+        bits = 0;
     }
     // a run of blocks per thread: how many lie above the key and at it, before it too
     const int run = (count + threads - 1) / threads;
@@ -536,7 +561,8 @@ gqa_status launch_select_blocks(const gqa_shape& s, int keep, int first, int rec
                       s.max_blocks_per_seq, s.num_blocks, keep, first, recent, 1};
     const long long bk = (long long)s.B * s.K;
     const long long tiles = (s.max_blocks_per_seq + 15) / 16;
-    long long splits = (sms * 16 + bk - 1) / bk;
+    // one wave of CTAs (seven fit on an SM), so that a CTA's start is paid once
+    long long splits = std::max<long long>(1, sms * 7 / bk);
     const long long most = (tiles + kScoreThreads / 32 - 1) / (kScoreThreads / 32);
     if (splits > most) splits = most;
     p.splits = (int)splits;

@@ -186,8 +186,8 @@ gqa_status chunk_entry(const gqa_shape* s, int64_t rows, int64_t q_stride, const
     if (st != GQA_OK) return st;
     if (rows < 0 || rows > (1ll << 31) - 1) return GQA_ERR_SHAPE;
     const long long row = (long long)s->N * s->H;
-    if (row * 2 >= (1ll << 40) || q_stride < row || q_stride % 8 != 0 ||
-        q_stride * 2 >= (1ll << 40))
+    // (the tensor map's strides; a row tile's outputs within 32 bits of 16-byte pieces)
+    if (row > (1ll << 27) || q_stride < row || q_stride % 8 != 0 || q_stride >= (1ll << 39))
         return GQA_ERR_SHAPE;
     if (s->B == 0 || rows == 0) return GQA_OK;
     if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !out ||

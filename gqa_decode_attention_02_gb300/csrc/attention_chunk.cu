@@ -12,28 +12,42 @@
 // running reference m, O and l scaled when a row's maximum passes m by more than 8
 // (in log2), O / l at the end.
 //
-// An item of work is a KV head and two tiles of 128 query rows of one sequence (a row
-// = a token and one of the G heads), and walks the 128-position tiles that its rows
-// see.  Both row tiles use one copy of K and V from shared memory, and while one
-// tile's softmax runs the tensor cores work for the other.  Items lie end to end
-// in units (a few for a start-up, then one per KV tile); every CTA takes an equal
-// range of units, so that ragged batches, one short chunk behind a long prefix and
-// single tokens all fill the GPU.  The pieces of an item that a range boundary cuts
-// are folded with log-sum-exp weights, in order, by the piece that finishes last
-// (no CTA waits for another; the result does not depend on which it is).
+// An item of work is a KV head and two row tiles (128 query rows each: tokens, and the G
+// heads of each) of one sequence, and walks the 128-position KV tiles that its rows
+// see.  Both row tiles use one copy of K and V in shared memory, and while one's softmax
+// runs the tensor cores work for the other.  Items lie end to end in units of about
+// equal time; every CTA takes an equal range of them, so that ragged batches, one short
+// chunk behind a long prefix and single tokens all fill the GPU.  An item that a range
+// boundary cuts (not near its ends) is shared: its pieces go to the workspace, and the CTA
+// that draws the item's last ticket folds them, in order, with log-sum-exp weights (no
+// CTA waits for another; the result does not depend on which CTA folds).
 //
-// One CTA per SM: warp 0 issues the MMAs, warp 1 loads K and V (one TMA box per
-// cache block and KV head), warp 2 loads Q, warps 4..7 and 8..11 are the softmax of
-// row tiles 0 and 1, one thread per row.
+// One CTA per SM.  A row tile in the works has a slot: its Q in shared memory, S and O in
+// tensor memory, four softmax warps and an issuer.
+//   warps 0, 3    issue the MMAs of slots 0 and 1 (in turns: chunk_mma)
+//   warp 1        loads K and V, one TMA box per cache block and KV head
+//   warp 2        makes the list of pieces (KV tiles of an item) and loads Q
+//   warps 4 - 11  softmax of slots 0 and 1, one thread per row, and the outputs
 //   S_i[128 x 128] = Q_i K^T     Q_i and K from shared memory
 //   P_i = exp2(S_i scale - m)    in q's dtype, over the first half of S_i's columns
 //   O_i[128 x H]  += P_i V       P_i from tensor memory, V MN-major
-// Tensor memory: S_0, S_1, O_0, O_1, 128 columns each.  The issuer's order is PV_0(j),
-// QK_0(j + 1), PV_1(j), QK_1(j + 1): S_i is overwritten by a product that
-// follows, in issue order, the one that reads P_i.
-// Shared memory: Q_0, Q_1 and a ring of slots, each a tile of K or V: per cache
-// block [2 groups of 8 rows][H / 64 halves][8 rows x 128 B], 128-byte swizzled, so a
-// block is one box and both operand layouts have one stride between row groups.
+// Tensor memory: S_0, S_1, O_0, O_1, 128 columns each, all there is.  An issuer's order is
+// PV(j), QK(j + 1): S is overwritten by a product that follows, from the same thread, the
+// one that reads P.  Shared memory: Q_0, Q_1 and a ring of K and V tiles, each per cache
+// block [2 groups of 8 rows][H / 64 halves][8 rows x 128 B], 128-byte swizzled, so a block
+// is one box and both operand layouts have one stride between row groups.
+//
+// What it rounds: probabilities to q's dtype before the product with V, the result; sums
+// of probabilities are taken before that rounding, in fp32 as the scores and O.
+//
+// Measured (one GB300, H = 128, bf16, 32 / 8 heads): 2,048 tokens behind 30,720 770 us, 1.38
+// PFLOP/s, 72 % of what a library product of 8192^3 reaches; a step takes 1.75 us (3,300 cycles)
+// for 2,048 cycles of MMAs.  The MMAs alone, with nothing to wait for, take 1.39 us here
+// (82 cycles each instead of 64); reading S and writing P costs them another 15 each (the
+// same tensor memory), and a slot's chain (softmax 1,350 cycles, hand-overs 400, its
+// products 1,600) is as long as that.  Short prompts (24 of 200..3,001): 525 us, of it some 100
+// at the items' ends, where both slots store outputs at once.  Single tokens, 256 x 2,048:
+// 358 us, 6.0 TB/s.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -125,14 +139,14 @@ struct ChunkSmem {
     Piece pieces[kPieces];
 };
 
-// Waits for the phase of a barrier with the given parity; false after kTries polls, each of
-// which lasts tens of cycles to some microseconds (a second at least).  A count instead
-// of ptx.cuh's clock: this kernel waits in forty places, and its code has to stay in the
-// instruction cache.
-constexpr uint32_t kTries = 1u << 26;
+// Waits for the phase of a barrier with the given parity; false after some four seconds: a
+// poll that fails lasts 1.97 us (measured).  (ptx.cuh's wait reads a clock; this kernel waits
+// in some thirty places, and what it runs in turn has to stay in the instruction cache: with
+// the clock prompts took 3 to 7 % longer.)
+constexpr uint32_t kPolls = 1u << 21;
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
 #pragma unroll 1
-    for (uint32_t n = 0; n < kTries; ++n)
+    for (uint32_t n = 0; n < kPolls; ++n)
         if (mbar_try_wait(bar, parity)) return true;
     return false;
 }
@@ -569,7 +583,7 @@ __device__ void chunk_schedule(const CUtensorMap* tmq, const ChunkParams& p, uin
 __device__ __forceinline__ bool take_turn(ChunkSmem& sm) {
     const uint32_t lock = smem_addr(&sm.lock);
 #pragma unroll 1
-    for (uint32_t n = 0; n < kTries; ++n) {  // a bounded wait
+    for (uint32_t n = 0; n < 32 * kPolls; ++n) {  // bounded: 17 ns a try
         uint32_t old;
         asm volatile("atom.acquire.cta.shared::cta.exch.b32 %0, [%1], 1;"
                      : "=r"(old)

@@ -151,6 +151,19 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
     return false;
 }
 
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // A sequence's new rows, or none where its lengths are out of range.
 struct Seq {
     int n, ctx, r0;
@@ -664,7 +677,7 @@ __device__ void chunk_mma(const ChunkParams& p, uint8_t* ring, uint8_t* qbuf, Ch
             if (!ok) break;
             tc_fence_after();
             const int rk = r + 1 == C::kSlots ? 0 : r + 1;
-            begun = j + 1 < jb && mbar_try_wait(full + 8 * rk, rk ? ph : ph ^ 1);
+            begun = j + 1 < jb && mbar_test(full + 8 * rk, rk ? ph : ph ^ 1);
             {
                 const uint64_t dv = dv0 + (uint32_t)(r * (C::kTile >> 4));
                 umma_ts(tO, tS, dv, id_o, j > ja);

@@ -121,15 +121,26 @@ __global__ void __launch_bounds__(kBoundThreads, 4) block_bounds_kernel(const Bo
         s_ctx[threadIdx.x] = ctx;
         __syncthreads();
         const long long units = (long long)blocks * K;
-        for (; id < base + units; id += W) {
-            const uint32_t v = (uint32_t)(id - base), u = v / K, k = v - u * K;
+        // block id, KV head and rows held of unit x
+        auto find = [&](long long x, int* blk, uint32_t* k, int* held) {
+            if (x >= base + units) return;
+            const uint32_t v = (uint32_t)(x - base), u = v / K;
+            *k = v - u * K;
             int src = 0;  // whose it is
 #pragma unroll
             for (int o = kBoundThreads / 2; o > 0; o >>= 1)
                 if (s_end[src + o - 1] <= (int)u) src += o;
             const int at = s_first[src] + (int)u;
-            const int held = min(16, s_ctx[src] - at * 16);
-            const int blk = __ldg(p.block_tables + (size_t)(b0 + src) * p.max_blocks + at);
+            *held = min(16, s_ctx[src] - at * 16);
+            *blk = __ldg(p.block_tables + (size_t)(b0 + src) * p.max_blocks + at);
+        };
+        int blk_next = 0, held_next = 0;
+        uint32_t k_next = 0;
+        find(id, &blk_next, &k_next, &held_next);
+        for (; id < base + units; id += W) {
+            const int blk = blk_next, held = held_next;
+            const uint32_t k = k_next;
+            find(id + W, &blk_next, &k_next, &held_next);
             if (blk < 0 || blk >= p.num_blocks) {
                 if (lane == 0) report(p.status, GQA_ERR_BLOCK_ID);
                 continue;
@@ -182,12 +193,33 @@ __global__ void __launch_bounds__(kBoundThreads, 4) block_bounds_kernel(const Bo
             if (sub < 2) {  // lanes of the first row write the largest, of the second the smallest
                 uint32_t word[2] = {0u, 0u};
                 if (s > 0.f) {
+                    // largest values as they are, smallest ones with the sign turned: both
+                    // are codes ceil(x / s)
+                    const float sign = sub ? -1.f : 1.f;
+                    float x[8], z[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const uint32_t x = sub ? low[e >> 1] : top[e >> 1];
-                        const float y = __fdiv_rn(e & 1 ? Elt<BF16>::hi(x) : Elt<BF16>::lo(x), s);
-                        const float z = sub ? floorf(y) : ceilf(y);
-                        const int code = (int)fminf(fmaxf(z, -127.f), 127.f);
+                        const uint32_t w2 = sub ? low[e >> 1] : top[e >> 1];
+                        x[e] = sign * (e & 1 ? Elt<BF16>::hi(w2) : Elt<BF16>::lo(w2));
+                    }
+                    // x / s is at most 127 and a bit, so x * (1 / s) is off by less than 2^-15: the
+                    // same ceiling as the quotient's unless an integer is nearer than that,
+                    // or the code 127 all the same
+                    const float r = __frcp_rn(s);
+                    bool near = !(s >= 1e-30f);  // (no reciprocal to speak of)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float y = x[e] * r;
+                        z[e] = ceilf(y);
+                        near |= fabsf(y - rintf(y)) < 0x1p-13f && y < 126.5f;
+                    }
+                    if (near) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) z[e] = ceilf(__fdiv_rn(x[e], s));
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int code = (int)(sign * fminf(fmaxf(z[e], -127.f), 127.f));
                         word[e >> 2] |= (uint32_t)(code & 0xff) << (8 * (e & 3));
                     }
                 }

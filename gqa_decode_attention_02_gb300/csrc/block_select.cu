@@ -233,8 +233,7 @@ __global__ void __launch_bounds__(kBoundThreads, 4) block_bounds_kernel(const Bo
     }
 }
 
-// ---- scores ------------------------------------------------------------------------
-constexpr int kScoreThreads = 128;
+// ---- scores and the choice -----------------------------------------------------------
 struct SelectParams {
     const void* q;
     const int8_t* bounds;
@@ -247,7 +246,7 @@ struct SelectParams {
     float* scores;  // [B][K][max_blocks]
     int32_t* status;
     int B, N, K, G, max_blocks, num_blocks;
-    int keep, first, recent, splits;
+    int keep, first, recent;
 };
 
 __device__ __forceinline__ int blocks_of(const SelectParams& p, int ctx) {
@@ -263,24 +262,20 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// A CTA per sequence, KV head and part of its blocks.  The score is one product of a
-// block's row [largest | smallest] with [max(c, 0) | min(c, 0)] of each query, 16 blocks
-// by 8 queries at a time.  A product's k positions are in the order in which 16-byte
-// loads bring them, the same for both sides.  Bound by reading the bounds.
+// Scores of a sequence's blocks for a KV head, by a cluster of CTAs, each a part of them.
+// The score is one product of a block's row [largest | smallest] with [max(c, 0) | min(c, 0)]
+// of each query, 16 blocks by 8 queries at a time.  A product's k positions are in the
+// order in which 16-byte loads bring them, the same for both sides.  Bound by reading the
+// bounds.
 template <bool BF16, int H>
-__global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const SelectParams p) {
+__device__ void block_scores(const SelectParams& p, int bk, int nb, int part, int parts,
+                             uint4* codes) {
     constexpr int V = 2 * H / 16;  // 16-byte pieces of a row
-    extern __shared__ uint4 codes[];  // [ceil(G / 8) * 8][V], then the scales
-    griddep_launch_dependents();
-    griddep_wait();
-    const int part = blockIdx.x % p.splits, bk = blockIdx.x / p.splits;
-    const int b = bk / p.K, k = bk - b * p.K;
-    const int ctx = __ldg(p.context_lens + b), nb = blocks_of(p, ctx);
-    if (nb <= p.keep) return;  // all of them
+    const int b = bk / p.K, k = bk - b * p.K, warps = blockDim.x / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G8 = (p.G + 7) / 8 * 8;
     float* qs = reinterpret_cast<float*>(codes + (size_t)G8 * V);
-    for (int g = warp; g < G8; g += kScoreThreads / 32) {
+    for (int g = warp; g < G8; g += warps) {
         constexpr int E = H / 32;  // elements of a lane
         float x[E], a = 0.f;
 #pragma unroll
@@ -310,8 +305,8 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const Select
     const int32_t* table = p.block_tables + (size_t)b * p.max_blocks;
     float* out = p.scores + (size_t)bk * p.max_blocks;
     const int tiles = (nb + 15) / 16, g = lane >> 2, t = lane & 3;
-    const int stride = p.splits * (kScoreThreads / 32);
-    int tile = part * (kScoreThreads / 32) + warp;
+    const int stride = parts * warps;
+    int tile = part * warps + warp;
     auto load_id = [&](int x) {
         const int i = x * 16 + (lane & 15);
         return i < nb ? __ldg(table + i) : 0;
@@ -367,7 +362,6 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const Select
     }
 }
 
-// ---- the choice --------------------------------------------------------------------
 constexpr int kPickHeld = 9600;  // scores held in shared memory; more are read again
 
 // Order-preserving bits of a score (-0 as 0; a NaN, which a scale that holds one gives,
@@ -383,41 +377,23 @@ __device__ __forceinline__ int before_warp(const int* sums, int warp, int lane, 
     return __reduce_add_sync(kFull, lane < warp && lane < warps ? sums[lane] : 0);
 }
 
-// A CTA per sequence and KV head: the key of the last block to take by passes over eleven
+// The choice, by one CTA: the key of the last block to take by passes over eleven
 // bits each (a histogram of the candidates that share the bits found so far), from the
 // first bit in which any two candidates differ -- the leading ones, sign and exponent, are
 // mostly alike, and a histogram of them would be one bin --, or, once no more than 32 are
 // left, by comparing those with one another; then the blocks above it and as many of those
 // at it as are left, in order.
-__global__ void __launch_bounds__(1024, 2) block_pick_kernel(const SelectParams p) {
+__device__ void block_pick(const SelectParams& p, int bk, int nb, uint32_t* keys) {
     constexpr int kBits = 11, kBins = 1 << kBits;
     __shared__ int hist[kBins];
     __shared__ int sums[2][32];
     __shared__ uint32_t s_or, s_and, s_prefix, s_few[32];
     __shared__ int s_left, s_bin, s_count;
-    extern __shared__ uint32_t keys[];
-    griddep_launch_dependents();
-    griddep_wait();
-    const int bk = blockIdx.x, b = bk / p.K, k = bk - b * p.K;
-    const int tid = threadIdx.x, threads = blockDim.x;
+    const int b = bk / p.K, tid = threadIdx.x, threads = blockDim.x;
     const int lane = tid & 31, warp = tid >> 5;
-    const int ctx = __ldg(p.context_lens + b), nb = blocks_of(p, ctx);
     const int32_t* table = p.block_tables + (size_t)b * p.max_blocks;
     int32_t* tables = p.tables + (size_t)bk * p.keep;
     int32_t* blocks = p.blocks + (size_t)bk * p.keep;
-    const int held = min(nb, p.keep);
-    if (k == 0 && tid == 0) {
-        p.lens[b] = nb ? (held - 1) * 16 + ctx - (nb - 1) * 16 : 0;
-        if (nb == 0) report(p.status, GQA_ERR_CONTEXT);
-    }
-    for (int i = held + tid; i < p.keep; i += threads) tables[i] = blocks[i] = -1;
-    if (nb <= p.keep) {
-        for (int i = tid; i < nb; i += threads) {
-            tables[i] = __ldg(table + i);
-            blocks[i] = i;
-        }
-        return;
-    }
     // blocks [lo, hi) compete for `left` places
     const int lo = p.first, hi = nb - p.recent, count = hi - lo;
     int left = p.keep - p.first - p.recent;
@@ -462,12 +438,11 @@ __global__ void __launch_bounds__(1024, 2) block_pick_kernel(const SelectParams 
             if ((u & known) == prefix) atomicAdd(&hist[u >> shift & (bins - 1)], 1);
         }
         __syncthreads();
-        // bin of the left-th largest: thread t < 512 has the `per` bins from the top's t-th
-        const int per = (bins + 511) / 512, t0 = bins - 1 - tid * per;
+        // bin of the left-th largest: thread t has the `per` bins from the top's (t * per)-th
+        const int per = (bins + threads - 1) / threads, t0 = bins - 1 - tid * per;
         int own = 0;
-        if (tid < 512)
-            for (int x = 0; x < per; ++x)
-                if (t0 - x >= 0) own += hist[t0 - x];
+        for (int x = 0; x < per; ++x)
+            if (t0 - x >= 0) own += hist[t0 - x];
         int incl = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -477,7 +452,7 @@ __global__ void __launch_bounds__(1024, 2) block_pick_kernel(const SelectParams 
         if (lane == 31) sums[0][warp] = incl;
         __syncthreads();
         incl += before_warp(sums[0], warp, lane, threads / 32);
-        if (tid < 512 && incl - own < left && left <= incl) {
+        if (incl - own < left && left <= incl) {
             int above = incl - own, x = 0;
             while (above + hist[t0 - x] < left) above += hist[t0 - x++];
             s_prefix = prefix | (uint32_t)(t0 - x) << shift;
@@ -549,6 +524,42 @@ __global__ void __launch_bounds__(1024, 2) block_pick_kernel(const SelectParams 
     }
 }
 
+// A cluster per sequence and KV head: scores, then its first CTA's choice.
+template <bool BF16, int H>
+__global__ void __launch_bounds__(512, 2) block_select_kernel(const SelectParams p) {
+    extern __shared__ uint4 scratch[];  // the queries' codes and scales, then the scores' keys
+    griddep_launch_dependents();
+    griddep_wait();
+    uint32_t part, parts;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(part));
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(parts));
+    const int bk = blockIdx.x / parts, b = bk / p.K, k = bk - b * p.K, tid = threadIdx.x;
+    const int ctx = __ldg(p.context_lens + b), nb = blocks_of(p, ctx);
+    const int held = min(nb, p.keep);
+    int32_t* tables = p.tables + (size_t)bk * p.keep;
+    int32_t* blocks = p.blocks + (size_t)bk * p.keep;
+    if (part == 0) {
+        if (k == 0 && tid == 0) {
+            p.lens[b] = nb ? (held - 1) * 16 + ctx - (nb - 1) * 16 : 0;
+            if (nb == 0) report(p.status, GQA_ERR_CONTEXT);
+        }
+        for (int i = held + tid; i < p.keep; i += blockDim.x) tables[i] = blocks[i] = -1;
+        if (nb <= p.keep)
+            for (int i = tid; i < nb; i += blockDim.x) {
+                tables[i] = __ldg(p.block_tables + (size_t)b * p.max_blocks + i);
+                blocks[i] = i;
+            }
+    }
+    if (nb <= p.keep) return;  // all of them (the whole cluster)
+    block_scores<BF16, H>(p, bk, nb, (int)part, (int)parts, scratch);
+    __syncthreads();  // the codes have been read
+    if (parts > 1)    // and every part of the scores is there
+        asm volatile(
+            "barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                : "memory");
+    if (part == 0) block_pick(p, bk, nb, reinterpret_cast<uint32_t*>(scratch));
+}
+
 }  // namespace
 
 gqa_status launch_block_bounds(const gqa_shape& s, const void* k_cache,
@@ -590,46 +601,40 @@ gqa_status launch_select_blocks(const gqa_shape& s, int keep, int first, int rec
     if (sms <= 0) return GQA_ERR_CUDA;
     SelectParams p = {q, bounds, bounds_scale, block_tables, context_lens, tables, lens, blocks,
                       static_cast<float*>(workspace), dev_status, s.B, s.N, s.K, s.N / s.K,
-                      s.max_blocks_per_seq, s.num_blocks, keep, first, recent, 1};
+                      s.max_blocks_per_seq, s.num_blocks, keep, first, recent};
     const long long bk = (long long)s.B * s.K;
+    const size_t codes = (size_t)(p.G + 7) / 8 * 8 * (2 * s.H + sizeof(float));
+    const size_t keys = sizeof(uint32_t) * (size_t)std::min(s.max_blocks_per_seq, kPickHeld);
+    const size_t smem = std::max(codes, keys);
+    if (smem > 39 * 1024 || bk * 8 > (1ll << 31) - 1) return GQA_ERR_SHAPE;
+    // As many CTAs per row as are resident at once (four of 256 threads on an SM), up to a
+    // cluster's eight, and no more than there are tiles of 16 blocks for their warps; rows
+    // so few that this leaves SMs idle get CTAs of 512.
+    const int threads = bk * 8 <= sms ? 512 : 256;
     const long long tiles = (s.max_blocks_per_seq + 15) / 16;
-    // one wave of CTAs (seven fit on an SM), so that a CTA's start is paid once
-    long long splits = std::max<long long>(1, sms * 7 / bk);
-    const long long most = (tiles + kScoreThreads / 32 - 1) / (kScoreThreads / 32);
-    if (splits > most) splits = most;
-    p.splits = (int)splits;
-    const size_t smem = (size_t)(p.G + 7) / 8 * 8 * (2 * s.H + sizeof(float));
-    if (smem > 48 * 1024 || bk * splits > (1ll << 31) - 1) return GQA_ERR_SHAPE;
+    int parts = 1;
+    while (parts < 8 && bk * parts * 2 <= sms * (threads == 512 ? 2 : 4) &&
+           parts * 2 * (threads / 32) <= tiles)
+        parts *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)(bk * parts));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)parts;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cudaError_t e = cudaSuccess;
-    if (s.max_blocks_per_seq > keep) {
-        cfg.numAttrs = (s.flags & (GQA_FLAG_PDL | GQA_FLAG_EARLY_KV)) ? 1 : 0;
-        cfg.gridDim = dim3((unsigned)(bk * splits));
-        cfg.blockDim = dim3(kScoreThreads);
-        cfg.dynamicSmemBytes = smem;
-        e = s.dtype == GQA_BF16
-                ? (s.H == 64 ? cudaLaunchKernelEx(&cfg, block_score_kernel<true, 64>, p)
-                             : cudaLaunchKernelEx(&cfg, block_score_kernel<true, 128>, p))
-                : (s.H == 64 ? cudaLaunchKernelEx(&cfg, block_score_kernel<false, 64>, p)
-                             : cudaLaunchKernelEx(&cfg, block_score_kernel<false, 128>, p));
-        if (e != cudaSuccess) return launch_status(e);
-        cfg.numAttrs = 1;  // it waits for the scores itself
-    } else {
-        cfg.numAttrs = (s.flags & (GQA_FLAG_PDL | GQA_FLAG_EARLY_KV)) ? 1 : 0;
-    }
-    cfg.gridDim = dim3((unsigned)bk);
-    // as many threads as let every row be resident at once, within 512 .. 1024
-    cfg.blockDim = dim3(bk <= 2 * sms ? 1024 : 512);
-    // (static and dynamic together within what needs no opt-in)
-    cfg.dynamicSmemBytes =
-        sizeof(uint32_t) * (size_t)(s.max_blocks_per_seq < kPickHeld ? s.max_blocks_per_seq
-                                                                           : kPickHeld);
-    return launch_status(cudaLaunchKernelEx(&cfg, block_pick_kernel, p));
+    cfg.numAttrs = (s.flags & (GQA_FLAG_PDL | GQA_FLAG_EARLY_KV)) ? 2 : 1;
+    return launch_status(
+        s.dtype == GQA_BF16
+            ? (s.H == 64 ? cudaLaunchKernelEx(&cfg, block_select_kernel<true, 64>, p)
+                         : cudaLaunchKernelEx(&cfg, block_select_kernel<true, 128>, p))
+            : (s.H == 64 ? cudaLaunchKernelEx(&cfg, block_select_kernel<false, 64>, p)
+                         : cudaLaunchKernelEx(&cfg, block_select_kernel<false, 128>, p)));
 }
 
 }  // namespace gqa

@@ -905,7 +905,7 @@ __device__ bool chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
         const bool whole = first_cta < 0;
         float* const part =
             p.partials + ((size_t)((int)blockIdx.x * 2 + w) * 2 + tile) * C::kPart;
-        const float inv = bad || !(l > 0.f) ? 0.f : 1.f / l;
+        const float inv = bad || l == 0.f ? 0.f : 1.f / l;  // (a NaN score: a NaN row)
         uint4* const dst = whole ? out : reinterpret_cast<uint4*>(part);
         if (warp_on && some) {
 #pragma unroll 1
@@ -1010,17 +1010,17 @@ __device__ void chunk_shared(const ChunkParams& p, ChunkSmem& sm, float* weight)
                 const float* q = c ? rest + (size_t)(c - 1) * 4 * C::kPart : rows;
                 const float mc = on ? __ldcg(q) : 0.f, lc = on ? __ldcg(q + kRows) : 0.f;
                 bad |= lc < 0.f;
-                const bool seen = lc > 0.f;  // else nothing in this piece
+                const bool seen = !(lc <= 0.f);  // else nothing in this piece
                 const float top = seen ? fmaxf(M, mc) : M;
                 const float f = M == -INFINITY ? 0.f : fast_exp2(M - top);
                 L = fmaf(L, f, seen ? lc * fast_exp2(mc - top) : 0.f);
                 M = top;
                 weight[c * 2 * kRows + tid] = seen ? mc : -INFINITY;
             }
-            const float inv = bad || !(L > 0.f) ? 0.f : 1.f / L;
+            const float inv = bad || L == 0.f ? 0.f : 1.f / L;
             for (int c = 0; c < pieces; ++c) {
                 float& x = weight[c * 2 * kRows + tid];
-                x = x == -INFINITY ? 0.f : fast_exp2(x - M) * inv;
+                x = (x == -INFINITY ? 0.f : fast_exp2(x - M)) * inv;  // (a NaN stays one)
             }
         }
         if (!meet()) return give_up(sm, p);

@@ -738,9 +738,10 @@ gqa_status gqa_kv_append_rotary(const gqa_shape *shape, int64_t rows, const void
  * them; blocks wholly below the earliest token's window are never read.  Otherwise as
  * gqa_verify_attention, for a cache in q's dtype: the softmax in fp32, probabilities
  * rounded to dtype for the product with V, fp32 sums.  Rows outside every sequence's are
- * neither read for a result nor written.  A NaN or infinity in V at a position that
- * the token's own 128 neighbours see and the token does not may reach its output; those
- * that no token of the call's sequence sees do not.
+ * neither read for a result nor written.  A score that is NaN makes its row NaN.  A NaN
+ * or infinity in V at a position j that some new tokens of the sequence see and others
+ * do not may reach the outputs of those others that see any of positions j / 128 * 128
+ * .. + 127; in K, or at a position that no new token of the sequence sees, it does not.
  * Requires B <= 16384, N / K <= 8192, H in {64, 128}; shape->T is not used (1);
  * GQA_FLAG_EARLY_KV acts as GQA_FLAG_PDL, the flags that force a kernel give
  * GQA_ERR_SHAPE.  out must not overlap an input.  Workspace: at least
@@ -751,7 +752,8 @@ gqa_status gqa_kv_append_rotary(const gqa_shape *shape, int64_t rows, const void
  * Device errors: context_lens[b] < n or > 16 * max_blocks_per_seq: the sequence's rows
  * are zeros (GQA_ERR_CONTEXT); cu_new[b] < 0, > cu_new[b+1] or cu_new[b+1] > M: the
  * sequence is left out (GQA_ERR_CONTEXT); a block id in use out of range: zeros for
- * the rows that would read it (GQA_ERR_BLOCK_ID). */
+ * the rows that would read it (GQA_ERR_BLOCK_ID), and maybe for rows computed with
+ * them, less than max(2, 256 / (N / K)) tokens away. */
 size_t gqa_chunk_workspace_size(const gqa_shape *shape);
 gqa_status gqa_chunk_attention(const gqa_shape *shape, int64_t rows, const void *q,
                                int64_t q_stride, const void *k_cache, const void *v_cache,
@@ -772,8 +774,10 @@ gqa_status gqa_chunk_attention(const gqa_shape *shape, int64_t rows, const void 
  * It makes anew those of the blocks that hold one of the newest cu_new[b+1] - cu_new[b]
  * tokens of a sequence (cu_new: int32 [B+1]), so one call after every append keeps
  * them all.  (Where acceptance has shortened a sequence they may still count rows that
- * were dropped, until the next append to that block.)  Device errors: lengths as in
- * gqa_chunk_attention, a bad block id: that sequence or block is left as it was.
+ * were dropped, until the next append to that block; after gqa_kv_compact, which moves
+ * rows, a call with the tokens that were kept makes them bounds again.)  Device errors:
+ * lengths as in gqa_chunk_attention, a bad block id: that sequence or block is left as
+ * it was.
  *
  * gqa_select_blocks chooses, for every sequence and KV head, `keep` of its blocks (all of
  * them if it has no more): the `first` ones and the `recent` newest ones always, the

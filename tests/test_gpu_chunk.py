@@ -315,3 +315,54 @@ def test_binding_refuses(gpu):
             gq.chunk_attention(*d, **kw)
     with pytest.raises(gq.GqaError):  # heads that do not divide
         gq.chunk_attention(d[0][:, :3].contiguous(), *d[1:])
+
+
+@pytest.mark.parametrize("n,ctx", [(40, 400), (40, 20000), (1, 20000)])
+@pytest.mark.parametrize("what", ["q", "k", "all", "inf"])
+def test_nan_scores_give_nan_rows(gpu, n, ctx, what):
+    """Of items that one CTA does and of shared ones; other rows and sequences as they were."""
+    c = Case([(3, 33), (n, ctx), (2, 90)], 8, 2, 128, BF16, seed=n)
+    want = c.run(gpu)
+    nan = torch.zeros_like(want, dtype=torch.bool)
+    at = ctx - n + n // 2  # a position; tokens from there on see it
+    blk, row = c.tables[1, at // 16].long(), at % 16
+    if what == "q":
+        c.q[3 + n // 2, 4:6] = float("nan")
+        nan[3 + n // 2, 4:6] = True
+    elif what == "k":
+        c.kc[blk, row, 1] = float("nan")
+        nan[3 + n // 2:3 + n, 4:] = True
+    elif what == "all":  # no score is a number
+        for b in range(-(-ctx // 16)):
+            c.kc[c.tables[1, b].long(), :, 0] = float("nan")
+        nan[3:3 + n, :4] = True
+    else:  # q . k = inf: inf - inf in the softmax
+        c.kc[blk, row, 0] = float("inf")
+        c.q[3:3 + n] = c.q[3:3 + n].abs()
+    got = c.run(gpu)
+    assert c.status == 0
+    if what == "inf":
+        assert torch.isnan(got[3 + n // 2:3 + n, :4]).all()
+        assert not torch.isnan(got[:3 + n // 2]).any() and not torch.isnan(got[3 + n:]).any()
+        return
+    assert torch.isnan(got[nan]).all()
+    assert torch.equal(got[~nan], want[~nan])
+
+
+def test_a_workspace_of_the_callers(gpu):
+    """Of the very size, with guards behind it; its tickets zero again after every call."""
+    c = Case([(1, 9000), (40, 4000)], 8, 2, 128, BF16, seed=6)
+    want = c.run(gpu)
+    shape = gq.Shape(B=2, T=1, N=8, K=2, H=128, block_size=16, num_blocks=c.kc.shape[0],
+                     max_blocks_per_seq=c.tables.shape[1], dtype=1, scale=0.0, flags=0,
+                     window=0, kv_dtype=0)
+    n = gq.chunk_workspace_size(shape)
+    ws = torch.zeros(n + 4096, dtype=torch.uint8, device=gpu)
+    ws[n:] = 77
+    for _ in range(3):
+        assert torch.equal(c.run(gpu, workspace=ws[:n]), want)
+    assert (ws[n:] == 77).all() and (ws[:1 << 14] == 0).all()
+    with pytest.raises(gq.GqaError):
+        c.run(gpu, workspace=ws[:n - 16])
+    with pytest.raises((ValueError, TypeError)):
+        c.run(gpu, workspace=ws[:n].cpu())

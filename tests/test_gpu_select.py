@@ -323,3 +323,67 @@ def test_a_serving_run(gpu):
         graph.replay()
         check(*captured)
     assert ctx.tolist() == [351, 322, 58]
+
+
+def test_streams_graphs_and_dependent_launches(gpu):
+    """Two graphs of bounds, choice and attention captured on one stream, replayed on two at
+    once between eager calls; then the three as dependent launches."""
+    cases = [Case([(1, 5000), (1, 900), (1, 16)], 8, 2, 128, BF16, seed=21),
+             Case([(1, 12000), (1, 300)], 8, 2, 128, BF16, seed=22)]
+    sets = []
+    for c in cases:
+        d = [x.to(gpu) for x in (c.kc, c.vc, c.tables, c.ctx, c.cu)]
+        codes, scale = buffers(c.kc.shape[0], 2, 128, gpu)
+        whole = torch.cumsum(torch.cat([c.ctx.new_zeros(1), c.ctx]), 0).to(torch.int32).to(gpu)
+        gq.kv_block_bounds(d[0], d[2], d[3], whole, codes, scale)
+        sets.append((c.q[:, None].to(gpu), d, codes, scale))
+
+    def step(q, d, codes, scale, **kw):
+        gq.kv_block_bounds(d[0], d[2], d[3], d[4], codes, scale, **kw)
+        ch = gq.select_blocks(q, codes, scale, d[2], d[3], 40, **kw)
+        return ch, gq.sparse_decode_attention(q, d[0], d[1], ch.tables, ch.lens, **kw)
+
+    def same(a, b):
+        return all(torch.equal(x, y) for x, y in zip((*a[0], a[1]), (*b[0], b[1])))
+
+    want = [step(*s) for s in sets]
+    torch.cuda.synchronize()
+    side, graphs, held = torch.cuda.Stream(), [], []
+    with torch.cuda.stream(side):
+        for s in sets:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                held.append(step(*s))
+            graphs.append(g)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        x = step(*sets[0])
+    torch.cuda.synchronize()
+    assert same(held[0], want[0]) and same(held[1], want[1]) and same(x, want[0])
+    for _ in range(20):
+        x = step(*sets[1], pdl=True)
+    torch.cuda.synchronize()
+    assert same(x, want[1])
+    x = step(*sets[0], stream=streams[0])
+    streams[0].synchronize()
+    assert same(x, want[0])
+
+
+def test_scratch_of_the_callers(gpu):
+    args = [x.to(gpu) for x in make_select(2, 8, 2, 64, F16, [4000, 333])]
+    want = gq.select_blocks(*args, 8)
+    n = 2 * 2 * args[3].shape[1] * 4
+    ws = torch.full((n + 256,), 77, dtype=torch.uint8, device=gpu)
+    got = gq.select_blocks(*args, 8, workspace=ws[:n])
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and (ws[n:] == 77).all()
+    with pytest.raises(gq.GqaError):
+        gq.select_blocks(*args, 8, workspace=ws[:n - 4])
+
+
+def test_more_places_than_the_table_is_wide(gpu):
+    args = make_select(3, 8, 2, 64, F16, [400, 333, 1])
+    check_select(gpu, args, args[3].shape[1] + 9, 4, 3)

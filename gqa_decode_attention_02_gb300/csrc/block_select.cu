@@ -245,10 +245,11 @@ struct SelectParams {
     int32_t* tables;
     int32_t* lens;
     int32_t* blocks;
-    float* scores;  // [B][K][max_blocks]
+    float* scores;  // [B][K][max_blocks], of sequences of more blocks than `hold`
     int32_t* status;
     int B, N, K, G, max_blocks, num_blocks;
     int keep, first, recent;
+    int hold;       // scores that a CTA holds in shared memory, behind the queries' codes
 };
 
 __device__ __forceinline__ int blocks_of(const SelectParams& p, int ctx) {
@@ -264,7 +265,16 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Scores of a sequence's blocks for a KV head, by a cluster of CTAs, each a part of them.
+// Order-preserving bits of a score (-0 as 0; a NaN, which a scale that holds one gives,
+// below every number).
+__device__ __forceinline__ uint32_t score_key(float x) {
+    if (x != x) return 0u;
+    const uint32_t u = __float_as_uint(x + 0.f);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// Scores of a sequence's blocks for a KV head, by a cluster of CTAs, each a part of them: as
+// keys in the first CTA's shared memory (`keys`), or, of more than that holds, in memory.
 // The score is one product of a block's row [largest | smallest] with [max(c, 0) | min(c, 0)]
 // of each query, 16 blocks by 8 queries at a time.  A product's k positions are in the
 // order in which 16-byte loads bring them, the same for both sides.  Bound by reading the
@@ -274,7 +284,7 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
 // took 72 to 91 us.)
 template <bool BF16, int H>
 __device__ void block_scores(const SelectParams& p, int bk, int nb, int part, int parts,
-                             uint4* codes) {
+                             uint4* codes, const uint32_t* keys) {
     constexpr int V = 2 * H / 16;  // 16-byte pieces of a row
     const int b = bk / p.K, k = bk - b * p.K, warps = blockDim.x / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -307,8 +317,21 @@ __device__ void block_scores(const SelectParams& p, int bk, int nb, int part, in
         if (lane == 0) qs[g] = t;
     }
     __syncthreads();
+    const bool held = nb <= p.hold;
+    uint32_t dst;  // of the first CTA's keys
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(dst) : "r"(smem_addr(keys)));
+    if (parts > 1)  // it has begun
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     const int32_t* table = p.block_tables + (size_t)b * p.max_blocks;
     float* out = p.scores + (size_t)bk * p.max_blocks;
+    auto store = [&](int i, float x) {
+        if (held)
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dst + 4u * (uint32_t)i),
+                         "r"(score_key(x))
+                         : "memory");
+        else
+            out[i] = x;
+    };
     const int tiles = (nb + 15) / 16, g = lane >> 2, t = lane & 3;
     const int stride = parts * warps;
     int tile = part * warps + warp;
@@ -361,20 +384,10 @@ __device__ void block_scores(const SelectParams& p, int bk, int nb, int part, in
         }
         if (t == 0) {
             const int ia = tile * 16 + g;
-            if (ia < nb) out[ia] = bads >> g & 1 ? -INFINITY : va;
-            if (ia + 8 < nb) out[ia + 8] = bads >> (g + 8) & 1 ? -INFINITY : vb;
+            if (ia < nb) store(ia, bads >> g & 1 ? -INFINITY : va);
+            if (ia + 8 < nb) store(ia + 8, bads >> (g + 8) & 1 ? -INFINITY : vb);
         }
     }
-}
-
-constexpr int kPickHeld = 9600;  // scores held in shared memory; more are read again
-
-// Order-preserving bits of a score (-0 as 0; a NaN, which a scale that holds one gives,
-// below every number).
-__device__ __forceinline__ uint32_t score_key(float x) {
-    if (x != x) return 0u;
-    const uint32_t u = __float_as_uint(x + 0.f);
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
 // Sum of the first `warp` of a CTA's per-warp counts (whole warp).
@@ -388,7 +401,7 @@ __device__ __forceinline__ int before_warp(const int* sums, int warp, int lane, 
 // mostly alike, and a histogram of them would be one bin --, or, once no more than 32 are
 // left, by comparing those with one another; then the blocks above it and as many of those
 // at it as are left, in order.
-__device__ void block_pick(const SelectParams& p, int bk, int nb, uint32_t* keys) {
+__device__ void block_pick(const SelectParams& p, int bk, int nb, const uint32_t* keys) {
     constexpr int kBits = 11, kBins = 1 << kBits;
     __shared__ int hist[kBins];
     __shared__ int sums[2][32];
@@ -410,7 +423,8 @@ __device__ void block_pick(const SelectParams& p, int bk, int nb, uint32_t* keys
     }
     if (left == 0) return;
     const float* scores = p.scores + (size_t)bk * p.max_blocks + lo;
-    const bool in_smem = count <= kPickHeld;
+    const bool held = nb <= p.hold;
+    auto key = [&](int i) { return held ? keys[lo + i] : score_key(__ldcg(scores + i)); };
     if (tid == 0) {
         s_or = 0u;
         s_and = ~0u;
@@ -418,8 +432,7 @@ __device__ void block_pick(const SelectParams& p, int bk, int nb, uint32_t* keys
     __syncthreads();
     uint32_t any = 0u, all = ~0u;
     for (int i = tid; i < count; i += threads) {
-        const uint32_t u = score_key(__ldcg(scores + i));
-        if (in_smem) keys[i] = u;
+        const uint32_t u = key(i);
         any |= u;
         all &= u;
     }
@@ -430,7 +443,6 @@ __device__ void block_pick(const SelectParams& p, int bk, int nb, uint32_t* keys
         atomicAnd(&s_and, all);
     }
     __syncthreads();
-    auto key = [&](int i) { return in_smem ? keys[i] : score_key(__ldcg(scores + i)); };
     int bits = 32 - __clz(s_or ^ s_and);  // low bits in which keys differ
     uint32_t prefix = bits == 32 ? 0u : s_and >> bits << bits;
     while (bits > 0) {
@@ -529,9 +541,12 @@ __device__ void block_pick(const SelectParams& p, int bk, int nb, uint32_t* keys
     }
 }
 
+constexpr int kMaxSelectThreads = 1024;
+
 // A cluster per sequence and KV head: scores, then its first CTA's choice.
 template <bool BF16, int H>
-__global__ void __launch_bounds__(512, 2) block_select_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kMaxSelectThreads, 1024 / kMaxSelectThreads)
+    block_select_kernel(const SelectParams p) {
     extern __shared__ uint4 scratch[];  // the queries' codes and scales, then the scores' keys
     griddep_launch_dependents();
     griddep_wait();
@@ -556,13 +571,16 @@ __global__ void __launch_bounds__(512, 2) block_select_kernel(const SelectParams
             }
     }
     if (nb <= p.keep) return;  // all of them (the whole cluster)
-    block_scores<BF16, H>(p, bk, nb, (int)part, (int)parts, scratch);
-    __syncthreads();  // the codes have been read
-    if (parts > 1)    // and every part of the scores is there
+    if (parts > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    uint32_t* const keys =
+        reinterpret_cast<uint32_t*>(scratch) + (p.G + 7) / 8 * 8 * (2 * H / 4 + 1);
+    block_scores<BF16, H>(p, bk, nb, (int)part, (int)parts, scratch, keys);
+    __syncthreads();
+    if (parts > 1)  // every part of the scores is there
         asm volatile(
             "barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                 : "memory");
-    if (part == 0) block_pick(p, bk, nb, reinterpret_cast<uint32_t*>(scratch));
+    if (part == 0) block_pick(p, bk, nb, keys);
 }
 
 }  // namespace
@@ -606,19 +624,21 @@ gqa_status launch_select_blocks(const gqa_shape& s, int keep, int first, int rec
     if (sms <= 0) return GQA_ERR_CUDA;
     SelectParams p = {q, bounds, bounds_scale, block_tables, context_lens, tables, lens, blocks,
                       static_cast<float*>(workspace), dev_status, s.B, s.N, s.K, s.N / s.K,
-                      s.max_blocks_per_seq, s.num_blocks, keep, first, recent};
+                      s.max_blocks_per_seq, s.num_blocks, keep, first, recent, 0};
     const long long bk = (long long)s.B * s.K;
     const size_t codes = (size_t)(p.G + 7) / 8 * 8 * (2 * s.H + sizeof(float));
-    const size_t keys = sizeof(uint32_t) * (size_t)std::min(s.max_blocks_per_seq, kPickHeld);
-    const size_t smem = std::max(codes, keys);
-    if (smem > 39 * 1024 || bk * 8 > (1ll << 31) - 1) return GQA_ERR_SHAPE;
+    constexpr size_t most = 39 * 1024;  // with what is static, what needs no opt-in
+    if (codes > most || bk * 8 > (1ll << 31) - 1) return GQA_ERR_SHAPE;
+    p.hold = (int)std::min((most - codes) / sizeof(uint32_t), (size_t)s.max_blocks_per_seq);
+    const size_t smem = codes + p.hold * sizeof(uint32_t);
     // As many CTAs per row as are resident at once (four of 256 threads on an SM), up to a
     // cluster's eight, and no more than there are tiles of 16 blocks for their warps; rows
-    // so few that this leaves SMs idle get CTAs of 512.
-    const int threads = bk * 8 <= sms ? 512 : 256;
+    // so few that this leaves SMs idle get CTAs of 1,024 (one row of 6,251 blocks, 8 heads:
+    // 17.4 us, of 512 18.1, with the scores by way of memory 19.3).
+    const int threads = bk * 8 <= sms ? kMaxSelectThreads : 256;
     const long long tiles = (s.max_blocks_per_seq + 15) / 16;
     int parts = 1;
-    while (parts < 8 && bk * parts * 2 <= sms * (threads == 512 ? 2 : 4) &&
+    while (parts < 8 && bk * parts * 2 <= sms * (1024 / threads) &&
            parts * 2 * (threads / 32) <= tiles)
         parts *= 2;
     cudaLaunchConfig_t cfg = {};

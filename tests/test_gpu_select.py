@@ -387,3 +387,14 @@ def test_scratch_of_the_callers(gpu):
 def test_more_places_than_the_table_is_wide(gpu):
     args = make_select(3, 8, 2, 64, F16, [400, 333, 1])
     check_select(gpu, args, args[3].shape[1] + 9, 4, 3)
+
+
+@pytest.mark.parametrize("N,K,H", [(4, 1, 128), (128, 1, 128), (9, 1, 64)])
+def test_scores_in_shared_memory_or_not(gpu, N, K, H):
+    """Around the number of blocks whose scores fit behind the queries' codes."""
+    most = (39 * 1024 - (N + 7) // 8 * 8 * (2 * H + 4)) // 4
+    for nb in (most - 1, most, most + 1):
+        args = make_select(1, N, K, H, BF16, [nb * 16 - 3], seed=nb)
+        assert check_select(gpu, args, 70, 2, 3)[0] == 0
+    args = make_select(3, N, K, H, BF16, [most * 16 + 16, most * 16, 900], seed=5)
+    assert check_select(gpu, args, 33, 0, 1)[0] == 0

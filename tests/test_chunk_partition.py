@@ -7,8 +7,8 @@ import random
 
 import pytest
 
-LONE, PAIR, START, QUOTA = 5, 6, 10, 20
-NEAR = {LONE: 2 * LONE, PAIR: 8 * PAIR}
+LONE, PAIR, START, QUOTA = 5, 6, 10, 10
+NEAR = {LONE: LONE, PAIR: 8 * PAIR}
 
 
 def items(seqs, heads, tpc, window):

@@ -236,6 +236,7 @@ __global__ void __launch_bounds__(kBoundThreads, 4) block_bounds_kernel(const Bo
 }
 
 // ---- scores and the choice -----------------------------------------------------------
+constexpr int kMaxSelectThreads = 1024;
 struct SelectParams {
     const void* q;
     const int8_t* bounds;
@@ -395,15 +396,14 @@ __device__ __forceinline__ int before_warp(const int* sums, int warp, int lane, 
     return __reduce_add_sync(kFull, lane < warp && lane < warps ? sums[lane] : 0);
 }
 
-// The choice, by one CTA: the key of the last block to take by passes over eleven
-// bits each (a histogram of the candidates that share the bits found so far), from the
+// The choice, by one CTA: the key of the last block to take by passes over as many bits
+// as give a bin per thread (a histogram of the candidates that share the bits found so far), from the
 // first bit in which any two candidates differ -- the leading ones, sign and exponent, are
 // mostly alike, and a histogram of them would be one bin --, or, once no more than 32 are
 // left, by comparing those with one another; then the blocks above it and as many of those
 // at it as are left, in order.
 __device__ void block_pick(const SelectParams& p, int bk, int nb, const uint32_t* keys) {
-    constexpr int kBits = 11, kBins = 1 << kBits;
-    __shared__ int hist[kBins];
+    __shared__ int hist[kMaxSelectThreads];  // a bin per thread
     __shared__ int sums[2][32];
     __shared__ uint32_t s_or, s_and, s_prefix, s_few[32];
     __shared__ int s_left, s_bin, s_count;
@@ -446,8 +446,8 @@ __device__ void block_pick(const SelectParams& p, int bk, int nb, const uint32_t
     int bits = 32 - __clz(s_or ^ s_and);  // low bits in which keys differ
     uint32_t prefix = bits == 32 ? 0u : s_and >> bits << bits;
     while (bits > 0) {
-        const int take = min(bits, kBits), shift = bits - take, bins = 1 << take;
-        for (int i = tid; i < bins; i += threads) hist[i] = 0;
+        const int take = min(bits, 31 - __clz(threads)), shift = bits - take, bins = 1 << take;
+        hist[tid] = 0;
         __syncthreads();
         const uint32_t known = bits == 32 ? 0u : ~0u << bits;
         for (int i = tid; i < count; i += threads) {
@@ -455,11 +455,8 @@ __device__ void block_pick(const SelectParams& p, int bk, int nb, const uint32_t
             if ((u & known) == prefix) atomicAdd(&hist[u >> shift & (bins - 1)], 1);
         }
         __syncthreads();
-        // bin of the left-th largest: thread t has the `per` bins from the top's (t * per)-th
-        const int per = (bins + threads - 1) / threads, t0 = bins - 1 - tid * per;
-        int own = 0;
-        for (int x = 0; x < per; ++x)
-            if (t0 - x >= 0) own += hist[t0 - x];
+        // bin of the left-th largest: thread t has the t-th from the top
+        const int bin = bins - 1 - tid, own = bin >= 0 ? hist[bin] : 0;
         int incl = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -470,11 +467,9 @@ __device__ void block_pick(const SelectParams& p, int bk, int nb, const uint32_t
         __syncthreads();
         incl += before_warp(sums[0], warp, lane, threads / 32);
         if (incl - own < left && left <= incl) {
-            int above = incl - own, x = 0;
-            while (above + hist[t0 - x] < left) above += hist[t0 - x++];
-            s_prefix = prefix | (uint32_t)(t0 - x) << shift;
-            s_left = left - above;
-            s_bin = hist[t0 - x];
+            s_prefix = prefix | (uint32_t)bin << shift;
+            s_left = left - (incl - own);
+            s_bin = own;
             s_count = 0;
         }
         __syncthreads();
@@ -540,8 +535,6 @@ __device__ void block_pick(const SelectParams& p, int bk, int nb, const uint32_t
         e += u == prefix;
     }
 }
-
-constexpr int kMaxSelectThreads = 1024;
 
 // A cluster per sequence and KV head: scores, then its first CTA's choice.
 template <bool BF16, int H>
@@ -633,8 +626,8 @@ gqa_status launch_select_blocks(const gqa_shape& s, int keep, int first, int rec
     const size_t smem = codes + p.hold * sizeof(uint32_t);
     // As many CTAs per row as are resident at once (four of 256 threads on an SM), up to a
     // cluster's eight, and no more than there are tiles of 16 blocks for their warps; rows
-    // so few that this leaves SMs idle get CTAs of 1,024 (one row of 6,251 blocks, 8 heads:
-    // 17.4 us, of 512 18.1, with the scores by way of memory 19.3).
+    // so few that this leaves SMs idle get CTAs of 1,024 (one sequence of 6,251 blocks, 8 heads:
+    // 17.2 us, of 512 18.1, with the scores by way of memory 19.3).
     const int threads = bk * 8 <= sms ? kMaxSelectThreads : 256;
     const long long tiles = (s.max_blocks_per_seq + 15) / 16;
     int parts = 1;

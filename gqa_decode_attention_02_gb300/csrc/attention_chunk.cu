@@ -42,12 +42,12 @@
 //
 // Measured (one GB300, H = 128, bf16, 32 / 8 heads): 2,048 tokens behind 30,720 770 us, 1.38
 // PFLOP/s, 72 % of what a library product of 8192^3 reaches; a step takes 1.75 us (3,300 cycles)
-// for 2,048 cycles of MMAs.  The MMAs alone, with nothing to wait for, take 1.39 us here
-// (82 cycles each instead of 64); reading S and writing P costs them another 15 each (the
-// same tensor memory), and a slot's chain (softmax 1,350 cycles, hand-overs 400, its
-// products 1,600) is as long as that.  Short prompts (24 of 200..3,001): 525 us, of it some 100
-// at the items' ends, where both slots store outputs at once.  Single tokens, 256 x 2,048:
-// 358 us, 6.0 TB/s.
+// for 2,048 cycles of MMAs.  A slot's chain is that long: softmax 1,350 cycles, hand-overs 400,
+// its PV and QK 1,600 from the first to the last (issued by one thread that waits for nothing,
+// the same products take 1,024; with the issuers' waits, turns and commits alone 1,310; the
+// rest is the other slot's, still in the queue).  Short prompts (24 of 200..3,001): 525 us, of
+// it some 100 at the items' ends, where both slots store outputs at once.  Single tokens,
+// 256 x 2,048: 358 us, 6.0 TB/s.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -76,7 +76,9 @@ static_assert(128 * kRegsIssue + 256 * kRegsSoft <= kThreadsCh * 168, "register 
 // MMAs: 1.8 us), an item's start and end; and per CTA at least.
 constexpr int kLone = 5, kPair = 6, kStart = 10, kQuota = 10;
 // A range boundary this near to an item's start or end moves there: a smaller piece is not
-// worth its fold (some 5 us with one row tile of few rows, 20 with two full ones).
+// worth its fold (some 5 us with one row tile of few rows, 20 with two full ones; for one
+// row tile 2 KV tiles are: 4,096 tokens of 8 heads 21.2 us, with twice kNearLone and kQuota
+// 23.7).
 constexpr int kNearLone = kLone, kNearPair = 8 * kPair;
 constexpr float kSlack = 8.f;  // log2 slack before O is rescaled
 constexpr int kPieces = 8;      // pieces between the scheduler and the last role

@@ -600,7 +600,8 @@ __device__ void chunk_schedule(const CUtensorMap* tmq, const ChunkParams& p, uin
 // MMAs deep: two issuers hide each other's waits.  They take turns by a lock, a PV and the
 // QK behind it at a time: interleaved, both slots' products would end together, then
 // both softmaxes run while the tensor cores rest (measured 2.4 us per pair of tiles).  A
-// turn ends four MMAs before its products do, about what handing it over takes.
+// turn ends two MMAs before its products do, about what handing it over takes (24 prompts:
+// none 523.6 us, one 523.8, two 521.6, three 523.0, four 525.3, six 540.3).
 __device__ __forceinline__ bool take_turn(ChunkSmem& sm) {
     const uint32_t lock = smem_addr(&sm.lock);
 #pragma unroll 1
@@ -644,7 +645,7 @@ __device__ void chunk_mma(const ChunkParams& p, uint8_t* ring, uint8_t* qbuf, Ch
         const uint64_t dk = dk0 + (uint32_t)(r * (C::kTile >> 4));
 #pragma unroll
         for (int kk = 0; kk < H / 16; ++kk) {
-            if (kk == H / 16 - 4) end_turn(sm);
+            if (kk == H / 16 - 2) end_turn(sm);
             umma_ss(tS, dq + (uint64_t)(((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4),
                     dk + (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id_s, kk > 0);
         }
@@ -691,7 +692,7 @@ __device__ void chunk_mma(const ChunkParams& p, uint8_t* ring, uint8_t* qbuf, Ch
                 umma_ts(tO, tS, dv, id_o, j > ja);
 #pragma unroll
                 for (int ks = 1; ks < kBlocks; ++ks) {
-                    if (ks == kBlocks - 4 && !begun) end_turn(sm);
+                    if (ks == kBlocks - 2 + 0 && !begun) end_turn(sm);
                     umma_ts(tO, tS + 8 * ks, dv + (uint64_t)((ks * 2 * C::kGroup) >> 4), id_o, true);
                 }
                 umma_commit(smem_addr(&sm.o_ready[I]));

@@ -692,7 +692,7 @@ __device__ void chunk_mma(const ChunkParams& p, uint8_t* ring, uint8_t* qbuf, Ch
                 umma_ts(tO, tS, dv, id_o, j > ja);
 #pragma unroll
                 for (int ks = 1; ks < kBlocks; ++ks) {
-                    if (ks == kBlocks - 2 + 0 && !begun) end_turn(sm);
+                    if (ks == kBlocks - 2 && !begun) end_turn(sm);
                     umma_ts(tO, tS + 8 * ks, dv + (uint64_t)((ks * 2 * C::kGroup) >> 4), id_o, true);
                 }
                 umma_commit(smem_addr(&sm.o_ready[I]));

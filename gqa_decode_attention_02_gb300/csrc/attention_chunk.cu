@@ -109,6 +109,11 @@ struct ChunkParams {
     float scale_log2;
 };
 
+// A sequence's new rows, or none where its lengths are out of range.
+struct Seq {
+    int n, ctx, r0;
+    int code;  // 0, or the error
+};
 // KV tiles [t0, t1) of an item, as the scheduler hands them to the other roles (t0 < 0: no
 // more).  Per slot: its row tile's KV tiles [a, b) within the piece, rows in use (0: none),
 // first row of q and out and its position.
@@ -128,7 +133,8 @@ struct ChunkSmem {
     uint64_t all;  // the softmax threads
     long long c0, c1, base;  // range of units; first unit of the first item
     long long quota;
-    int b0, vh0, qi0;
+    int b0, vh0, qi0, nq0;
+    Seq seq0;                // sequence b0, its items per virtual head
     uint32_t tmem, lock;
     volatile int abort_flag;
     volatile int bad[kPieces];
@@ -166,11 +172,6 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-// A sequence's new rows, or none where its lengths are out of range.
-struct Seq {
-    int n, ctx, r0;
-    int code;  // 0, or the error
-};
 __device__ __forceinline__ Seq seq_of(const ChunkParams& p, int r0, int r1, int ctx) {
     Seq s = {r1 - r0, ctx, r0, 0};
     if (r0 < 0 || r1 < r0 || r1 > p.M) {
@@ -234,8 +235,9 @@ struct Walk {
         qi = sm.qi0;
         nq = turn = 0;
         if (c0 < c1) {
-            ahead = read_seq(p, b);
-            load(p);
+            s = sm.seq0;
+            nq = sm.nq0;
+            if (b + 1 < p.B) ahead = read_seq(p, b + 1);
         } else {
             base = c1;  // nothing for this CTA
         }
@@ -420,16 +422,31 @@ __device__ void chunk_plan(const ChunkParams& p, ChunkSmem& sm, long long* cost)
         sm.c1 = max(c0, c1);
         sm.quota = quota;
         sm.b0 = b0;
-        sm.base = 0;
-        sm.vh0 = sm.qi0 = 0;
+        sm.qi0 = 0;
     }
     __syncwarp();
     if (owners) {
         // the virtual head, then the item in it (a run of items per lane)
-        const Seq t = read_seq(p, b0);
+        Seq t;
+        if (few) {
+            t.n = __shfl_sync(kAll, s.n, owner);
+            t.ctx = __shfl_sync(kAll, s.ctx, owner);
+            t.r0 = __shfl_sync(kAll, s.r0, owner);
+            t.code = 0;
+        } else {
+            t = read_seq(p, b0);
+        }
         const int nq = items_of(p, t);
         const int vh = (int)div_ll(c0 - base, one);
         base += vh * one;
+        if (lane == 0) {
+            sm.seq0 = t;
+            sm.nq0 = nq;
+            sm.vh0 = vh;
+            sm.base = base;
+        }
+        if (nq == 1) return;
+        __syncwarp();
         const int run = (nq + 31) / 32;
         const int qlo = min(nq, lane * run), qhi = min(nq, qlo + run);
         long long x = 0;
@@ -445,7 +462,6 @@ __device__ void chunk_plan(const ChunkParams& p, ChunkSmem& sm, long long* cost)
                 at += u;
                 ++qi;
             }
-            sm.vh0 = vh;
             sm.qi0 = qi;
             sm.base = at;
         }
@@ -967,6 +983,7 @@ __device__ bool chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
         if (!whole) {
             __stcg(part + kRows * H + row, m);
             __stcg(part + kRows * (H + 1) + row, bad ? -1.f : l);  // a bad block shows as -1
+            __threadfence();  // before the item's ticket
         }
     }
     if (!ok) give_up(sm, p);
@@ -980,7 +997,6 @@ template <bool BF16, int H>
 __device__ void chunk_shared(const ChunkParams& p, ChunkSmem& sm, float* weight) {
     using C = Ch<H>;
     const int tid = threadIdx.x - 32 * kSoftWarp;
-    __threadfence();  // partial results before the ticket
     int meets = 0;
     auto meet = [&]() {  // the softmax threads
         mbar_arrive(smem_addr(&sm.all));

@@ -40,14 +40,14 @@
 // What it rounds: probabilities to q's dtype before the product with V, the result; sums
 // of probabilities are taken before that rounding, in fp32 as the scores and O.
 //
-// Measured (one GB300, H = 128, bf16, 32 / 8 heads): 2,048 tokens behind 30,720 770 us, 1.38
+// Measured (one GB300, H = 128, bf16, 32 / 8 heads): 2,048 tokens behind 30,720 765 us, 1.39
 // PFLOP/s, 72 % of what a library product of 8192^3 reaches; a step takes 1.75 us (3,300 cycles)
 // for 2,048 cycles of MMAs.  A slot's chain is that long: softmax 1,350 cycles, hand-overs 400,
 // its PV and QK 1,600 from the first to the last (issued by one thread that waits for nothing,
 // the same products take 1,024; with the issuers' waits, turns and commits alone 1,310; the
-// rest is the other slot's, still in the queue).  Short prompts (24 of 200..3,001): 525 us, of
+// rest is the other slot's, still in the queue).  Short prompts (24 of 200..3,001): 519 us, of
 // it some 100 at the items' ends, where both slots store outputs at once.  Single tokens,
-// 256 x 2,048: 358 us, 6.0 TB/s.
+// 256 x 2,048: 353 us, 6.1 TB/s.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -81,6 +81,12 @@ constexpr int kLone = 5, kPair = 6, kStart = 10, kQuota = 10;
 // 23.7).
 constexpr int kNearLone = kLone, kNearPair = 8 * kPair;
 constexpr float kSlack = 8.f;  // log2 slack before O is rescaled
+// Scores from which on fp32 numbers are so far apart (2 in f16, 64 in bf16) that a score
+// scaled in the fma that takes the reference off, not rounded as the reference was, could
+// lie above the slack by more than the type's range (see far_tile).
+template <bool BF16>
+constexpr float kFar = BF16 ? 0x1p29f : 0x1p24f;
+constexpr int kFarBit = 1 << 30;  // positions are below
 constexpr int kPieces = 8;      // pieces between the scheduler and the last role
 constexpr int kMaxSeqs = 16384;
 constexpr uint32_t kColS = 0, kColO = 256;  // tensor-memory columns, 128 per slot
@@ -746,6 +752,84 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+// O's row scaled by f.
+template <int H>
+__device__ __forceinline__ void scale_o(uint32_t tO, float f) {
+#pragma unroll 1
+    for (int c = 0; c < H / 16; ++c) {
+        uint32_t o[16];
+        tmem_ld16(tO + 16 * c, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+        tmem_st16(tO + 16 * c, o);
+    }
+    tmem_wait_st();
+}
+// Columns [a, b) of the 32 from 0 on, as bits.
+__device__ __forceinline__ uint32_t columns(int a, int b) {
+    return (b >= 32 ? ~0u : b <= 0 ? 0u : ~(~0u << b)) & (a <= 0 ? ~0u : a >= 32 ? 0u : ~0u << a);
+}
+
+// The softmax of a tile whose scores, or an earlier tile's, lie beyond kFar, of a warp's 32
+// rows: as chunk_softmax does it, but with the scaled scores rounded before the reference
+// is taken off.  Rare, and a call: with the mask's loop scaling the scores too, inline, prompts
+// took 3.5 % longer; so 24 prompts 543 us, 543 without any of it.
+struct Sums {
+    float m, l;
+    bool ok;
+};
+template <bool BF16, int H>
+__device__ __noinline__ Sums far_tile(uint32_t tS, uint32_t tO, int from, int to, float scale,
+                                      float m, float l, uint32_t bO, int o_phase) {
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        const uint32_t seen = columns(from - 32 * c, to - 32 * c);
+        uint32_t x[32];
+        tmem_ld32(tS + 32 * c, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            const float y = seen >> e & 1u ? __fmul_rn(__uint_as_float(x[e]), scale) : -INFINITY;
+            top = fmaxf(top, y);
+            x[e] = __float_as_uint(y);
+        }
+        tmem_st32(tS + 32 * c, x);
+    }
+    tmem_wait_st();
+    const bool need = __fsub_rn(top, m) > kSlack;
+    if (__any_sync(kAll, need)) {
+        const float f = need && m != -INFINITY ? fast_exp2(m - top) : 1.f;
+        if (o_phase >= 0 && __any_sync(kAll, f != 1.f)) {
+            if (!__all_sync(kAll, wait_for(bO, o_phase))) return {m, l, false};
+            tc_fence_after();
+            scale_o<H>(tO, f);
+        }
+        if (need) {
+            l *= f;
+            m = top;
+        }
+    }
+    const float ref = m == -INFINITY ? 0.f : -m;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        uint32_t x[32], w[16];
+        tmem_ld32(tS + 32 * c, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const float a = fast_exp2(__fadd_rn(__uint_as_float(x[2 * e]), ref));
+            const float b = fast_exp2(__fadd_rn(__uint_as_float(x[2 * e + 1]), ref));
+            w[e] = Elt<BF16>::pack(a, b);
+            l += a + b;
+        }
+        tmem_st16(tS + 16 * c, w);
+    }
+    tmem_wait_st();
+    return {m, l, true};
+}
+
 // Softmax of the row tiles in slot i, a thread per row.
 template <bool BF16, int H>
 __device__ bool chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm) {
@@ -790,24 +874,36 @@ __device__ bool chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
         const bool active = row < count;
         const bool warp_on = 32 * (warp & 3) < count;
         const int lim = pc.pos[i] + (active ? row_t : 0);
-        const int low = p.window > 0 ? lim - p.window + 1 : 0;
+        // (with kFarBit once a row of the warp had scores beyond kFar: no tile is seen whole)
+        int low = p.window > 0 ? max(0, lim - p.window + 1) : 0;
         const int see_lo = pc.see_lo, see_hi = pc.see_hi;
         float m = -INFINITY, l = 0.f;
         for (int j = ja; j < jb; ++j, ++step) {
             ok = __all_sync(kAll, wait_for(bS, step & 1));
             if (!ok) break;
             const int tok = j * kStep;
-            if (warp_on) {
+            auto far = [&]() {
+                low |= kFarBit;
+                const Sums x = far_tile<BF16, H>(tS, tO, low - kFarBit - tok, lim + 1 - tok,
+                                                 p.scale_log2, m, l, bO,
+                                                 j > ja ? (step - 1) & 1 : -1);
+                m = x.m;
+                l = x.l;
+                ok = x.ok;
+            };
+            if (warp_on) do {
                 tc_fence_after();
                 const int from = low - tok, to = lim + 1 - tok;  // columns seen
                 if (!__all_sync(kAll, from <= 0 && to >= kStep)) {
+                    if (low >= kFarBit) {
+                        far();
+                        break;
+                    }
                     // some are not: -inf there, in tensor memory (a loop of its own, so
                     // that the code of the tiles seen whole stays short)
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
-                        const int a = from - 32 * c, b = to - 32 * c;
-                        const uint32_t seen = (b >= 32 ? ~0u : b <= 0 ? 0u : ~(~0u << b)) &
-                                              (a <= 0 ? ~0u : a >= 32 ? 0u : ~0u << a);
+                        const uint32_t seen = columns(from - 32 * c, to - 32 * c);
                         if (__all_sync(kAll, seen == ~0u)) continue;
                         uint32_t x[32];
                         tmem_ld32(tS + 32 * c, x);
@@ -831,25 +927,20 @@ __device__ bool chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
                     for (int x = 2; x < 32; x += 2)
                         mx[c] = max3(mx[c], __uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1]));
                 }
-                const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
-                const bool need = top > m + kSlack;
+                const float top =
+                    __fmul_rn(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]), p.scale_log2);
+                const bool need = __fsub_rn(top, m) > kSlack;
                 if (__any_sync(kAll, need)) {
+                    if (__any_sync(kAll, need && active && fabsf(top) >= kFar<BF16>)) {
+                        far();
+                        break;
+                    }
                     const float f = need && m != -INFINITY ? fast_exp2(m - top) : 1.f;
                     if (j > ja && __any_sync(kAll, f != 1.f)) {  // the last PV has ended
                         ok = __all_sync(kAll, wait_for(bO, (step - 1) & 1));
                         if (!ok) break;
                         tc_fence_after();
-#pragma unroll 1
-                        for (int c = 0; c < H / 16; ++c) {
-                            uint32_t o[16];
-                            tmem_ld16(tO + 16 * c, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int x = 0; x < 16; ++x)
-                                o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                            tmem_st16(tO + 16 * c, o);
-                        }
-                        tmem_wait_st();
+                        scale_o<H>(tO, f);
                     }
                     if (need) {
                         l *= f;
@@ -876,7 +967,8 @@ __device__ bool chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
                 const uint64_t both = add2(sum[0], sum[1]);
                 l += lo2(both) + hi2(both);
                 tmem_wait_st();
-            }
+            } while (false);
+            if (!ok) break;
             // V rows of a block that rows of the item see in part: the others hold anything
             // and become zeros, since 0 * NaN counts (whole blocks came as zeros)
             const int v0 = max(0, see_lo - tok), v1 = min(kStep, see_hi - tok);

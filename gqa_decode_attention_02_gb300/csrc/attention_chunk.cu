@@ -9,8 +9,8 @@
 //     out[i][n] = sum_j softmax_j(scale <q[i][n], K_b[j][k]>) V_b[j][k]
 // over the positions j <= a (with a window W: a - W < j <= a), by an online softmax
 // over tiles of 128 positions: O += exp2(S - m) V and l += sum exp2(S - m) for a
-// running reference m, O and l scaled when a row's maximum passes m by more than 8
-// (in log2), O / l at the end.
+// running reference m (the row's maximum when it is set, in f16 7 less), O and l scaled when
+// the maximum passes the one it was set by by more than 8 (in log2), O / l at the end.
 //
 // An item of work is a KV head and two row tiles (128 query rows each: tokens, and the G
 // heads of each) of one sequence, and walks the 128-position KV tiles that its rows
@@ -37,8 +37,9 @@
 // block [2 groups of 8 rows][H / 64 halves][8 rows x 128 B], 128-byte swizzled, so a block
 // is one box and both operand layouts have one stride between row groups.
 //
-// What it rounds: probabilities to q's dtype before the product with V, the result; sums
-// of probabilities are taken before that rounding, in fp32 as the scores and O.
+// What it rounds: probabilities to q's dtype before the product with V (by half a step, in f16
+// at most 2^-32 of the row's sum where that is more), the result; sums of probabilities are taken before
+// that rounding, in fp32 as the scores and O.
 //
 // Measured (one GB300, H = 128, bf16, 32 / 8 heads): 2,048 tokens behind 30,720 765 us, 1.39
 // PFLOP/s, 72 % of what a library product of 8192^3 reaches; a step takes 1.75 us (3,300 cycles)
@@ -81,6 +82,12 @@ constexpr int kLone = 5, kPair = 6, kStart = 10, kQuota = 10;
 // 23.7).
 constexpr int kNearLone = kLone, kNearPair = 8 * kPair;
 constexpr float kSlack = 8.f;  // log2 slack before O is rescaled
+// How far below a row's maximum its reference is set (log2).  In f16 the largest probability
+// is then 2^7 .. 2^15, near the top of the type's range, and what rounding takes from small
+// ones (2^-25 each) is 2^-32 of it: with the reference at the maximum, positions 17 nats behind
+// it were lost altogether, however many they are.  bf16 has fp32's range.
+template <bool BF16>
+constexpr float kLift = BF16 ? 0.f : 7.f;
 // Scores from which on fp32 numbers are so far apart (2 in f16, 64 in bf16) that a score
 // scaled in the fma that takes the reference off, not rounded as the reference was, could
 // lie above the slack by more than the type's range (see far_tile).
@@ -798,9 +805,10 @@ __device__ __noinline__ Sums far_tile(uint32_t tS, uint32_t tO, int from, int to
         tmem_st32(tS + 32 * c, x);
     }
     tmem_wait_st();
-    const bool need = __fsub_rn(top, m) > kSlack;
+    const bool need = __fsub_rn(top, m) > kSlack + kLift<BF16>;
     if (__any_sync(kAll, need)) {
-        const float f = need && m != -INFINITY ? fast_exp2(m - top) : 1.f;
+        const float next = __fsub_rn(top, kLift<BF16>);
+        const float f = need && m != -INFINITY ? fast_exp2(m - next) : 1.f;
         if (o_phase >= 0 && __any_sync(kAll, f != 1.f)) {
             if (!__all_sync(kAll, wait_for(bO, o_phase))) return {m, l, false};
             tc_fence_after();
@@ -808,7 +816,7 @@ __device__ __noinline__ Sums far_tile(uint32_t tS, uint32_t tO, int from, int to
         }
         if (need) {
             l *= f;
-            m = top;
+            m = next;
         }
     }
     const float ref = m == -INFINITY ? 0.f : -m;
@@ -929,13 +937,14 @@ __device__ bool chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
                 }
                 const float top =
                     __fmul_rn(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]), p.scale_log2);
-                const bool need = __fsub_rn(top, m) > kSlack;
+                const bool need = __fsub_rn(top, m) > kSlack + kLift<BF16>;
                 if (__any_sync(kAll, need)) {
                     if (__any_sync(kAll, need && active && fabsf(top) >= kFar<BF16>)) {
                         far();
                         break;
                     }
-                    const float f = need && m != -INFINITY ? fast_exp2(m - top) : 1.f;
+                    const float next = __fsub_rn(top, kLift<BF16>);
+                    const float f = need && m != -INFINITY ? fast_exp2(m - next) : 1.f;
                     if (j > ja && __any_sync(kAll, f != 1.f)) {  // the last PV has ended
                         ok = __all_sync(kAll, wait_for(bO, (step - 1) & 1));
                         if (!ok) break;
@@ -944,7 +953,7 @@ __device__ bool chunk_softmax(const ChunkParams& p, uint8_t* ring, ChunkSmem& sm
                     }
                     if (need) {
                         l *= f;
-                        m = top;
+                        m = next;
                     }
                 }
                 const float ref = m == -INFINITY ? 0.f : -m;

@@ -737,7 +737,8 @@ gqa_status gqa_kv_append_rotary(const gqa_shape *shape, int64_t rows, const void
  * Row i at position a sees positions 0 .. a, or with shape->window = W > 0 the last W of
  * them; blocks wholly below the earliest token's window are never read.  Otherwise as
  * gqa_verify_attention, for a cache in q's dtype: the softmax in fp32, probabilities
- * rounded to dtype for the product with V, fp32 sums.  Rows outside every sequence's are
+ * rounded to dtype for the product with V (each by half a step of it, in f16 by at most
+ * 2^-32 of their sum where that is more), fp32 sums.  Rows outside every sequence's are
  * neither read for a result nor written.  A score that is NaN makes its row NaN.  A NaN
  * or infinity in V at a position j that some new tokens of the sequence see and others
  * do not may reach the outputs of those others that see any of positions j / 128 * 128

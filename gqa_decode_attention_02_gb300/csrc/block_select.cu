@@ -266,7 +266,7 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Order-preserving bits of a score (-0 as 0; a NaN, which a scale that holds one gives,
+// Order-preserving bits of a score (-0 as 0; a NaN, the score of a block without bounds,
 // below every number).
 __device__ __forceinline__ uint32_t score_key(float x) {
     if (x != x) return 0u;
@@ -384,6 +384,9 @@ __device__ void block_scores(const SelectParams& p, int bk, int nb, int part, in
             vb = fmaxf(vb, __shfl_xor_sync(kFull, vb, o));
         }
         if (t == 0) {
+            // (the limit above made a number of a scale that is none, or minus infinity)
+            if (!(sa >= -kMaxFinite)) va = NAN;
+            if (!(sb >= -kMaxFinite)) vb = NAN;
             const int ia = tile * 16 + g;
             if (ia < nb) store(ia, bads >> g & 1 ? -INFINITY : va);
             if (ia + 8 < nb) store(ia + 8, bads >> (g + 8) & 1 ? -INFINITY : vb);

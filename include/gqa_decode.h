@@ -794,9 +794,11 @@ gqa_status gqa_chunk_attention(const gqa_shape *shape, int64_t rows, const void 
  *   lens         int32 [B]: the tokens that the chosen blocks hold
  *   workspace    gqa_select_workspace_size(shape) bytes of scratch, not cleared
  * Requires 1 <= recent, 0 <= first, first + recent <= keep, shape->T = 1, B <= 16384.
+ * A block whose scale is NaN or minus infinity (its bounds were never made) comes behind
+ * all others; an infinite scale counts as fp32's largest number.
  * Device errors: a length < 1 or too long gives lens 0 and -1 (GQA_ERR_CONTEXT); a bad
- * block id scores lowest (GQA_ERR_BLOCK_ID) and shows in tables if it is chosen all
- * the same.
+ * block id scores minus infinity (GQA_ERR_BLOCK_ID) and shows in tables if it is chosen
+ * all the same.
  *
  * gqa_sparse_decode_attention is gqa_decode_attention with a block table per KV head:
  * tables int32 [B][K][S] (S = shape->max_blocks_per_seq) and lens int32 [B] as chosen, the

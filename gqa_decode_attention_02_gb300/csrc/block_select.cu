@@ -4,7 +4,7 @@
 // KV cache for every token and is bound by that) and §"PagedAttention" (the cache is
 // blocks of 16 tokens, found through a table): a query whose weights lie on few blocks
 // need read only those.  What stands for a block is, per KV head and element d, the
-// largest and the smallest key of its rows; for a query q
+// largest and the smallest key of its rows; for any q
 //     sum_d max(q_d max_d, q_d min_d) >= <q, k>   for every key k of the block
 // bounds every score in it, at a thirtieth of the block's bytes:
 //   bounds  int8 [num_blocks][K][2][H]  (0: largest, 1: smallest), and a scale
@@ -15,7 +15,9 @@
 // that the sums are whole numbers, at most 127 * 127 * 128 < 2^21 + 2^19, the same in any
 // order, exact in fp32; a block's score for a KV head is the largest over its G queries of
 //     (t * s) * sum_d max(c_d max_d, c_d min_d)       (both products rounded in fp32)
-// and equal scores go to the lower block: the choice does not depend on the schedule.
+// (a bound for t c; for q itself, of which c holds the nearest codes, an estimate: <q, k> may
+// pass it by up to t / 2 sum_d |k_d|), and equal scores go to the lower block: the choice does
+// not depend on the schedule.
 #include <cuda_runtime.h>
 
 #include <algorithm>

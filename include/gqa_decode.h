@@ -785,8 +785,10 @@ gqa_status gqa_chunk_attention(const gqa_shape *shape, int64_t rows, const void 
  * others by score, equal scores by the lower block.  With c = rn(q / t), t = max |q| / 127
  * of each of the head's G = N / K queries, a block's score is the largest over them of
  *   (t * s) * sum_d max(c_d max_d, c_d min_d)
- * (whole numbers; the two products rounded in fp32): a bound of what a key of the
- * block can score.  (Of q too a NaN counts as 0, an infinity as the largest number.)
+ * (whole numbers; the two products rounded in fp32): an estimate of what a key of the block
+ * can score.  It bounds <t c, k>, the rounded query's products with the block's keys k; for
+ * q itself a key may pass it by up to t / 2 * sum_d |k_d|, so nothing may be left out by
+ * it as by a guarantee.  (Of q too a NaN counts as 0, an infinity as the largest number.)
  *   q            [B][1][N][H] in dtype; N / K <= 128
  *   tables       int32 [B][K][keep]: the cache blocks chosen, in the sequence's order
  *   blocks       int32 [B][K][keep]: which block of the sequence each is; both -1 past

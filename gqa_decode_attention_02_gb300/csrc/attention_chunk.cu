@@ -74,7 +74,8 @@ constexpr int kThreadsCh = 384;
 constexpr int kRegsIssue = 88, kRegsSoft = 208;
 static_assert(128 * kRegsIssue + 256 * kRegsSoft <= kThreadsCh * 168, "register split");
 // Units of work: a KV tile of an item with one row tile (its bytes: 1.5 us) or two (its
-// MMAs: 1.8 us), an item's start and end; and per CTA at least.
+// MMAs: 1.8 us), an item's start and end; and per CTA at least.  Measured at H = 128, 16-bit
+// rows, G = 4, and used for H = 64 and every G too: they only steer the balance.
 constexpr int kLone = 5, kPair = 6, kStart = 10, kQuota = 10;
 // A range boundary this near to an item's start or end moves there: a smaller piece is not
 // worth its fold (some 5 us with one row tile of few rows, 20 with two full ones; for one
@@ -115,7 +116,7 @@ struct ChunkParams {
     int32_t* status;
     int32_t* flags;         // tickets: of the item whose first piece a CTA holds
     float* partials;        // [grid][2][2][kPart]: slot 0 a later piece, slot 1 a first one
-    int B, M, N, K, G;
+    int B, M, N, G;
     int tpc, hpc, cpt, KC;  // tokens and heads of a row tile; head chunks per KV head
     int max_blocks, num_blocks, window;
     long long table_b, table_k;  // strides of the block tables
@@ -384,8 +385,8 @@ __device__ long long warp_units(const ChunkParams& p, int first, Seq& s) {
     return c;
 }
 
-// Warps 0 .. 3: units of every sequence (`cost`, shared memory, where there are more than
-// a lane each), then warp 0: this CTA's range and the item it starts in.
+// All warps: units of every sequence (`cost`, shared memory; with no more than a lane each
+// warp 0 alone), then warp 0: this CTA's range and the item it starts in.
 template <int H>
 __device__ void chunk_plan(const ChunkParams& p, ChunkSmem& sm, long long* cost) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1361,7 +1362,6 @@ gqa_status launch_chunk_attention(const gqa_shape& s, long long rows, long long 
     p.B = s.B;
     p.M = (int)rows;
     p.N = s.N;
-    p.K = s.K;
     p.max_blocks = s.max_blocks_per_seq;
     p.num_blocks = s.num_blocks;
     p.window = s.window;

@@ -69,3 +69,17 @@ def test_sparse_scores_of_any_size(gpu, dtype):
                                          c.tables[:, None].repeat(1, 2, 1).to(gpu),
                                          c.ctx.to(gpu), scale=2.0 ** power)
         c.check(got[:, 0], scale=2.0 ** power)
+
+
+@pytest.mark.parametrize("dtype,H", [(F16, 128), (BF16, 64)])
+@pytest.mark.parametrize("window", [1, 17, 128, 300, 5000])
+@pytest.mark.parametrize("power", [26, 36])
+def test_windows_of_large_scores(gpu, dtype, H, window, power):
+    g = torch.Generator().manual_seed(window)
+    c = Case([(33, 900), (1, 9000), (300, 300), (3, 3), (64, 30000)], 8, 2, H, dtype, seed=window)
+    whole_scores(c, torch.arange(-3.0, 4.0), g)
+    got = c.run(gpu, scale=2.0 ** power, window=window)
+    assert c.status == 0
+    # (the plain form multiplies what a row does not see by 0: finite numbers there)
+    c.kc, c.vc = (torch.nan_to_num(x, nan=0.0, posinf=0.0) for x in (c.kc, c.vc))
+    c.check(got, window=window, scale=2.0 ** power)

@@ -1015,7 +1015,8 @@ def kv_append_rotary(q, k_new, v_new, k_cache, v_cache, slots, positions, cos_si
     first R elements of a row turn); pairs (i, i + R/2), or (2i, 2i + 1) with
     interleaved=True.  q, k_new and v_new may be parts of one wider row each (a fused
     projection's output).  Returns the rotated queries in q_out (may be q itself;
-    default: a new tensor), whose rows without a token stay as they are."""
+    default: a new tensor of zeros, which is one more write of its bytes), whose rows
+    without a token stay as they are."""
     try:
         dev = q.get_device()
         key = ("rotary", dev, kv, interleaved, pdl, q.shape, q.stride(), q.dtype, k_new.shape,
@@ -1127,7 +1128,8 @@ def chunk_attention(q, k_cache, v_cache, block_tables, context_lens, cu_new, *, 
     positions context_lens[b] - n .. context_lens[b] - 1; their keys and values are in the
     cache [NB,16,K,H] already.  A token sees the positions up to its own, or the last
     `window` of them.  q may be a part of wider rows.  Returns out [M,N,H] (dense), whose
-    rows from cu_new[B] on stay as they are (default out: zeros)."""
+    rows from cu_new[B] on stay as they are (default out: a new tensor of zeros, which is
+    one more write of its bytes)."""
     scale, window = float(scale or 0.0), int(window)
     try:
         dev = q.get_device()

@@ -794,7 +794,9 @@ gqa_status gqa_chunk_attention(const gqa_shape *shape, int64_t rows, const void 
  *   blocks       int32 [B][K][keep]: which block of the sequence each is; both -1 past
  *                the last one
  *   lens         int32 [B]: the tokens that the chosen blocks hold
- *   workspace    gqa_select_workspace_size(shape) bytes of scratch, not cleared
+ *   workspace    gqa_select_workspace_size(shape) bytes of scratch, not cleared (written
+ *                only for sequences of more blocks than fit on the chip: some 9,400 with up
+ *                to 8 query heads per KV head, fewer with more)
  * Requires 1 <= recent, 0 <= first, first + recent <= keep, shape->T = 1, B <= 16384.
  * A block whose scale is NaN or minus infinity (its bounds were never made) comes behind
  * all others; an infinite scale counts as fp32's largest number.
